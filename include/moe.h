@@ -65,13 +65,16 @@ typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
 
 /* operation ids for moe_workspace_bytes */
 enum { MOE_OP_ROUTE = 0, MOE_OP_DISPATCH = 1, MOE_OP_EXPERT_FFN = 2, MOE_OP_ROUTE_BWD = 3, MOE_OP_MOD_SELECT = 4,
-       MOE_OP_EXPERT_FFN_BWD = 5 };
+       MOE_OP_EXPERT_FFN_BWD = 5, MOE_OP_COMBINE_NORM_BWD = 6 };
+
+/* moe_gate modes: the score function, and bits that may be or-ed in */
+enum { MOE_GATE_SOFTMAX = 0, MOE_GATE_SIGMOID = 1, MOE_GATE_RENORM = 0x10, MOE_GATE_GROUP_MAX = 0x20 };
 
 /* moe_route_bwd modes; MOE_ROUTE_DX_WRITE may be or-ed in to overwrite dx instead
  * of accumulating into it, MOE_ROUTE_GATE_RENORM when the forward renormalised the
  * gates (moe_route_ex with MOE_ROUTE_RENORM) */
-enum { MOE_ROUTE_SOFTMAX_TOPK = 0, MOE_ROUTE_MOD_LINEAR = 1, MOE_ROUTE_DX_WRITE = 0x100,
-       MOE_ROUTE_GATE_RENORM = 0x200 };
+enum { MOE_ROUTE_SOFTMAX_TOPK = 0, MOE_ROUTE_MOD_LINEAR = 1, MOE_ROUTE_LOGIT_GRAD = 2,
+       MOE_ROUTE_DX_WRITE = 0x100, MOE_ROUTE_GATE_RENORM = 0x200 };
 
 /* moe_route_ex gate options (bit flags) */
 enum { MOE_ROUTE_RENORM = 0x1, MOE_ROUTE_BIAS_SELECT = 0x2 };
@@ -150,6 +153,64 @@ MOE_API int moe_route_ex(const void* x, const void* w_router, const float* logit
               int T, int H, int E, int K, int dtype, int flags,
               float* logits, int32_t* topk_idx, float* topk_gate,
               void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Gate with expert groups: scores, selection bias, group limit, top-K
+ *
+ *   s[t,e] = softmax(logits[t,:])[e]  (MOE_GATE_SOFTMAX)  or
+ *            1 / (1 + exp(-logits[t,e]))  (MOE_GATE_SIGMOID)
+ *   c[t,e] = s[t,e] + sel_bias[e]       (the bias shifts the selection only)
+ *   The E experts form `groups` runs of E / groups neighbours.  A group ranks by the sum
+ *   of its two largest c (by its largest with MOE_GATE_GROUP_MAX, or where it has one
+ *   expert); the topk_groups highest stay, equal ranks by lower group.
+ *   topk_idx[t,:]  = the K experts of those groups with the largest c, ordered by
+ *                    decreasing c, equal c by increasing expert
+ *   topk_gate[t,k] = scale * s[t,topk_idx[t,k]], with MOE_GATE_RENORM
+ *                    scale * s[t,topk_idx[t,k]] / sum_k' s[t,topk_idx[t,k']]
+ *
+ *   The choice is that of scores in 64 bits: scores are compared in fp32 where they are
+ *   further apart than fp32's error and in fp64 where they are not.  Without sel_bias and
+ *   without a group limit (topk_groups = groups) the logits themselves are compared.
+ *   A logit of -inf takes an expert out of service: it ranks behind every other expert of
+ *   its group (lower expert first), adds nothing to its group's rank (a group with one
+ *   expert in service ranks by that one alone, one with none last), and its gate is 0;
+ *   chosen gates that sum to 0 stay 0 under MOE_GATE_RENORM.  A NaN logit, or a c that is
+ *   NaN, ranks like -inf; a row that holds a NaN logit has NaN gates.
+ *
+ *   logits [T,E] float; sel_bias [E] float, nullable; topk_idx [T,K] int32 out;
+ *   topk_gate [T,K] float out.  1 <= K <= E <= 1024, K <= 16, E a multiple of groups,
+ *   1 <= topk_groups <= groups <= 32, topk_groups * (E / groups) >= K, scale finite.
+ *   No workspace.
+ */
+MOE_API int moe_gate(const float* logits, const float* sel_bias, int T, int E, int K, int groups,
+              int topk_groups, int mode, float scale, int32_t* topk_idx, float* topk_gate, void* stream);
+
+/*
+ * Router GEMM followed by moe_gate: logits = x w_router (kept for moe_gate_bwd), then the
+ * gate above.  x, w_router, dtype, workspace and shape rules as moe_route; the rest as
+ * moe_gate.  The gate reads the logits as stored, in fp32.
+ */
+MOE_API int moe_route_group(const void* x, const void* w_router, const float* sel_bias, int T, int H, int E,
+              int K, int dtype, int groups, int topk_groups, int mode, float scale, float* logits,
+              int32_t* topk_idx, float* topk_gate, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Backward of moe_gate (no gradient through the selection; sel_bias has none)
+ *
+ *   with s, q = the chosen scores and the chosen scores rescaled to sum to 1:
+ *   MOE_GATE_SIGMOID                  d_logits = scale * d_gate * s (1 - s) at the chosen experts
+ *   MOE_GATE_SIGMOID|MOE_GATE_RENORM  d_logits = scale * q (1 - s) (d_gate - <d_gate, q>)
+ *   MOE_GATE_SOFTMAX                  d_logits = scale * s (G - <d_gate, s>) over the whole row,
+ *                                     G = d_gate at the chosen experts, 0 elsewhere
+ *   MOE_GATE_SOFTMAX|MOE_GATE_RENORM  d_logits = scale * q (d_gate - <d_gate, q>)
+ *   and 0 elsewhere; an expert listed twice in a row receives the sum of its shares.
+ *   d_gate [T,K], logits [T,E] float; topk_idx [T,K] int32 as moe_gate wrote it (an index
+ *   outside [0,E) sets MOE_ERR_DEVICE_BOUNDS and has no share); d_logits [T,E] float out,
+ *   every element written.  MOE_GATE_GROUP_MAX is accepted and changes nothing.  Sizes as
+ *   moe_gate.  dw_router and dx follow with moe_route_bwd(MOE_ROUTE_LOGIT_GRAD).
+ */
+MOE_API int moe_gate_bwd(const float* d_gate, const float* logits, const int32_t* topk_idx, int T, int E, int K,
+              int mode, float scale, float* d_logits, void* stream);
 
 /*
  * Dispatch: expert histogram, prefix sum, permutation, gather
@@ -314,6 +375,8 @@ MOE_API int moe_combine(const void* h, const float* gate, const int32_t* dst_row
  *   w_router = w [H], d_gate = d_score [T], logits/topk_idx unused):
  *   d_logits = d_score (nullable), dw_router[h] = sum_t d_score[t] x[t,h],
  *   dx[t,h] += d_score[t] * w[h].
+ * mode MOE_ROUTE_LOGIT_GRAD (d_gate holds the logit gradient [T,E] itself, e.g. from
+ *   moe_gate_bwd; E % 4 == 0; logits and topk_idx unused, d_logits NULL): dw_router and dx as above.
  * The weight gradient is reduced deterministically through the workspace:
  *   moe_workspace_bytes(MOE_OP_ROUTE_BWD, T, H, E, K, 0) bytes.
  */
@@ -337,6 +400,91 @@ MOE_API int moe_permute_bwd(const void* dy, const void* h, const float* gate, co
                     const float* row_scale, const int32_t* out_row, const void* dxs,
                     int T, int H, int K, int dtype,
                     void* dh, float* d_gate, float* d_scale, void* dx, void* stream);
+
+/*
+ * Combine fused with the norms around the block, its gate and its residual scale
+ *
+ *   z[t,:]  = sum_k gate[t,k] * h[dst_row[t*K+k],:]
+ *   n[t,:]  = z[t,:] / sqrt(mean(z[t,:]^2) + eps) * w_post      (w_post NULL: n = z)
+ *   y[t,:]  = residual[t,:] + row_scale[t] * res_scale[:] * n[t,:]
+ *   xn[t,:] = y[t,:] / sqrt(mean(y[t,:]^2) + eps) * w_next      (w_next NULL: no xn)
+ *
+ *   One pass: the block's output never returns to memory, and xn is computed from y before
+ *   y is rounded to dtype.  Sums and means are fp32.
+ *   h [T*K,H] dtype, nullable: without it y = residual, and only xn is written (the norm
+ *   before the first block); gate, dst_row, row_scale, w_post, res_scale and y must then be
+ *   NULL and K 0.
+ *   gate [T,K] float, nullable (1); dst_row [T*K] int32 in [0,T*K), nullable (t*K+k; an
+ *   index outside sets MOE_ERR_DEVICE_BOUNDS and counts as a row of zeros);
+ *   row_scale [T] float, nullable (1); residual [T,H] dtype, nullable (0; required without
+ *   h); w_post, res_scale, w_next [H] float, nullable; y, xn [T,H] dtype out.  y may be
+ *   the same buffer as residual; no other overlap.  eps > 0, finite.  1 <= K <= 16 with h;
+ *   H <= 16384.  No workspace.
+ */
+MOE_API int moe_combine_norm(const void* h, const float* gate, const int32_t* dst_row, const float* row_scale,
+              const void* residual, const float* w_post, const float* res_scale, const float* w_next, float eps,
+              int T, int H, int K, int dtype, void* y, void* xn, void* stream);
+
+/*
+ * Backward of moe_combine_norm
+ *
+ *   dy, dxn = dL/dy and dL/dxn of the forward above, y as it stored it (its norm's
+ *   statistics and the block's are recomputed: nothing else is kept).  With
+ *   v = y / sqrt(mean(y^2) + eps), r = 1 / sqrt(mean(z^2) + eps), u = r z (u = z without w_post),
+ *   a missing w_post, res_scale or row_scale read as 1:
+ *     D        = dy + (w_next dxn - v mean(w_next dxn v)) / sqrt(mean(y^2) + eps)
+ *     d_res    = D
+ *     P        = row_scale res_scale w_post D
+ *     dz       = r (P - u mean(P u))                (dz = P without w_post)
+ *     dh[dst_row[t*K+k],:] = gate[t,k] dz[t,:];  d_gate[t,k] = <dz[t,:], h[dst_row[t*K+k],:]>
+ *     d_scale[t] = sum_c D res_scale w_post u
+ *     dw_post = sum_t row_scale res_scale D u;  d_res_scale = sum_t row_scale w_post D u
+ *     dw_next = sum_t dxn v
+ *   dy [T,H] dtype, nullable (0) where dxn is given; dxn and w_next both or neither, and y
+ *   with them (otherwise y is unused).  h, gate, dst_row, row_scale, w_post, res_scale, eps,
+ *   T, H, K, dtype as in the forward (h NULL: the norm alone).
+ *   Outputs, each nullable: d_res [T,H], dh [T*K,H] dtype (dst_row a permutation);
+ *   d_gate [T,K], d_scale [T] float; dw_post (needs w_post), d_res_scale (needs res_scale),
+ *   dw_next (needs w_next) [H] float, written, not accumulated.  d_res may be the same
+ *   buffer as dy or dxn; no other overlap.
+ *   Workspace: moe_workspace_bytes(MOE_OP_COMBINE_NORM_BWD, T, H, 0, K, 0) bytes (partial
+ *   column sums, added in a fixed order); it may be NULL where the three column sums are.
+ *   Calls that may run at the same time need distinct workspaces.
+ */
+MOE_API int moe_combine_norm_bwd(const void* dy, const void* dxn, const void* h, const float* gate,
+              const int32_t* dst_row, const float* row_scale, const void* y, const float* w_post,
+              const float* res_scale, const float* w_next, float eps, int T, int H, int K, int dtype,
+              void* d_res, void* dh, float* d_gate, float* d_scale, float* dw_post, float* d_res_scale,
+              float* dw_next, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Activation checkpoint in 8 bits
+ *
+ *   Every run of 32 neighbours of a row (the last one of a row may be shorter) shares one
+ *   power of two: with a = max |x| of the run, e = the least integer >= -126 with
+ *   a <= 127 * 2^e, scale[row, run] = e + 127, q = x / 2^e rounded to the nearest integer,
+ *   halves to even.  A value is off by at most 2^(e-1), at most a / 127 (a / 254 to a / 127
+ *   by where a lies between powers of two).  A run that holds an infinity or a NaN has
+ *   scale 255 and q 0, and is restored as NaN.
+ *   x [rows,N] dtype; q [rows,N] int8 out; scale [rows, ceil(N/32)] uint8 out.  N a
+ *   multiple of 8 (bf16) or 4 (fp32).
+ */
+MOE_API int moe_ckpt_pack(const void* x, int rows, int N, int dtype, int8_t* q, uint8_t* scale, void* stream);
+
+/* x[row, c] = q[row, c] * 2^(scale - 127): what the checkpoint stands for (exact in both types
+ * unless the power of two falls below the type's range). */
+MOE_API int moe_ckpt_unpack(const int8_t* q, const uint8_t* scale, int rows, int N, int dtype, void* x, void* stream);
+
+/*
+ * The checkpoint of [g | u] in the expert FFN's backward
+ *
+ *   q [rows, 2*Hp], scale [rows, ceil(2*Hp/32)] = moe_ckpt_pack of the gu that
+ *   moe_expert_ffn_ex wrote.  gu [rows, 2*Hp] dtype out (nullable) = the restored g and u;
+ *   act [rows, Hp] dtype out (nullable) = silu(g) * u of the restored values: the two inputs
+ *   that moe_expert_ffn_bwd takes from the forward.  Hp a multiple of 8 (bf16) or 4 (fp32).
+ */
+MOE_API int moe_ckpt_swiglu(const int8_t* q, const uint8_t* scale, int rows, int Hp, int dtype, void* gu, void* act,
+              void* stream);
 
 /*
  * Mixture-of-Depths capacity router                       [FW, MoD paragraph]

@@ -31,9 +31,16 @@ MOE_OP_EXPERT_FFN = 2
 MOE_OP_ROUTE_BWD = 3
 MOE_OP_MOD_SELECT = 4
 MOE_OP_EXPERT_FFN_BWD = 5
+MOE_OP_COMBINE_NORM_BWD = 6
+
+MOE_GATE_SOFTMAX = 0
+MOE_GATE_SIGMOID = 1
+MOE_GATE_RENORM = 0x10
+MOE_GATE_GROUP_MAX = 0x20
 
 MOE_ROUTE_SOFTMAX_TOPK = 0
 MOE_ROUTE_MOD_LINEAR = 1
+MOE_ROUTE_LOGIT_GRAD = 2
 MOE_ROUTE_DX_WRITE = 0x100
 MOE_ROUTE_GATE_RENORM = 0x200
 
@@ -44,7 +51,8 @@ EXPORTS = ("moe_status_str", "moe_version", "moe_kernel_launches", "moe_workspac
            "moe_check_wait_timeout",
            "moe_route", "moe_route_ex", "moe_dispatch", "moe_dispatch_noalloc", "moe_expert_ffn",
            "moe_expert_ffn_ex", "moe_expert_ffn_gather", "moe_expert_ffn_bwd", "moe_combine", "moe_route_bwd",
-           "moe_permute_bwd", "mod_select", "moe_ep_plan")
+           "moe_permute_bwd", "mod_select", "moe_ep_plan", "moe_gate", "moe_gate_bwd", "moe_route_group",
+           "moe_combine_norm", "moe_combine_norm_bwd", "moe_ckpt_pack", "moe_ckpt_unpack", "moe_ckpt_swiglu")
 
 
 class MoEError(RuntimeError):
@@ -58,6 +66,7 @@ _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _Z = ctypes.c_size_t
+_F = ctypes.c_float
 
 _SIGS = {
     "moe_status_str": (ctypes.c_char_p, [_I]),
@@ -78,6 +87,14 @@ _SIGS = {
     "moe_route_bwd": (_I, [_I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _Z, _P]),
     "moe_permute_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P]),
     "mod_select": (_I, [_P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _Z, _P]),
+    "moe_gate": (_I, [_P, _P, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P]),
+    "moe_gate_bwd": (_I, [_P, _P, _P, _I, _I, _I, _I, _F, _P, _P]),
+    "moe_route_group": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P, _Z, _P]),
+    "moe_combine_norm": (_I, [_P] * 8 + [_F, _I, _I, _I, _I, _P, _P, _P]),
+    "moe_combine_norm_bwd": (_I, [_P] * 10 + [_F, _I, _I, _I, _I] + [_P] * 8 + [_Z, _P]),
+    "moe_ckpt_pack": (_I, [_P, _I, _I, _I, _P, _P, _P]),
+    "moe_ckpt_unpack": (_I, [_P, _P, _I, _I, _I, _P, _P]),
+    "moe_ckpt_swiglu": (_I, [_P, _P, _I, _I, _I, _P, _P, _P]),
     "moe_ep_plan": (_I, [_I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
 }
 
@@ -231,6 +248,111 @@ def mod_select(x, w_mod, B, L, H, C, dtype, score, sel, sel_score, mask, x_sel, 
     _check("mod_select", lib().mod_select(_ptr(x), _ptr(w_mod), B, L, H, C, dtype, _ptr(score),
                                           _ptr(sel), _ptr(sel_score), _ptr(mask), _ptr(x_sel),
                                           _ptr(y_skip), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def _args(fn, *tensors):
+    """Addresses of (name, tensor, dtype, elements) arguments: each None, a raw address, or a
+    contiguous tensor of that type and at least that many elements on the current device."""
+    dev = None
+    out = []
+    for name, t, dtype, n in tensors:
+        if t is None or isinstance(t, int):
+            out.append(t)
+            continue
+        if dev is None:
+            import torch
+            dev = torch.cuda.current_device() if t.is_cuda else -2
+        if t.get_device() != dev:
+            raise ValueError(f"{fn}: {name} is not on the current CUDA device")
+        if t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
+            raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of at least {n} elements, "
+                             f"not {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+        out.append(t.data_ptr())
+    return out
+
+
+def _tdt(fn, dtype):
+    import torch
+    if dtype not in (MOE_F32, MOE_BF16):
+        raise MoEError(fn, MOE_ERR_INVALID_ARG, moe_status_str(MOE_ERR_INVALID_ARG))
+    return torch.bfloat16 if dtype == MOE_BF16 else torch.float32
+
+
+def moe_gate(logits, sel_bias, T, E, K, groups, topk_groups, mode, scale, topk_idx, topk_gate, stream=None):
+    import torch
+    f32 = torch.float32
+    l, b, i, g = _args("moe_gate", ("logits", logits, f32, T * E), ("sel_bias", sel_bias, f32, E),
+                       ("topk_idx", topk_idx, torch.int32, T * K), ("topk_gate", topk_gate, f32, T * K))
+    _check("moe_gate", lib().moe_gate(l, b, T, E, K, groups, topk_groups, mode, scale, i, g, _stream(stream)))
+
+
+def moe_gate_bwd(d_gate, logits, topk_idx, T, E, K, mode, scale, d_logits, stream=None):
+    import torch
+    f32 = torch.float32
+    dg, l, i, dl = _args("moe_gate_bwd", ("d_gate", d_gate, f32, T * K), ("logits", logits, f32, T * E),
+                         ("topk_idx", topk_idx, torch.int32, T * K), ("d_logits", d_logits, f32, T * E))
+    _check("moe_gate_bwd", lib().moe_gate_bwd(dg, l, i, T, E, K, mode, scale, dl, _stream(stream)))
+
+
+def moe_route_group(x, w_router, sel_bias, T, H, E, K, dtype, groups, topk_groups, mode, scale, logits, topk_idx,
+                    topk_gate, ws=None, ws_bytes=0, stream=None):
+    import torch
+    f32, tdt = torch.float32, _tdt("moe_route_group", dtype)
+    xp, wp, b, l, i, g, w = _args(
+        "moe_route_group", ("x", x, tdt, T * H), ("w_router", w_router, tdt, H * E), ("sel_bias", sel_bias, f32, E),
+        ("logits", logits, f32, T * E), ("topk_idx", topk_idx, torch.int32, T * K),
+        ("topk_gate", topk_gate, f32, T * K), ("ws", ws, torch.uint8, ws_bytes))
+    _check("moe_route_group", lib().moe_route_group(xp, wp, b, T, H, E, K, dtype, groups, topk_groups, mode, scale, l,
+                                                    i, g, w, ws_bytes, _stream(stream)))
+
+
+def moe_combine_norm(h, gate, dst_row, row_scale, residual, w_post, res_scale, w_next, eps, T, H, K, dtype, y, xn,
+                     stream=None):
+    import torch
+    f32, tdt = torch.float32, _tdt("moe_combine_norm", dtype)
+    a = _args("moe_combine_norm", ("h", h, tdt, T * K * H), ("gate", gate, f32, T * K),
+              ("dst_row", dst_row, torch.int32, T * K), ("row_scale", row_scale, f32, T),
+              ("residual", residual, tdt, T * H), ("w_post", w_post, f32, H), ("res_scale", res_scale, f32, H),
+              ("w_next", w_next, f32, H), ("y", y, tdt, T * H), ("xn", xn, tdt, T * H))
+    _check("moe_combine_norm", lib().moe_combine_norm(*a[:8], eps, T, H, K, dtype, a[8], a[9], _stream(stream)))
+
+
+def moe_combine_norm_bwd(dy, dxn, h, gate, dst_row, row_scale, y, w_post, res_scale, w_next, eps, T, H, K, dtype,
+                         d_res, dh, d_gate, d_scale, dw_post, d_res_scale, dw_next, ws=None, ws_bytes=0, stream=None):
+    import torch
+    f32, tdt = torch.float32, _tdt("moe_combine_norm_bwd", dtype)
+    n, R = T * H, T * K
+    a = _args("moe_combine_norm_bwd", ("dy", dy, tdt, n), ("dxn", dxn, tdt, n), ("h", h, tdt, R * H),
+              ("gate", gate, f32, R), ("dst_row", dst_row, torch.int32, R), ("row_scale", row_scale, f32, T),
+              ("y", y, tdt, n), ("w_post", w_post, f32, H), ("res_scale", res_scale, f32, H),
+              ("w_next", w_next, f32, H), ("d_res", d_res, tdt, n), ("dh", dh, tdt, R * H), ("d_gate", d_gate, f32, R),
+              ("d_scale", d_scale, f32, T), ("dw_post", dw_post, f32, H), ("d_res_scale", d_res_scale, f32, H),
+              ("dw_next", dw_next, f32, H), ("ws", ws, torch.uint8, ws_bytes))
+    _check("moe_combine_norm_bwd", lib().moe_combine_norm_bwd(*a[:10], eps, T, H, K, dtype, *a[10:], ws_bytes,
+                                                              _stream(stream)))
+
+
+def moe_ckpt_pack(x, rows, N, dtype, q, scale, stream=None):
+    import torch
+    a = _args("moe_ckpt_pack", ("x", x, _tdt("moe_ckpt_pack", dtype), rows * N), ("q", q, torch.int8, rows * N),
+              ("scale", scale, torch.uint8, rows * ((N + 31) // 32)))
+    _check("moe_ckpt_pack", lib().moe_ckpt_pack(a[0], rows, N, dtype, a[1], a[2], _stream(stream)))
+
+
+def moe_ckpt_unpack(q, scale, rows, N, dtype, x, stream=None):
+    import torch
+    a = _args("moe_ckpt_unpack", ("q", q, torch.int8, rows * N), ("scale", scale, torch.uint8, rows * ((N + 31) // 32)),
+              ("x", x, _tdt("moe_ckpt_unpack", dtype), rows * N))
+    _check("moe_ckpt_unpack", lib().moe_ckpt_unpack(a[0], a[1], rows, N, dtype, a[2], _stream(stream)))
+
+
+def moe_ckpt_swiglu(q, scale, rows, Hp, dtype, gu, act, stream=None):
+    import torch
+    tdt = _tdt("moe_ckpt_swiglu", dtype)
+    a = _args("moe_ckpt_swiglu", ("q", q, torch.int8, 2 * rows * Hp),
+              ("scale", scale, torch.uint8, rows * ((2 * Hp + 31) // 32)), ("gu", gu, tdt, 2 * rows * Hp),
+              ("act", act, tdt, rows * Hp))
+    _check("moe_ckpt_swiglu", lib().moe_ckpt_swiglu(a[0], a[1], rows, Hp, dtype, a[2], a[3], _stream(stream)))
 
 
 def moe_ep_plan(R, E, S, K, B, counts):

@@ -246,6 +246,20 @@ __global__ void copy_f32_kernel(const float* __restrict__ a, float* __restrict__
     b[i] = a[i];
 }
 
+// the exact three-part split of a logit gradient that is already there
+__global__ void __launch_bounds__(256) split_logit_grad_kernel(const float* __restrict__ dl, long long n,
+                                                               bf16* __restrict__ dl3) {
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < n / 4; i += gridDim.x * 256LL) {
+    const float4 f = __ldg(reinterpret_cast<const float4*>(dl) + i);
+    const float v[4] = {f.x, f.y, f.z, f.w};
+    __align__(8) bf16 part[3][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) split3(v[j], part[0][j], part[1][j], part[2][j]);
+#pragma unroll
+    for (int s = 0; s < 3; ++s) *reinterpret_cast<uint2*>(dl3 + s * n + 4 * i) = *reinterpret_cast<const uint2*>(part[s]);
+  }
+}
+
 // dw[i] = sum_s part[s][i] in a fixed order (the same result every run).  A
 // block covers 32 consecutive outputs with 8 warps: warp q adds splits q, q+8,
 // q+16, ... in increasing order for output base + lane, so every load
@@ -689,6 +703,27 @@ int launch_route(const void* x, const void* w, const float* bias, int T, int H, 
   return launch_status();
 }
 
+int launch_route_logits(const void* x, const void* w, int T, int H, int E, int K, int dtype, float* logits,
+                        int32_t* idx, float* gate, void* ws, int* S, cudaStream_t s) {
+  *S = 1;
+  if (router_stream_applies(dtype, H, E))
+    return launch_router_stream(x, w, nullptr, nullptr, false, T, H, E, K, logits, idx, gate, s);
+  if (dtype == MOE_BF16) {
+    *S = router_tc_splits(T, H, E);
+    if (*S == 1 && E <= 64)
+      return launch_router_tc(x, w, nullptr, nullptr, false, T, H, E, logits, 1, K, idx, gate, s);
+    return launch_router_tc(x, w, nullptr, nullptr, false, T, H, E, *S > 1 ? static_cast<float*>(ws) : logits, *S, 0,
+                            nullptr, nullptr, s);
+  }
+  SimtGemmArgs a{};
+  a.A = x; a.a_sm = H; a.a_sk = 1;
+  a.B = w; a.b_sg = 0; a.b_sk = E; a.b_sn = 1;
+  a.C = logits; a.c_sm = E;
+  a.M = T; a.N = E; a.K = H; a.groups = 1;
+  a.epilogue = 2; a.swiglu = false;
+  return launch_simt_gemm(a, dtype, dtype, MOE_F32, s);
+}
+
 int router_dw_tc_splits(int T, int H, int E);
 int launch_router_dw_tc(const void* x, const void* dl3, int T, int H, int E, float* part, cudaStream_t s);
 bool router_bwd_tc_applies(int H, int E);
@@ -699,8 +734,11 @@ int launch_router_dx_tc(const void* dl3, const void* w, int T, int H, int E, boo
 
 // The tensor-core router backward serves bf16 layers whose W_r rows are
 // 16-byte multiples (E % 8 == 0) and whose dx rows tile by 64 columns.
+// A given logit gradient of 8 or 16 experts stays on FFMA: the streaming passes
+// that serve these counts form the gradient themselves.
 static bool route_bwd_on_tensor_cores(int mode, int dtype, int H, int E) {
-  return mode == MOE_ROUTE_SOFTMAX_TOPK && dtype == MOE_BF16 && E % 8 == 0 && H % 64 == 0;
+  if (mode == MOE_ROUTE_LOGIT_GRAD && E < 32) return false;
+  return mode != MOE_ROUTE_MOD_LINEAR && dtype == MOE_BF16 && E % 8 == 0 && H % 64 == 0;
 }
 
 // workspace: [fp32 partials of dW][fp32 dl (when d_logits is not given)][bf16 dl in three parts]
@@ -769,8 +807,9 @@ int launch_route_bwd(int mode, const float* d_gate, const float* logits, const i
     if (st == MOE_OK && dw) st = launch_reduce(part, router_bwd_stream_splits(T, H, E), H, E, dw, s);
     return st;
   }
-  // linear score (E = K = 1): the score gradient is the logit gradient, used as is
-  float* dl = mode == MOE_ROUTE_MOD_LINEAR ? const_cast<float*>(d_gate)
+  // linear score (E = K = 1): the score gradient is the logit gradient, used as is;
+  // MOE_ROUTE_LOGIT_GRAD hands the logit gradient in
+  float* dl = mode != MOE_ROUTE_SOFTMAX_TOPK ? const_cast<float*>(d_gate)
               : d_logits ? d_logits : reinterpret_cast<float*>(wsb + lay.part);
   const bool tc = route_bwd_on_tensor_cores(mode, dtype, H, E);
   bf16* dl3 = tc ? reinterpret_cast<bf16*>(wsb + lay.part + lay.dl) : nullptr;
@@ -787,11 +826,13 @@ int launch_route_bwd(int mode, const float* d_gate, const float* logits, const i
       softmax_topk_bwd_kernel<16><<<grid, 32 * ROWS_PER_CTA, 0, s>>>(logits, idx, d_gate, rn, T, E, K, dl, dl3);
     else
       softmax_topk_bwd_kernel<32><<<grid, 32 * ROWS_PER_CTA, 0, s>>>(logits, idx, d_gate, rn, T, E, K, dl, dl3);
+  } else if (mode == MOE_ROUTE_LOGIT_GRAD) {
+    if (tc) split_logit_grad_kernel<<<rows_grid(T), 256, 0, s>>>(dl, (long long)T * E, dl3);
   } else if (d_logits) {
     // the logit gradient output of the linear score is d_score itself
     copy_f32_kernel<<<rows_grid(T), 256, 0, s>>>(d_gate, d_logits, (long long)T);
   }
-  int st = (mode == MOE_ROUTE_SOFTMAX_TOPK || d_logits) ? launch_status() : MOE_OK;
+  int st = (mode == MOE_ROUTE_SOFTMAX_TOPK || d_logits || (mode == MOE_ROUTE_LOGIT_GRAD && tc)) ? launch_status() : MOE_OK;
   if (st != MOE_OK) return st;
 
   if (tc && router_bwd_tc_applies(H, E) && (dw || dx)) {

@@ -1,4 +1,5 @@
 // The C ABI: argument validation, workspace sizing and launches.
+#include <math.h>
 #include <stdint.h>
 
 #include <atomic>
@@ -84,6 +85,7 @@ size_t moe_workspace_bytes(int op, int T, int H, int E, int K, int Hp) {
     case MOE_OP_DISPATCH: return E > 0 ? dispatch_ws_bytes(T, E, K) : 0;
     case MOE_OP_ROUTE_BWD: return (E > 0 && H > 0) ? route_bwd_ws_bytes(T, H, E) : 0;
     case MOE_OP_EXPERT_FFN: return expert_ffn_ws_bytes();
+    case MOE_OP_COMBINE_NORM_BWD: return H > 0 ? combine_norm_bwd_ws_bytes(T, H) : 0;
     case MOE_OP_EXPERT_FFN_BWD: return Hp > 0 ? expert_ffn_bwd_ws_bytes((int)((long long)T * K), Hp) : 0;
     default: return 0;
   }
@@ -129,6 +131,128 @@ int moe_route(const void* x, const void* w_router, const float* logit_bias, int 
               size_t ws_bytes, void* stream) {
   return moe_route_ex(x, w_router, logit_bias, T, H, E, K, dtype, 0, logits, topk_idx, topk_gate, ws, ws_bytes,
                       stream);
+}
+
+static int check_gate(int T, int E, int K, int groups, int topk_groups, int mode, float scale) {
+  if (T < 0 || E < 1 || E > 1024 || K < 1 || K > E || K > 16 || !isfinite(scale)) return MOE_ERR_INVALID_ARG;
+  if (groups < 1 || groups > 32 || E % groups != 0 || topk_groups < 1 || topk_groups > groups ||
+      topk_groups * (E / groups) < K)
+    return MOE_ERR_INVALID_ARG;
+  if ((mode & ~(MOE_GATE_SIGMOID | MOE_GATE_RENORM | MOE_GATE_GROUP_MAX)) != 0) return MOE_ERR_INVALID_ARG;
+  return (long long)T * K > 0x7fffffffll ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+int moe_gate(const float* logits, const float* sel_bias, int T, int E, int K, int groups, int topk_groups, int mode,
+             float scale, int32_t* topk_idx, float* topk_gate, void* stream) {
+  int st = check_gate(T, E, K, groups, topk_groups, mode, scale);
+  if (st != MOE_OK) return st;
+  if (T > 0 && (!logits || !topk_idx || !topk_gate)) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned({logits, sel_bias, topk_idx, topk_gate})) return MOE_ERR_MISALIGNED;
+  return launch_gate(const_cast<float*>(logits), nullptr, 1, sel_bias, T, E, K, groups, topk_groups, mode, scale,
+                     topk_idx, topk_gate, as_stream(stream));
+}
+
+int moe_route_group(const void* x, const void* w_router, const float* sel_bias, int T, int H, int E, int K, int dtype,
+                    int groups, int topk_groups, int mode, float scale, float* logits, int32_t* topk_idx,
+                    float* topk_gate, void* ws, size_t ws_bytes, void* stream) {
+  if (!valid_dtype(dtype) || H < 1) return MOE_ERR_INVALID_ARG;
+  int st = check_gate(T, E, K, groups, topk_groups, mode, scale);
+  if (st != MOE_OK) return st;
+  if ((T > 0 && (!x || !logits || !topk_idx || !topk_gate)) || !w_router) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned({x, w_router, sel_bias, logits, topk_idx, topk_gate, ws})) return MOE_ERR_MISALIGNED;
+  if (H % vec_elems(dtype) != 0 || E % vec_elems(dtype) != 0) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  const size_t need = dtype == MOE_BF16 ? route_ws_bytes(T, H, E) : 0;
+  if (need > 0 && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  int S = 1;
+  st = launch_route_logits(x, w_router, T, H, E, K, dtype, logits, topk_idx, topk_gate, ws, &S, as_stream(stream));
+  if (st != MOE_OK) return st;
+  return launch_gate(logits, S > 1 ? static_cast<const float*>(ws) : nullptr, S, sel_bias, T, E, K, groups,
+                     topk_groups, mode, scale, topk_idx, topk_gate, as_stream(stream));
+}
+
+int moe_gate_bwd(const float* d_gate, const float* logits, const int32_t* topk_idx, int T, int E, int K, int mode,
+                 float scale, float* d_logits, void* stream) {
+  int st = check_gate(T, E, K, 1, 1, mode, scale);
+  if (st != MOE_OK) return st;
+  if (T > 0 && (!d_gate || !logits || !topk_idx || !d_logits)) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned({d_gate, logits, topk_idx, d_logits})) return MOE_ERR_MISALIGNED;
+  return launch_gate_bwd(d_gate, logits, topk_idx, T, E, K, mode, scale, d_logits, as_stream(stream));
+}
+
+static int check_combine_norm(const void* h, const float* gate, const int32_t* dst_row, const float* row_scale,
+                              const float* w_post, const float* res_scale, float eps, int T, int H, int K, int dtype) {
+  if (!valid_dtype(dtype) || T < 0 || H < 1 || !(eps > 0) || !isfinite(eps)) return MOE_ERR_INVALID_ARG;
+  if (K < 0 || K > 16) return MOE_ERR_INVALID_ARG;
+  if (K == 0 && (h || gate || dst_row || row_scale || w_post || res_scale)) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && K > 0 && !h) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned({h, gate, dst_row, row_scale, w_post, res_scale})) return MOE_ERR_MISALIGNED;
+  if (H % vec_elems(dtype) != 0 || H > 16384 || (long long)T * K > 0x7fffffffll) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+int moe_combine_norm(const void* h, const float* gate, const int32_t* dst_row, const float* row_scale,
+                     const void* residual, const float* w_post, const float* res_scale, const float* w_next, float eps,
+                     int T, int H, int K, int dtype, void* y, void* xn, void* stream) {
+  int st = check_combine_norm(h, gate, dst_row, row_scale, w_post, res_scale, eps, T, H, K, dtype);
+  if (st != MOE_OK) return st;
+  if (K == 0 && (y || !w_next || (T > 0 && !residual))) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && ((K > 0 && !y) || (w_next != nullptr) != (xn != nullptr))) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned({residual, w_next, y, xn})) return MOE_ERR_MISALIGNED;
+  return launch_combine_norm(h, gate, dst_row, row_scale, residual, w_post, res_scale, w_next, eps, T, H, K, dtype, y,
+                             xn, as_stream(stream));
+}
+
+int moe_combine_norm_bwd(const void* dy, const void* dxn, const void* h, const float* gate, const int32_t* dst_row,
+                         const float* row_scale, const void* y, const float* w_post, const float* res_scale,
+                         const float* w_next, float eps, int T, int H, int K, int dtype, void* d_res, void* dh,
+                         float* d_gate, float* d_scale, float* dw_post, float* d_res_scale, float* dw_next, void* ws,
+                         size_t ws_bytes, void* stream) {
+  int st = check_combine_norm(h, gate, dst_row, row_scale, w_post, res_scale, eps, T, H, K, dtype);
+  if (st != MOE_OK) return st;
+  if (T > 0 && ((w_next != nullptr) != (dxn != nullptr) || (dxn && !y) || (!dy && !dxn))) return MOE_ERR_INVALID_ARG;
+  if (K == 0 && (dh || d_gate || d_scale)) return MOE_ERR_INVALID_ARG;
+  if ((dw_post && !w_post) || (d_res_scale && !res_scale) || (dw_next && !w_next)) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned({dy, dxn, y, w_next, d_res, dh, d_gate, d_scale, dw_post, d_res_scale, dw_next, ws}))
+    return MOE_ERR_MISALIGNED;
+  if ((dw_post || d_res_scale || dw_next) && (!ws || ws_bytes < combine_norm_bwd_ws_bytes(T, H)))
+    return MOE_ERR_WORKSPACE;
+  return launch_combine_norm_bwd(dy, dxn, h, gate, dst_row, row_scale, y, w_post, res_scale, w_next, eps, T, H, K,
+                                 dtype, d_res, dh, d_gate, d_scale, dw_post, d_res_scale, dw_next, ws,
+                                 as_stream(stream));
+}
+
+static int check_ckpt(const void* q, const void* scale, int rows, int N, int dtype) {
+  if (!valid_dtype(dtype) || rows < 0 || N < 1) return MOE_ERR_INVALID_ARG;
+  if (rows > 0 && (!q || !scale)) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned({q, scale})) return MOE_ERR_MISALIGNED;
+  return N % vec_elems(dtype) != 0 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+int moe_ckpt_pack(const void* x, int rows, int N, int dtype, int8_t* q, uint8_t* scale, void* stream) {
+  int st = check_ckpt(q, scale, rows, N, dtype);
+  if (st != MOE_OK) return st;
+  if (rows > 0 && !x) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x)) return MOE_ERR_MISALIGNED;
+  return launch_ckpt_pack(x, rows, N, dtype, q, scale, as_stream(stream));
+}
+
+int moe_ckpt_unpack(const int8_t* q, const uint8_t* scale, int rows, int N, int dtype, void* x, void* stream) {
+  int st = check_ckpt(q, scale, rows, N, dtype);
+  if (st != MOE_OK) return st;
+  if (rows > 0 && !x) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x)) return MOE_ERR_MISALIGNED;
+  return launch_ckpt_unpack(q, scale, rows, N, dtype, x, as_stream(stream));
+}
+
+int moe_ckpt_swiglu(const int8_t* q, const uint8_t* scale, int rows, int Hp, int dtype, void* gu, void* act,
+                    void* stream) {
+  if (Hp < 1 || Hp > 0x3fffffff) return MOE_ERR_INVALID_ARG;
+  int st = check_ckpt(q, scale, rows, 2 * Hp, dtype);
+  if (st != MOE_OK) return st;
+  if (Hp % vec_elems(dtype) != 0) return MOE_ERR_UNSUPPORTED;
+  if (!all_aligned({gu, act})) return MOE_ERR_MISALIGNED;
+  return launch_ckpt_swiglu(q, scale, rows, Hp, dtype, gu, act, as_stream(stream));
 }
 
 int moe_dispatch(const void* x, const int32_t* topk_idx, int T, int H, int E, int K, int dtype,
@@ -240,6 +364,9 @@ int moe_route_bwd(int mode, const float* d_gate, const float* logits, const int3
   if (renorm && mode != MOE_ROUTE_SOFTMAX_TOPK) return MOE_ERR_INVALID_ARG;
   if (mode == MOE_ROUTE_SOFTMAX_TOPK) {
     if (T > 0 && (!logits || !topk_idx)) return MOE_ERR_INVALID_ARG;
+    if (E % 4 != 0) return MOE_ERR_UNSUPPORTED;
+  } else if (mode == MOE_ROUTE_LOGIT_GRAD) {
+    if (d_logits) return MOE_ERR_INVALID_ARG;
     if (E % 4 != 0) return MOE_ERR_UNSUPPORTED;
   } else if (mode == MOE_ROUTE_MOD_LINEAR) {
     if (E != 1 || K != 1) return MOE_ERR_INVALID_ARG;

@@ -137,6 +137,34 @@ int launch_router_bwd_stream(int mode, const float* d_gate, const float* logits,
                              const void* w, int T, int H, int E, int K, bool renorm, float* d_logits, float* part,
                              void* dx, bool dx_write, cudaStream_t s);
 
+// the router GEMM alone: logits, or with *S > 1 partial sums [S][T][E] over slices of H left in `ws`.
+// Forms whose epilogue already chooses write idx and gate too (softmax top-K), for the caller to overwrite.
+int launch_route_logits(const void* x, const void* w, int T, int H, int E, int K, int dtype, float* logits,
+                        int32_t* idx, float* gate, void* ws, int* S, cudaStream_t s);
+
+// gate with expert groups.  part (nullable): S partial sums of the logits, added in order and stored first
+int launch_gate(float* logits, const float* part, int S, const float* bias, int T, int E, int K, int G, int KG,
+                int mode, float scale, int32_t* idx, float* gate, cudaStream_t s);
+int launch_gate_bwd(const float* d_gate, const float* logits, const int32_t* idx, int T, int E, int K, int mode,
+                    float scale, float* d_logits, cudaStream_t s);
+
+// combine fused with its norms
+size_t combine_norm_bwd_ws_bytes(int T, int H);
+int launch_combine_norm(const void* h, const float* gate, const int32_t* dst_row, const float* row_scale,
+                        const void* residual, const float* w_post, const float* res_scale, const float* w_next,
+                        float eps, int T, int H, int K, int dtype, void* y, void* xn, cudaStream_t s);
+int launch_combine_norm_bwd(const void* dy, const void* dxn, const void* h, const float* gate, const int32_t* dst_row,
+                            const float* row_scale, const void* y, const float* w_post, const float* res_scale,
+                            const float* w_next, float eps, int T, int H, int K, int dtype, void* d_res, void* dh,
+                            float* d_gate, float* d_scale, float* dw_post, float* d_res_scale, float* dw_next, void* ws,
+                            cudaStream_t s);
+
+// 8-bit activation checkpoint
+int launch_ckpt_pack(const void* x, int rows, int N, int dtype, int8_t* q, uint8_t* scale, cudaStream_t s);
+int launch_ckpt_unpack(const int8_t* q, const uint8_t* scale, int rows, int N, int dtype, void* x, cudaStream_t s);
+int launch_ckpt_swiglu(const int8_t* q, const uint8_t* scale, int rows, int Hp, int dtype, void* gu, void* act,
+                       cudaStream_t s);
+
 // dispatch / combine / permute backward
 size_t dispatch_ws_bytes(int T, int E, int K);
 int launch_dispatch(const void* x, const int32_t* idx, int T, int H, int E, int K, int dtype,
