@@ -20,37 +20,133 @@ __device__ __forceinline__ int run_exponent(float a) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((unsigned)(e + 127) << 23); }
 
-// a warp per run, a lane per value
-template <typename T>
-__global__ void __launch_bounds__(256) ckpt_pack_kernel(const T* __restrict__ x, long long rows, int N, int runs,
-                                                        int8_t* __restrict__ q, uint8_t* __restrict__ scale) {
-  const int lane = threadIdx.x & 31;
-  const long long total = rows * runs;
-  for (long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += (long long)gridDim.x * 8) {
-    const long long row = i / runs;
-    const int c = (int)(i - row * runs) * RUN + lane;
-    const float v = c < N ? to_f32(x[row * N + c]) : 0.f;
-    const bool bad = __any_sync(0xffffffffu, !(fabsf(v) < INFINITY));
-    const float a = warp_max(fabsf(v));
+// A thread takes 16 neighbours, so a run is a pair of lanes: the largest magnitude
+// meets in one shuffle, and whole rows of runs (FLAT: N % 32 == 0) move as 16-byte
+// pieces without an index division for each.  Other widths move the same 16 values
+// in pieces of one 16-byte load, the last run of a row in fewer of them.
+constexpr int PER = 16, NT = 256;
+
+// where thread i's 16 values are: value 0 at `at`, `live` of them in the row, run `run`
+struct Place {
+  long long at, run;
+  int live;
+};
+template <bool FLAT>
+__device__ __forceinline__ Place place_of(long long i, int N, int runs) {
+  if (FLAT) return {i * PER, i >> 1, PER};
+  const long long run = i >> 1, row = run / runs;
+  const int c = (int)(run - row * runs) * RUN + (int)(i & 1) * PER;
+  return {row * N + c, run, max(0, min(PER, N - c))};
+}
+
+template <typename T, bool FLAT>
+__global__ void __launch_bounds__(NT) ckpt_pack_kernel(const T* __restrict__ x, long long threads, int N, int runs,
+                                                       int8_t* __restrict__ q, uint8_t* __restrict__ scale) {
+  constexpr int V = Vec16<T>::N;
+  // both lanes of a pair are in range together (threads is even); whole warps stay for the shuffle
+  const long long last = (threads + 31) / 32 * 32;
+  for (long long i = (long long)blockIdx.x * NT + threadIdx.x; i < last; i += (long long)gridDim.x * NT) {
+    Place p = place_of<FLAT>(i, N, runs);
+    if (i >= threads) p.live = 0;
+    uint4 raw[PER / V];
+#pragma unroll
+    for (int k = 0; k < PER / V; ++k)
+      raw[k] = k * V < p.live ? __ldg(reinterpret_cast<const uint4*>(x + p.at) + k) : make_uint4(0, 0, 0, 0);
+    float v[PER], a = 0.f;
+#pragma unroll
+    for (int k = 0; k < PER / V; ++k) Vec16<T>::load_raw_unpack(raw[k], v + k * V);
+    // magnitudes as integers: they order as the numbers do, with infinity and NaN above
+    unsigned top = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    const bool bad = top >= 0x7f800000u;
+    a = __uint_as_float(top);
     const int e = bad ? 128 : run_exponent(a);
-    if (c < N) q[row * N + c] = bad ? 0 : (int8_t)__float2int_rn(v * pow2(-e));
-    if (lane == 0) scale[i] = (uint8_t)(e + 127);
+    const float inv = bad ? 0.f : pow2(-e);
+    // x / 2^e + 1.5 * 2^23 rounds to an integer, halves to even, and leaves it in the low byte
+    unsigned w[PER / 4];
+#pragma unroll
+    for (int k = 0; k < PER / 4; ++k) {
+      unsigned b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[j] = __float_as_uint(fmaf(v[4 * k + j], inv, 12582912.f));
+      w[k] = __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+      if (bad) w[k] = 0;
+    }
+    if (FLAT) {
+      if (p.live) *reinterpret_cast<uint4*>(q + p.at) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < PER / V; ++k) {
+        if (k * V >= p.live) continue;
+        if (V == 8) *reinterpret_cast<uint2*>(q + p.at + 8 * k) = make_uint2(w[(2 * k) % (PER / 4)], w[(2 * k + 1) % (PER / 4)]);
+        else *reinterpret_cast<unsigned*>(q + p.at + 4 * k) = w[k % (PER / 4)];
+      }
+    }
+    if (!(i & 1) && i < threads) scale[p.run] = (uint8_t)(e + 127);
   }
 }
 
-__device__ __forceinline__ float restore(int8_t q, uint8_t scale) {
-  // scale 0 is 2^-127 and never written; 255 marks a run with an infinity or a NaN
-  const float s = scale == 255 ? __int_as_float(0x7fffffff) : scale == 0 ? 5.877471754e-39f : pow2((int)scale - 127);
-  return (float)q * s;
+// the factor that a scale byte stands for; 255 marks a run with an infinity or a NaN, 0 is
+// 2^-127 and never written
+__device__ __forceinline__ float factor(uint8_t s) {
+  return __uint_as_float(s == 255 ? 0x7fffffffu : s == 0 ? 0x00400000u : (unsigned)s << 23);
+}
+// four integers of a word times f: a byte under the exponent of 2^23 is the number 2^23 +
+// q + 128 (its sign bit flipped), so one subtraction converts it
+__device__ __forceinline__ void restore4(unsigned w, float f, float* v) {
+  w ^= 0x80808080u;
+  v[0] = (__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440)) - 8388736.f) * f;
+  v[1] = (__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7441)) - 8388736.f) * f;
+  v[2] = (__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7442)) - 8388736.f) * f;
+  v[3] = (__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7443)) - 8388736.f) * f;
+}
+
+// 16 restored values of a row
+template <typename T, bool FLAT>
+__device__ __forceinline__ void restore16(const int8_t* q, int live, float f, float (&v)[PER]) {
+  constexpr int V = Vec16<T>::N;
+  unsigned w[PER / 4];
+  if (FLAT) {
+    const uint4 r = __ldg(reinterpret_cast<const uint4*>(q));
+    w[0] = r.x; w[1] = r.y; w[2] = r.z; w[3] = r.w;
+  } else {
+#pragma unroll
+    for (int k = 0; k < PER / 4; ++k) w[k] = 0;
+#pragma unroll
+    for (int k = 0; k < PER / V; ++k) {
+      if (k * V >= live) continue;
+      if (V == 8) {
+        const uint2 r = __ldg(reinterpret_cast<const uint2*>(q) + k);
+        w[(2 * k) % (PER / 4)] = r.x;
+        w[(2 * k + 1) % (PER / 4)] = r.y;
+      } else {
+        w[k % (PER / 4)] = __ldg(reinterpret_cast<const unsigned*>(q) + k);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < PER / 4; ++k) restore4(w[k], f, v + 4 * k);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) ckpt_unpack_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ scale,
-                                                          long long rows, int N, int runs, T* __restrict__ x) {
-  const long long n = rows * N;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
-    const long long row = i / N;
-    x[i] = from_f32<T>(restore(q[i], scale[row * runs + (i - row * N) / RUN]));
+__device__ __forceinline__ void store16(T* x, int live, const float (&v)[PER]) {
+  constexpr int V = Vec16<T>::N;
+#pragma unroll
+  for (int k = 0; k < PER / V; ++k)
+    if (k * V < live) Vec16<T>::store(x + k * V, v + k * V);
+}
+
+template <typename T, bool FLAT>
+__global__ void __launch_bounds__(NT) ckpt_unpack_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ scale,
+                                                         long long threads, int N, int runs, T* __restrict__ x) {
+  for (long long i = (long long)blockIdx.x * NT + threadIdx.x; i < threads; i += (long long)gridDim.x * NT) {
+    const Place p = place_of<FLAT>(i, N, runs);
+    if (p.live == 0) continue;
+    float v[PER];
+    restore16<T, FLAT>(q + p.at, p.live, factor(__ldg(scale + p.run)), v);
+    store16<T>(x + p.at, p.live, v);
   }
 }
 
@@ -58,59 +154,95 @@ __global__ void __launch_bounds__(256) ckpt_unpack_kernel(const int8_t* __restri
 // small values (exp(-g) itself overflows from g = -89 on)
 __device__ __forceinline__ float silu(float g) {
   const float e = expf(-fabsf(g));
-  return (g < 0.f ? g * e : g) / (1.f + e);
+  return __fdividef(g < 0.f ? g * e : g, 1.f + e);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) ckpt_swiglu_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ scale,
-                                                          long long rows, int Hp, int runs, T* __restrict__ gu,
-                                                          T* __restrict__ act) {
-  const long long n = rows * Hp;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
-    const long long row = i / Hp;
-    const int c = (int)(i - row * Hp);
+// FLAT (Hp % 32 == 0): 16 columns of g and the same of u; otherwise the columns of one 16-byte
+// vector, which lie in one run of g and one of u whatever Hp is
+template <typename T, bool FLAT>
+__global__ void __launch_bounds__(NT) ckpt_swiglu_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ scale,
+                                                         int rows, int Hp, int runs, int per_row, T* __restrict__ gu,
+                                                         T* __restrict__ act) {
+  constexpr int STEP = FLAT ? PER : Vec16<T>::N;
+  for (long long i = (long long)blockIdx.x * NT + threadIdx.x; i < (long long)rows * per_row;
+       i += (long long)gridDim.x * NT) {
+    const long long row = i / per_row;
+    const int c = (int)(i - row * per_row) * STEP;
     const long long at = row * 2 * Hp + c;
-    const float g = restore(q[at], scale[row * runs + c / RUN]);
-    const float u = restore(q[at + Hp], scale[row * runs + (Hp + c) / RUN]);
+    const uint8_t* s = scale + row * runs;
+    float g[PER], u[PER];
+    restore16<T, FLAT>(q + at, STEP, factor(__ldg(s + c / RUN)), g);
+    restore16<T, FLAT>(q + at + Hp, STEP, factor(__ldg(s + (Hp + c) / RUN)), u);
     if (gu) {
-      gu[at] = from_f32<T>(g);
-      gu[at + Hp] = from_f32<T>(u);
+      store16<T>(gu + at, STEP, g);
+      store16<T>(gu + at + Hp, STEP, u);
     }
-    if (act) act[i] = from_f32<T>(silu(g) * u);
+    if (act) {
+#pragma unroll
+      for (int j = 0; j < PER; ++j) g[j] = silu(g[j]) * u[j];
+      store16<T>(act + row * Hp + c, STEP, g);
+    }
   }
 }
 
-int grid_for(long long work, int per_cta) {
-  const long long ctas = (work + per_cta - 1) / per_cta, cap = (long long)sm_count() * 32;
+int grid_for(long long threads) {
+  const long long ctas = (threads + NT - 1) / NT, cap = (long long)sm_count() * 64;
   return (int)(ctas < cap ? ctas : cap);
+}
+
+template <typename T>
+void pack_t(const void* x, int rows, int N, int8_t* q, uint8_t* scale, cudaStream_t s) {
+  const int runs = (N + RUN - 1) / RUN;
+  const long long threads = 2LL * rows * runs;
+  if (N % RUN == 0)
+    ckpt_pack_kernel<T, true><<<grid_for(threads), NT, 0, s>>>(static_cast<const T*>(x), threads, N, runs, q, scale);
+  else
+    ckpt_pack_kernel<T, false><<<grid_for(threads), NT, 0, s>>>(static_cast<const T*>(x), threads, N, runs, q, scale);
+}
+
+template <typename T>
+void unpack_t(const int8_t* q, const uint8_t* scale, int rows, int N, void* x, cudaStream_t s) {
+  const int runs = (N + RUN - 1) / RUN;
+  const long long threads = 2LL * rows * runs;
+  if (N % RUN == 0)
+    ckpt_unpack_kernel<T, true><<<grid_for(threads), NT, 0, s>>>(q, scale, threads, N, runs, static_cast<T*>(x));
+  else
+    ckpt_unpack_kernel<T, false><<<grid_for(threads), NT, 0, s>>>(q, scale, threads, N, runs, static_cast<T*>(x));
+}
+
+template <typename T>
+void swiglu_t(const int8_t* q, const uint8_t* scale, int rows, int Hp, void* gu, void* act, cudaStream_t s) {
+  const int runs = (2 * Hp + RUN - 1) / RUN;
+  const bool flat = Hp % RUN == 0;
+  const int per_row = Hp / (flat ? PER : Vec16<T>::N);
+  const int grid = grid_for((long long)rows * per_row);
+  if (flat)
+    ckpt_swiglu_kernel<T, true><<<grid, NT, 0, s>>>(q, scale, rows, Hp, runs, per_row, static_cast<T*>(gu), static_cast<T*>(act));
+  else
+    ckpt_swiglu_kernel<T, false><<<grid, NT, 0, s>>>(q, scale, rows, Hp, runs, per_row, static_cast<T*>(gu), static_cast<T*>(act));
 }
 
 }  // namespace
 
 int launch_ckpt_pack(const void* x, int rows, int N, int dtype, int8_t* q, uint8_t* scale, cudaStream_t s) {
   if (rows == 0) return MOE_OK;
-  const int runs = (N + RUN - 1) / RUN, grid = grid_for((long long)rows * runs, 8);
-  if (dtype == MOE_BF16) ckpt_pack_kernel<bf16><<<grid, 256, 0, s>>>(static_cast<const bf16*>(x), rows, N, runs, q, scale);
-  else ckpt_pack_kernel<float><<<grid, 256, 0, s>>>(static_cast<const float*>(x), rows, N, runs, q, scale);
+  if (dtype == MOE_BF16) pack_t<bf16>(x, rows, N, q, scale, s);
+  else pack_t<float>(x, rows, N, q, scale, s);
   return launch_status();
 }
 
 int launch_ckpt_unpack(const int8_t* q, const uint8_t* scale, int rows, int N, int dtype, void* x, cudaStream_t s) {
   if (rows == 0) return MOE_OK;
-  const int runs = (N + RUN - 1) / RUN, grid = grid_for((long long)rows * N, 256);
-  if (dtype == MOE_BF16) ckpt_unpack_kernel<bf16><<<grid, 256, 0, s>>>(q, scale, rows, N, runs, static_cast<bf16*>(x));
-  else ckpt_unpack_kernel<float><<<grid, 256, 0, s>>>(q, scale, rows, N, runs, static_cast<float*>(x));
+  if (dtype == MOE_BF16) unpack_t<bf16>(q, scale, rows, N, x, s);
+  else unpack_t<float>(q, scale, rows, N, x, s);
   return launch_status();
 }
 
 int launch_ckpt_swiglu(const int8_t* q, const uint8_t* scale, int rows, int Hp, int dtype, void* gu, void* act,
                        cudaStream_t s) {
   if (rows == 0 || (!gu && !act)) return MOE_OK;
-  const int runs = (2 * Hp + RUN - 1) / RUN, grid = grid_for((long long)rows * Hp, 256);
-  if (dtype == MOE_BF16)
-    ckpt_swiglu_kernel<bf16><<<grid, 256, 0, s>>>(q, scale, rows, Hp, runs, static_cast<bf16*>(gu), static_cast<bf16*>(act));
-  else
-    ckpt_swiglu_kernel<float><<<grid, 256, 0, s>>>(q, scale, rows, Hp, runs, static_cast<float*>(gu), static_cast<float*>(act));
+  if (dtype == MOE_BF16) swiglu_t<bf16>(q, scale, rows, Hp, gu, act, s);
+  else swiglu_t<float>(q, scale, rows, Hp, gu, act, s);
   return launch_status();
 }
 
