@@ -17,55 +17,109 @@ namespace moe {
 namespace {
 
 constexpr unsigned FULL = 0xffffffffu;
-constexpr int META = 16, AHEAD = 15;  // tokens whose row numbers and gates are at hand; how far ahead they are read
-constexpr int MAXK = 16, MAXW = 32;
+constexpr int META = 16, AHEAD = 15;  // tokens whose row addresses and gates are at hand; how far ahead they are read
+constexpr int MAXK = 16, MAXA = 3;    // rows of h, and of y, dxn and dy, of a token
+constexpr int MAXW = 16;              // warps of a CTA
 
-__device__ __forceinline__ void copy16(uint4* dst, const void* src, bool live) {  // zeros where not live
+__device__ __forceinline__ void copy16(uint4* dst, const void* src, int bytes) {  // 16, or 0 for zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((unsigned)__cvta_generic_to_shared(dst)), "l"(src),
-               "r"(live ? 16 : 0)
+               "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-template <typename T> __device__ __forceinline__ void unpack(const uint4& q, float* v) { Vec16<T>::load_raw_unpack(q, v); }
-
-// 4 or 8 floats of a weight vector from column c on, 1 without one
-template <int V> __device__ __forceinline__ void load_w(const float* w, int c, float* v) {
+// A thread's values in pairs: the packed fp32 operations of this architecture take two at
+// a time, and instructions are what these kernels run short of first.
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+template <typename T> struct Pairs;
+template <> struct Pairs<bf16> {
+  static constexpr int N = 4;
+  __device__ __forceinline__ static void unpack(const uint4& q, float2* v) {
+    const unsigned w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-  for (int j = 0; j < V; j += 4) {
-    const float4 f = w ? __ldg(reinterpret_cast<const float4*>(w + c + j)) : make_float4(1.f, 1.f, 1.f, 1.f);
-    v[j] = f.x; v[j + 1] = f.y; v[j + 2] = f.z; v[j + 3] = f.w;
+    for (int i = 0; i < 4; ++i) v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   }
+  __device__ __forceinline__ static uint4 pack(const float2* v) {
+    uint4 q;
+    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&q);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[i].x, v[i].y);
+    return q;
+  }
+};
+template <> struct Pairs<float> {
+  static constexpr int N = 2;
+  __device__ __forceinline__ static void unpack(const uint4& q, float2* v) {
+    v[0] = make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
+    v[1] = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
+  }
+  __device__ __forceinline__ static uint4 pack(const float2* v) {
+    return make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
+  }
+};
+
+// N pairs of a weight vector from column c on; 1 without one, 0 beside the row
+template <int N> __device__ __forceinline__ void load_w(const float* w, int c, bool live, float2* v) {
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    float4 f = make_float4(1.f, 1.f, 1.f, 1.f);
+    if (!live) f = make_float4(0.f, 0.f, 0.f, 0.f);
+    else if (w) f = __ldg(reinterpret_cast<const float4*>(w + c + 2 * i));
+    v[i] = make_float2(f.x, f.y);
+    v[i + 1] = make_float2(f.z, f.w);
+  }
+}
+
+// Sums of four values over the warp's lanes by halving: every step gives half of the
+// values to half of the lanes.  Value i ends in the lanes with (lane >> 3) == i.
+__device__ __forceinline__ float warp_sum4(const float (&v)[4]) {
+  const int lane = threadIdx.x & 31;
+  const bool a = lane & 16, b = lane & 8;
+  float x = (a ? v[2] : v[0]) + __shfl_xor_sync(FULL, a ? v[0] : v[2], 16);
+  float y = (a ? v[3] : v[1]) + __shfl_xor_sync(FULL, a ? v[1] : v[3], 16);
+  x = (b ? y : x) + __shfl_xor_sync(FULL, b ? x : y, 8);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(FULL, x, o);
+  return x;
 }
 
 // Sums over the CTA, in a fixed order and the same in every thread.  Two buffers in
 // turn: one barrier for each call.
-template <int N> struct CtaSum {
-  float buf[2][N][MAXW];
-  __device__ __forceinline__ void run(float (&v)[N], int turn) {
+struct CtaSum {
+  float buf[2][MAXW];
+  __device__ __forceinline__ float run(float v, int turn) {
     const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    v = warp_sum(v);
+    if (lane == 0) buf[turn & 1][threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = lane < nw ? buf[turn & 1][lane] : 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-    if (nw == 1) {
-      __syncthreads();
-      return;
-    }
-    if (lane == 0) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) buf[turn & 1][i][threadIdx.x >> 5] = v[i];
+    for (int o = MAXW / 2; o > 0; o >>= 1) v += __shfl_xor_sync(FULL, v, o);
+    return __shfl_sync(FULL, v, 0);
+  }
+};
+struct CtaSum8 {  // of up to eight values
+  float buf[2][MAXW][8];
+  __device__ __forceinline__ void run(float (&v)[8], int turn) {
+    const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
+    const float x = warp_sum4(lo), y = warp_sum4(hi);
+    if ((lane & 7) == 0) {
+      buf[turn & 1][threadIdx.x >> 5][lane >> 3] = x;
+      buf[turn & 1][threadIdx.x >> 5][4 + (lane >> 3)] = y;
     }
     __syncthreads();
+    float s = 0.f;  // value lane % 8 of warps lane / 8, + 4, + 8, + 12
+    for (int w = lane >> 3; w < nw; w += 4) s += buf[turn & 1][w][lane & 7];
+    s += __shfl_xor_sync(FULL, s, 8);
+    s += __shfl_xor_sync(FULL, s, 16);
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = warp_sum(lane < nw ? buf[turn & 1][i][lane] : 0.f);
+    for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(FULL, s, i);
   }
 };
 
-// row numbers and gates of the tokens to come; row -1 for an index outside [0, R)
-struct Meta {
-  int row[META][MAXK];
-  float gate[META][MAXK];
-};
+// gates and row numbers of the tokens: row -1 for an index outside [0, R)
 struct MetaSource {
   const float* gate;
   const int32_t* dst_row;
@@ -84,6 +138,11 @@ struct MetaSource {
   }
 };
 
+// the address to copy a row from; the lowest bit marks a row of zeros (rows are 16-byte aligned)
+__device__ __forceinline__ unsigned long long row_address(const void* base, long long row, long long row_bytes) {
+  return row < 0 ? (unsigned long long)base | 1ull : (unsigned long long)base + row * row_bytes;
+}
+
 struct FwdArgs {
   const void* h;
   MetaSource meta;
@@ -95,146 +154,144 @@ struct FwdArgs {
   void *y, *xn;
 };
 
-// VPT vectors of a row for each thread, S rows of ring.  Order of a token's rows: its
-// K rows of h, then residual.
-template <typename T, int VPT, int S>
-__global__ void __launch_bounds__(896) combine_norm_kernel(const FwdArgs a) {
+// X values of a row for each thread, S rows of ring, CTAS of at most MAXT threads to an SM.
+// Order of a token's rows: its K rows of h, then residual.
+template <typename T, int X, int S, int MAXT, int CTAS>
+__global__ void __launch_bounds__(MAXT, CTAS) combine_norm_kernel(const FwdArgs a) {
   extern __shared__ uint4 ring[];
-  __shared__ Meta meta;
-  __shared__ CtaSum<1> sum;
-  constexpr int V = Vec16<T>::N, X = VPT * V;
-  constexpr bool HOLD_W = X <= 8;  // the weights fit in registers beside the row
+  __shared__ unsigned long long src[META * (MAXK + 1)];
+  __shared__ float2 gates[META][MAXK];  // twice, as a pair
+  __shared__ CtaSum sum;
+  constexpr int N = Pairs<T>::N, V = 2 * N, VPT = X / V, P = X / 2;
+  constexpr bool HOLD_W = X <= 16;  // the weights fit in registers beside the row
   const int tid = threadIdx.x, NT = blockDim.x, nvec = a.H / V, K = a.K, R = K + (a.residual ? 1 : 0);
-  const uint4* h = static_cast<const uint4*>(a.h);
-  const uint4* residual = static_cast<const uint4*>(a.residual);
-  for (int i = tid; i < AHEAD * MAXK; i += NT) {
-    const int j = i / MAXK, k = i % MAXK;
-    a.meta.get(blockIdx.x + (long long)j * gridDim.x, k, meta.row[j][k], meta.gate[j][k]);
-  }
-  float aw[HOLD_W ? X : 1], wn[HOLD_W ? X : 1];
-  auto weights = [&](int v, float* p, float* n) {
-    const int c = (tid + v * NT) * V;
-    float r[V];
-    load_w<V>(c < a.H ? a.w_post : nullptr, c, p);
-    load_w<V>(c < a.H ? a.res_scale : nullptr, c, r);
-    load_w<V>(c < a.H ? a.w_next : nullptr, c, n);
+  const long long row_bytes = (long long)a.H * sizeof(T);
+  int offset[VPT];
+  bool live[VPT];  // columns beside the row read as zeros
 #pragma unroll
-    for (int j = 0; j < V; ++j) p[j] *= r[j];
+  for (int v = 0; v < VPT; ++v) {
+    const int i = tid + v * NT;
+    live[v] = i < nvec;
+    offset[v] = live[v] ? 16 * i : 0;
+  }
+  auto note = [&](int j, int k, long long t, int row, float g) {  // row k of token t, which is at place j
+    src[j * R + k] = k < K ? row_address(a.h, row, row_bytes) : row_address(a.residual, t < a.T ? t : -1, row_bytes);
+    if (k < K) gates[j][k] = both(g);
+  };
+  for (int i = tid; i < AHEAD * R; i += NT) {
+    const int k = i / AHEAD, j = i - k * AHEAD;
+    const long long t = blockIdx.x + (long long)j * gridDim.x;
+    int row = -1;
+    float g = 0.f;
+    a.meta.get(t, k, row, g);
+    note(j, k, t, row, g);
+  }
+  float2 aw[HOLD_W ? P : 1], wn[HOLD_W ? P : 1];
+  auto weights = [&](int v, float2* p, float2* n) {
+    float2 r[N];
+    load_w<N>(a.w_post, offset[v] / 16 * V, live[v], p);
+    load_w<N>(a.res_scale, offset[v] / 16 * V, live[v], r);
+    load_w<N>(a.w_next, offset[v] / 16 * V, live[v], n);
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = __fmul2_rn(p[i], r[i]);
   };
   if (HOLD_W) {
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) weights(v, aw + v * V, wn + v * V);
+    for (int v = 0; v < VPT; ++v) weights(v, aw + v * N, wn + v * N);
   }
   __syncthreads();
 
-  // the next row to be copied: row qk of the CTA's qj-th token, into place qs
-  int qj = 0, qk = 0, qs = 0;
-  long long qt = blockIdx.x;
-  auto issue = [&]() {
-    if (qt < a.T) {
-      const int row = qk < K ? meta.row[qj % META][qk] : 0;
-      const uint4* src = qk < K ? h + (long long)max(row, 0) * nvec : residual + qt * nvec;
+  const int step = VPT * NT, total = S * step, QN = META * R;
+  int qn = 0, at = tid;  // the next row to be copied; the thread's place of the oldest row in the ring
+  auto issue = [&](int place) {
+    const unsigned long long p = src[qn];
+    qn = qn + 1 == QN ? 0 : qn + 1;
+    const char* from = reinterpret_cast<const char*>(p & ~1ull);
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        const int i = tid + v * NT;
-        if (i < nvec) copy16(ring + (qs * VPT + v) * NT + tid, src + i, row >= 0);
-      }
-      if (++qk == R) {
-        qk = 0;
-        ++qj;
-        qt += gridDim.x;
-      }
-    }
+    for (int v = 0; v < VPT; ++v) copy16(ring + place + v * NT, from + offset[v], live[v] && !(p & 1) ? 16 : 0);
     copies_commit();
-    qs = qs + 1 == S ? 0 : qs + 1;
   };
-#pragma unroll
-  for (int i = 0; i < S; ++i) issue();
+  for (int i = 0; i < S; ++i) issue(tid + i * step);
+  auto next_row = [&]() {  // the oldest row has been read: its place takes the next one
+    issue(at);
+    at += step;
+    if (at >= total) at -= total;
+  };
 
-  int slot = 0, turn = 0, j = 0;
-  for (long long t = blockIdx.x; t < a.T; t += gridDim.x, ++j) {
+  int turn = 0, j = 0;
+  for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const long long t_ahead = t + (long long)AHEAD * gridDim.x;
     int m_row = -1;
     float m_gate = 0.f;
-    if (tid < MAXK) a.meta.get(t + (long long)AHEAD * gridDim.x, tid, m_row, m_gate);
-    const float rs = a.row_scale ? __ldg(a.row_scale + t) : 1.f;
+    if (tid < K) a.meta.get(t_ahead, tid, m_row, m_gate);
+    float f = a.row_scale ? __ldg(a.row_scale + t) : 1.f;
 
-    float z[X];
+    float2 z[P];
 #pragma unroll
-    for (int i = 0; i < X; ++i) z[i] = 0.f;
+    for (int i = 0; i < P; ++i) z[i] = both(0.f);
     for (int k = 0; k < K; ++k) {
-      const float g = meta.gate[j % META][k];
+      const float2 g = gates[j][k];
       copies_wait<S - 1>();
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
-        if (tid + v * NT >= nvec) continue;
-        float x[V];
-        unpack<T>(ring[(slot * VPT + v) * NT + tid], x);
+        float2 x[N];
+        Pairs<T>::unpack(ring[at + v * NT], x);
 #pragma unroll
-        for (int i = 0; i < V; ++i) z[v * V + i] = fmaf(g, x[i], z[v * V + i]);
+        for (int i = 0; i < N; ++i) z[v * N + i] = __ffma2_rn(g, x[i], z[v * N + i]);
       }
-      issue();
-      slot = slot + 1 == S ? 0 : slot + 1;
+      next_row();
     }
-    float s[1];
-    float f = rs;
     if (a.w_post) {
-      s[0] = 0.f;
+      float2 s = both(0.f);
 #pragma unroll
-      for (int i = 0; i < X; ++i) s[0] = fmaf(z[i], z[i], s[0]);
-      sum.run(s, turn++);
-      f *= 1.f / sqrtf(s[0] / a.H + a.eps);
+      for (int i = 0; i < P; ++i) s = __ffma2_rn(z[i], z[i], s);
+      f *= 1.f / sqrtf(sum.run(s.x + s.y, turn++) / a.H + a.eps);
     }
-    if (residual) copies_wait<S - 1>();
-    s[0] = 0.f;
+    if (a.residual) copies_wait<S - 1>();
+    float2 s = both(0.f);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      if (tid + v * NT >= nvec) continue;
-      float x[V], p[V], n[V];
+      float2 x[N], p[N], n[N];
       if (HOLD_W) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) p[i] = aw[(v * V + i) % (HOLD_W ? X : 1)];
+        for (int i = 0; i < N; ++i) p[i] = aw[(v * N + i) % (HOLD_W ? P : 1)];
       } else {
         weights(v, p, n);
       }
 #pragma unroll
-      for (int i = 0; i < V; ++i) x[i] = 0.f;
-      if (residual) unpack<T>(ring[(slot * VPT + v) * NT + tid], x);
+      for (int i = 0; i < N; ++i) x[i] = both(0.f);
+      if (a.residual) Pairs<T>::unpack(ring[at + v * NT], x);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        x[i] = fmaf(f * z[v * V + i], p[i], x[i]);
-        z[v * V + i] = x[i];
-        s[0] = fmaf(x[i], x[i], s[0]);
+      for (int i = 0; i < N; ++i) {
+        x[i] = __ffma2_rn(__fmul2_rn(both(f), z[v * N + i]), p[i], x[i]);
+        z[v * N + i] = x[i];
+        s = __ffma2_rn(x[i], x[i], s);
       }
-      if (a.y) Vec16<T>::store(static_cast<T*>(a.y) + t * a.H + (long long)(tid + v * NT) * V, x);
+      if (a.y && live[v])
+        *reinterpret_cast<uint4*>(static_cast<char*>(a.y) + t * row_bytes + offset[v]) = Pairs<T>::pack(x);
     }
-    if (residual) {
-      issue();
-      slot = slot + 1 == S ? 0 : slot + 1;
-    }
+    if (a.residual) next_row();
     if (a.w_next) {
-      sum.run(s, turn++);
-      const float q = 1.f / sqrtf(s[0] / a.H + a.eps);
+      const float q = 1.f / sqrtf(sum.run(s.x + s.y, turn++) / a.H + a.eps);
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
-        if (tid + v * NT >= nvec) continue;
-        float x[V], p[V], n[V];
+        float2 x[N], p[N], n[N];
         if (HOLD_W) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) n[i] = wn[(v * V + i) % (HOLD_W ? X : 1)];
+          for (int i = 0; i < N; ++i) n[i] = wn[(v * N + i) % (HOLD_W ? P : 1)];
         } else {
           weights(v, p, n);
         }
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = z[v * V + i] * q * n[i];
-        Vec16<T>::store(static_cast<T*>(a.xn) + t * a.H + (long long)(tid + v * NT) * V, x);
+        for (int i = 0; i < N; ++i) x[i] = __fmul2_rn(__fmul2_rn(z[v * N + i], both(q)), n[i]);
+        if (live[v])
+          *reinterpret_cast<uint4*>(static_cast<char*>(a.xn) + t * row_bytes + offset[v]) = Pairs<T>::pack(x);
       }
     } else if (!a.w_post) {
-      __syncthreads();  // a token takes one barrier at least: the numbers below are read behind it
+      __syncthreads();  // a token takes one barrier at least: the addresses below are read behind it
     }
-    if (tid < MAXK) {
-      meta.row[(j + AHEAD) % META][tid] = m_row;
-      meta.gate[(j + AHEAD) % META][tid] = m_gate;
-    }
+    if (tid < R) note(j == 0 ? META - 1 : j - 1, tid, t_ahead, m_row, m_gate);
+    j = j + 1 == META ? 0 : j + 1;
   }
   copies_wait<0>();
 }
@@ -267,251 +324,290 @@ __device__ __forceinline__ void wait_all_but(int n) {  // n of 0, 2, 4, 8
 // One reduction serves both norms.  With D = dy + q (w_next dxn - q vm y):
 //   <aw D, z> = <aw dy, z> + q <aw w_next dxn, z> - q^2 vm <aw y, z>,
 // so its three products are summed along with y^2, w_next dxn y and z^2.
-template <typename T, int VPT, bool HOLD>
+template <typename T, int X, bool HOLD>
 __global__ void __launch_bounds__(512) combine_norm_bwd_kernel(const BwdArgs a) {
   extern __shared__ uint4 ring[];
-  __shared__ Meta meta;
-  __shared__ CtaSum<6> sum;
-  __shared__ float dots[2][MAXK][MAXW / 2 + 1];
-  constexpr int V = Vec16<T>::N, X = VPT * V;
+  constexpr int MAXR = (HOLD ? 1 : 2) * (MAXK + MAXA);
+  __shared__ unsigned long long src[META * MAXR];
+  __shared__ float2 gates[META][MAXK];  // twice, as a pair
+  __shared__ int rows[META][MAXK];
+  __shared__ CtaSum8 sum;
+  __shared__ float dots[2][MAXK][MAXW + 1];
+  constexpr int N = Pairs<T>::N, V = 2 * N, VPT = X / V, P = X / 2;
+  constexpr bool HOLD_W = X <= 16;
   const int tid = threadIdx.x, NT = blockDim.x, nvec = a.H / V, K = a.K, S = a.S;
   const int lane = tid & 31, warp = tid >> 5, nw = NT >> 5;
   const bool next = a.w_next != nullptr;
   const int A = (next ? 2 : 0) + (a.dy ? 1 : 0), R = HOLD ? A + K : 2 * (A + K);
-  const uint4 *h = static_cast<const uint4*>(a.h), *dy = static_cast<const uint4*>(a.dy);
-  const uint4 *y = static_cast<const uint4*>(a.y), *dxn = static_cast<const uint4*>(a.dxn);
-  for (int i = tid; i < AHEAD * MAXK; i += NT) {
-    const int j = i / MAXK, k = i % MAXK;
-    a.meta.get(blockIdx.x + (long long)j * gridDim.x, k, meta.row[j][k], meta.gate[j][k]);
+  const long long row_bytes = (long long)a.H * sizeof(T);
+  int offset[VPT];
+  bool live[VPT];  // columns beside the row read as zeros
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    const int i = tid + v * NT;
+    live[v] = i < nvec;
+    offset[v] = live[v] ? 16 * i : 0;
   }
+  auto note = [&](int j, int k, long long t, int row, float g) {  // row k (of h, then y, dxn, dy) of token t, at place j
+    unsigned long long p;
+    if (k < K) {
+      p = row_address(a.h, row, row_bytes);
+      gates[j][k] = both(g);
+      rows[j][k] = row;
+    } else {
+      const int x = k - K;
+      p = row_address(next && x < 2 ? (x == 0 ? a.y : a.dxn) : a.dy, t < a.T ? t : -1, row_bytes);
+    }
+    unsigned long long* q = src + j * R;
+    if (HOLD) {
+      q[k < K ? A + k : k - K] = p;
+    } else {
+      q[k] = p;
+      q[K + A + (k < K ? A + k : k - K)] = p;
+    }
+  };
+  for (int i = tid; i < AHEAD * (K + A); i += NT) {
+    const int k = i / AHEAD, j = i - k * AHEAD;
+    const long long t = blockIdx.x + (long long)j * gridDim.x;
+    int row = -1;
+    float g = 0.f;
+    a.meta.get(t, k, row, g);
+    note(j, k, t, row, g);
+  }
+  float2 aw[HOLD_W ? P : 1], wn[HOLD_W ? P : 1];
+  auto weights = [&](int v, float2* p, float2* n) {
+    float2 r[N];
+    load_w<N>(a.w_post, offset[v] / 16 * V, live[v], p);
+    load_w<N>(a.res_scale, offset[v] / 16 * V, live[v], r);
+    load_w<N>(a.w_next, offset[v] / 16 * V, live[v], n);
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = __fmul2_rn(p[i], r[i]);
+  };
+  if (HOLD_W) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) weights(v, aw + v * N, wn + v * N);
+  }
+  auto weights_of = [&](int v, float2* p, float2* n) {
+    if (HOLD_W) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        p[i] = aw[(v * N + i) % (HOLD_W ? P : 1)];
+        n[i] = wn[(v * N + i) % (HOLD_W ? P : 1)];
+      }
+    } else {
+      weights(v, p, n);
+    }
+  };
   __syncthreads();
 
-  int qj = 0, qk = 0, qs = 0;
-  long long qt = blockIdx.x;
-  auto issue = [&]() {
-    if (qt < a.T) {
-      int k, x;  // row k of h where k >= 0, otherwise row x of (y, dxn, dy)
-      if (HOLD) {
-        k = qk - A;
-        x = qk;
-      } else {
-        k = qk < K ? qk : qk - K - 2 * A;
-        x = qk - K >= A ? qk - K - A : qk - K;
-      }
-      const uint4* src;
-      bool live = true;
-      if (k >= 0) {
-        const int row = meta.row[qj % META][k];
-        live = row >= 0;
-        src = h + (long long)max(row, 0) * nvec;
-      } else {
-        src = (next && x < 2 ? (x == 0 ? y : dxn) : dy) + qt * nvec;
-      }
+  const int step = VPT * NT, total = S * step, QN = META * R;
+  int qn = 0, at = tid;  // the next row to be copied; the thread's place of the oldest row in the ring
+  auto issue = [&](int place) {
+    const unsigned long long p = src[qn];
+    qn = qn + 1 == QN ? 0 : qn + 1;
+    const char* from = reinterpret_cast<const char*>(p & ~1ull);
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        const int i = tid + v * NT;
-        if (i < nvec) copy16(ring + (qs * VPT + v) * NT + tid, src + i, live);
-      }
-      if (++qk == R) {
-        qk = 0;
-        ++qj;
-        qt += gridDim.x;
-      }
-    }
+    for (int v = 0; v < VPT; ++v) copy16(ring + place + v * NT, from + offset[v], live[v] && !(p & 1) ? 16 : 0);
     copies_commit();
-    qs = qs + 1 == S ? 0 : qs + 1;
   };
-  for (int i = 0; i < S; ++i) issue();
-  // place of the row i behind the oldest one in the ring
-  int slot = 0;
-  auto at = [&](int i, int v) -> const uint4& {
-    const int p = slot + i;
-    return ring[((p >= S ? p - S : p) * VPT + v) * NT + tid];
+  for (int i = 0; i < S; ++i) issue(tid + i * step);
+  auto next_row = [&]() {
+    issue(at);
+    at += step;
+    if (at >= total) at -= total;
   };
-  auto pass = [&](int n) {
-    for (int i = 0; i < n; ++i) issue();
-    slot = slot + n >= S ? slot + n - S : slot + n;
+  auto behind = [&](int rows_on) {  // the thread's place of the row that many behind the oldest
+    const int p = at + rows_on * step;
+    return p >= total ? p - total : p;
   };
 
-  float Q[X], N[X];
+  float2 Q[P], M[P];
 #pragma unroll
-  for (int i = 0; i < X; ++i) Q[i] = N[i] = 0.f;
+  for (int i = 0; i < P; ++i) Q[i] = M[i] = both(0.f);
   int turn = 0, j = 0;
   long long before = -1;  // the token whose d_gate is still in `dots`
-  auto write_gates = [&](long long t, int b) {
+  auto write_gates = [&](int b) {
     if (a.d_gate && tid < K) {
       float d = 0.f;
       for (int w = 0; w < nw; ++w) d += dots[b][tid][w];
-      a.d_gate[t * K + tid] = d;
+      a.d_gate[before * K + tid] = d;
     }
   };
 
-  for (long long t = blockIdx.x; t < a.T; t += gridDim.x, ++j) {
+  for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const long long t_ahead = t + (long long)AHEAD * gridDim.x;
     int m_row = -1;
     float m_gate = 0.f;
-    if (tid < MAXK) a.meta.get(t + (long long)AHEAD * gridDim.x, tid, m_row, m_gate);
+    if (tid < K) a.meta.get(t_ahead, tid, m_row, m_gate);
     const float rs = a.row_scale ? __ldg(a.row_scale + t) : 1.f;
 
-    float z[X];
+    float2 z[P];
 #pragma unroll
-    for (int i = 0; i < X; ++i) z[i] = 0.f;
+    for (int i = 0; i < P; ++i) z[i] = both(0.f);
     if (HOLD) wait_all_but(S - R);
+    int place = HOLD ? behind(A) : at;
     for (int k = 0; k < K; ++k) {
-      const float g = meta.gate[j % META][k];
-      if (!HOLD) copies_wait<2>();  // S >= 3 rows are on their way: the oldest is here
+      const float2 g = gates[j][k];
+      if (!HOLD) copies_wait<2>();  // three rows are on their way: the oldest is here
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
-        if (tid + v * NT >= nvec) continue;
-        float x[V];
-        unpack<T>(at(HOLD ? A + k : 0, v), x);
+        float2 x[N];
+        Pairs<T>::unpack(ring[place + v * NT], x);
 #pragma unroll
-        for (int i = 0; i < V; ++i) z[v * V + i] = fmaf(g, x[i], z[v * V + i]);
+        for (int i = 0; i < N; ++i) z[v * N + i] = __ffma2_rn(g, x[i], z[v * N + i]);
       }
-      if (!HOLD) pass(1);
+      if (!HOLD) next_row();
+      place += step;
+      if (place >= total) place -= total;
     }
     if (!HOLD) copies_wait<0>();
-    float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const int at_y = at, at_x = behind(1), at_d = behind(A - 1);
+    float2 s2[6];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) s2[i] = both(0.f);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      if (tid + v * NT >= nvec) continue;
-      const int c = (tid + v * NT) * V;
-      float aw[V], w[V];
-      load_w<V>(a.w_post, c, aw);
-      load_w<V>(a.res_scale, c, w);
+      float2 p[N], n[N], x[N], y[N];
+      weights_of(v, p, n);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        aw[i] *= w[i] * z[v * V + i];
-        s[2] = fmaf(z[v * V + i], z[v * V + i], s[2]);
+      for (int i = 0; i < N; ++i) {
+        p[i] = __fmul2_rn(p[i], z[v * N + i]);
+        s2[2] = __ffma2_rn(z[v * N + i], z[v * N + i], s2[2]);
       }
       if (next) {
-        float yv[V], xv[V];
-        load_w<V>(a.w_next, c, w);
-        unpack<T>(at(0, v), yv);
-        unpack<T>(at(1, v), xv);
+        Pairs<T>::unpack(ring[at_y + v * NT], y);
+        Pairs<T>::unpack(ring[at_x + v * NT], x);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float p = w[i] * xv[i];
-          s[0] = fmaf(yv[i], yv[i], s[0]);
-          s[1] = fmaf(p, yv[i], s[1]);
-          s[4] = fmaf(aw[i], p, s[4]);
-          s[5] = fmaf(aw[i], yv[i], s[5]);
+        for (int i = 0; i < N; ++i) {
+          const float2 e = __fmul2_rn(n[i], x[i]);
+          s2[0] = __ffma2_rn(y[i], y[i], s2[0]);
+          s2[1] = __ffma2_rn(e, y[i], s2[1]);
+          s2[4] = __ffma2_rn(p[i], e, s2[4]);
+          s2[5] = __ffma2_rn(p[i], y[i], s2[5]);
         }
       }
-      if (dy) {
-        unpack<T>(at(A - 1, v), w);
+      if (a.dy) {
+        Pairs<T>::unpack(ring[at_d + v * NT], x);
 #pragma unroll
-        for (int i = 0; i < V; ++i) s[3] = fmaf(aw[i], w[i], s[3]);
+        for (int i = 0; i < N; ++i) s2[3] = __ffma2_rn(p[i], x[i], s2[3]);
       }
     }
-    if (!HOLD) pass(A);
+    if (!HOLD)
+      for (int i = 0; i < A; ++i) next_row();
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) s[i] = s2[i].x + s2[i].y;
     sum.run(s, turn++);
-    if (before >= 0) write_gates(before, (j & 1) ^ 1);
-    const float q = next ? 1.f / sqrtf(s[0] / a.H + a.eps) : 0.f, vm = s[1] * q / a.H;
-    const float r = a.w_post ? 1.f / sqrtf(s[2] / a.H + a.eps) : 1.f;
+    if (before >= 0) write_gates((j & 1) ^ 1);
+    const float inv_h = 1.f / a.H;
+    const float q = next ? 1.f / sqrtf(s[0] * inv_h + a.eps) : 0.f, vm = s[1] * q * inv_h;
+    const float r = a.w_post ? 1.f / sqrtf(s[2] * inv_h + a.eps) : 1.f;
     const float sd = r * (s[3] + q * (s[4] - q * vm * s[5]));
-    const float um = a.w_post ? rs * sd / a.H : 0.f;
+    const float um = a.w_post ? rs * sd * inv_h : 0.f;
     if (tid == 0 && a.d_scale) a.d_scale[t] = sd;
 
     if (!HOLD) copies_wait<0>();
+    const int by_x = HOLD ? at_x : behind(1), by_d = HOLD ? at_d : behind(A - 1);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      if (tid + v * NT >= nvec) continue;
-      const int c = (tid + v * NT) * V;
-      float d[V], w[V];
+      float2 p[N], n[N], d[N];
+      weights_of(v, p, n);
 #pragma unroll
-      for (int i = 0; i < V; ++i) d[i] = 0.f;
-      if (dy) unpack<T>(at(A - 1, v), d);
+      for (int i = 0; i < N; ++i) d[i] = both(0.f);
+      if (a.dy) Pairs<T>::unpack(ring[by_d + v * NT], d);
       if (next) {
-        float yv[V], xv[V];
-        load_w<V>(a.w_next, c, w);
-        unpack<T>(at(0, v), yv);
-        unpack<T>(at(1, v), xv);
+        float2 x[N], y[N];
+        Pairs<T>::unpack(ring[at + v * NT], y);
+        Pairs<T>::unpack(ring[by_x + v * NT], x);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float u = yv[i] * q;
-          d[i] += q * (xv[i] * w[i] - u * vm);
-          N[v * V + i] = fmaf(xv[i], u, N[v * V + i]);
+        for (int i = 0; i < N; ++i) {
+          const float2 u = __fmul2_rn(y[i], both(q));
+          const float2 e = __ffma2_rn(x[i], n[i], __fmul2_rn(u, both(-vm)));
+          d[i] = __ffma2_rn(both(q), e, d[i]);
+          M[v * N + i] = __ffma2_rn(x[i], u, M[v * N + i]);
         }
       }
-      if (a.d_res) Vec16<T>::store(static_cast<T*>(a.d_res) + t * a.H + c, d);
-      if (K > 0) {
-        float aw[V];
-        load_w<V>(a.w_post, c, aw);
-        load_w<V>(a.res_scale, c, w);
+      if (a.d_res && live[v])
+        *reinterpret_cast<uint4*>(static_cast<char*>(a.d_res) + t * row_bytes + offset[v]) = Pairs<T>::pack(d);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float u = z[v * V + i] * r, e = rs * d[i];
-          Q[v * V + i] = fmaf(e, u, Q[v * V + i]);
-          z[v * V + i] = r * (e * aw[i] * w[i] - u * um);  // dz
-        }
+      for (int i = 0; i < N; ++i) {
+        const float2 u = __fmul2_rn(z[v * N + i], both(r)), e = __fmul2_rn(d[i], both(rs));
+        Q[v * N + i] = __ffma2_rn(e, u, Q[v * N + i]);
+        z[v * N + i] = __fmul2_rn(both(r), __ffma2_rn(e, p[i], __fmul2_rn(u, both(-um))));  // dz
       }
     }
-    pass(A);
-    for (int k = 0; k < K; ++k) {
-      const float g = meta.gate[j % META][k];
-      const int row = meta.row[j % META][k];
-      if (!HOLD) copies_wait<2>();
-      float dot = 0.f;
+    for (int i = 0; i < A; ++i) next_row();
+    for (int k0 = 0; k0 < K; k0 += 4) {
+      float dot[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        if (tid + v * NT >= nvec) continue;
-        float x[V];
-        unpack<T>(at(0, v), x);
+      for (int kk = 0; kk < 4; ++kk) {
+        const int k = k0 + kk;
+        if (k >= K) break;
+        const float2 g = gates[j][k];
+        const int row = rows[j][k];
+        if (!HOLD) copies_wait<2>();
+        float2 c = both(0.f);
+        char* out = static_cast<char*>(a.dh) + row * row_bytes;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          dot = fmaf(z[v * V + i], x[i], dot);
-          x[i] = g * z[v * V + i];
+        for (int v = 0; v < VPT; ++v) {
+          float2 x[N];
+          Pairs<T>::unpack(ring[at + v * NT], x);
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            c = __ffma2_rn(z[v * N + i], x[i], c);
+            x[i] = __fmul2_rn(g, z[v * N + i]);
+          }
+          if (a.dh && row >= 0 && live[v]) *reinterpret_cast<uint4*>(out + offset[v]) = Pairs<T>::pack(x);
         }
-        if (a.dh && row >= 0) Vec16<T>::store(static_cast<T*>(a.dh) + (long long)row * a.H + (tid + v * NT) * V, x);
+        dot[kk] = c.x + c.y;
+        next_row();
       }
-      pass(1);
       if (a.d_gate) {
-        dot = warp_sum(dot);
-        if (lane == 0) dots[j & 1][k][warp] = dot;
+        const float d = warp_sum4(dot);
+        if ((lane & 7) == 0) dots[j & 1][k0 + (lane >> 3)][warp] = d;
       }
     }
     before = t;
-    if (tid < MAXK) {
-      meta.row[(j + AHEAD) % META][tid] = m_row;
-      meta.gate[(j + AHEAD) % META][tid] = m_gate;
-    }
+    if (tid < K + A) note(j == 0 ? META - 1 : j - 1, tid, t_ahead, m_row, m_gate);
+    j = j + 1 == META ? 0 : j + 1;
   }
   copies_wait<0>();
   __syncthreads();
-  if (before >= 0) write_gates(before, (j & 1) ^ 1);
+  if (before >= 0) write_gates((j & 1) ^ 1);
   if (a.part) {
     float* p = a.part + (size_t)blockIdx.x * 2 * a.H;
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      if (tid + v * NT >= nvec) continue;
-      const int c = (tid + v * NT) * V;
+      if (!live[v]) continue;
+      const int c = offset[v] / 16 * V;
 #pragma unroll
-      for (int i = 0; i < V; i += 4) {
-        *reinterpret_cast<float4*>(p + c + i) = make_float4(Q[v * V + i], Q[v * V + i + 1], Q[v * V + i + 2], Q[v * V + i + 3]);
-        *reinterpret_cast<float4*>(p + a.H + c + i) =
-            make_float4(N[v * V + i], N[v * V + i + 1], N[v * V + i + 2], N[v * V + i + 3]);
+      for (int i = 0; i < N; i += 2) {
+        const float2 *e = Q + v * N + i, *f = M + v * N + i;
+        *reinterpret_cast<float4*>(p + c + 2 * i) = make_float4(e[0].x, e[0].y, e[1].x, e[1].y);
+        *reinterpret_cast<float4*>(p + a.H + c + 2 * i) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
       }
     }
   }
 }
 
-// The column sums: a CTA takes 32 columns of [2][H], 16 warps the parts w, w + 16, ... in
-// order; the warps' sums are added in warp order and multiplied by their column factors.
-__global__ void __launch_bounds__(512)
+// The column sums: a CTA takes 32 columns of [2][H], its 32 warps the parts w, w + 32, ...
+// in order; the warps' sums are added in warp order and multiplied by their column factors.
+__global__ void __launch_bounds__(1024)
 column_sums_kernel(const float* __restrict__ part, int parts, int H, const float* __restrict__ w_post,
                    const float* __restrict__ res_scale, float* dw_post, float* d_res_scale, float* dw_next) {
-  __shared__ float red[16][33];
+  __shared__ float red[32][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int i = blockIdx.x * 32 + lane;
   float acc = 0.f;
   if (i < 2 * H) {
-#pragma unroll 4
-    for (int p = w; p < parts; p += 16) acc += __ldg(part + (size_t)p * 2 * H + i);
+#pragma unroll 8
+    for (int p = w; p < parts; p += 32) acc += __ldg(part + (size_t)p * 2 * H + i);
   }
   red[w][lane] = acc;
   __syncthreads();
   if (w > 0 || i >= 2 * H) return;
-  for (int k = 1; k < 16; ++k) acc += red[k][lane];
+#pragma unroll
+  for (int k = 1; k < 32; ++k) acc += red[k][lane];
   if (i >= H) {
     if (dw_next) dw_next[i - H] = acc;
   } else {
@@ -521,6 +617,7 @@ column_sums_kernel(const float* __restrict__ part, int parts, int H, const float
 }
 
 constexpr int RING_BYTES = 200 * 1024;  // at most; a CTA's 227 KB also hold the sums and row numbers
+constexpr int SM_BYTES = 227 * 1024, BWD_STATIC = 12 * 1024;  // an SM's; a backward CTA's beside the ring, rounded up
 
 int threads_for(int nvec, int vpt) { return ((nvec + vpt - 1) / vpt + 31) / 32 * 32; }
 
@@ -535,23 +632,30 @@ template <typename F> int persistent_grid(F kernel, int threads, int smem, int c
   return MOE_OK;
 }
 
-template <typename T, int VPT, int S> int fwd_v(const FwdArgs& a, cudaStream_t s) {
+template <typename T, int X, int S, int MAXT, int CTAS> int fwd_v(const FwdArgs& a, cudaStream_t s) {
+  constexpr int VPT = X / Vec16<T>::N;
   const int threads = threads_for(a.H / Vec16<T>::N, VPT), smem = S * VPT * threads * 16;
   int grid = 0;
-  const int st = persistent_grid(combine_norm_kernel<T, VPT, S>, threads, smem, 32, a.T, &grid);
+  const int st = persistent_grid(combine_norm_kernel<T, X, S, MAXT, CTAS>, threads, smem, 32, a.T, &grid);
   if (st != MOE_OK) return st;
-  combine_norm_kernel<T, VPT, S><<<grid, threads, smem, s>>>(a);
+  combine_norm_kernel<T, X, S, MAXT, CTAS><<<grid, threads, smem, s>>>(a);
   return launch_status();
 }
 
-// The widest rows a thread's vectors reach with at most 896 threads; the ring takes what
-// 200 KB hold: 12 rows of up to 14 KB, 6 of up to 28 KB, 3 beyond.
+// 16 values a thread up to H = 8192, 32 beyond.  Rows of up to 8 KB: three CTAs or more to
+// an SM, 8 rows of ring each, so that some stream while others reduce; wider rows: one CTA
+// with 12 rows of up to 16 KB, 6 of up to 32 KB, 3 beyond.
 template <typename T> int fwd_t(const FwdArgs& a, cudaStream_t s) {
-  const int nvec = a.H / Vec16<T>::N;
-  if (nvec <= 896) return fwd_v<T, 1, 12>(a, s);
-  if (nvec <= 2 * 896) return fwd_v<T, 2, 6>(a, s);
-  if (nvec <= 4 * 896) return fwd_v<T, 4, 3>(a, s);
-  return fwd_v<T, 8, 3>(a, s);
+  constexpr bool WIDE = sizeof(T) == 4;
+  const int row = a.H * (int)sizeof(T);
+  if (row <= 8192 && a.H <= 4096) return fwd_v<T, 16, 8, 256, 3>(a, s);
+  if (row <= 16384 && a.H <= 8192) return fwd_v<T, 16, 12, 512, 1>(a, s);
+  if constexpr (WIDE) {
+    if (a.H <= 8192) return fwd_v<T, 16, 6, 512, 1>(a, s);
+    return fwd_v<T, 32, 3, 512, 1>(a, s);
+  } else {
+    return fwd_v<T, 32, 6, 512, 1>(a, s);
+  }
 }
 
 // column sums kept per CTA: at most this many CTAs to an SM
@@ -559,32 +663,32 @@ int bwd_ctas_per_sm(int H) { return H >= 8192 ? 2 : H >= 1024 ? 16384 / H : 16; 
 
 int bwd_rows(const BwdArgs& a) { return a.K + (a.w_next ? 2 : 0) + (a.dy ? 1 : 0); }
 
-template <typename T, int VPT, bool HOLD> int bwd_v(BwdArgs& a, int* grid, cudaStream_t s) {
+template <typename T, int X, bool HOLD> int bwd_v(BwdArgs& a, int* grid, cudaStream_t s) {
+  constexpr int VPT = X / Vec16<T>::N;
   const int threads = threads_for(a.H / Vec16<T>::N, VPT), row = VPT * threads * 16, R = bwd_rows(a);
-  // rows of the next tokens behind a token's own: 8, or what two CTAs, then one leave room for
-  auto fits = [&](int rows, int bytes) { return (long long)rows * row <= bytes; };
-  a.S = !HOLD                       ? 3
-        : fits(R + 8, RING_BYTES / 2) ? R + 8
-        : fits(R + 4, RING_BYTES / 2) ? R + 4
-        : fits(R + 8, RING_BYTES)     ? R + 8
-        : fits(R + 4, RING_BYTES)     ? R + 4
-                                      : R + 2;
+  // 128 registers leave room for 512 threads to an SM: as many CTAs as that, and behind a
+  // token's own rows 8, 4 or 2 of the next tokens, what the SM's shared memory has room for
+  a.S = HOLD ? R + 2 : 3;
+  for (int ctas = 512 / threads; HOLD && ctas > 0; --ctas) {
+    const int room = (SM_BYTES / ctas - BWD_STATIC) / row;
+    if (room < R + 2) continue;
+    a.S = R + (room >= R + 8 ? 8 : room >= R + 4 ? 4 : 2);
+    break;
+  }
   const int smem = a.S * row;
-  const int st = persistent_grid(combine_norm_bwd_kernel<T, VPT, HOLD>, threads, smem, bwd_ctas_per_sm(a.H), a.T, grid);
+  const int st = persistent_grid(combine_norm_bwd_kernel<T, X, HOLD>, threads, smem, bwd_ctas_per_sm(a.H), a.T, grid);
   if (st != MOE_OK) return st;
-  combine_norm_bwd_kernel<T, VPT, HOLD><<<*grid, threads, smem, s>>>(a);
+  combine_norm_bwd_kernel<T, X, HOLD><<<*grid, threads, smem, s>>>(a);
   return launch_status();
 }
 
-// 8 values a thread up to H = 4096, 16 up to 8192, 32 beyond (their column sums spill a
-// little); a token's rows are held where two more fit beside them
+// 16 values a thread up to H = 8192, 32 beyond; a token's rows are held where two more fit
+// beside them
 template <typename T> int bwd_t(BwdArgs& a, int* grid, cudaStream_t s) {
-  constexpr int V = Vec16<T>::N;
-  const int nvec = a.H / V;
-  auto holds = [&](int vpt) { return (long long)(bwd_rows(a) + 2) * vpt * threads_for(nvec, vpt) * 16 <= RING_BYTES; };
-  if (a.H <= 4096 && holds(8 / V)) return bwd_v<T, 8 / V, true>(a, grid, s);
-  if (a.H <= 8192) return holds(16 / V) ? bwd_v<T, 16 / V, true>(a, grid, s) : bwd_v<T, 16 / V, false>(a, grid, s);
-  return bwd_v<T, 32 / V, false>(a, grid, s);
+  constexpr int VPT = 16 / Vec16<T>::N;
+  if (a.H > 8192) return bwd_v<T, 32, false>(a, grid, s);
+  const long long row = VPT * threads_for(a.H / Vec16<T>::N, VPT) * 16;
+  return (bwd_rows(a) + 2) * row <= RING_BYTES ? bwd_v<T, 16, true>(a, grid, s) : bwd_v<T, 16, false>(a, grid, s);
 }
 
 long long bwd_max_ctas(int T, int H) {
@@ -621,7 +725,7 @@ int launch_combine_norm_bwd(const void* dy, const void* dxn, const void* h, cons
   int grid = 0;
   const int st = dtype == MOE_BF16 ? bwd_t<bf16>(a, &grid, s) : bwd_t<float>(a, &grid, s);
   if (st != MOE_OK || !sums) return st;
-  column_sums_kernel<<<(2 * H + 31) / 32, 512, 0, s>>>(a.part, grid, H, w_post, res_scale, dw_post, d_res_scale, dw_next);
+  column_sums_kernel<<<(2 * H + 31) / 32, 1024, 0, s>>>(a.part, grid, H, w_post, res_scale, dw_post, d_res_scale, dw_next);
   return launch_status();
 }
 
