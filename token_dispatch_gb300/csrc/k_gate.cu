@@ -44,6 +44,26 @@ __device__ __forceinline__ int order_key(float x) {  // integers that order as t
 }
 __device__ __forceinline__ float from_key(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7fffffff)); }
 
+// 2^x, 1/x: relative errors of 4u and 2u (u = 2^-24), numbers below 2^-126 as zero.  The
+// selection's scores alone are made with them; the gates are not.
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float U = 5.9604645e-8f;  // half a step of fp32
+
 struct Row64 {  // what a row's 64-bit scores need
   const float* row;
   const float* bias;
@@ -57,6 +77,11 @@ struct Row64 {  // what a row's 64-bit scores need
     const float l = row[e];
     const double v = bias ? score(l) + (double)bias[e] : score(l);
     return l == -INFINITY || v != v ? -INFINITY : v;
+  }
+  // what orders the experts: c, without a bias the logits
+  __device__ double order(int e) const {
+    const float l = row[e];
+    return bias ? value(e) : l != l ? -INFINITY : (double)l;
   }
 };
 
@@ -72,7 +97,7 @@ __device__ __noinline__ Row64 row64(const float* row, const float* bias, int E, 
   return r;
 }
 
-// groups ranked by 64-bit scores: lane g of a group's first lane returns whether its group stays
+// groups ranked by 64-bit scores: whether the lane's group stays
 __device__ __noinline__ bool keep_groups64(const Row64& r, const GateShape& p, int g, int lig, float second,
                                            float margin) {
   const int lane = threadIdx.x & 31;
@@ -87,7 +112,7 @@ __device__ __noinline__ bool keep_groups64(const Row64& r, const GateShape& p, i
       float c = r.row[e];
       if (r.bias) c = (r.sigmoid ? 1.f / (1.f + expf(-c)) : expf(c - (float)r.m) / (float)r.z) + r.bias[e];
       if (c < second - margin) continue;
-      const double v = r.value(e);
+      const double v = group_max ? r.order(e) : r.value(e);
       if (v > a) { b = a; a = v; } else if (v > b) b = v;
     }
   for (int o = 1; o < p.lpg; o <<= 1) {
@@ -121,8 +146,7 @@ __device__ __noinline__ int choose64(const Row64& r, const GateShape& p, unsigne
     int e = 0x7fffffff;
     for (int i = lane; i < p.E; i += 32) {
       if (!((keep >> (i / p.gs)) & 1u)) continue;
-      const float l = r.row[i];
-      double w = r.bias ? r.value(i) : (l != l ? -INFINITY : (double)l);
+      const double w = r.order(i);
       if (w > last || (w == last && i <= last_e)) continue;
       if (e == 0x7fffffff || w > v) {
         v = w;
@@ -149,7 +173,7 @@ __device__ __noinline__ int choose64(const Row64& r, const GateShape& p, unsigne
 __device__ __forceinline__ float gate_value(float l, bool on, bool sigmoid, bool renorm, float m, float z) {
   float base = 0.f;
   if (renorm) {  // a common factor of the row: its largest chosen score becomes about 1
-    base = warp_max(on ? l : -INFINITY);
+    base = from_key(__reduce_max_sync(FULL, on ? order_key(l) : INT_MIN));
     if (sigmoid) base = fminf(base, 0.f);
   }
   float s = 0.f;
@@ -166,10 +190,9 @@ template <int VMAX>
 __global__ void __launch_bounds__(32 * WARPS)
 gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, const float* __restrict__ bias,
             GateShape p, int32_t* __restrict__ idx, float* __restrict__ gate) {
-  __shared__ float cand_c[WARPS][32], cand_l[WARPS][32];
+  __shared__ __align__(16) float cand_c[WARPS][32];
   __shared__ int cand_e[WARPS][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const unsigned below = (1u << lane) - 1;
   const bool sigmoid = (p.mode & 0xf) == MOE_GATE_SIGMOID, renorm = p.mode & MOE_GATE_RENORM;
   const bool group_max = p.mode & MOE_GATE_GROUP_MAX;
   const int g = lane / p.lpg, lig = lane - g * p.lpg;
@@ -201,78 +224,64 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
     load(bias, 0.f, b);
     float mb = 0.f;
 #pragma unroll
-    for (int j = 0; j < VMAX; ++j) mb = fmaxf(mb, fabsf(b[j]) < INFINITY ? fabsf(b[j]) : 0.f);
+    for (int j = 0; j < VMAX; ++j) {
+      mb = fmaxf(mb, fabsf(b[j]) < INFINITY ? fabsf(b[j]) : 0.f);
+      if (b[j] != b[j]) b[j] = -INFINITY;
+    }
     mb = warp_max(mb);
-    // twice the error of a score (u = 2^-24): expf 4u, the sum and quotient 4u; softmax: the
-    // sum over vpl values and 5 shuffles; then the rounding of s + b
-    const float u = 5.9604645e-8f;
-    margin = 2.f * u * ((sigmoid ? 12.f : 20.f + p.vpl) + mb);
+    // How far two scores must be apart to be surely in order: the errors of both.  A logistic
+    // score s is off by 4u of its exponential and |l| u of that one's argument, both times
+    // s (1 - s), and by 3u of the sum and reciprocal: under 6u; a softmax score by the
+    // same of its exponential and by its sum over vpl values and 5 shuffles; then s + b rounds.
+    margin = 2.f * U * ((sigmoid ? 8.f : 22.f + p.vpl) + mb);
   }
 
   for (long long t = (long long)blockIdx.x * WARPS + warp; t < p.T; t += (long long)gridDim.x * WARPS) {
     float* row = logits + t * p.E;
-    float l[VMAX];
+    float c[VMAX];  // the logits, then the selection values
     if (part) {
-      load(part + t * p.E, -INFINITY, l);
+      load(part + t * p.E, -INFINITY, c);
       for (int i = 1; i < S; ++i) {
         float w[VMAX];
         load(part + ((long long)i * p.T + t) * p.E, 0.f, w);
 #pragma unroll
-        for (int j = 0; j < VMAX; ++j) l[j] += w[j];
+        for (int j = 0; j < VMAX; ++j) c[j] += w[j];
       }
 #pragma unroll
       for (int j = 0; j < VMAX; ++j)
-        if (j < count) row[e0 + j] = l[j];
+        if (j < count) row[e0 + j] = c[j];
       __syncwarp();
     } else {
-      load(row, -INFINITY, l);
+      load(row, -INFINITY, c);
     }
-    bool bad = false;
+    float m = -INFINITY, z = 1.f, rz = 1.f;
 #pragma unroll
-    for (int j = 0; j < VMAX; ++j) bad |= l[j] != l[j];
-    bad = __any_sync(FULL, bad);
-
+    for (int j = 0; j < VMAX; ++j) m = max_nan(m, c[j]);
+    const bool bad = __any_sync(FULL, m != m);
     // softmax: the row's maximum and sum, where something needs them
-    float m = 0.f, z = 1.f;
     const bool by_sum = p.KG < p.G && !group_max;
     if (!sigmoid && (bias || !renorm || by_sum)) {
-      m = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < VMAX; ++j) m = fmaxf(m, l[j]);
-      m = from_key(__reduce_max_sync(FULL, order_key(m)));
-    }
-    // the selection values: scores plus bias, or the logits
-    float c[VMAX];
-    if (bias) {
-      if (sigmoid) {
-#pragma unroll
-        for (int j = 0; j < VMAX; ++j) c[j] = __fdividef(1.f, 1.f + expf(-l[j]));
-      } else {
+      m = bad ? __int_as_float(0x7fffffff) : from_key(__reduce_max_sync(FULL, order_key(m)));
+      if (bias || !renorm) {
         z = 0.f;
 #pragma unroll
-        for (int j = 0; j < VMAX; ++j) {
-          c[j] = l[j] == -INFINITY ? 0.f : expf(l[j] - m);
-          z += c[j];
-        }
+        for (int j = 0; j < VMAX; ++j) z += c[j] == -INFINITY ? 0.f : fast_exp2((c[j] - m) * LOG2E);
         z = warp_sum(z);
-        const float r = 1.f / z;
-#pragma unroll
-        for (int j = 0; j < VMAX; ++j) c[j] *= r;
+        rz = 1.f / z;
       }
+    }
+    // the score of a logit, fast
+    auto score = [&](float l) { return sigmoid ? fast_rcp(1.f + fast_exp2(l * -LOG2E)) : fast_exp2((l - m) * LOG2E) * rz; };
+    if (bias) {
 #pragma unroll
-      for (int j = 0; j < VMAX; ++j) {
-        c[j] += b[j];
-        if (l[j] == -INFINITY || c[j] != c[j]) c[j] = -INFINITY;
+      for (int j = 0; j < VMAX; ++j) c[j] = c[j] > -INFINITY ? score(c[j]) + b[j] : -INFINITY;
+      if (!sigmoid && !(z < INFINITY)) {  // a softmax over NaN or +inf: nothing can be said of the scores
+#pragma unroll
+        for (int j = 0; j < VMAX; ++j) c[j] = -INFINITY;
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < VMAX; ++j) c[j] = l[j] != l[j] ? -INFINITY : l[j];
-      if (!sigmoid && !renorm) {
-        z = 0.f;
-#pragma unroll
-        for (int j = 0; j < VMAX; ++j) z += l[j] == -INFINITY ? 0.f : expf(l[j] - m);
-        z = warp_sum(z);
-      }
+      for (int j = 0; j < VMAX; ++j) c[j] = fmaxf(c[j], -INFINITY);  // NaN ranks last
     }
 
     bool stay = g < p.G;
@@ -283,47 +292,52 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
         a2 = fmaxf(a2, fminf(a1, c[j]));
         a1 = fmaxf(a1, c[j]);
       }
-      for (int o = 1; o < p.lpg; o <<= 1) {
-        const float d1 = __shfl_down_sync(FULL, a1, o), d2 = __shfl_down_sync(FULL, a2, o);
-        if (lig + o < p.lpg) {
+      if ((p.lpg & (p.lpg - 1)) == 0) {
+        for (int o = 1; o < p.lpg; o <<= 1) {
+          const float d1 = __shfl_xor_sync(FULL, a1, o), d2 = __shfl_xor_sync(FULL, a2, o);
           a2 = fmaxf(fminf(a1, d1), fmaxf(a2, d2));
           a1 = fmaxf(a1, d1);
         }
+      } else {
+        for (int o = 1; o < p.lpg; o <<= 1) {
+          const float d1 = __shfl_down_sync(FULL, a1, o), d2 = __shfl_down_sync(FULL, a2, o);
+          if (lig + o < p.lpg) {
+            a2 = fmaxf(fminf(a1, d1), fmaxf(a2, d2));
+            a1 = fmaxf(a1, d1);
+          }
+        }
+        a1 = __shfl_sync(FULL, a1, lane - lig);
+        a2 = __shfl_sync(FULL, a2, lane - lig);
       }
-      // a group's rank and how far it may be off
-      float rank, off = 0.f;
+      // a group's rank, and how far two ranks must be apart to be surely in order
+      float rank, off;
       if (group_max) {
         rank = a1;
         off = margin;
       } else if (bias) {
         rank = a2 == -INFINITY ? a1 : a1 + a2;
-        off = 2.f * margin + fabsf(rank) * 1.2e-7f;
+        off = 2.f * margin + fabsf(rank) * 2.f * U;
       } else {
+        // relative: 12u of the scores and the sum, twice |a1 - base| u of the exponential's argument
         const float base = sigmoid ? 0.f : m;
-        auto score = [&](float x) {
-          return x == -INFINITY ? 0.f : sigmoid ? 1.f / (1.f + expf(-x)) : expf(x - base);
-        };
-        rank = a1 == -INFINITY ? a1 : score(a1) + score(a2);
-        // u = 2^-24: expf 4u, the rounding of its argument |a1 - m| u, sum and quotient 4u, on
-        // both sides; and what numbers below 2^-126 lose
-        off = rank * 1.2e-7f * (12.f + (sigmoid || a1 == -INFINITY ? 0.f : fabsf(a1 - m))) + 4e-45f;
+        rank = a1 == -INFINITY ? a1 : (sigmoid ? score(a1) : fast_exp2((a1 - m) * LOG2E)) +
+                                          (a2 == -INFINITY ? 0.f : sigmoid ? score(a2) : fast_exp2((a2 - m) * LOG2E));
+        off = rank * 2.f * U * (12.f + 2.f * fabsf(a1 - base)) + 3e-38f;
       }
-      const int first = lane - lig;
-      rank = __shfl_sync(FULL, rank, first);
-      off = __shfl_sync(FULL, off, first);
-      a2 = __shfl_sync(FULL, a2, first);
-      int ahead = 0, surely = 0, maybe = 0;
-      for (int o = 0; o < p.G; ++o) {
-        const float w = __shfl_sync(FULL, rank, o * p.lpg);
-        ahead += w > rank || (w == rank && o < g);
-        surely += w > rank + off;
-        maybe += w >= rank - off;
+      // the KG-th largest rank and the next; equal ones go together
+      const int mine = g < p.G ? order_key(rank) : INT_MIN;
+      int key = mine, kth = INT_MIN;
+      for (int i = 0; i < p.KG; ++i) {
+        kth = __reduce_max_sync(FULL, key);
+        if (key == kth) key = INT_MIN;
       }
-      stay = stay && ahead < p.KG;
-      // the comparison of logits, or of groups that are out altogether, is exact
-      const bool exact = (group_max && !bias) || rank == -INFINITY;
-      const bool open = g < p.G && !exact && maybe > p.KG && surely < p.KG;  // `maybe` counts the group itself
-      if (__any_sync(FULL, open))
+      const int after = __reduce_max_sync(FULL, key);
+      stay = mine >= kth && g < p.G;
+      const int kept = __popc(__ballot_sync(FULL, stay && lig == 0));
+      // the lanes at the border know how near the next rank is
+      const bool near = mine == kth && after != INT_MIN && rank != -INFINITY && rank - from_key(after) <= off &&
+                        !(group_max && !bias);
+      if (kept != p.KG || __any_sync(FULL, near))
         stay = keep_groups64(row64(row, bias, p.E, sigmoid, m), p, g, lig, group_max ? a1 : a2, margin) && g < p.G;
       if (!stay) {
 #pragma unroll
@@ -341,22 +355,34 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
       if (key == kth) key = INT_MIN;
     }
     float limit = kth == INT_MIN ? -INFINITY : from_key(kth);
+    // the scores at or above it, one to a lane
     auto collect = [&]() {
-      unsigned n = 0;
-      const float lim = limit - margin;
+      const float lim = fmaxf(limit - margin, -3.4028235e38f);
+      unsigned in[(VMAX + 31) / 32];
+      int mine = 0;
 #pragma unroll
-      for (int j = 0; j < VMAX; ++j) {
-        const bool in = c[j] >= lim && c[j] > -INFINITY;
-        const unsigned who = __ballot_sync(FULL, in);
-        const unsigned at = n + __popc(who & below);
-        if (in && at < 32) {
-          cand_c[warp][at] = c[j];
-          cand_l[warp][at] = l[j];
-          cand_e[warp][at] = e0 + j;
-        }
-        n += __popc(who);
+      for (int w = 0; w < (VMAX + 31) / 32; ++w) {
+        in[w] = 0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (32 * w + j < VMAX && c[32 * w + j] >= lim) in[w] |= 1u << j;
+        mine += __popc(in[w]);
       }
-      return (int)n;
+      int at = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(FULL, at, o);
+        if (lane >= o) at += up;
+      }
+      const int n = __shfl_sync(FULL, at, 31);
+      at -= mine;
+#pragma unroll
+      for (int w = 0; w < (VMAX + 31) / 32; ++w)
+        for (; in[w] && at < 32; ++at) {
+          cand_e[warp][at] = e0 + 32 * w + __ffs(in[w]) - 1;
+          in[w] &= in[w] - 1;
+        }
+      return n;
     };
     int n = collect();
     if (n > 32) {
@@ -392,30 +418,37 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
     int e = 0, place = 32;
     float mine = -INFINITY;
     if (n >= p.K && n <= 32) {
+      const bool in = lane < n;
       float v = -INFINITY;
-      if (lane < n) {
-        v = cand_c[warp][lane];
-        mine = cand_l[warp][lane];
+      if (in) {
         e = cand_e[warp][lane];
+        mine = row[e];
+        v = bias ? score(mine) + __ldg(bias + e) : mine;
       }
-      int ahead = 0, near = 0;
-      for (int i = 0; i < n; ++i) {
-        const float w = cand_c[warp][i];
-        ahead += w > v || (w == v && cand_e[warp][i] < e);
-        near += fabsf(w - v) <= margin;
+      cand_c[warp][lane] = v;
+      __syncwarp();
+      int ahead = 0, close = 0;  // how many are larger; how many are not surely smaller
+      const float lim = v - margin;
+      for (int i = 0; i < n; i += 4) {
+        const float4 w = *reinterpret_cast<const float4*>(&cand_c[warp][i]);
+        ahead += (w.x > v) + (w.y > v) + (w.z > v) + (w.w > v);
+        close += (w.x >= lim) + (w.y >= lim) + (w.z >= lim) + (w.w >= lim);
       }
-      place = lane < n ? ahead : 32;
-      // `near` counts the lane itself; without a bias values compare exactly
-      if (bias && __any_sync(FULL, lane < n && near > 1)) {
-        const Row64 r = row64(row, bias, p.E, sigmoid, m);
-        const double x = lane < n ? r.value(e) : 0.0;
+      place = in ? ahead : 32;
+      // `close` counts the lane itself and those ahead
+      if (__any_sync(FULL, in && ahead < p.K && close > ahead + 1)) {
+        double x = mine;
+        if (bias) {
+          const Row64 r = row64(row, bias, p.E, sigmoid, m);
+          x = in ? r.value(e) : 0.0;
+        }
         place = 0;
         for (int i = 0; i < n; ++i) {
           const double w = __shfl_sync(FULL, x, i);
           const int f = __shfl_sync(FULL, e, i);
           place += w > x || (w == x && f < e);
         }
-        if (lane >= n) place = 32;
+        if (!in) place = 32;
       }
     } else {
       const unsigned who = __ballot_sync(FULL, stay && lig == 0);
@@ -437,40 +470,80 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
   }
 }
 
+// Backward: a warp to a token.  All but the softmax without RENORM have a gradient at the
+// chosen experts alone: the row is filled with zeros while the chosen logits are on their
+// way, then their lanes overwrite K of them.  The softmax's row goes through registers in VQ
+// 16-byte pieces a lane (VQ = 0: rows of any length, one value at a time, read twice).
+template <int VQ>
 __global__ void __launch_bounds__(32 * WARPS)
 gate_bwd_kernel(const float* __restrict__ d_gate, const float* __restrict__ logits, const int32_t* __restrict__ idx,
                 int T, int E, int K, int mode, float scale, float* __restrict__ d_logits, unsigned* err) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const bool sigmoid = (mode & 0xf) == MOE_GATE_SIGMOID, renorm = mode & MOE_GATE_RENORM;
+  const bool whole = !sigmoid && !renorm;
   for (long long t = (long long)blockIdx.x * WARPS + warp; t < T; t += (long long)gridDim.x * WARPS) {
     const float* row = logits + t * E;
+    float* out = d_logits + t * E;
     int e = -1;
     float dg = 0.f, l = -INFINITY;
     if (lane < K) {
-      e = idx[t * K + lane];
+      e = __ldg(idx + t * K + lane);
+      dg = __ldg(d_gate + t * K + lane);
+    }
+    float4 v[VQ > 0 ? VQ : 1];
+    float m = -INFINITY, z = 0.f;
+    if (whole) {
+      if (VQ > 0) {
+#pragma unroll
+        for (int q = 0; q < VQ; ++q) {
+          const int i = (q * 32 + lane) * 4;
+          v[q] = i < E ? __ldg(reinterpret_cast<const float4*>(row + i)) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+          m = fmaxf(m, fmaxf(fmaxf(v[q].x, v[q].y), fmaxf(v[q].z, v[q].w)));
+        }
+      } else {
+        for (int i = lane; i < E; i += 32) m = fmaxf(m, row[i]);
+      }
+      m = warp_max(m);
+    } else if (VQ > 0) {
+#pragma unroll
+      for (int q = 0; q < VQ; ++q) {
+        const int i = (q * 32 + lane) * 4;
+        if (i < E) *reinterpret_cast<float4*>(out + i) = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    } else {
+      for (int i = lane; i < E; i += 32) out[i] = 0.f;
+    }
+    if (lane < K) {
       if (e < 0 || e >= E) {
         set_error(err, DEV_BOUNDS);
         e = -1;
+        dg = 0.f;
       } else {
-        dg = d_gate[t * K + lane];
         l = row[e];
       }
     }
-    float m = l, z = 0.f;
-    if (!sigmoid && !renorm)
-      for (int i = lane; i < E; i += 32) m = fmaxf(m, row[i]);
-    m = warp_max(m);
-    if (sigmoid) m = fminf(m, 0.f);
-    if (!sigmoid && !renorm) {
-      for (int i = lane; i < E; i += 32) z += m == -INFINITY ? 0.f : expf(row[i] - m);
+    if (whole) {
+      auto power = [&](float x) { return x == -INFINITY ? 0.f : expf(x - m); };  // a row of -inf has m = -inf
+      if (VQ > 0) {
+#pragma unroll
+        for (int q = 0; q < VQ; ++q) {
+          v[q] = make_float4(power(v[q].x), power(v[q].y), power(v[q].z), power(v[q].w));
+          z += (v[q].x + v[q].y) + (v[q].z + v[q].w);
+        }
+      } else {
+        for (int i = lane; i < E; i += 32) z += power(row[i]);
+      }
       z = warp_sum(z);
+    } else if (renorm) {  // a common factor of the chosen scores: the largest becomes about 1
+      m = warp_max(l);
+      if (sigmoid) m = fminf(m, 0.f);
+    } else {
+      m = 0.f;
     }
-    // a chosen score, up to the factor exp(m) (a common factor of the row, or 1 without RENORM)
     float s = 0.f, rest = 1.f;
     if (l != -INFINITY) {
       if (sigmoid) {
-        const float base = renorm ? m : 0.f;
-        s = expf(fminf(l, 0.f) - base) / (1.f + expf(-fabsf(l)));
+        s = expf(fminf(l, 0.f) - m) / (1.f + expf(-fabsf(l)));
         rest = 1.f / (1.f + expf(l));
       } else {
         s = expf(l - m);
@@ -478,29 +551,36 @@ gate_bwd_kernel(const float* __restrict__ d_gate, const float* __restrict__ logi
     }
     const float sum = renorm ? warp_sum(s) : z;
     const float q = sigmoid && !renorm ? s : sum > 0.f ? s / sum : 0.f;
-    const float inner = warp_sum(dg * q);
-    float d;
-    if (sigmoid) d = renorm ? q * rest * (dg - inner) : q * rest * dg;
-    else d = q * (renorm ? dg - inner : dg);
+    const float inner = sigmoid && !renorm ? 0.f : warp_sum(dg * q);
+    float d = q * (whole ? dg : rest * (dg - inner));
     // an expert listed more than once: its first place takes the sum
-    float all = 0.f;
-    int first = K;
-    for (int k = 0; k < K; ++k) {
-      const int f = __shfl_sync(FULL, e, k);
-      const float o = __shfl_sync(FULL, d, k);
-      if (f == e) {
-        all += o;
-        first = min(first, k);
+    const unsigned same = __match_any_sync(FULL, e) & ((1u << K) - 1);
+    bool first = e >= 0;
+    if (__any_sync(FULL, lane < K && e >= 0 && __popc(same) > 1)) {
+      float all = 0.f;
+      for (int k = 0; k < K; ++k) {
+        const float o = __shfl_sync(FULL, d, k);
+        if ((same >> k) & 1u) all += o;
       }
+      d = all;
+      first = first && __ffs(same) - 1 == lane;
     }
-    float* out = d_logits + t * E;
-    for (int i = lane; i < E; i += 32) {
-      float v = 0.f;
-      if (!sigmoid && !renorm) v = row[i] == -INFINITY ? 0.f : -scale * inner * (expf(row[i] - m) / z);
-      out[i] = v;
+    if (whole) {
+      const float f = z > 0.f ? -scale * inner / z : 0.f;
+      if (VQ > 0) {
+#pragma unroll
+        for (int q4 = 0; q4 < VQ; ++q4) {
+          const int i = (q4 * 32 + lane) * 4;
+          if (i < E)
+            *reinterpret_cast<float4*>(out + i) = make_float4(f * v[q4].x, f * v[q4].y, f * v[q4].z, f * v[q4].w);
+        }
+      } else {
+        for (int i = lane; i < E; i += 32) out[i] = row[i] == -INFINITY ? 0.f : f * expf(row[i] - m);
+      }
+      d -= q * inner;
     }
     __syncwarp();
-    if (e >= 0 && first == lane) out[e] = scale * (sigmoid || renorm ? all : all - q * inner);
+    if (first) out[e] = scale * d;
     __syncwarp();
   }
 }
@@ -535,8 +615,15 @@ int launch_gate(float* logits, const float* part, int S, const float* bias, int 
 int launch_gate_bwd(const float* d_gate, const float* logits, const int32_t* idx, int T, int E, int K, int mode,
                     float scale, float* d_logits, cudaStream_t s) {
   if (T == 0) return MOE_OK;
-  gate_bwd_kernel<<<warp_grid(T), 32 * WARPS, 0, s>>>(d_gate, logits, idx, T, E, K, mode, scale, d_logits,
-                                                      device_error_word());
+  const int grid = warp_grid(T), pieces = E % 4 == 0 ? (E + 127) / 128 : 0;
+#define MOE_GATE_BWD(V) \
+  gate_bwd_kernel<V><<<grid, 32 * WARPS, 0, s>>>(d_gate, logits, idx, T, E, K, mode, scale, d_logits, device_error_word())
+  if (pieces == 0) MOE_GATE_BWD(0);
+  else if (pieces <= 1) MOE_GATE_BWD(1);
+  else if (pieces <= 2) MOE_GATE_BWD(2);
+  else if (pieces <= 4) MOE_GATE_BWD(4);
+  else MOE_GATE_BWD(8);
+#undef MOE_GATE_BWD
   return launch_status();
 }
 
