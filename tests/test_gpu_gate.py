@@ -251,3 +251,32 @@ def test_gate_on_another_stream_and_in_a_graph():
     assert all(torch.equal(a, c) for a, c in zip(got, (*out, dl)))
     r_idx, _ = O.gate_group(l.cpu().numpy(), 8, 8, 4, True, b.cpu().numpy())
     assert np.array_equal(got[0].cpu().numpy(), r_idx)
+
+
+def test_gate_zeros_of_both_signs_and_the_lowest_number():
+    """Equal zeros of either sign rank by index; the type's lowest number is a number."""
+    low = np.finfo(np.float32).min
+    l = np.zeros((6, 64), np.float32)
+    l[0, 1::2] = -0.0
+    l[1, ::3] = -0.0
+    l[2, :] = low
+    l[2, 40] = 1.0
+    l[3, :60] = low
+    l[4, :] = -1e-42
+    l[4, 7] = 1e-44
+    l[5, 5:9] = [1e-45, -1e-45, 3e-45, 0.0]
+    for G, KG in ((1, 1), (8, 8), (8, 3), (1, 1)):
+        for group_max in (False, True):
+            check(l, 6, G, KG, False, None, True, group_max)
+            check(l, 6, G, KG, True, None, False, group_max)
+            check(l, 6, G, KG, True, np.zeros(64), True, group_max)
+
+
+@pytest.mark.parametrize("E,K,G,KG", [(384, 8, 8, 1), (512, 16, 32, 1), (1024, 16, 2, 1), (640, 12, 16, 2)])
+def test_gate_of_few_lanes(E, K, G, KG):
+    """Kept groups that lie in one lane or a few: a lane gives more than it keeps at hand."""
+    for sigmoid, biased in ((False, False), (True, True)):
+        l = np.sort(draw(40, E, "plain", E), axis=1)
+        l[::2] = l[::2, ::-1]
+        b = np.random.default_rng(1).standard_normal(E) * 0.01 if biased else None
+        check(l, K, G, KG, sigmoid, b, True, False)

@@ -7,10 +7,8 @@
 // A row of at most 1024 logits is a few instructions for each score and a
 // selection, so a warp takes a token and keeps the row in registers: the lanes
 // are dealt out to the groups, neighbours of a group to neighbouring lanes, and
-// a group's two largest scores meet in a segmented shuffle.  The selection goes
-// through a threshold: the K-th largest of the lanes' maxima is a lower bound of
-// the K-th largest score, and the few scores at or above it (K plus about a
-// quarter) are collected into one lane each and ranked by counting.
+// a group's two largest scores meet in shuffles.  Each lane keeps its three largest
+// scores, and K + 1 rounds of a warp-wide integer maximum take the largest one by one.
 //
 // The choice is that of 64-bit scores.  fp32 scores carry a bound on their error;
 // where two scores that decide something (a rank among the first K, a group in or
@@ -63,6 +61,17 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either i
 }
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float U = 5.9604645e-8f;  // half a step of fp32
+
+// exp(x), x <= 0, within 6u: x log2(e) in two parts, the second one (the first's rounding and
+// the constant's, at most 2^-15) by 1 + d ln 2; below -200, where nothing is left, as -200
+__device__ __forceinline__ float exp_neg(float x) {
+  x = x < -200.f ? -200.f : x;
+  const float t = x * LOG2E;
+  const float d = fmaf(x, LOG2E, -t) + x * 1.9259630e-8f;  // log2(e) - LOG2E
+  float y;
+  asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(t));
+  return fmaf(y, d * 0.69314718f, y);
+}
 
 struct Row64 {  // what a row's 64-bit scores need
   const float* row;
@@ -170,20 +179,22 @@ __device__ __noinline__ int choose64(const Row64& r, const GateShape& p, unsigne
 }
 
 // the gates of the chosen experts from their logits; lanes with on = false take no part
-__device__ __forceinline__ float gate_value(float l, bool on, bool sigmoid, bool renorm, float m, float z) {
-  float base = 0.f;
+__device__ __forceinline__ float gate_value(float l, bool on, bool sigmoid, bool renorm, float m, float rz) {
+  float base = sigmoid ? 0.f : m;
   if (renorm) {  // a common factor of the row: its largest chosen score becomes about 1
     base = from_key(__reduce_max_sync(FULL, on ? order_key(l) : INT_MIN));
     if (sigmoid) base = fminf(base, 0.f);
   }
   float s = 0.f;
-  if (on && l != -INFINITY)
-    s = sigmoid ? expf(fminf(l, 0.f) - base) / (1.f + expf(-fabsf(l))) : expf(l - (renorm ? base : m));
-  if (renorm) {
-    const float sum = warp_sum(s);
-    return sum > 0.f || sum != sum ? s / sum : 0.f;
+  if (on && l != -INFINITY) {
+    s = exp_neg((sigmoid ? fminf(l, 0.f) : l) - base);
+    if (sigmoid) s *= fast_rcp(1.f + exp_neg(-fabsf(l)));  // a divisor of 1 to 2
   }
-  return sigmoid || s == 0.f ? s : s / z;
+  if (renorm) {
+    const float sum = warp_sum(s);  // 1/2 to K, or 0
+    return sum > 0.f || sum != sum ? s * fast_rcp(sum) : 0.f;
+  }
+  return sigmoid || s == 0.f ? s : s * rz;
 }
 
 template <int VMAX>
@@ -220,15 +231,19 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
   };
 
   float b[VMAX], margin = 0.f;
+  bool odd = false;  // a bias that is no number
   if (bias) {
     load(bias, 0.f, b);
     float mb = 0.f;
 #pragma unroll
     for (int j = 0; j < VMAX; ++j) {
-      mb = fmaxf(mb, fabsf(b[j]) < INFINITY ? fabsf(b[j]) : 0.f);
+      const bool number = fabsf(b[j]) < INFINITY;
+      mb = fmaxf(mb, number ? fabsf(b[j]) : 0.f);
+      odd = odd || !number;
       if (b[j] != b[j]) b[j] = -INFINITY;
     }
     mb = warp_max(mb);
+    odd = __any_sync(FULL, odd);
     // How far two scores must be apart to be surely in order: the errors of both.  A logistic
     // score s is off by 4u of its exponential and |l| u of that one's argument, both times
     // s (1 - s), and by 3u of the sum and reciprocal: under 6u; a softmax score by the
@@ -254,20 +269,21 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
     } else {
       load(row, -INFINITY, c);
     }
-    float m = -INFINITY, z = 1.f, rz = 1.f;
+    float m = -INFINITY, rz = 1.f;
 #pragma unroll
     for (int j = 0; j < VMAX; ++j) m = max_nan(m, c[j]);
-    const bool bad = __any_sync(FULL, m != m);
+    const bool finite = !__any_sync(FULL, !(m < INFINITY));  // neither NaN nor +inf in the row
+    const bool bad = !finite && __any_sync(FULL, m != m);
     // softmax: the row's maximum and sum, where something needs them
     const bool by_sum = p.KG < p.G && !group_max;
     if (!sigmoid && (bias || !renorm || by_sum)) {
       m = bad ? __int_as_float(0x7fffffff) : from_key(__reduce_max_sync(FULL, order_key(m)));
       if (bias || !renorm) {
-        z = 0.f;
+        float z = 0.f;
 #pragma unroll
         for (int j = 0; j < VMAX; ++j) z += c[j] == -INFINITY ? 0.f : fast_exp2((c[j] - m) * LOG2E);
         z = warp_sum(z);
-        rz = 1.f / z;
+        rz = fast_rcp(z);
       }
     }
     // the score of a logit, fast
@@ -275,13 +291,13 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
     if (bias) {
 #pragma unroll
       for (int j = 0; j < VMAX; ++j) c[j] = c[j] > -INFINITY ? score(c[j]) + b[j] : -INFINITY;
-      if (!sigmoid && !(z < INFINITY)) {  // a softmax over NaN or +inf: nothing can be said of the scores
+      if (!sigmoid && !finite) {  // a softmax over NaN or +inf has no scores
 #pragma unroll
         for (int j = 0; j < VMAX; ++j) c[j] = -INFINITY;
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < VMAX; ++j) c[j] = fmaxf(c[j], -INFINITY);  // NaN ranks last
+      for (int j = 0; j < VMAX; ++j) c[j] = fmaxf(c[j], -INFINITY) + 0.f;  // NaN ranks last, -0 as 0
     }
 
     bool stay = g < p.G;
@@ -339,22 +355,65 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
                         !(group_max && !bias);
       if (kept != p.KG || __any_sync(FULL, near))
         stay = keep_groups64(row64(row, bias, p.E, sigmoid, m), p, g, lig, group_max ? a1 : a2, margin) && g < p.G;
+    }
+
+    // Each lane keeps its three largest, and K + 1 rounds take the warp's largest one by one.
+    // The place of a value in its lane rides in its lowest bits: what that moves a value by is
+    // added to the margin.  (-inf turns to NaN and back; rows with +inf go the other way.)
+    constexpr int BITS = VMAX <= 2 ? 1 : VMAX <= 4 ? 2 : VMAX <= 8 ? 3 : VMAX <= 16 ? 4 : VMAX <= 32 ? 5 : 6;
+    int e = 0, place = 32;
+    float mine = -INFINITY;
+    bool sure = finite && !odd;
+    float limit = -INFINITY;
+    if (sure) {
+      float f1 = -INFINITY, f2 = -INFINITY, f3 = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < VMAX; ++j) {
+        const float f = fmaxf(__uint_as_float((__float_as_uint(c[j]) & ~((1u << BITS) - 1)) | j), -INFINITY);
+        const float lo = fminf(f1, f), lo2 = fminf(f2, lo);
+        f1 = fmaxf(f1, f);
+        f2 = fmaxf(f2, lo);
+        f3 = fmaxf(f3, lo2);
+      }
+      int k1 = order_key(f1), k2 = order_key(f2), k3 = order_key(f3);
+      const int none = order_key(-INFINITY);  // what a lane with no more values offers
+      if (!stay) k1 = k2 = k3 = none;
+      int left = 3, best = none, rounds = 0;
+      for (; rounds <= p.K; ++rounds) {
+        const int top = __reduce_max_sync(FULL, k1);
+        if (top == none) break;
+        if (lane == rounds) best = top;
+        if (k1 == top) {
+          cand_e[warp][rounds] = e0 + (__float_as_uint(from_key(top)) & ((1u << BITS) - 1));
+          k1 = k2;
+          k2 = k3;
+          k3 = none;
+          --left;
+        }
+      }
+      // the values in order: lane k holds the k-th, and looks at the next one.  The K + 1 rounds
+      // are what they seem where each took one value, the values are clear of each other, K
+      // experts were in service and no lane gave all that it had kept while it has more.
+      const float v = from_key(best), after = __shfl_down_sync(FULL, v, 1);
+      const float apart = margin + fabsf(v) * (2.f * U * (2 << BITS)) + 2e-43f;  // and zeros are denormals there
+      const bool clear = lane >= p.K || (best != none && (v - after > apart || after == -INFINITY));
+      sure = __all_sync(FULL, clear && (VMAX <= 3 || left > 0 || count <= 3)) &&
+             __reduce_add_sync(FULL, 3 - left) == rounds;
+      // where that does not hold, the K-th value (or one below it) bounds the candidates
+      limit = __shfl_sync(FULL, v, p.K - 1);
+      limit -= fabsf(limit) * (2.f * U * (1 << BITS));
+      __syncwarp();
+      if (sure && lane < p.K) {
+        e = cand_e[warp][lane];
+        mine = row[e];
+        place = lane;
+      }
+    }
+    if (!sure) {
       if (!stay) {
 #pragma unroll
         for (int j = 0; j < VMAX; ++j) c[j] = -INFINITY;
       }
-    }
-
-    // a bound of the K-th largest from the lanes' maxima
-    float top = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < VMAX; ++j) top = fmaxf(top, c[j]);
-    int key = order_key(top), kth = key;
-    for (int k = 0; k < p.K; ++k) {
-      kth = __reduce_max_sync(FULL, key);
-      if (key == kth) key = INT_MIN;
-    }
-    float limit = kth == INT_MIN ? -INFINITY : from_key(kth);
     // the scores at or above it, one to a lane
     auto collect = [&]() {
       const float lim = fmaxf(limit - margin, -3.4028235e38f);
@@ -384,9 +443,10 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
         }
       return n;
     };
+    __syncwarp();
     int n = collect();
     if (n > 32) {
-      // few lanes hold the kept groups: the K-th largest itself, K rounds over the registers
+      // a bound too low: the K-th largest itself, K rounds over the registers
       float lower = INFINITY;
       int taken = 0;
       while (taken < p.K) {
@@ -414,9 +474,6 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
       n = collect();
     }
     __syncwarp();
-
-    int e = 0, place = 32;
-    float mine = -INFINITY;
     if (n >= p.K && n <= 32) {
       const bool in = lane < n;
       float v = -INFINITY;
@@ -460,8 +517,9 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
         mine = row[e];
       }
     }
+    }
     const bool on = place < p.K;
-    const float s = gate_value(mine, on, sigmoid, renorm, m, z);
+    const float s = gate_value(mine, on, sigmoid, renorm, m, rz);
     if (on) {
       idx[t * p.K + place] = e;
       gate[t * p.K + place] = bad ? __int_as_float(0x7fffffff) : s * p.scale;
