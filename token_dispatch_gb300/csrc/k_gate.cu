@@ -59,6 +59,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either i
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
   return y;
 }
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float U = 5.9604645e-8f;  // half a step of fp32
 
@@ -141,6 +146,44 @@ __device__ __noinline__ bool keep_groups64(const Row64& r, const GateShape& p, i
   return ahead < p.KG;
 }
 
+// The groups at the border in 64 bits, from the values that the lanes have at hand: f1 >= f2 >= f3
+// with their places in the lowest bits, of which those from `bound` on may be among their
+// group's two largest.  `open`: the lane's group is at the border; `in`: it surely stays.
+// Returns whether the lane's group stays.
+__device__ __noinline__ bool settle_groups64(const Row64& r, const GateShape& p, int g, int lig, int e0, const float3& f,
+                                             unsigned places, float bound, bool open, bool in) {
+  const int lane = threadIdx.x & 31;
+  const bool group_max = p.mode & MOE_GATE_GROUP_MAX;
+  double a = -INFINITY, b = -INFINITY;
+  const float at[3] = {f.x, f.y, f.z};
+  for (int i = 0; i < 3; ++i) {
+    const bool need = open && at[i] >= bound && at[i] > -INFINITY;
+    if (!__any_sync(FULL, need)) break;
+    if (need) {
+      const int e = e0 + (__float_as_uint(at[i]) & places);
+      const double v = group_max ? r.order(e) : r.value(e);
+      if (v > a) { b = a; a = v; } else if (v > b) b = v;
+    }
+  }
+  for (int o = 1; o < p.lpg; o <<= 1) {
+    const double c = __shfl_down_sync(FULL, a, o), d = __shfl_down_sync(FULL, b, o);
+    if (lig + o < p.lpg) {
+      b = fmax(fmin(a, c), fmax(b, d));
+      a = fmax(a, c);
+    }
+  }
+  double rank = group_max || b == -INFINITY ? a : a + b;
+  rank = __shfl_sync(FULL, rank, lane - lig);
+  const unsigned ins = __ballot_sync(FULL, in && lig == 0), opens = __ballot_sync(FULL, open && lig == 0);
+  int ahead = __popc(ins);
+  for (unsigned left = opens; left; left &= left - 1) {
+    const int from = __ffs(left) - 1;
+    const double w = __shfl_sync(FULL, rank, from);
+    ahead += w > rank || (w == rank && from < lane - lig);
+  }
+  return in || (open && ahead < p.KG);
+}
+
 // the K best of the kept groups in 64 bits, K rounds over the row: rows with fewer than K
 // experts in service, or with more equal scores than a warp holds.  keep: bit g set where
 // group g stays.  Lane k returns the k-th chosen expert.
@@ -198,7 +241,7 @@ __device__ __forceinline__ float gate_value(float l, bool on, bool sigmoid, bool
 }
 
 template <int VMAX>
-__global__ void __launch_bounds__(32 * WARPS)
+__global__ void __launch_bounds__(32 * WARPS, VMAX <= 4 ? 8 : VMAX <= 12 ? 6 : 1)
 gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, const float* __restrict__ bias,
             GateShape p, int32_t* __restrict__ idx, float* __restrict__ gate) {
   __shared__ __align__(16) float cand_c[WARPS][32];
@@ -269,45 +312,69 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
     } else {
       load(row, -INFINITY, c);
     }
+    // `bad`: a NaN in the row; `usual`: no NaN, nor a +inf where the logits are compared
+    bool bad, usual;
     float m = -INFINITY, rz = 1.f;
-#pragma unroll
-    for (int j = 0; j < VMAX; ++j) m = max_nan(m, c[j]);
-    const bool finite = !__any_sync(FULL, !(m < INFINITY));  // neither NaN nor +inf in the row
-    const bool bad = !finite && __any_sync(FULL, m != m);
-    // softmax: the row's maximum and sum, where something needs them
-    const bool by_sum = p.KG < p.G && !group_max;
-    if (!sigmoid && (bias || !renorm || by_sum)) {
-      m = bad ? __int_as_float(0x7fffffff) : from_key(__reduce_max_sync(FULL, order_key(m)));
-      if (bias || !renorm) {
-        float z = 0.f;
-#pragma unroll
-        for (int j = 0; j < VMAX; ++j) z += c[j] == -INFINITY ? 0.f : fast_exp2((c[j] - m) * LOG2E);
-        z = warp_sum(z);
-        rz = fast_rcp(z);
-      }
-    }
     // the score of a logit, fast
     auto score = [&](float l) { return sigmoid ? fast_rcp(1.f + fast_exp2(l * -LOG2E)) : fast_exp2((l - m) * LOG2E) * rz; };
-    if (bias) {
+    const bool by_sum = p.KG < p.G && !group_max;
+    if (bias && sigmoid) {
+      float zero = 0.f;  // NaN where a score is
 #pragma unroll
-      for (int j = 0; j < VMAX; ++j) c[j] = c[j] > -INFINITY ? score(c[j]) + b[j] : -INFINITY;
-      if (!sigmoid && !finite) {  // a softmax over NaN or +inf has no scores
-#pragma unroll
-        for (int j = 0; j < VMAX; ++j) c[j] = -INFINITY;
+      for (int j = 0; j < VMAX; ++j) {
+        const float x = score(c[j]);
+        zero = fmaf(x, 0.f, zero);
+        // -inf for a logit of -inf, whatever the score
+        c[j] = fminf(x + b[j], fmaf(c[j], 5.4210109e-20f, 1e30f));
       }
+      bad = __any_sync(FULL, zero != zero);
+      usual = !bad && !odd;
     } else {
 #pragma unroll
-      for (int j = 0; j < VMAX; ++j) c[j] = fmaxf(c[j], -INFINITY) + 0.f;  // NaN ranks last, -0 as 0
+      for (int j = 0; j < VMAX; ++j) m = max_nan(m, c[j]);
+      usual = !__any_sync(FULL, !(m < INFINITY)) && !odd;
+      bad = !usual && __any_sync(FULL, m != m);
+      // softmax: the row's maximum and sum, where something needs them
+      if (!sigmoid && (bias || !renorm || by_sum)) {
+        m = bad ? __int_as_float(0x7fffffff) : from_key(__reduce_max_sync(FULL, order_key(m)));
+        if (bias || !renorm) {
+          float z = 0.f;
+          if (m > -INFINITY) {
+#pragma unroll
+            for (int j = 0; j < VMAX; ++j) z += fast_exp2((c[j] - m) * LOG2E);
+          } else if (m != m) {
+            z = m;
+          }
+          z = warp_sum(z);
+          rz = fast_rcp(z);
+        }
+      }
+      if (bias) {
+#pragma unroll
+        for (int j = 0; j < VMAX; ++j) c[j] = c[j] > -INFINITY && usual ? score(c[j]) + b[j] : -INFINITY;
+      } else {
+#pragma unroll
+        for (int j = 0; j < VMAX; ++j) c[j] += 0.f;  // -0 as 0; NaN is never larger than anything
+      }
+    }
+
+    // Each lane's three largest, in order.  The place of a value in its lane rides in its lowest
+    // bits (which makes NaN of -inf, and that is passed over): Q is what that moves a value by.
+    constexpr int BITS = VMAX <= 2 ? 1 : VMAX <= 4 ? 2 : VMAX <= 8 ? 3 : VMAX <= 16 ? 4 : VMAX <= 32 ? 5 : 6;
+    constexpr float Q = 2.f * U * (1 << BITS), LEAST = 2e-43f;  // relative; and of numbers near zero
+    float f1 = -INFINITY, f2 = -INFINITY, f3 = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < VMAX; ++j) {
+      const float f = __uint_as_float((__float_as_uint(c[j]) & ~((1u << BITS) - 1)) | j);
+      const float lo = min_nan(f1, f), lo2 = min_nan(f2, lo);
+      f1 = fmaxf(f1, f);
+      f2 = fmaxf(f2, lo);
+      f3 = fmaxf(f3, lo2);
     }
 
     bool stay = g < p.G;
     if (p.KG < p.G) {
-      float a1 = -INFINITY, a2 = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < VMAX; ++j) {
-        a2 = fmaxf(a2, fminf(a1, c[j]));
-        a1 = fmaxf(a1, c[j]);
-      }
+      float a1 = f1, a2 = f2;
       if ((p.lpg & (p.lpg - 1)) == 0) {
         for (int o = 1; o < p.lpg; o <<= 1) {
           const float d1 = __shfl_xor_sync(FULL, a1, o), d2 = __shfl_xor_sync(FULL, a2, o);
@@ -326,19 +393,24 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
         a2 = __shfl_sync(FULL, a2, lane - lig);
       }
       // a group's rank, and how far two ranks must be apart to be surely in order
-      float rank, off;
-      if (group_max) {
-        rank = a1;
-        off = margin;
-      } else if (bias) {
-        rank = a2 == -INFINITY ? a1 : a1 + a2;
-        off = 2.f * margin + fabsf(rank) * 2.f * U;
-      } else {
-        // relative: 12u of the scores and the sum, twice |a1 - base| u of the exponential's argument
-        const float base = sigmoid ? 0.f : m;
-        rank = a1 == -INFINITY ? a1 : (sigmoid ? score(a1) : fast_exp2((a1 - m) * LOG2E)) +
-                                          (a2 == -INFINITY ? 0.f : sigmoid ? score(a2) : fast_exp2((a2 - m) * LOG2E));
-        off = rank * 2.f * U * (12.f + 2.f * fabsf(a1 - base)) + 3e-38f;
+      float rank = a1, off = margin + 2.f * Q * fabsf(a1) + LEAST;
+      if (!group_max && bias) {
+        if (a2 > -INFINITY) {
+          rank += a2;
+          off += off + 2.f * Q * fabsf(a2) + 4.f * U * fabsf(rank);
+        }
+      } else if (!group_max && a1 > -INFINITY) {
+        // relative: 12u of each score and the sum, twice |a - base| u of its exponential's argument,
+        // |a| Q of the logit's lowest bits
+        auto one = [&](float x) { return sigmoid ? score(x) : fast_exp2((x - m) * LOG2E); };
+        auto off_of = [&](float x) { return 2.f * U * (12.f + 2.f * fabsf(sigmoid ? x : x - m)) + 2.f * Q * fabsf(x); };
+        rank = one(a1);
+        off = rank * off_of(a1) + 4e-38f;
+        if (a2 > -INFINITY) {
+          const float s2 = one(a2);
+          rank += s2;
+          off += s2 * off_of(a2);
+        }
       }
       // the KG-th largest rank and the next; equal ones go together
       const int mine = g < p.G ? order_key(rank) : INT_MIN;
@@ -351,60 +423,74 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
       stay = mine >= kth && g < p.G;
       const int kept = __popc(__ballot_sync(FULL, stay && lig == 0));
       // the lanes at the border know how near the next rank is
-      const bool near = mine == kth && after != INT_MIN && rank != -INFINITY && rank - from_key(after) <= off &&
-                        !(group_max && !bias);
-      if (kept != p.KG || __any_sync(FULL, near))
-        stay = keep_groups64(row64(row, bias, p.E, sigmoid, m), p, g, lig, group_max ? a1 : a2, margin) && g < p.G;
+      const float border = from_key(kth);
+      const bool near = mine == kth && after != INT_MIN && rank != -INFINITY && rank - from_key(after) <= off;
+      if (kept != p.KG || __any_sync(FULL, near)) {
+        const float bound = (group_max ? a1 : a2) - 2.f * Q * fabsf(group_max ? a1 : a2) - LEAST - margin;
+        const float slack = fmaxf(off, from_key(__reduce_max_sync(FULL, mine == kth ? order_key(off) : INT_MIN)));
+        const bool open = g < p.G && fabsf(rank - border) <= slack;
+        const bool in = g < p.G && rank - border > slack;
+        // from the values at hand, unless equal ranks put the border too low or a lane may have more of them
+        const bool plain = kth != INT_MIN && border > -INFINITY && usual &&
+                           __popc(__ballot_sync(FULL, in && lig == 0)) < p.KG &&
+                           !__any_sync(FULL, open && f3 >= bound && f3 > -INFINITY && count > 3);
+        const Row64 r = row64(row, bias, p.E, sigmoid, m);
+        stay = plain ? settle_groups64(r, p, g, lig, e0, make_float3(f1, f2, f3), (1u << BITS) - 1, bound, open,
+                                       in)
+                     : keep_groups64(r, p, g, lig, bound + margin, margin) && g < p.G;
+      }
     }
 
-    // Each lane keeps its three largest, and K + 1 rounds take the warp's largest one by one.
-    // The place of a value in its lane rides in its lowest bits: what that moves a value by is
-    // added to the margin.  (-inf turns to NaN and back; rows with +inf go the other way.)
-    constexpr int BITS = VMAX <= 2 ? 1 : VMAX <= 4 ? 2 : VMAX <= 8 ? 3 : VMAX <= 16 ? 4 : VMAX <= 32 ? 5 : 6;
+    // K + 1 rounds take the warp's largest one by one
     int e = 0, place = 32;
     float mine = -INFINITY;
-    bool sure = finite && !odd;
+    bool sure = usual;
     float limit = -INFINITY;
     if (sure) {
-      float f1 = -INFINITY, f2 = -INFINITY, f3 = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < VMAX; ++j) {
-        const float f = fmaxf(__uint_as_float((__float_as_uint(c[j]) & ~((1u << BITS) - 1)) | j), -INFINITY);
-        const float lo = fminf(f1, f), lo2 = fminf(f2, lo);
-        f1 = fmaxf(f1, f);
-        f2 = fmaxf(f2, lo);
-        f3 = fmaxf(f3, lo2);
-      }
-      int k1 = order_key(f1), k2 = order_key(f2), k3 = order_key(f3);
       const int none = order_key(-INFINITY);  // what a lane with no more values offers
-      if (!stay) k1 = k2 = k3 = none;
-      int left = 3, best = none, rounds = 0;
-      for (; rounds <= p.K; ++rounds) {
-        const int top = __reduce_max_sync(FULL, k1);
-        if (top == none) break;
-        if (lane == rounds) best = top;
-        if (k1 == top) {
-          cand_e[warp][rounds] = e0 + (__float_as_uint(from_key(top)) & ((1u << BITS) - 1));
-          k1 = k2;
-          k2 = k3;
-          k3 = none;
-          --left;
-        }
+      int k1 = none, k2 = none, k3 = none;
+      if (stay) {
+        k1 = order_key(f1);
+        k2 = order_key(f2);
+        k3 = order_key(f3);
       }
-      // the values in order: lane k holds the k-th, and looks at the next one.  The K + 1 rounds
-      // are what they seem where each took one value, the values are clear of each other, K
-      // experts were in service and no lane gave all that it had kept while it has more.
+      int best = none;
+      unsigned from = 0;
+#pragma unroll 3
+      for (int k = 0; k <= p.K; ++k) {
+        const int top = __reduce_max_sync(FULL, k1);
+        const bool gives = k1 == top;
+        const unsigned who = __ballot_sync(FULL, gives);
+        if (lane == k) {
+          best = top;
+          from = who;
+        }
+        k1 = gives ? k2 : k1;
+        k2 = gives ? k3 : k2;
+        k3 = gives ? none : k3;
+      }
+      // The values in order: lane k holds the k-th, and looks at the next one.  The rounds are
+      // what they seem where each took one value, the values are clear of each other and K
+      // experts were in service.
       const float v = from_key(best), after = __shfl_down_sync(FULL, v, 1);
-      const float apart = margin + fabsf(v) * (2.f * U * (2 << BITS)) + 2e-43f;  // and zeros are denormals there
-      const bool clear = lane >= p.K || (best != none && (v - after > apart || after == -INFINITY));
-      sure = __all_sync(FULL, clear && (VMAX <= 3 || left > 0 || count <= 3)) &&
-             __reduce_add_sync(FULL, 3 - left) == rounds;
+      const bool clear = best != none && (from & (from - 1)) == 0 &&
+                         (v - after > margin + 2.f * Q * fabsf(v) + LEAST || after == -INFINITY);
+      sure = __all_sync(FULL, lane >= p.K || clear);
+      const bool gave_all = stay && f3 > -INFINITY && k1 == none;
+      if (VMAX > 3 && sure && __any_sync(FULL, gave_all)) {
+        // a lane gave all three: none of its others may come before the last one taken
+        const float last = __shfl_sync(FULL, v, p.K);
+        const float lim = last > -INFINITY ? last - (margin + 2.f * Q * fabsf(last) + LEAST) : -3.4028235e38f;
+        int above = 0;
+#pragma unroll
+        for (int j = 0; j < VMAX; ++j) above += c[j] >= lim;
+        sure = !__any_sync(FULL, gave_all && above > 3);
+      }
+      e = __shfl_sync(FULL, e0, __ffs(from) - 1 & 31) + (__float_as_uint(v) & ((1u << BITS) - 1));
       // where that does not hold, the K-th value (or one below it) bounds the candidates
       limit = __shfl_sync(FULL, v, p.K - 1);
-      limit -= fabsf(limit) * (2.f * U * (1 << BITS));
-      __syncwarp();
+      limit -= Q * fabsf(limit) + LEAST;
       if (sure && lane < p.K) {
-        e = cand_e[warp][lane];
         mine = row[e];
         place = lane;
       }
@@ -443,7 +529,6 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
         }
       return n;
     };
-    __syncwarp();
     int n = collect();
     if (n > 32) {
       // a bound too low: the K-th largest itself, K rounds over the registers
@@ -643,9 +728,28 @@ gate_bwd_kernel(const float* __restrict__ d_gate, const float* __restrict__ logi
   }
 }
 
-int warp_grid(long long T) {
-  const long long ctas = (T + WARPS - 1) / WARPS, cap = (long long)sm_count() * 16;
+// one CTA for WARPS tokens, at most as many as the GPU holds at once: each then walks its
+// even share (more would run as a second, partly filled round)
+template <typename F> int resident_grid(F kernel, long long T) {
+  static const int per_sm = [&] {
+    int n = 0;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, 32 * WARPS, 0) == cudaSuccess && n > 0 ? n : 1;
+  }();
+  const long long ctas = (T + WARPS - 1) / WARPS, cap = (long long)sm_count() * per_sm;
   return (int)(ctas < cap ? ctas : cap);
+}
+
+template <int VMAX>
+void gate_v(float* logits, const float* part, int S, const float* bias, const GateShape& p, int32_t* idx, float* gate,
+            cudaStream_t s) {
+  gate_kernel<VMAX><<<resident_grid(gate_kernel<VMAX>, p.T), 32 * WARPS, 0, s>>>(logits, part, S, bias, p, idx, gate);
+}
+
+template <int VQ>
+void gate_bwd_v(const float* d_gate, const float* logits, const int32_t* idx, int T, int E, int K, int mode,
+                float scale, float* d_logits, cudaStream_t s) {
+  gate_bwd_kernel<VQ><<<resident_grid(gate_bwd_kernel<VQ>, T), 32 * WARPS, 0, s>>>(
+      d_gate, logits, idx, T, E, K, mode, scale, d_logits, device_error_word());
 }
 
 }  // namespace
@@ -657,8 +761,7 @@ int launch_gate(float* logits, const float* part, int S, const float* bias, int 
   GateShape p{T, E, K, G, KG, E / G, 32 / G, 0, mode, scale};
   p.vpl = (p.gs + p.lpg - 1) / p.lpg;
   if (p.gs % 4 == 0 && p.vpl > 2) p.vpl = (p.vpl + 3) / 4 * 4;  // 16-byte loads
-  const int grid = warp_grid(T);
-#define MOE_GATE(V) gate_kernel<V><<<grid, 32 * WARPS, 0, s>>>(logits, part, S, bias, p, idx, gate)
+#define MOE_GATE(V) gate_v<V>(logits, part, S, bias, p, idx, gate, s)
   if (p.vpl <= 2) MOE_GATE(2);
   else if (p.vpl <= 4) MOE_GATE(4);
   else if (p.vpl <= 8) MOE_GATE(8);
@@ -673,9 +776,8 @@ int launch_gate(float* logits, const float* part, int S, const float* bias, int 
 int launch_gate_bwd(const float* d_gate, const float* logits, const int32_t* idx, int T, int E, int K, int mode,
                     float scale, float* d_logits, cudaStream_t s) {
   if (T == 0) return MOE_OK;
-  const int grid = warp_grid(T), pieces = E % 4 == 0 ? (E + 127) / 128 : 0;
-#define MOE_GATE_BWD(V) \
-  gate_bwd_kernel<V><<<grid, 32 * WARPS, 0, s>>>(d_gate, logits, idx, T, E, K, mode, scale, d_logits, device_error_word())
+  const int pieces = E % 4 == 0 ? (E + 127) / 128 : 0;
+#define MOE_GATE_BWD(V) gate_bwd_v<V>(d_gate, logits, idx, T, E, K, mode, scale, d_logits, s)
   if (pieces == 0) MOE_GATE_BWD(0);
   else if (pieces <= 1) MOE_GATE_BWD(1);
   else if (pieces <= 2) MOE_GATE_BWD(2);
