@@ -265,118 +265,109 @@ def mod_select(x, w_mod, B, L, H, C, dtype, score, sel, sel_score, mask, x_sel, 
                                           _ptr(y_skip), _ptr(ws), ws_bytes, _stream(stream)))
 
 
-def _args(fn, *tensors):
-    """Addresses of (name, tensor, dtype, elements) arguments: each None, a raw address, or a
-    contiguous tensor of that type and at least that many elements on the current device."""
+# Tensor arguments of the calls below: names, in the order of the C arguments, and types
+# ("x": the call's dtype).
+_TENSORS = {
+    "moe_gate": "logits:f sel_bias:f topk_idx:i topk_gate:f",
+    "moe_gate_bwd": "d_gate:f logits:f topk_idx:i d_logits:f",
+    "moe_route_group": "x:x w_router:x sel_bias:f logits:f topk_idx:i topk_gate:f ws:b",
+    "moe_combine_norm": "h:x gate:f dst_row:i row_scale:f residual:x w_post:f res_scale:f w_next:f y:x xn:x",
+    "moe_combine_norm_bwd": "dy:x dxn:x h:x gate:f dst_row:i row_scale:f y:x w_post:f res_scale:f w_next:f d_res:x dh:x "
+                            "d_gate:f d_scale:f dw_post:f d_res_scale:f dw_next:f ws:b",
+    "moe_ckpt_pack": "x:x q:c scale:b",
+    "moe_ckpt_unpack": "q:c scale:b x:x",
+    "moe_ckpt_swiglu": "q:c scale:b gu:x act:x",
+}
+_types = {}  # (call, dtype): the types of its tensors
+_cuda = None
+
+
+def _types_of(fn, dtype):
+    global _cuda
+    import torch
+    if dtype not in (MOE_F32, MOE_BF16):
+        raise MoEError(fn, MOE_ERR_INVALID_ARG, moe_status_str(MOE_ERR_INVALID_ARG))
+    kinds = {"f": torch.float32, "i": torch.int32, "c": torch.int8, "b": torch.uint8,
+             "x": torch.bfloat16 if dtype == MOE_BF16 else torch.float32}
+    _cuda = torch.cuda
+    _types[fn, dtype] = t = tuple(kinds[w.split(":")[1]] for w in _TENSORS[fn].split())
+    return t
+
+
+def _args(fn, dtype, tensors, sizes):
+    """Addresses of a call's tensors: each None, a raw address, or a contiguous tensor of its
+    type and at least its size, on the current device."""
+    types = _types.get((fn, dtype)) or _types_of(fn, dtype)
     dev = None
     out = []
-    for name, t, dtype, n in tensors:
+    for t, want, n in zip(tensors, types, sizes):
         if t is None or type(t) is int:
             out.append(t)
             continue
         if dev is None:
-            dev = _torch().cuda.current_device() if t.is_cuda else -2
-        if t.get_device() != dev:
-            raise ValueError(f"{fn}: {name} is not on the current CUDA device")
-        if t.dtype is not dtype or t.numel() < n or not t.is_contiguous():
-            raise ValueError(f"{fn}: {name} must be a contiguous {dtype} tensor of at least {n} elements, "
+            dev = _cuda.current_device() if t.is_cuda else -2
+        if t.dtype is not want or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
+            name = _TENSORS[fn].split()[len(out)].split(":")[0]
+            if t.get_device() != dev:
+                raise ValueError(f"{fn}: {name} is not on the current CUDA device")
+            raise ValueError(f"{fn}: {name} must be a contiguous {want} tensor of at least {n} elements, "
                              f"not {t.dtype} {tuple(t.shape)} with strides {t.stride()}")
         out.append(t.data_ptr())
     return out
 
 
-_torch_module = None
-
-
-def _torch():
-    global _torch_module
-    if _torch_module is None:
-        import torch
-        _torch_module = torch
-    return _torch_module
-
-
-def _tdt(fn, dtype):
-    torch = _torch()
-    if dtype not in (MOE_F32, MOE_BF16):
-        raise MoEError(fn, MOE_ERR_INVALID_ARG, moe_status_str(MOE_ERR_INVALID_ARG))
-    return torch.bfloat16 if dtype == MOE_BF16 else torch.float32
-
-
 def moe_gate(logits, sel_bias, T, E, K, groups, topk_groups, mode, scale, topk_idx, topk_gate, stream=None):
-    torch = _torch()
-    f32 = torch.float32
-    l, b, i, g = _args("moe_gate", ("logits", logits, f32, T * E), ("sel_bias", sel_bias, f32, E),
-                       ("topk_idx", topk_idx, torch.int32, T * K), ("topk_gate", topk_gate, f32, T * K))
+    l, b, i, g = _args("moe_gate", MOE_F32, (logits, sel_bias, topk_idx, topk_gate), (T * E, E, T * K, T * K))
     _check("moe_gate", lib().moe_gate(l, b, T, E, K, groups, topk_groups, mode, scale, i, g, _stream(stream)))
 
 
 def moe_gate_bwd(d_gate, logits, topk_idx, T, E, K, mode, scale, d_logits, stream=None):
-    torch = _torch()
-    f32 = torch.float32
-    dg, l, i, dl = _args("moe_gate_bwd", ("d_gate", d_gate, f32, T * K), ("logits", logits, f32, T * E),
-                         ("topk_idx", topk_idx, torch.int32, T * K), ("d_logits", d_logits, f32, T * E))
+    dg, l, i, dl = _args("moe_gate_bwd", MOE_F32, (d_gate, logits, topk_idx, d_logits), (T * K, T * E, T * K, T * E))
     _check("moe_gate_bwd", lib().moe_gate_bwd(dg, l, i, T, E, K, mode, scale, dl, _stream(stream)))
 
 
 def moe_route_group(x, w_router, sel_bias, T, H, E, K, dtype, groups, topk_groups, mode, scale, logits, topk_idx,
                     topk_gate, ws=None, ws_bytes=0, stream=None):
-    torch = _torch()
-    f32, tdt = torch.float32, _tdt("moe_route_group", dtype)
-    xp, wp, b, l, i, g, w = _args(
-        "moe_route_group", ("x", x, tdt, T * H), ("w_router", w_router, tdt, H * E), ("sel_bias", sel_bias, f32, E),
-        ("logits", logits, f32, T * E), ("topk_idx", topk_idx, torch.int32, T * K),
-        ("topk_gate", topk_gate, f32, T * K), ("ws", ws, torch.uint8, ws_bytes))
+    xp, wp, b, l, i, g, w = _args("moe_route_group", dtype, (x, w_router, sel_bias, logits, topk_idx, topk_gate, ws),
+                                  (T * H, H * E, E, T * E, T * K, T * K, ws_bytes))
     _check("moe_route_group", lib().moe_route_group(xp, wp, b, T, H, E, K, dtype, groups, topk_groups, mode, scale, l,
                                                     i, g, w, ws_bytes, _stream(stream)))
 
 
 def moe_combine_norm(h, gate, dst_row, row_scale, residual, w_post, res_scale, w_next, eps, T, H, K, dtype, y, xn,
                      stream=None):
-    torch = _torch()
-    f32, tdt = torch.float32, _tdt("moe_combine_norm", dtype)
-    a = _args("moe_combine_norm", ("h", h, tdt, T * K * H), ("gate", gate, f32, T * K),
-              ("dst_row", dst_row, torch.int32, T * K), ("row_scale", row_scale, f32, T),
-              ("residual", residual, tdt, T * H), ("w_post", w_post, f32, H), ("res_scale", res_scale, f32, H),
-              ("w_next", w_next, f32, H), ("y", y, tdt, T * H), ("xn", xn, tdt, T * H))
+    n, R = T * H, T * K
+    a = _args("moe_combine_norm", dtype, (h, gate, dst_row, row_scale, residual, w_post, res_scale, w_next, y, xn),
+              (R * H, R, R, T, n, H, H, H, n, n))
     _check("moe_combine_norm", lib().moe_combine_norm(*a[:8], eps, T, H, K, dtype, a[8], a[9], _stream(stream)))
 
 
 def moe_combine_norm_bwd(dy, dxn, h, gate, dst_row, row_scale, y, w_post, res_scale, w_next, eps, T, H, K, dtype,
                          d_res, dh, d_gate, d_scale, dw_post, d_res_scale, dw_next, ws=None, ws_bytes=0, stream=None):
-    torch = _torch()
-    f32, tdt = torch.float32, _tdt("moe_combine_norm_bwd", dtype)
     n, R = T * H, T * K
-    a = _args("moe_combine_norm_bwd", ("dy", dy, tdt, n), ("dxn", dxn, tdt, n), ("h", h, tdt, R * H),
-              ("gate", gate, f32, R), ("dst_row", dst_row, torch.int32, R), ("row_scale", row_scale, f32, T),
-              ("y", y, tdt, n), ("w_post", w_post, f32, H), ("res_scale", res_scale, f32, H),
-              ("w_next", w_next, f32, H), ("d_res", d_res, tdt, n), ("dh", dh, tdt, R * H), ("d_gate", d_gate, f32, R),
-              ("d_scale", d_scale, f32, T), ("dw_post", dw_post, f32, H), ("d_res_scale", d_res_scale, f32, H),
-              ("dw_next", dw_next, f32, H), ("ws", ws, torch.uint8, ws_bytes))
+    a = _args("moe_combine_norm_bwd", dtype,
+              (dy, dxn, h, gate, dst_row, row_scale, y, w_post, res_scale, w_next, d_res, dh, d_gate, d_scale, dw_post,
+               d_res_scale, dw_next, ws),
+              (n, n, R * H, R, R, T, n, H, H, H, n, R * H, R, T, H, H, H, ws_bytes))
     _check("moe_combine_norm_bwd", lib().moe_combine_norm_bwd(*a[:10], eps, T, H, K, dtype, *a[10:], ws_bytes,
                                                               _stream(stream)))
 
 
 def moe_ckpt_pack(x, rows, N, dtype, q, scale, stream=None):
-    torch = _torch()
-    a = _args("moe_ckpt_pack", ("x", x, _tdt("moe_ckpt_pack", dtype), rows * N), ("q", q, torch.int8, rows * N),
-              ("scale", scale, torch.uint8, rows * ((N + 31) // 32)))
+    n, runs = rows * N, rows * ((N + 31) // 32)
+    a = _args("moe_ckpt_pack", dtype, (x, q, scale), (n, n, runs))
     _check("moe_ckpt_pack", lib().moe_ckpt_pack(a[0], rows, N, dtype, a[1], a[2], _stream(stream)))
 
 
 def moe_ckpt_unpack(q, scale, rows, N, dtype, x, stream=None):
-    torch = _torch()
-    a = _args("moe_ckpt_unpack", ("q", q, torch.int8, rows * N), ("scale", scale, torch.uint8, rows * ((N + 31) // 32)),
-              ("x", x, _tdt("moe_ckpt_unpack", dtype), rows * N))
+    n, runs = rows * N, rows * ((N + 31) // 32)
+    a = _args("moe_ckpt_unpack", dtype, (q, scale, x), (n, runs, n))
     _check("moe_ckpt_unpack", lib().moe_ckpt_unpack(a[0], a[1], rows, N, dtype, a[2], _stream(stream)))
 
 
 def moe_ckpt_swiglu(q, scale, rows, Hp, dtype, gu, act, stream=None):
-    torch = _torch()
-    tdt = _tdt("moe_ckpt_swiglu", dtype)
-    a = _args("moe_ckpt_swiglu", ("q", q, torch.int8, 2 * rows * Hp),
-              ("scale", scale, torch.uint8, rows * ((2 * Hp + 31) // 32)), ("gu", gu, tdt, 2 * rows * Hp),
-              ("act", act, tdt, rows * Hp))
+    n, runs = rows * Hp, rows * ((2 * Hp + 31) // 32)
+    a = _args("moe_ckpt_swiglu", dtype, (q, scale, gu, act), (2 * n, runs, 2 * n, n))
     _check("moe_ckpt_swiglu", lib().moe_ckpt_swiglu(a[0], a[1], rows, Hp, dtype, a[2], a[3], _stream(stream)))
 
 

@@ -11,6 +11,8 @@
 // reductions, while the copies of the rows behind are under way.
 #include <math.h>
 
+#include <atomic>
+
 #include "moe_internal.cuh"
 
 namespace moe {
@@ -617,16 +619,29 @@ column_sums_kernel(const float* __restrict__ part, int parts, int H, const float
 }
 
 constexpr int RING_BYTES = 200 * 1024;  // at most; a CTA's 227 KB also hold the sums and row numbers
+constexpr int RING_LIMIT = 215 * 1024;  // the most that a kernel here is launched with
 constexpr int SM_BYTES = 227 * 1024, BWD_STATIC = 12 * 1024;  // an SM's; a backward CTA's beside the ring, rounded up
 
 int threads_for(int nvec, int vpt) { return ((nvec + vpt - 1) / vpt + 31) / 32 * 32; }
 
-// CTAs of a persistent grid: as many as fit, at most `cap` to an SM, at most one a token
-template <typename F> int persistent_grid(F kernel, int threads, int smem, int cap, int T, int* grid) {
-  int per_sm = 0;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1)
-    return MOE_ERR_CUDA;
+// CTAs of a persistent grid: as many as fit, at most `cap` to an SM, at most one a token.
+// The answer to the last question is kept for each kernel (asking the runtime takes 0.7 us):
+// one word holds device, threads, shared memory and CTAs to an SM.
+template <typename F> int persistent_grid(F kernel, std::atomic<unsigned long long>& known, int threads, int smem, int cap,
+                                          int T, int* grid) {
+  int dev = 0, per_sm = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+  const unsigned long long ask = (unsigned long long)(dev + 1) << 48 | (unsigned long long)threads << 32 |
+                                 (unsigned long long)smem << 8;
+  const unsigned long long k = known.load(std::memory_order_relaxed);
+  if ((k & ~0xffull) == ask) {
+    per_sm = (int)(k & 0xff);
+  } else {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_LIMIT) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1)
+      return MOE_ERR_CUDA;
+    known.store(ask | (unsigned)per_sm, std::memory_order_relaxed);
+  }
   const long long n = (long long)sm_count() * (per_sm < cap ? per_sm : cap);
   *grid = (int)(T < n ? T : n);
   return MOE_OK;
@@ -636,7 +651,8 @@ template <typename T, int X, int S, int MAXT, int CTAS> int fwd_v(const FwdArgs&
   constexpr int VPT = X / Vec16<T>::N;
   const int threads = threads_for(a.H / Vec16<T>::N, VPT), smem = S * VPT * threads * 16;
   int grid = 0;
-  const int st = persistent_grid(combine_norm_kernel<T, X, S, MAXT, CTAS>, threads, smem, 32, a.T, &grid);
+  static std::atomic<unsigned long long> known{0};
+  const int st = persistent_grid(combine_norm_kernel<T, X, S, MAXT, CTAS>, known, threads, smem, 32, a.T, &grid);
   if (st != MOE_OK) return st;
   combine_norm_kernel<T, X, S, MAXT, CTAS><<<grid, threads, smem, s>>>(a);
   return launch_status();
@@ -676,7 +692,8 @@ template <typename T, int X, bool HOLD> int bwd_v(BwdArgs& a, int* grid, cudaStr
     break;
   }
   const int smem = a.S * row;
-  const int st = persistent_grid(combine_norm_bwd_kernel<T, X, HOLD>, threads, smem, bwd_ctas_per_sm(a.H), a.T, grid);
+  static std::atomic<unsigned long long> known{0};
+  const int st = persistent_grid(combine_norm_bwd_kernel<T, X, HOLD>, known, threads, smem, bwd_ctas_per_sm(a.H), a.T, grid);
   if (st != MOE_OK) return st;
   combine_norm_bwd_kernel<T, X, HOLD><<<*grid, threads, smem, s>>>(a);
   return launch_status();
