@@ -12,6 +12,10 @@ device: the row split per expert stays on the device (cu_seqlens).
                   selected tokens -> moe_combine(row_scale = score, residual = x,
                   out_row = selected rows); route backward through
                   moe_permute_bwd(d_scale) and moe_route_bwd(MOE_ROUTE_MOD_LINEAR).
+    MoE block:    moe_combine_norm (the norm before it) -> moe_route_group -> moe_dispatch ->
+                  moe_expert_ffn -> moe_combine_norm (combine, norm after the block, gate and
+                  residual scale, residual, norm before the next block); backward in the
+                  reverse order, its expert activations kept in 8 bits where asked.
 """
 from __future__ import annotations
 
@@ -171,3 +175,110 @@ def mod_route_backward(m: MoDBuffers, w_router, w_mod, dy, stream=None):
                     K, dt, b.d_logits, b.dw_router, b.dx, b.ws_bwd, b.ws_bwd_bytes, stream=stream)
     L.moe_route_bwd(L.MOE_ROUTE_MOD_LINEAR, m.d_score, None, None, m.x_sel, w_mod, T, H, 1, 1, dt,
                     None, m.dw_mod, b.dx, m.ws_lin, m.ws_lin_bytes, stream=stream)
+
+
+class GroupGate:
+    """Options of the group-limited gate (moe_gate): expert groups, how many of them a token
+    may use, and the mode bits and scale of its gates."""
+
+    def __init__(self, groups=1, topk_groups=None, sigmoid=False, renorm=False, group_max=False, scale=1.0):
+        self.groups, self.topk_groups = groups, groups if topk_groups is None else topk_groups
+        self.mode = (L.MOE_GATE_SIGMOID if sigmoid else L.MOE_GATE_SOFTMAX) | (L.MOE_GATE_RENORM if renorm else 0) | \
+            (L.MOE_GATE_GROUP_MAX if group_max else 0)
+        self.scale = scale
+
+
+class ExpertCheckpoint:
+    """What the expert FFN's backward reads of the forward, in 8 bits: the dispatched rows and
+    [g | u] (moe_ckpt_pack), 1.03 bytes a value instead of 2.  act is computed again.  One for
+    each layer; the layers share one MoEBuffers to save from and restore into."""
+
+    def __init__(self, b: MoEBuffers):
+        if b.gu is None:
+            raise ValueError("ExpertCheckpoint: the buffers were made without train=True")
+        dev, R = b.gu.device, b.T * b.K
+        self.gu = torch.empty((R, 2 * b.Hp), dtype=torch.int8, device=dev)
+        self.gu_scale = torch.empty((R, (2 * b.Hp + 31) // 32), dtype=torch.uint8, device=dev)
+        self.xs = torch.empty((R, b.H), dtype=torch.int8, device=dev)
+        self.xs_scale = torch.empty((R, (b.H + 31) // 32), dtype=torch.uint8, device=dev)
+
+    def save(self, b: MoEBuffers, stream=None):
+        R = b.T * b.K
+        L.moe_ckpt_pack(b.gu, R, 2 * b.Hp, b.cdt, self.gu, self.gu_scale, stream=stream)
+        L.moe_ckpt_pack(b.xs, R, b.H, b.cdt, self.xs, self.xs_scale, stream=stream)
+
+    def restore(self, b: MoEBuffers, stream=None):
+        R = b.T * b.K
+        L.moe_ckpt_swiglu(self.gu, self.gu_scale, R, b.Hp, b.cdt, b.gu, b.act, stream=stream)
+        L.moe_ckpt_unpack(self.xs, self.xs_scale, R, b.H, b.cdt, b.xs, stream=stream)
+
+
+class MoEBlockBuffers:
+    """Buffers of a MoE block: MoEBuffers of its layer (``moe``), the normed input ``x0``, the
+    residual stream ``y`` behind the block and the normed input ``xn`` of the next one; for
+    training the gradients of all of them and of the norm weights."""
+
+    def __init__(self, T, H, E, K, Hp, dtype: str, device, train: bool = False):
+        tdt, f32 = _TDT[dtype], torch.float32
+        self.moe = MoEBuffers(T, H, E, K, Hp, dtype, device, backward=train, train=train)
+        self.x0, self.y, self.xn = (torch.empty((T, H), dtype=tdt, device=device) for _ in range(3))
+        if train:
+            self.d_x = torch.empty((T, H), dtype=tdt, device=device)
+            self.dw_pre, self.dw_post, self.d_res_scale, self.dw_next = (
+                torch.empty((H,), dtype=f32, device=device) for _ in range(4))
+            self.ws_norm_bytes = L.moe_workspace_bytes(L.MOE_OP_COMBINE_NORM_BWD, T, H, 0, K, 0)
+            self.ws_norm = _ws(self.ws_norm_bytes, device)
+
+
+def moe_block_forward(m: MoEBlockBuffers, x, w_pre, w_router, sel_bias, gate: GroupGate, w_gate, w_up, w_down,
+                      w_post=None, res_scale=None, w_next=None, eps=1e-5, x0=None, ckpt: ExpertCheckpoint | None = None,
+                      stream=None):
+    """One MoE block: m.y = x + res_scale * norm(MoE(norm(x))), m.xn = norm(m.y).
+
+    w_pre, w_post, w_next (float [H]): weights of the norms before the block, after it and
+    before the next one; w_post and w_next may be None (no such norm).  x0: norm(x) where
+    the block before has written it (its m.xn); w_pre is then unused.  ckpt: keep the expert
+    activations there, so that m.moe may serve other layers before the backward."""
+    b = m.moe
+    T, H, E, K, Hp, dt = b.T, b.H, b.E, b.K, b.Hp, b.cdt
+    if x0 is None:
+        x0 = m.x0
+        L.moe_combine_norm(None, None, None, None, x, None, None, w_pre, eps, T, H, 0, dt, None, x0, stream=stream)
+    L.moe_route_group(x0, w_router, sel_bias, T, H, E, K, dt, gate.groups, gate.topk_groups, gate.mode, gate.scale,
+                      b.logits, b.idx, b.gate, b.ws_route, b.ws_route_bytes, stream=stream)
+    L.moe_dispatch(x0, b.idx, T, H, E, K, dt, b.cu, b.dst_row, b.src_tok, b.xs, b.ws_dispatch, b.ws_dispatch_bytes,
+                   stream=stream)
+    L.moe_expert_ffn_ex(b.xs, b.cu, T * K, w_gate, w_up, w_down, E, H, Hp, dt, b.act, b.gu, b.h, b.ws_ffn,
+                        b.ws_ffn_bytes, stream=stream)
+    if ckpt is not None:
+        ckpt.save(b, stream=stream)
+    L.moe_combine_norm(b.h, b.gate, b.dst_row, None, x, w_post, res_scale, w_next, eps, T, H, K, dt, m.y,
+                       None if w_next is None else m.xn, stream=stream)
+
+
+def moe_block_backward(m: MoEBlockBuffers, x, w_pre, w_router, gate: GroupGate, w_gate, w_up, w_down, dy, dxn=None,
+                       w_post=None, res_scale=None, w_next=None, eps=1e-5, x0=None,
+                       ckpt: ExpertCheckpoint | None = None, stream=None):
+    """Backward of moe_block_forward on the buffers it filled (with ckpt: on its checkpoint),
+    given dy = dL/dy and, with w_next, dxn = dL/dxn.  Leaves m.d_x = dL/dx, the weight
+    gradients in m.moe (dw_gate, dw_up, dw_down, dw_router) and those of the norms.  With x0
+    given (the norm belongs to the block before) m.d_x holds the residual's share alone and
+    m.moe.dx = dL/dx0."""
+    b = m.moe
+    T, H, E, K, Hp, dt = b.T, b.H, b.E, b.K, b.Hp, b.cdt
+    L.moe_combine_norm_bwd(dy, dxn, b.h, b.gate, b.dst_row, None, None if w_next is None else m.y, w_post, res_scale,
+                           w_next, eps, T, H, K, dt, m.d_x, b.dh, b.d_gate, None,
+                           None if w_post is None else m.dw_post, None if res_scale is None else m.d_res_scale,
+                           None if w_next is None else m.dw_next, m.ws_norm, m.ws_norm_bytes, stream=stream)
+    if ckpt is not None:
+        ckpt.restore(b, stream=stream)
+    L.moe_expert_ffn_bwd(b.xs, b.cu, T * K, w_gate, w_up, w_down, E, H, Hp, dt, b.gu, b.act, b.dh, b.dxs,
+                         b.dw_gate, b.dw_up, b.dw_down, b.ws_ffn_bwd, b.ws_ffn_bwd_bytes, stream=stream)
+    L.moe_permute_bwd(None, None, b.gate, b.dst_row, None, None, b.dxs, T, H, K, dt, None, None, None, b.dx,
+                      stream=stream)
+    L.moe_gate_bwd(b.d_gate, b.logits, b.idx, T, E, K, gate.mode, gate.scale, b.d_logits, stream=stream)
+    L.moe_route_bwd(L.MOE_ROUTE_LOGIT_GRAD, b.d_logits, None, None, m.x0 if x0 is None else x0, w_router, T, H, E, K,
+                    dt, None, b.dw_router, b.dx, b.ws_bwd, b.ws_bwd_bytes, stream=stream)
+    if x0 is None:
+        L.moe_combine_norm_bwd(m.d_x, b.dx, None, None, None, None, x, None, None, w_pre, eps, T, H, 0, dt, m.d_x,
+                               None, None, None, None, None, m.dw_pre, m.ws_norm, m.ws_norm_bytes, stream=stream)
