@@ -205,7 +205,7 @@ MOE_API int moe_route_group(const void* x, const void* w_router, const float* se
  *   MOE_GATE_SOFTMAX|MOE_GATE_RENORM  d_logits = scale * q (d_gate - <d_gate, q>)
  *   and 0 elsewhere; an expert listed twice in a row receives the sum of its shares.
  *   d_gate [T,K], logits [T,E] float; topk_idx [T,K] int32 as moe_gate wrote it (an index
- *   outside [0,E) sets MOE_ERR_DEVICE_BOUNDS and has no share); d_logits [T,E] float out,
+ *   outside [0,E) sets MOE_ERR_DEVICE_BOUNDS and has no share); d_logits [T,E] float out, apart from logits,
  *   every element written.  MOE_GATE_GROUP_MAX is accepted and changes nothing.  Sizes as
  *   moe_gate.  dw_router and dx follow with moe_route_bwd(MOE_ROUTE_LOGIT_GRAD).
  */

@@ -124,3 +124,19 @@ def test_offsets_past_32_bits():
     assert torch.equal(gu[-100:], gu2) and torch.equal(act[-100:], act2)
     L.moe_ckpt_unpack(q, s, rows, N, L.MOE_BF16, x)
     assert torch.equal(x, gu)
+
+
+def test_empty_batch_and_another_stream():
+    e = torch.empty((0, 64), dtype=torch.bfloat16, device=DEV)
+    q, s = pack(e, "bf16")
+    L.moe_ckpt_unpack(q, s, 0, 64, L.MOE_BF16, e)
+    L.moe_ckpt_swiglu(q, s, 0, 32, L.MOE_BF16, e, e)
+    x = torch.randn((500, 1408), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(DEV)
+    ref = pack(x, "bf16")
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        got = pack(x, "bf16")
+    st.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(ref, got))
+    assert L.moe_last_device_error() == L.MOE_OK

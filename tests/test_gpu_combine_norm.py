@@ -300,3 +300,41 @@ def test_offsets_past_32_bits():
     L.moe_combine_norm_bwd(tail[0], xs, last, tail[1], None, None, ys, w, None, w, 1e-5, 64, H, K, L.MOE_BF16, None, dhs, dgs,
                            None, None, None, None)
     assert torch.equal(dh[-64 * K:], dhs) and torch.equal(dg[-64:], dgs)
+
+
+# rows that pass through the ring twice, and rows of 32 values a thread, over more tokens than
+# the GPU has CTAs for, so that every CTA walks several
+@pytest.mark.parametrize("size", [("bf16", 700, 8200, 2), ("f32", 400, 8196, 1), ("bf16", 350, 8192, 12), ("f32", 340, 5000, 8),
+                                  ("bf16", 1500, 4096, 2)], ids=lambda s: "%s_T%d_H%d_K%d" % s)
+def test_many_tokens_of_wide_rows(size):
+    c = Case(*size, seed=5)
+    y, _ = check_forward(c, 1e-5)
+    check_backward(c, 1e-5, y)
+
+
+@pytest.mark.parametrize("K", [1, 4])
+def test_gradient_through_the_next_norm_alone(K):
+    """No dy: the next block's norm is the only reader of y."""
+    c = Case("bf16", 70, 520, K)
+    y, _ = c.forward(1e-5)
+    check_backward(c, 1e-5, y, skip=("dy",))
+
+
+def test_two_streams_at_once():
+    """Two calls that run at the same time, each with its own workspace, and the default stream behind them."""
+    cases = [Case("bf16", 2000, 1032, 4, seed=s) for s in (1, 2)]
+    alone = []
+    for c in cases:
+        y, xn = c.forward(1e-5)
+        alone.append((y, xn, c.backward(1e-5, y)))
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(3):
+        for i, (c, s) in enumerate(zip(cases, streams)):
+            with torch.cuda.stream(s):
+                y, xn = c.forward(1e-5)
+                got[i] = (y, xn, c.backward(1e-5, y))
+    torch.cuda.synchronize()
+    for a, g in zip(alone, got):
+        assert torch.equal(a[0], g[0]) and torch.equal(a[1], g[1]) and all(torch.equal(a[2][n], g[2][n]) for n in a[2])

@@ -280,3 +280,30 @@ def test_gate_of_few_lanes(E, K, G, KG):
         l[::2] = l[::2, ::-1]
         b = np.random.default_rng(1).standard_normal(E) * 0.01 if biased else None
         check(l, K, G, KG, sigmoid, b, True, False)
+
+
+def test_gate_offsets_past_32_bits():
+    T, E, K = 2200000, 1024, 4  # 2.25e9 logits
+    l = torch.empty((T, E), device=DEV)
+    l[-300:].normal_(generator=torch.Generator(device=DEV).manual_seed(2))
+    l[:-300] = 0
+    tail = l[-300:].contiguous()
+
+    def run(x):
+        n = len(x)
+        idx, gate, dl = torch.empty((n, K), dtype=torch.int32, device=DEV), torch.empty((n, K), device=DEV), torch.empty_like(x)
+        L.moe_gate(x, None, n, E, K, 8, 4, mode_of(True, True), 1.0, idx, gate)
+        L.moe_gate_bwd(gate, x, idx, n, E, K, mode_of(False, False), 1.0, dl)
+        return idx, gate, dl
+    big, small = run(l), run(tail)
+    assert all(torch.equal(a[-300:], b) for a, b in zip(big, small))
+    # a row of equal scores takes the first experts of the first groups, with equal gates
+    assert (big[0][:-300] == torch.arange(K, device=DEV)).all() and (big[1][:-300] == 0.25).all()
+
+
+def test_empty_batch():
+    e = torch.empty((0, 8), device=DEV)
+    i = torch.empty((0, 2), dtype=torch.int32, device=DEV)
+    L.moe_gate(e, None, 0, 8, 2, 1, 1, 0, 1.0, i, e)
+    L.moe_gate_bwd(e, e, i, 0, 8, 2, 0, 1.0, e)
+    assert L.moe_last_device_error() == L.MOE_OK
