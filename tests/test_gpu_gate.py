@@ -307,3 +307,14 @@ def test_empty_batch():
     L.moe_gate(e, None, 0, 8, 2, 1, 1, 0, 1.0, i, e)
     L.moe_gate_bwd(e, e, i, 0, 8, 2, 0, 1.0, e)
     assert L.moe_last_device_error() == L.MOE_OK
+
+
+@pytest.mark.parametrize("E,K,G,KG", [(64, 6, 8, 3), (384, 8, 8, 4), (128, 8, 16, 5), (96, 4, 4, 2), (256, 8, 8, 2)])
+def test_gate_groups_of_saturated_scores(E, K, G, KG):
+    """Scores at and just below 1: many groups of equal fp32 rank, others a little below, which
+    hide where the border of the kept groups is."""
+    rng = np.random.default_rng(E + G)
+    l = rng.uniform(4, 70, (600, E)).astype(np.float32)
+    l[::3] = np.where(rng.random((200, E)) < 0.7, -5, l[::3])
+    for sigmoid, b in ((True, None), (True, np.round(rng.standard_normal(E) * 2) / 64), (False, None)):
+        check(l, K, G, KG, sigmoid, b, True, False)

@@ -429,10 +429,12 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
         const float bound = (group_max ? a1 : a2) - 2.f * Q * fabsf(group_max ? a1 : a2) - LEAST - margin;
         const float slack = fmaxf(off, from_key(__reduce_max_sync(FULL, mine == kth ? order_key(off) : INT_MIN)));
         const bool open = g < p.G && fabsf(rank - border) <= slack;
+        // Surely in: apart from the border, which is the KG-th largest unless equal ranks, taken
+        // together above, put it lower; then as many groups or more are above it
         const bool in = g < p.G && rank - border > slack;
-        // from the values at hand, unless equal ranks put the border too low or a lane may have more of them
-        const bool plain = kth != INT_MIN && border > -INFINITY && usual &&
-                           __popc(__ballot_sync(FULL, in && lig == 0)) < p.KG &&
+        const bool low = __popc(__ballot_sync(FULL, mine > kth && lig == 0)) >= p.KG;
+        // from the values at hand, unless the border is too low or a lane may have more of them
+        const bool plain = kth != INT_MIN && border > -INFINITY && usual && !low &&
                            !__any_sync(FULL, open && f3 >= bound && f3 > -INFINITY && count > 3);
         const Row64 r = row64(row, bias, p.E, sigmoid, m);
         stay = plain ? settle_groups64(r, p, g, lig, e0, make_float3(f1, f2, f3), (1u << BITS) - 1, bound, open,
