@@ -86,6 +86,10 @@ __device__ __forceinline__ float warp_sum4(const float (&v)[4]) {
   return x;
 }
 
+__device__ __forceinline__ void team_sync(int id, int warps) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(warps * 32) : "memory");
+}
+
 // Sums over the CTA, in a fixed order and the same in every thread.  Two buffers in
 // turn: one barrier for each call.
 struct CtaSum {
@@ -101,25 +105,24 @@ struct CtaSum {
     return __shfl_sync(FULL, v, 0);
   }
 };
-struct CtaSum8 {  // of up to eight values
-  float buf[2][MAXW][8];
-  __device__ __forceinline__ void run(float (&v)[8], int turn) {
-    const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-    const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
-    const float x = warp_sum4(lo), y = warp_sum4(hi);
-    if ((lane & 7) == 0) {
-      buf[turn & 1][threadIdx.x >> 5][lane >> 3] = x;
-      buf[turn & 1][threadIdx.x >> 5][4 + (lane >> 3)] = y;
-    }
-    __syncthreads();
-    float s = 0.f;  // value lane % 8 of warps lane / 8, + 4, + 8, + 12
-    for (int w = lane >> 3; w < nw; w += 4) s += buf[turn & 1][w][lane & 7];
-    s += __shfl_xor_sync(FULL, s, 8);
-    s += __shfl_xor_sync(FULL, s, 16);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(FULL, s, i);
+// of up to eight values over the nw warps of a team, which barrier `id` holds together; buf [2][nw][8]
+__device__ __forceinline__ void team_sum8(float (&v)[8], float* buf, int turn, int warp, int nw, int id) {
+  const int lane = threadIdx.x & 31;
+  buf += (turn & 1) * nw * 8;
+  const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
+  const float x = warp_sum4(lo), y = warp_sum4(hi);
+  if ((lane & 7) == 0) {
+    buf[warp * 8 + (lane >> 3)] = x;
+    buf[warp * 8 + 4 + (lane >> 3)] = y;
   }
-};
+  team_sync(id, nw);
+  float s = 0.f;  // value lane % 8 of warps lane / 8, + 4, + 8, + 12
+  for (int w = lane >> 3; w < nw; w += 4) s += buf[w * 8 + (lane & 7)];
+  s += __shfl_xor_sync(FULL, s, 8);
+  s += __shfl_xor_sync(FULL, s, 16);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(FULL, s, i);
+}
 
 // gates and row numbers of the tokens: row -1 for an index outside [0, R)
 struct MetaSource {
@@ -307,16 +310,30 @@ struct BwdArgs {
   void *d_res, *dh;
   float *d_gate, *d_scale;
   float* part;  // [gridDim.x][2][H]: this CTA's sums over its tokens of s D u and of dxn v
-  int S;        // rows of ring
+  int S;        // rows of ring of a team
+  int teams;
 };
 
-__device__ __forceinline__ void wait_all_but(int n) {  // n of 0, 2, 4, 8
+// What a team keeps beside its ring, in 16-byte pieces from its place in shared memory on: the
+// sums' shares [2][nw][8] of its nw warps, the gate gradients' [2][MAXK][nw + 1], the tokens'
+// row addresses [META][R], gates [META][K] and row numbers [META][K].
+__host__ __device__ constexpr int beside_dots(int nw) { return 4 * nw; }
+__host__ __device__ constexpr int beside_src(int nw) { return beside_dots(nw) + 2 * MAXK * (nw + 1) / 4; }
+__host__ __device__ constexpr int beside_gates(int nw, int R) { return beside_src(nw) + META * R / 2; }
+__host__ __device__ constexpr int beside_rows(int nw, int R, int K) { return beside_gates(nw, R) + META * K / 2; }
+__host__ __device__ constexpr int beside_all(int nw, int R, int K) { return beside_rows(nw, R, K) + META * K / 4; }
+
+__device__ __forceinline__ void wait_all_but(int n) {  // n or fewer
   if (n >= 8) copies_wait<8>();
   else if (n >= 4) copies_wait<4>();
   else if (n >= 2) copies_wait<2>();
   else copies_wait<0>();
 }
 
+// TEAMS: a CTA has several teams of threads, each with a ring and a barrier of its own, and each
+// takes a token; they meet at the end, where the CTA's column sums are added.  Otherwise a
+// CTA is one team.
+//
 // HOLD: a token's rows (y, dxn, dy, then h) stay in the ring from the sums to the
 // gradients, and the ring holds S - R rows of the next tokens behind them.  Otherwise
 // (rows too many or too wide for that) a token's rows pass through the ring twice, h and
@@ -326,21 +343,26 @@ __device__ __forceinline__ void wait_all_but(int n) {  // n of 0, 2, 4, 8
 // One reduction serves both norms.  With D = dy + q (w_next dxn - q vm y):
 //   <aw D, z> = <aw dy, z> + q <aw w_next dxn, z> - q^2 vm <aw y, z>,
 // so its three products are summed along with y^2, w_next dxn y and z^2.
-template <typename T, int X, bool HOLD>
+template <typename T, int X, bool HOLD, bool TEAMS>
 __global__ void __launch_bounds__(512) combine_norm_bwd_kernel(const BwdArgs a) {
-  extern __shared__ uint4 ring[];
-  constexpr int MAXR = (HOLD ? 1 : 2) * (MAXK + MAXA);
-  __shared__ unsigned long long src[META * MAXR];
-  __shared__ float2 gates[META][MAXK];  // twice, as a pair
-  __shared__ int rows[META][MAXK];
-  __shared__ CtaSum8 sum;
-  __shared__ float dots[2][MAXK][MAXW + 1];
+  extern __shared__ uint4 smem[];
   constexpr int N = Pairs<T>::N, V = 2 * N, VPT = X / V, P = X / 2;
   constexpr bool HOLD_W = X <= 16;
-  const int tid = threadIdx.x, NT = blockDim.x, nvec = a.H / V, K = a.K, S = a.S;
-  const int lane = tid & 31, warp = tid >> 5, nw = NT >> 5;
+  const int teams = TEAMS ? a.teams : 1;
+  const int NT = blockDim.x / teams, team = TEAMS ? threadIdx.x / NT : 0, tid = threadIdx.x - team * NT;
+  const int nvec = a.H / V, K = a.K, S = a.S;
+  const int lane = tid & 31, warp = tid >> 5, nw = NT >> 5, bar = TEAMS ? 1 + team : 0;
+  uint4* ring = smem + team * S * VPT * NT;
+  // T < 2^31: a token's number, and those of the ones ahead, fit in 32 bits without sign
+  const unsigned first = blockIdx.x * teams + team, stride = gridDim.x * teams;
   const bool next = a.w_next != nullptr;
   const int A = (next ? 2 : 0) + (a.dy ? 1 : 0), R = HOLD ? A + K : 2 * (A + K);
+  const int beside = teams * S * VPT * NT + team * beside_all(nw, R, K);
+  unsigned long long* src = reinterpret_cast<unsigned long long*>(smem + beside + beside_src(nw));
+  float2* gates = reinterpret_cast<float2*>(smem + beside + beside_gates(nw, R));  // twice, as a pair
+  int* rows = reinterpret_cast<int*>(smem + beside + beside_rows(nw, R, K));
+  float* sums = reinterpret_cast<float*>(smem + beside);
+  float* dots = reinterpret_cast<float*>(smem + beside + beside_dots(nw));
   const long long row_bytes = (long long)a.H * sizeof(T);
   int offset[VPT];
   bool live[VPT];  // columns beside the row read as zeros
@@ -350,15 +372,15 @@ __global__ void __launch_bounds__(512) combine_norm_bwd_kernel(const BwdArgs a) 
     live[v] = i < nvec;
     offset[v] = live[v] ? 16 * i : 0;
   }
-  auto note = [&](int j, int k, long long t, int row, float g) {  // row k (of h, then y, dxn, dy) of token t, at place j
+  auto note = [&](int j, int k, unsigned t, int row, float g) {  // row k (of h, then y, dxn, dy) of token t, at place j
     unsigned long long p;
     if (k < K) {
       p = row_address(a.h, row, row_bytes);
-      gates[j][k] = both(g);
-      rows[j][k] = row;
+      gates[j * K + k] = both(g);
+      rows[j * K + k] = row;
     } else {
       const int x = k - K;
-      p = row_address(next && x < 2 ? (x == 0 ? a.y : a.dxn) : a.dy, t < a.T ? t : -1, row_bytes);
+      p = row_address(next && x < 2 ? (x == 0 ? a.y : a.dxn) : a.dy, t < (unsigned)a.T ? (long long)t : -1ll, row_bytes);
     }
     unsigned long long* q = src + j * R;
     if (HOLD) {
@@ -370,7 +392,7 @@ __global__ void __launch_bounds__(512) combine_norm_bwd_kernel(const BwdArgs a) 
   };
   for (int i = tid; i < AHEAD * (K + A); i += NT) {
     const int k = i / AHEAD, j = i - k * AHEAD;
-    const long long t = blockIdx.x + (long long)j * gridDim.x;
+    const unsigned t = first + j * stride;
     int row = -1;
     float g = 0.f;
     a.meta.get(t, k, row, g);
@@ -400,7 +422,7 @@ __global__ void __launch_bounds__(512) combine_norm_bwd_kernel(const BwdArgs a) 
       weights(v, p, n);
     }
   };
-  __syncthreads();
+  team_sync(bar, nw);
 
   const int step = VPT * NT, total = S * step, QN = META * R;
   int qn = 0, at = tid;  // the next row to be copied; the thread's place of the oldest row in the ring
@@ -427,17 +449,16 @@ __global__ void __launch_bounds__(512) combine_norm_bwd_kernel(const BwdArgs a) 
 #pragma unroll
   for (int i = 0; i < P; ++i) Q[i] = M[i] = both(0.f);
   int turn = 0, j = 0;
-  long long before = -1;  // the token whose d_gate is still in `dots`
-  auto write_gates = [&](int b) {
+  auto write_gates = [&](unsigned t, int b) {  // of token t, from the shares in `dots`
     if (a.d_gate && tid < K) {
       float d = 0.f;
-      for (int w = 0; w < nw; ++w) d += dots[b][tid][w];
-      a.d_gate[before * K + tid] = d;
+      for (int w = 0; w < nw; ++w) d += dots[(b * MAXK + tid) * (nw + 1) + w];
+      a.d_gate[(long long)t * K + tid] = d;
     }
   };
 
-  for (long long t = blockIdx.x; t < a.T; t += gridDim.x) {
-    const long long t_ahead = t + (long long)AHEAD * gridDim.x;
+  for (unsigned t = first; t < (unsigned)a.T; t += stride) {
+    const unsigned t_ahead = t + AHEAD * stride;
     int m_row = -1;
     float m_gate = 0.f;
     if (tid < K) a.meta.get(t_ahead, tid, m_row, m_gate);
@@ -449,7 +470,7 @@ __global__ void __launch_bounds__(512) combine_norm_bwd_kernel(const BwdArgs a) 
     if (HOLD) wait_all_but(S - R);
     int place = HOLD ? behind(A) : at;
     for (int k = 0; k < K; ++k) {
-      const float2 g = gates[j][k];
+      const float2 g = gates[j * K + k];
       if (!HOLD) copies_wait<2>();  // three rows are on their way: the oldest is here
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
@@ -499,8 +520,8 @@ __global__ void __launch_bounds__(512) combine_norm_bwd_kernel(const BwdArgs a) 
     float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 6; ++i) s[i] = s2[i].x + s2[i].y;
-    sum.run(s, turn++);
-    if (before >= 0) write_gates((j & 1) ^ 1);
+    team_sum8(s, sums, turn++, warp, nw, bar);
+    if (t != first) write_gates(t - stride, (j & 1) ^ 1);
     const float inv_h = 1.f / a.H;
     const float q = next ? 1.f / sqrtf(s[0] * inv_h + a.eps) : 0.f, vm = s[1] * q * inv_h;
     const float r = a.w_post ? 1.f / sqrtf(s[2] * inv_h + a.eps) : 1.f;
@@ -545,8 +566,8 @@ __global__ void __launch_bounds__(512) combine_norm_bwd_kernel(const BwdArgs a) 
       for (int kk = 0; kk < 4; ++kk) {
         const int k = k0 + kk;
         if (k >= K) break;
-        const float2 g = gates[j][k];
-        const int row = rows[j][k];
+        const float2 g = gates[j * K + k];
+        const int row = rows[j * K + k];
         if (!HOLD) copies_wait<2>();
         float2 c = both(0.f);
         char* out = static_cast<char*>(a.dh) + row * row_bytes;
@@ -566,29 +587,40 @@ __global__ void __launch_bounds__(512) combine_norm_bwd_kernel(const BwdArgs a) 
       }
       if (a.d_gate) {
         const float d = warp_sum4(dot);
-        if ((lane & 7) == 0) dots[j & 1][k0 + (lane >> 3)][warp] = d;
+        if ((lane & 7) == 0) dots[((j & 1) * MAXK + k0 + (lane >> 3)) * (nw + 1) + warp] = d;
       }
     }
-    before = t;
     if (tid < K + A) note(j == 0 ? META - 1 : j - 1, tid, t_ahead, m_row, m_gate);
     j = j + 1 == META ? 0 : j + 1;
   }
   copies_wait<0>();
-  __syncthreads();
-  if (before >= 0) write_gates((j & 1) ^ 1);
-  if (a.part) {
-    float* p = a.part + (size_t)blockIdx.x * 2 * a.H;
+  team_sync(bar, nw);
+  if (first < (unsigned)a.T) write_gates(first + ((unsigned)a.T - 1 - first) / stride * stride, (j & 1) ^ 1);
+  if (!a.part) return;
+  // a team alone writes its sums; several put them into their rings (2 H floats, at most four
+  // rows of bf16) and the CTA adds them in the order of the teams
+  float* part = a.part + (size_t)blockIdx.x * 2 * a.H;
+  float* to = !TEAMS ? part : reinterpret_cast<float*>(ring);
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      if (!live[v]) continue;
-      const int c = offset[v] / 16 * V;
+  for (int v = 0; v < VPT; ++v) {
+    if (!live[v]) continue;
+    const int c = offset[v] / 16 * V;
 #pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        const float2 *e = Q + v * N + i, *f = M + v * N + i;
-        *reinterpret_cast<float4*>(p + c + 2 * i) = make_float4(e[0].x, e[0].y, e[1].x, e[1].y);
-        *reinterpret_cast<float4*>(p + a.H + c + 2 * i) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-      }
+    for (int i = 0; i < N; i += 2) {
+      const float2 *e = Q + v * N + i, *f = M + v * N + i;
+      *reinterpret_cast<float4*>(to + c + 2 * i) = make_float4(e[0].x, e[0].y, e[1].x, e[1].y);
+      *reinterpret_cast<float4*>(to + a.H + c + 2 * i) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
     }
+  }
+  if (!TEAMS) return;
+  __syncthreads();
+  for (int i = threadIdx.x; i < a.H / 2; i += blockDim.x) {
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = 0; w < teams; ++w) {
+      const float4 x = reinterpret_cast<const float4*>(smem + (size_t)w * S * VPT * NT)[i];
+      sum = make_float4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
+    }
+    reinterpret_cast<float4*>(part)[i] = sum;
   }
 }
 
@@ -618,17 +650,16 @@ column_sums_kernel(const float* __restrict__ part, int parts, int H, const float
   }
 }
 
-constexpr int RING_BYTES = 200 * 1024;  // at most; a CTA's 227 KB also hold the sums and row numbers
-constexpr int RING_LIMIT = 215 * 1024;  // the most that a kernel here is launched with
-constexpr int SM_BYTES = 227 * 1024, BWD_STATIC = 12 * 1024;  // an SM's; a backward CTA's beside the ring, rounded up
+constexpr int RING_BYTES = 200 * 1024;  // of a CTA with one team; its 227 KB also hold what is beside the ring
+constexpr int SM_BYTES = 227 * 1024;
 
 int threads_for(int nvec, int vpt) { return ((nvec + vpt - 1) / vpt + 31) / 32 * 32; }
 
 // CTAs of a persistent grid: as many as fit, at most `cap` to an SM, at most one a token.
 // The answer to the last question is kept for each kernel (asking the runtime takes 0.7 us):
 // one word holds device, threads, shared memory and CTAs to an SM.
-template <typename F> int persistent_grid(F kernel, std::atomic<unsigned long long>& known, int threads, int smem, int cap,
-                                          int T, int* grid) {
+template <typename F> int persistent_grid(F kernel, std::atomic<unsigned long long>& known, int threads, int smem,
+                                          int limit, int cap, int T, int* grid) {
   int dev = 0, per_sm = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
   const unsigned long long ask = (unsigned long long)(dev + 1) << 48 | (unsigned long long)threads << 32 |
@@ -637,7 +668,7 @@ template <typename F> int persistent_grid(F kernel, std::atomic<unsigned long lo
   if ((k & ~0xffull) == ask) {
     per_sm = (int)(k & 0xff);
   } else {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RING_LIMIT) != cudaSuccess ||
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, limit) != cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1)
       return MOE_ERR_CUDA;
     known.store(ask | (unsigned)per_sm, std::memory_order_relaxed);
@@ -652,7 +683,7 @@ template <typename T, int X, int S, int MAXT, int CTAS> int fwd_v(const FwdArgs&
   const int threads = threads_for(a.H / Vec16<T>::N, VPT), smem = S * VPT * threads * 16;
   int grid = 0;
   static std::atomic<unsigned long long> known{0};
-  const int st = persistent_grid(combine_norm_kernel<T, X, S, MAXT, CTAS>, known, threads, smem, 32, a.T, &grid);
+  const int st = persistent_grid(combine_norm_kernel<T, X, S, MAXT, CTAS>, known, threads, smem, RING_BYTES, 32, a.T, &grid);
   if (st != MOE_OK) return st;
   combine_norm_kernel<T, X, S, MAXT, CTAS><<<grid, threads, smem, s>>>(a);
   return launch_status();
@@ -679,33 +710,54 @@ int bwd_ctas_per_sm(int H) { return H >= 8192 ? 2 : H >= 1024 ? 16384 / H : 16; 
 
 int bwd_rows(const BwdArgs& a) { return a.K + (a.w_next ? 2 : 0) + (a.dy ? 1 : 0); }
 
-template <typename T, int X, bool HOLD> int bwd_v(BwdArgs& a, int* grid, cudaStream_t s) {
+// 128 registers leave room for 512 threads to an SM
+constexpr int BWD_THREADS = 512, MAX_TEAMS = 8;
+
+template <typename T, int X, bool HOLD, bool TEAMS> int bwd_v(BwdArgs& a, int threads, int smem, int* grid, cudaStream_t s) {
+  static std::atomic<unsigned long long> known{0};
+  const int tokens = (a.T + a.teams - 1) / a.teams;
+  const int st = persistent_grid(combine_norm_bwd_kernel<T, X, HOLD, TEAMS>, known, threads, smem, SM_BYTES,
+                                 bwd_ctas_per_sm(a.H), tokens, grid);
+  if (st != MOE_OK) return st;
+  combine_norm_bwd_kernel<T, X, HOLD, TEAMS><<<*grid, threads, smem, s>>>(a);
+  return launch_status();
+}
+
+template <typename T, int X, bool HOLD> int bwd_x(BwdArgs& a, int* grid, cudaStream_t s) {
   constexpr int VPT = X / Vec16<T>::N;
   const int threads = threads_for(a.H / Vec16<T>::N, VPT), row = VPT * threads * 16, R = bwd_rows(a);
-  // 128 registers leave room for 512 threads to an SM: as many CTAs as that, and behind a
-  // token's own rows 8, 4 or 2 of the next tokens, what the SM's shared memory has room for
+  const int beside = 16 * beside_all(threads / 32, HOLD ? R : 2 * R, a.K);
+  a.teams = 1;
   a.S = HOLD ? R + 2 : 3;
-  for (int ctas = 512 / threads; HOLD && ctas > 0; --ctas) {
-    const int room = (SM_BYTES / ctas - BWD_STATIC) / row;
-    if (room < R + 2) continue;
-    a.S = R + (room >= R + 8 ? 8 : room >= R + 4 ? 4 : 2);
-    break;
+  if constexpr (HOLD) {
+    // As many teams as there are tokens to an SM, where the GPU holds them all at once: a CTA's
+    // one set of column sums instead of one for each token (1001 tokens of 1000 fp32 columns:
+    // 24.5 us without, 21 with).  A ring then holds a token's rows, and the team's 2 H sums.
+    const int per_sm = (a.T + sm_count() - 1) / sm_count(), sums = (8 * a.H + row - 1) / row, S = R > sums ? R : sums;
+    if (per_sm > 1 && per_sm <= MAX_TEAMS && per_sm * threads <= BWD_THREADS && per_sm * (S * row + beside) <= SM_BYTES) {
+      a.teams = per_sm;
+      a.S = S;
+      return bwd_v<T, X, HOLD, true>(a, a.teams * threads, a.teams * (S * row + beside), grid, s);
+    }
+    // otherwise as many CTAs as the registers have room for, and behind a token's own rows 8, 4
+    // or 2 of the next ones, what shared memory has room for
+    for (int ctas = BWD_THREADS / threads; ctas > 0; --ctas) {
+      const int room = (SM_BYTES / ctas - beside - 1024) / row;
+      if (room < R + 2) continue;
+      a.S = R + (room >= R + 8 ? 8 : room >= R + 4 ? 4 : 2);
+      break;
+    }
   }
-  const int smem = a.S * row;
-  static std::atomic<unsigned long long> known{0};
-  const int st = persistent_grid(combine_norm_bwd_kernel<T, X, HOLD>, known, threads, smem, bwd_ctas_per_sm(a.H), a.T, grid);
-  if (st != MOE_OK) return st;
-  combine_norm_bwd_kernel<T, X, HOLD><<<*grid, threads, smem, s>>>(a);
-  return launch_status();
+  return bwd_v<T, X, HOLD, false>(a, threads, a.S * row + beside, grid, s);
 }
 
 // 16 values a thread up to H = 8192, 32 beyond; a token's rows are held where two more fit
 // beside them
 template <typename T> int bwd_t(BwdArgs& a, int* grid, cudaStream_t s) {
   constexpr int VPT = 16 / Vec16<T>::N;
-  if (a.H > 8192) return bwd_v<T, 32, false>(a, grid, s);
+  if (a.H > 8192) return bwd_x<T, 32, false>(a, grid, s);
   const long long row = VPT * threads_for(a.H / Vec16<T>::N, VPT) * 16;
-  return (bwd_rows(a) + 2) * row <= RING_BYTES ? bwd_v<T, 16, true>(a, grid, s) : bwd_v<T, 16, false>(a, grid, s);
+  return (bwd_rows(a) + 2) * row <= RING_BYTES ? bwd_x<T, 16, true>(a, grid, s) : bwd_x<T, 16, false>(a, grid, s);
 }
 
 long long bwd_max_ctas(int T, int H) {
@@ -738,7 +790,7 @@ int launch_combine_norm_bwd(const void* dy, const void* dxn, const void* h, cons
     return MOE_OK;
   }
   BwdArgs a{dy, dxn, h, y, MetaSource{gate, dst_row, T, (long long)T * K, K, device_error_word()}, row_scale, w_post,
-            res_scale, w_next, eps, T, H, K, d_res, dh, d_gate, d_scale, sums ? static_cast<float*>(ws) : nullptr, 0};
+            res_scale, w_next, eps, T, H, K, d_res, dh, d_gate, d_scale, sums ? static_cast<float*>(ws) : nullptr, 0, 1};
   int grid = 0;
   const int st = dtype == MOE_BF16 ? bwd_t<bf16>(a, &grid, s) : bwd_t<float>(a, &grid, s);
   if (st != MOE_OK || !sums) return st;
