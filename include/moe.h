@@ -168,11 +168,11 @@ MOE_API int moe_route_ex(const void* x, const void* w_router, const float* logit
  *   topk_gate[t,k] = scale * s[t,topk_idx[t,k]], with MOE_GATE_RENORM
  *                    scale * s[t,topk_idx[t,k]] / sum_k' s[t,topk_idx[t,k']]
  *
- *   The choice is that of scores in 64 bits: scores are compared in fp32 where they are
- *   further apart than fp32's error and in fp64 where they are not.  Without sel_bias and
- *   without a group limit (topk_groups = groups) the logits themselves are compared.
- *   A logit of -inf takes an expert out of service: it ranks behind every other expert of
- *   its group (lower expert first), adds nothing to its group's rank (a group with one
+ *   The choice is that of scores in 64 bits: they are compared in fp32 where they are
+ *   further apart than fp32's error and in fp64 where they are not.  Without sel_bias the
+ *   logits order as the scores do, and they are compared (but for the groups' sums).
+ *   A logit of -inf takes an expert out of service: it ranks behind every expert in
+ *   service (lower expert first), adds nothing to its group's rank (a group with one
  *   expert in service ranks by that one alone, one with none last), and its gate is 0;
  *   chosen gates that sum to 0 stay 0 under MOE_GATE_RENORM.  A NaN logit, or a c that is
  *   NaN, ranks like -inf; a row that holds a NaN logit has NaN gates.
@@ -205,8 +205,8 @@ MOE_API int moe_route_group(const void* x, const void* w_router, const float* se
  *   MOE_GATE_SOFTMAX|MOE_GATE_RENORM  d_logits = scale * q (d_gate - <d_gate, q>)
  *   and 0 elsewhere; an expert listed twice in a row receives the sum of its shares.
  *   d_gate [T,K], logits [T,E] float; topk_idx [T,K] int32 as moe_gate wrote it (an index
- *   outside [0,E) sets MOE_ERR_DEVICE_BOUNDS and has no share); d_logits [T,E] float out, apart from logits,
- *   every element written.  MOE_GATE_GROUP_MAX is accepted and changes nothing.  Sizes as
+ *   outside [0,E) sets MOE_ERR_DEVICE_BOUNDS and has no share); d_logits [T,E] float out,
+ *   apart from logits, every element written.  MOE_GATE_GROUP_MAX is accepted and changes nothing.  Sizes as
  *   moe_gate.  dw_router and dx follow with moe_route_bwd(MOE_ROUTE_LOGIT_GRAD).
  */
 MOE_API int moe_gate_bwd(const float* d_gate, const float* logits, const int32_t* topk_idx, int T, int E, int K,

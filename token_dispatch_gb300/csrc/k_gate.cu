@@ -103,6 +103,7 @@ __device__ __noinline__ Row64 row64(const float* row, const float* bias, int E, 
   Row64 r{row, bias, (double)m, 1.0, sigmoid};
   if (!sigmoid) {
     double z = 0;
+#pragma unroll 4
     for (int e = threadIdx.x & 31; e < E; e += 32) z += m == -INFINITY ? 0.0 : exp((double)row[e] - r.m);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(FULL, z, o);
@@ -273,11 +274,10 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
     }
   };
 
-  float b[VMAX], margin = 0.f;
+  float b[VMAX], mb = 0.f;
   bool odd = false;  // a bias that is no number
   if (bias) {
     load(bias, 0.f, b);
-    float mb = 0.f;
 #pragma unroll
     for (int j = 0; j < VMAX; ++j) {
       const bool number = fabsf(b[j]) < INFINITY;
@@ -287,11 +287,6 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
     }
     mb = warp_max(mb);
     odd = __any_sync(FULL, odd);
-    // How far two scores must be apart to be surely in order: the errors of both.  A logistic
-    // score s is off by 4u of its exponential and |l| u of that one's argument, both times
-    // s (1 - s), and by 3u of the sum and reciprocal: under 6u; a softmax score by the
-    // same of its exponential and by its sum over vpl values and 5 shuffles; then s + b rounds.
-    margin = 2.f * U * ((sigmoid ? 8.f : 22.f + p.vpl) + mb);
   }
 
   for (long long t = (long long)blockIdx.x * WARPS + warp; t < p.T; t += (long long)gridDim.x * WARPS) {
@@ -317,6 +312,10 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
     float m = -INFINITY, rz = 1.f;
     // the score of a logit, fast
     auto score = [&](float l) { return sigmoid ? fast_rcp(1.f + fast_exp2(l * -LOG2E)) : fast_exp2((l - m) * LOG2E) * rz; };
+    // How far two scores must be apart to be surely in order: the errors of both.  A logistic
+    // score s is off by 4u of its exponential and |l| u of that one's argument, both times
+    // s (1 - s), and by 3u of the sum and reciprocal: under 6u; then s + b rounds.
+    float margin = bias ? 2.f * U * (8.f + mb) : 0.f;
     const bool by_sum = p.KG < p.G && !group_max;
     if (bias && sigmoid) {
       float zero = 0.f;  // NaN where a score is
@@ -350,6 +349,9 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
         }
       }
       if (bias) {
+        // a softmax score, at most 1/z, by the same of its exponential and quotient and by its sum
+        // over vpl values and 5 shuffles
+        if (!sigmoid) margin = 2.f * U * ((22.f + p.vpl) * rz + 1.f + mb);
 #pragma unroll
         for (int j = 0; j < VMAX; ++j) c[j] = c[j] > -INFINITY && usual ? score(c[j]) + b[j] : -INFINITY;
       } else {
@@ -732,10 +734,10 @@ gate_bwd_kernel(const float* __restrict__ d_gate, const float* __restrict__ logi
 
 // one CTA for WARPS tokens, at most as many as the GPU holds at once: each then walks its
 // even share (more would run as a second, partly filled round)
-template <typename F> int resident_grid(F kernel, long long T) {
-  static const int per_sm = [&] {
+template <auto KERNEL> int resident_grid(long long T) {
+  static const int per_sm = [] {
     int n = 0;
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, 32 * WARPS, 0) == cudaSuccess && n > 0 ? n : 1;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, KERNEL, 32 * WARPS, 0) == cudaSuccess && n > 0 ? n : 1;
   }();
   const long long ctas = (T + WARPS - 1) / WARPS, cap = (long long)sm_count() * per_sm;
   return (int)(ctas < cap ? ctas : cap);
@@ -744,13 +746,13 @@ template <typename F> int resident_grid(F kernel, long long T) {
 template <int VMAX>
 void gate_v(float* logits, const float* part, int S, const float* bias, const GateShape& p, int32_t* idx, float* gate,
             cudaStream_t s) {
-  gate_kernel<VMAX><<<resident_grid(gate_kernel<VMAX>, p.T), 32 * WARPS, 0, s>>>(logits, part, S, bias, p, idx, gate);
+  gate_kernel<VMAX><<<resident_grid<gate_kernel<VMAX>>(p.T), 32 * WARPS, 0, s>>>(logits, part, S, bias, p, idx, gate);
 }
 
 template <int VQ>
 void gate_bwd_v(const float* d_gate, const float* logits, const int32_t* idx, int T, int E, int K, int mode,
                 float scale, float* d_logits, cudaStream_t s) {
-  gate_bwd_kernel<VQ><<<resident_grid(gate_bwd_kernel<VQ>, T), 32 * WARPS, 0, s>>>(
+  gate_bwd_kernel<VQ><<<resident_grid<gate_bwd_kernel<VQ>>(T), 32 * WARPS, 0, s>>>(
       d_gate, logits, idx, T, E, K, mode, scale, d_logits, device_error_word());
 }
 
