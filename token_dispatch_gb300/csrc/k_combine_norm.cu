@@ -346,6 +346,7 @@ __device__ __forceinline__ void wait_all_but(int n) {  // n or fewer
 template <typename T, int X, bool HOLD, bool TEAMS>
 __global__ void __launch_bounds__(512) combine_norm_bwd_kernel(const BwdArgs a) {
   extern __shared__ uint4 smem[];
+  asm volatile("griddepcontrol.launch_dependents;");  // the column sums may get ready
   constexpr int N = Pairs<T>::N, V = 2 * N, VPT = X / V, P = X / 2;
   constexpr bool HOLD_W = X <= 16;
   const int teams = TEAMS ? a.teams : 1;
@@ -627,15 +628,16 @@ __global__ void __launch_bounds__(512) combine_norm_bwd_kernel(const BwdArgs a) 
 // The column sums: a CTA takes 32 columns of [2][H], its 32 warps the parts w, w + 32, ...
 // in order; the warps' sums are added in warp order and multiplied by their column factors.
 __global__ void __launch_bounds__(1024)
-column_sums_kernel(const float* __restrict__ part, int parts, int H, const float* __restrict__ w_post,
+column_sums_kernel(const float* part, int parts, int H, const float* __restrict__ w_post,
                    const float* __restrict__ res_scale, float* dw_post, float* d_res_scale, float* dw_next) {
   __shared__ float red[32][33];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int i = blockIdx.x * 32 + lane;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the launch before it has ended and its writes are visible
   float acc = 0.f;
   if (i < 2 * H) {
 #pragma unroll 8
-    for (int p = w; p < parts; p += 32) acc += __ldg(part + (size_t)p * 2 * H + i);
+    for (int p = w; p < parts; p += 32) acc += part[(size_t)p * 2 * H + i];
   }
   red[w][lane] = acc;
   __syncthreads();
@@ -794,7 +796,22 @@ int launch_combine_norm_bwd(const void* dy, const void* dxn, const void* h, cons
   int grid = 0;
   const int st = dtype == MOE_BF16 ? bwd_t<bf16>(a, &grid, s) : bwd_t<float>(a, &grid, s);
   if (st != MOE_OK || !sums) return st;
-  column_sums_kernel<<<(2 * H + 31) / 32, 1024, 0, s>>>(a.part, grid, H, w_post, res_scale, dw_post, d_res_scale, dw_next);
+  // launched while the first kernel runs, so that its own start costs nothing
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t config{};
+  config.gridDim = dim3((2 * H + 31) / 32);
+  config.blockDim = dim3(1024);
+  config.stream = s;
+  config.attrs = &early;
+  config.numAttrs = 1;
+  const float* part = a.part;
+  if (cudaLaunchKernelEx(&config, column_sums_kernel, part, grid, H, w_post, res_scale, dw_post, d_res_scale, dw_next) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
   return launch_status();
 }
 
