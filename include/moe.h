@@ -173,9 +173,10 @@ MOE_API int moe_route_ex(const void* x, const void* w_router, const float* logit
  *   logits order as the scores do, and they are compared (but for the groups' sums).
  *   A logit of -inf takes an expert out of service: it ranks behind every expert in
  *   service (lower expert first), adds nothing to its group's rank (a group with one
- *   expert in service ranks by that one alone, one with none last), and its gate is 0;
- *   chosen gates that sum to 0 stay 0 under MOE_GATE_RENORM.  A NaN logit, or a c that is
- *   NaN, ranks like -inf; a row that holds a NaN logit has NaN gates.
+ *   expert in service ranks by that one alone, one with none last), and its gate is 0,
+ *   under MOE_GATE_RENORM too.  Scores too small for a float still have their quotients
+ *   there: chosen logits that are all the type's lowest number have gates of scale / K.  A
+ *   NaN logit, or a c that is NaN, ranks like -inf; a row that holds a NaN logit has NaN gates.
  *
  *   logits [T,E] float; sel_bias [E] float, nullable; topk_idx [T,K] int32 out;
  *   topk_gate [T,K] float out.  1 <= K <= E <= 1024, K <= 16, E a multiple of groups,

@@ -22,6 +22,19 @@ def _scores(logits, sigmoid):
         return np.divide(e, z, out=np.zeros_like(e), where=z != 0)
 
 
+def _shares(logits, sigmoid):
+    """The chosen scores over their sum, which a common factor leaves alone: by their logarithms, so that
+    scores below the smallest number have their shares too; 0 where all are out of service."""
+    l = np.asarray(logits, np.float64)
+    log_s = np.minimum(l, 0) - np.log1p(np.exp(-np.abs(l))) if sigmoid else l
+    top = log_s.max()
+    if np.isneginf(top):
+        return np.zeros_like(l)
+    with np.errstate(over="ignore", invalid="ignore"):
+        w = np.exp(log_s - top)
+    return w / w.sum()
+
+
 def gate_group(logits, K, groups, topk_groups, sigmoid=False, bias=None, renorm=False, group_max=False, scale=1.0):
     """idx [T,K] and gate [T,K] of the group-limited gate, one row at a time.
 
@@ -49,8 +62,7 @@ def gate_group(logits, K, groups, topk_groups, sigmoid=False, bias=None, renorm=
         idx[t] = sorted(allowed, key=lambda e: (-c[e], e))[:K]
     gate = np.take_along_axis(s, idx.astype(np.int64), axis=1)
     if renorm:
-        total = gate.sum(axis=1, keepdims=True)
-        gate = np.divide(gate, total, out=np.zeros_like(gate), where=total != 0)
+        gate = np.stack([_shares(l[t, idx[t]], sigmoid) for t in range(T)]) if T else gate
     gate = scale * gate
     gate[np.isnan(l).any(axis=1)] = np.nan
     return idx, gate
@@ -64,16 +76,15 @@ def gate_group_bwd(d_gate, logits, idx, sigmoid=False, renorm=False, scale=1.0):
     s = _scores(l, sigmoid)
     d = np.zeros((T, E))
     for t in range(T):
+        if renorm:
+            q = _shares(l[t, idx[t]], sigmoid)
+            inner = sum(d_gate[t, k] * q[k] for k in range(K))
+            for k, e in enumerate(idx[t]):
+                d[t, e] += scale * q[k] * (d_gate[t, k] - inner) * (1 - s[t, e] if sigmoid else 1)
+            continue
         ds = np.zeros(E)
-        chosen = [s[t, e] for e in idx[t]]
-        total = sum(chosen)
-        for k in range(K):
-            e = idx[t, k]
-            if not renorm:
-                ds[e] += scale * d_gate[t, k]
-            elif total > 0:
-                inner = sum(d_gate[t, j] * chosen[j] for j in range(K)) / total
-                ds[e] += scale * (d_gate[t, k] - inner) / total
+        for k, e in enumerate(idx[t]):
+            ds[e] += scale * d_gate[t, k]
         d[t] = ds * s[t] * (1 - s[t]) if sigmoid else s[t] * (ds - ds @ s[t])
     return d
 

@@ -318,3 +318,34 @@ def test_gate_groups_of_saturated_scores(E, K, G, KG):
     l[::3] = np.where(rng.random((200, E)) < 0.7, -5, l[::3])
     for sigmoid, b in ((True, None), (True, np.round(rng.standard_normal(E) * 2) / 64), (False, None)):
         check(l, K, G, KG, sigmoid, b, True, False)
+
+
+@pytest.mark.parametrize("E,K,G,KG", [(64, 6, 8, 4), (384, 8, 8, 4), (384, 8, 8, 3), (160, 6, 8, 6), (96, 4, 6, 2)])
+def test_gate_equal_groups_around_the_border(E, K, G, KG):
+    """Groups come in pairs of equal rank (a group holds its neighbour's logits in another order), so that equal
+    ranks lie above the border of the kept groups, on it and below it."""
+    rng = np.random.default_rng(E + KG)
+    l = rng.standard_normal((300, G, E // G)).astype(np.float32) * 2
+    l[:, 1::2] = rng.permuted(l[:, ::2], axis=2)
+    l = l.reshape(300, E)
+    for sigmoid, b in ((True, None), (True, np.zeros(E)), (False, None), (False, np.zeros(E))):
+        check(l, K, G, KG, sigmoid, b, True, False)
+
+
+@pytest.mark.parametrize("low", [-3.4028235e38, -1e38, -3e4])
+@pytest.mark.parametrize("E,K,G,KG", [(64, 6, 8, 3), (384, 8, 8, 4), (256, 8, 8, 2), (24, 3, 4, 3)])
+def test_gate_groups_at_the_lowest_number(E, K, G, KG, low):
+    """Masks of the type's lowest value: all but a few groups at it (fewer, as many and more than stay), half of
+    a group at it, whole rows of it; and the same with numbers as large the other way."""
+    rng = np.random.default_rng(E + KG)
+    l = rng.standard_normal((240, G, E // G)).astype(np.float32)
+    for t in range(240):
+        l[t, rng.permutation(G)[:t % (G + 1)]] = low
+    l[60:120, :, ::2] = low
+    l[120:150] *= 1e37
+    l[150:160] = -low
+    l = l.reshape(240, E)
+    for sigmoid in (True, False):
+        for group_max in (True, False):
+            for b in (None, rng.standard_normal(E) * 0.1):
+                check(l, K, G, KG, sigmoid, b, not sigmoid, group_max)

@@ -215,7 +215,7 @@ __device__ __noinline__ int choose64(const Row64& r, const GateShape& p, unsigne
         e = f;
       }
     }
-    if (lane == k) mine = e;
+    if (lane == k) mine = e < p.E ? e : 0;  // KG gs >= K: there always is a next one
     last = v;
     last_e = e;
   }
@@ -403,9 +403,11 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
         }
       } else if (!group_max && a1 > -INFINITY) {
         // relative: 12u of each score and the sum, twice |a - base| u of its exponential's argument,
-        // |a| Q of the logit's lowest bits
+        // |a| Q of the logit's lowest bits; each bounded, so that it is a number times a score of 0
         auto one = [&](float x) { return sigmoid ? score(x) : fast_exp2((x - m) * LOG2E); };
-        auto off_of = [&](float x) { return 2.f * U * (12.f + 2.f * fabsf(sigmoid ? x : x - m)) + 2.f * Q * fabsf(x); };
+        auto off_of = [&](float x) {
+          return 2.f * U * (12.f + 2.f * fminf(fabsf(sigmoid ? x : x - m), 1e30f)) + 2.f * Q * fminf(fabsf(x), 1e30f);
+        };
         rank = one(a1);
         off = rank * off_of(a1) + 4e-38f;
         if (a2 > -INFINITY) {
@@ -426,11 +428,12 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
       const int kept = __popc(__ballot_sync(FULL, stay && lig == 0));
       // the lanes at the border know how near the next rank is
       const float border = from_key(kth);
-      const bool near = mine == kth && after != INT_MIN && rank != -INFINITY && rank - from_key(after) <= off;
+      const bool near = mine == kth && after != INT_MIN && rank != -INFINITY && !(rank - from_key(after) > off);
       if (kept != p.KG || __any_sync(FULL, near)) {
         const float bound = (group_max ? a1 : a2) - 2.f * Q * fabsf(group_max ? a1 : a2) - LEAST - margin;
         const float slack = fmaxf(off, from_key(__reduce_max_sync(FULL, mine == kth ? order_key(off) : INT_MIN)));
-        const bool open = g < p.G && fabsf(rank - border) <= slack;
+        // ranks that overflowed have no distance: they are open
+        const bool open = g < p.G && !(fabsf(rank - border) > slack);
         // Surely in: apart from the border, which is the KG-th largest unless equal ranks, taken
         // together above, put it lower; then as many groups or more are above it
         const bool in = g < p.G && rank - border > slack;
