@@ -423,6 +423,16 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
         kth = __reduce_max_sync(FULL, key);
         if (key == kth) key = INT_MIN;
       }
+      if (__popc(__ballot_sync(FULL, mine > kth && lig == 0)) >= p.KG) {
+        // equal ranks above put that too low: again, counting them
+        key = mine;
+        for (int n = 0;;) {
+          kth = __reduce_max_sync(FULL, key);
+          n += __popc(__ballot_sync(FULL, key == kth && lig == 0));
+          if (key == kth) key = INT_MIN;
+          if (n >= p.KG || kth == INT_MIN) break;
+        }
+      }
       const int after = __reduce_max_sync(FULL, key);
       stay = mine >= kth && g < p.G;
       const int kept = __popc(__ballot_sync(FULL, stay && lig == 0));
@@ -434,12 +444,9 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
         const float slack = fmaxf(off, from_key(__reduce_max_sync(FULL, mine == kth ? order_key(off) : INT_MIN)));
         // ranks that overflowed have no distance: they are open
         const bool open = g < p.G && !(fabsf(rank - border) > slack);
-        // Surely in: apart from the border, which is the KG-th largest unless equal ranks, taken
-        // together above, put it lower; then as many groups or more are above it
         const bool in = g < p.G && rank - border > slack;
-        const bool low = __popc(__ballot_sync(FULL, mine > kth && lig == 0)) >= p.KG;
-        // from the values at hand, unless the border is too low or a lane may have more of them
-        const bool plain = kth != INT_MIN && border > -INFINITY && usual && !low &&
+        // from the values at hand, unless a lane may have more of them
+        const bool plain = border > -INFINITY && usual &&
                            !__any_sync(FULL, open && f3 >= bound && f3 > -INFINITY && count > 3);
         const Row64 r = row64(row, bias, p.E, sigmoid, m);
         stay = plain ? settle_groups64(r, p, g, lig, e0, make_float3(f1, f2, f3), (1u << BITS) - 1, bound, open,
@@ -507,108 +514,108 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
 #pragma unroll
         for (int j = 0; j < VMAX; ++j) c[j] = -INFINITY;
       }
-    // the scores at or above it, one to a lane
-    auto collect = [&]() {
-      const float lim = fmaxf(limit - margin, -3.4028235e38f);
-      unsigned in[(VMAX + 31) / 32];
-      int mine = 0;
+      // the scores at or above it, one to a lane
+      auto collect = [&]() {
+        const float lim = fmaxf(limit - margin, -3.4028235e38f);
+        unsigned in[(VMAX + 31) / 32];
+        int mine = 0;
 #pragma unroll
-      for (int w = 0; w < (VMAX + 31) / 32; ++w) {
-        in[w] = 0;
+        for (int w = 0; w < (VMAX + 31) / 32; ++w) {
+          in[w] = 0;
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (32 * w + j < VMAX && c[32 * w + j] >= lim) in[w] |= 1u << j;
-        mine += __popc(in[w]);
-      }
-      int at = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(FULL, at, o);
-        if (lane >= o) at += up;
-      }
-      const int n = __shfl_sync(FULL, at, 31);
-      at -= mine;
-#pragma unroll
-      for (int w = 0; w < (VMAX + 31) / 32; ++w)
-        for (; in[w] && at < 32; ++at) {
-          cand_e[warp][at] = e0 + 32 * w + __ffs(in[w]) - 1;
-          in[w] &= in[w] - 1;
+          for (int j = 0; j < 32; ++j)
+            if (32 * w + j < VMAX && c[32 * w + j] >= lim) in[w] |= 1u << j;
+          mine += __popc(in[w]);
         }
-      return n;
-    };
-    int n = collect();
-    if (n > 32) {
-      // a bound too low: the K-th largest itself, K rounds over the registers
-      float lower = INFINITY;
-      int taken = 0;
-      while (taken < p.K) {
-        float best = -INFINITY;
+        int at = mine;
 #pragma unroll
-        for (int j = 0; j < VMAX; ++j)
-          if (c[j] < lower) best = fmaxf(best, c[j]);
-        best = from_key(__reduce_max_sync(FULL, order_key(best)));
-        int same = 0;
-#pragma unroll
-        for (int j = 0; j < VMAX; ++j) same += c[j] == best;
-        if (lower == INFINITY) {  // values of +inf come first and are never below `lower`
-          int inf = 0;
-#pragma unroll
-          for (int j = 0; j < VMAX; ++j) inf += c[j] == INFINITY;
-          taken += __reduce_add_sync(FULL, inf);
-          if (taken >= p.K) best = INFINITY;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int up = __shfl_up_sync(FULL, at, o);
+          if (lane >= o) at += up;
         }
-        if (best != INFINITY) taken += __reduce_add_sync(FULL, same);
-        lower = best;
-        if (best == INFINITY) break;
+        const int n = __shfl_sync(FULL, at, 31);
+        at -= mine;
+#pragma unroll
+        for (int w = 0; w < (VMAX + 31) / 32; ++w)
+          for (; in[w] && at < 32; ++at) {
+            cand_e[warp][at] = e0 + 32 * w + __ffs(in[w]) - 1;
+            in[w] &= in[w] - 1;
+          }
+        return n;
+      };
+      int n = collect();
+      if (n > 32) {
+        // a bound too low: the K-th largest itself, K rounds over the registers
+        float lower = INFINITY;
+        int taken = 0;
+        while (taken < p.K) {
+          float best = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < VMAX; ++j)
+            if (c[j] < lower) best = fmaxf(best, c[j]);
+          best = from_key(__reduce_max_sync(FULL, order_key(best)));
+          int same = 0;
+#pragma unroll
+          for (int j = 0; j < VMAX; ++j) same += c[j] == best;
+          if (lower == INFINITY) {  // values of +inf come first and are never below `lower`
+            int inf = 0;
+#pragma unroll
+            for (int j = 0; j < VMAX; ++j) inf += c[j] == INFINITY;
+            taken += __reduce_add_sync(FULL, inf);
+            if (taken >= p.K) best = INFINITY;
+          }
+          if (best != INFINITY) taken += __reduce_add_sync(FULL, same);
+          lower = best;
+          if (best == INFINITY) break;
+        }
+        limit = lower;
+        __syncwarp();
+        n = collect();
       }
-      limit = lower;
       __syncwarp();
-      n = collect();
-    }
-    __syncwarp();
-    if (n >= p.K && n <= 32) {
-      const bool in = lane < n;
-      float v = -INFINITY;
-      if (in) {
-        e = cand_e[warp][lane];
-        mine = row[e];
-        v = bias ? score(mine) + __ldg(bias + e) : mine;
-      }
-      cand_c[warp][lane] = v;
-      __syncwarp();
-      int ahead = 0, close = 0;  // how many are larger; how many are not surely smaller
-      const float lim = v - margin;
-      for (int i = 0; i < n; i += 4) {
-        const float4 w = *reinterpret_cast<const float4*>(&cand_c[warp][i]);
-        ahead += (w.x > v) + (w.y > v) + (w.z > v) + (w.w > v);
-        close += (w.x >= lim) + (w.y >= lim) + (w.z >= lim) + (w.w >= lim);
-      }
-      place = in ? ahead : 32;
-      // `close` counts the lane itself and those ahead
-      if (__any_sync(FULL, in && ahead < p.K && close > ahead + 1)) {
-        double x = mine;
-        if (bias) {
-          const Row64 r = row64(row, bias, p.E, sigmoid, m);
-          x = in ? r.value(e) : 0.0;
+      if (n >= p.K && n <= 32) {
+        const bool in = lane < n;
+        float v = -INFINITY;
+        if (in) {
+          e = cand_e[warp][lane];
+          mine = row[e];
+          v = bias ? score(mine) + __ldg(bias + e) : mine;
         }
-        place = 0;
-        for (int i = 0; i < n; ++i) {
-          const double w = __shfl_sync(FULL, x, i);
-          const int f = __shfl_sync(FULL, e, i);
-          place += w > x || (w == x && f < e);
+        cand_c[warp][lane] = v;
+        __syncwarp();
+        int ahead = 0, close = 0;  // how many are larger; how many are not surely smaller
+        const float lim = v - margin;
+        for (int i = 0; i < n; i += 4) {
+          const float4 w = *reinterpret_cast<const float4*>(&cand_c[warp][i]);
+          ahead += (w.x > v) + (w.y > v) + (w.z > v) + (w.w > v);
+          close += (w.x >= lim) + (w.y >= lim) + (w.z >= lim) + (w.w >= lim);
         }
-        if (!in) place = 32;
+        place = in ? ahead : 32;
+        // `close` counts the lane itself and those ahead
+        if (__any_sync(FULL, in && ahead < p.K && close > ahead + 1)) {
+          double x = mine;
+          if (bias) {
+            const Row64 r = row64(row, bias, p.E, sigmoid, m);
+            x = in ? r.value(e) : 0.0;
+          }
+          place = 0;
+          for (int i = 0; i < n; ++i) {
+            const double w = __shfl_sync(FULL, x, i);
+            const int f = __shfl_sync(FULL, e, i);
+            place += w > x || (w == x && f < e);
+          }
+          if (!in) place = 32;
+        }
+      } else {
+        const unsigned who = __ballot_sync(FULL, stay && lig == 0);
+        unsigned keep = 0;
+        for (int o = 0; o < p.G; ++o) keep |= ((who >> (o * p.lpg)) & 1u) << o;
+        e = choose64(row64(row, bias, p.E, sigmoid, m), p, keep);
+        if (lane < p.K) {
+          place = lane;
+          mine = row[e];
+        }
       }
-    } else {
-      const unsigned who = __ballot_sync(FULL, stay && lig == 0);
-      unsigned keep = 0;
-      for (int o = 0; o < p.G; ++o) keep |= ((who >> (o * p.lpg)) & 1u) << o;
-      e = choose64(row64(row, bias, p.E, sigmoid, m), p, keep);
-      if (lane < p.K) {
-        place = lane;
-        mine = row[e];
-      }
-    }
     }
     const bool on = place < p.K;
     const float s = gate_value(mine, on, sigmoid, renorm, m, rz);
