@@ -20,49 +20,56 @@ __device__ __forceinline__ int run_exponent(float a) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float((unsigned)(e + 127) << 23); }
 
-// A thread takes 16 neighbours, so a run is a pair of lanes: the largest magnitude
-// meets in one shuffle, and whole rows of runs (FLAT: N % 32 == 0) move as 16-byte
-// pieces without an index division for each.  Other widths move the same 16 values
-// in pieces of one 16-byte load, the last run of a row in fewer of them.
-constexpr int PER = 16, NT = 256;
+// A thread takes VECS 16-byte vectors of neighbours, so a run is 32 / (VECS V) lanes, and whole
+// rows of runs (FLAT: N % 32 == 0) move without an index division for each.  Other widths move
+// the same values in pieces of one vector, the last run of a row in fewer of them.
+//
+// 16 values a thread, but one vector where fp32 is written: four to a thread left each sector
+// to two stores (16384 x 4096 fp32, unpack 71 -> 55 us, [g | u] and act 102 -> 74).  Reading is the
+// other way round, it wants the bytes in flight (pack 51 us with four, 60 with one).
+constexpr int NT = 256;
+template <typename T> constexpr int IN = 16 / Vec16<T>::N;           // vectors of a thread that reads them
+template <typename T> constexpr int OUT = sizeof(T) == 2 ? 2 : 1;  // and of one that writes them
 
-// where thread i's 16 values are: value 0 at `at`, `live` of them in the row, run `run`
+// where thread i's values are: value 0 at `at`, `live` of them in the row, run `run`
 struct Place {
   long long at, run;
   int live;
 };
-template <bool FLAT>
+template <int PER, bool FLAT>
 __device__ __forceinline__ Place place_of(long long i, int N, int runs) {
-  if (FLAT) return {i * PER, i >> 1, PER};
-  const long long run = i >> 1, row = run / runs;
-  const int c = (int)(run - row * runs) * RUN + (int)(i & 1) * PER;
+  constexpr int LANES = RUN / PER;
+  const long long run = i / LANES;
+  if (FLAT) return {i * PER, run, PER};
+  const long long row = run / runs;
+  const int c = (int)(run - row * runs) * RUN + (int)(i % LANES) * PER;
   return {row * N + c, run, max(0, min(PER, N - c))};
 }
 
 template <typename T, bool FLAT>
 __global__ void __launch_bounds__(NT) ckpt_pack_kernel(const T* __restrict__ x, long long threads, int N, int runs,
                                                        int8_t* __restrict__ q, uint8_t* __restrict__ scale) {
-  constexpr int V = Vec16<T>::N;
-  // both lanes of a pair are in range together (threads is even); whole warps stay for the shuffle
+  constexpr int V = Vec16<T>::N, VECS = IN<T>, PER = VECS * V, LANES = RUN / PER;
+  // the lanes of a run are in range together; whole warps stay for the shuffles
   const long long last = (threads + 31) / 32 * 32;
   for (long long i = (long long)blockIdx.x * NT + threadIdx.x; i < last; i += (long long)gridDim.x * NT) {
-    Place p = place_of<FLAT>(i, N, runs);
+    Place p = place_of<PER, FLAT>(i, N, runs);
     if (i >= threads) p.live = 0;
-    uint4 raw[PER / V];
+    uint4 raw[VECS];
 #pragma unroll
-    for (int k = 0; k < PER / V; ++k)
+    for (int k = 0; k < VECS; ++k)
       raw[k] = k * V < p.live ? __ldg(reinterpret_cast<const uint4*>(x + p.at) + k) : make_uint4(0, 0, 0, 0);
-    float v[PER], a = 0.f;
+    float v[PER];
 #pragma unroll
-    for (int k = 0; k < PER / V; ++k) Vec16<T>::load_raw_unpack(raw[k], v + k * V);
+    for (int k = 0; k < VECS; ++k) Vec16<T>::load_raw_unpack(raw[k], v + k * V);
     // magnitudes as integers: they order as the numbers do, with infinity and NaN above
     unsigned top = 0;
 #pragma unroll
     for (int j = 0; j < PER; ++j) top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     const bool bad = top >= 0x7f800000u;
-    a = __uint_as_float(top);
-    const int e = bad ? 128 : run_exponent(a);
+    const int e = bad ? 128 : run_exponent(__uint_as_float(top));
     const float inv = bad ? 0.f : pow2(-e);
     // x / 2^e + 1.5 * 2^23 rounds to an integer, halves to even, and leaves it in the low byte
     unsigned w[PER / 4];
@@ -78,13 +85,13 @@ __global__ void __launch_bounds__(NT) ckpt_pack_kernel(const T* __restrict__ x, 
       if (p.live) *reinterpret_cast<uint4*>(q + p.at) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
 #pragma unroll
-      for (int k = 0; k < PER / V; ++k) {
+      for (int k = 0; k < VECS; ++k) {
         if (k * V >= p.live) continue;
-        if (V == 8) *reinterpret_cast<uint2*>(q + p.at + 8 * k) = make_uint2(w[(2 * k) % (PER / 4)], w[(2 * k + 1) % (PER / 4)]);
-        else *reinterpret_cast<unsigned*>(q + p.at + 4 * k) = w[k % (PER / 4)];
+        if constexpr (V == 8) *reinterpret_cast<uint2*>(q + p.at + 8 * k) = make_uint2(w[2 * k], w[2 * k + 1]);
+        else *reinterpret_cast<unsigned*>(q + p.at + 4 * k) = w[k];
       }
     }
-    if (!(i & 1) && i < threads) scale[p.run] = (uint8_t)(e + 127);
+    if (i % LANES == 0 && i < threads) scale[p.run] = (uint8_t)(e + 127);
   }
 }
 
@@ -103,50 +110,46 @@ __device__ __forceinline__ void restore4(unsigned w, float f, float* v) {
   v[3] = (__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7443)) - 8388736.f) * f;
 }
 
-// 16 restored values of a row
+// a thread's restored values, `live` of them in the row
 template <typename T, bool FLAT>
-__device__ __forceinline__ void restore16(const int8_t* q, int live, float f, float (&v)[PER]) {
-  constexpr int V = Vec16<T>::N;
-  unsigned w[PER / 4];
-  if (FLAT) {
+__device__ __forceinline__ void restore(const int8_t* q, int live, float f, float (&v)[OUT<T> * Vec16<T>::N]) {
+  constexpr int V = Vec16<T>::N, VECS = OUT<T>;
+  unsigned w[VECS * V / 4];
+  if constexpr (V == 4) {
+    w[0] = __ldg(reinterpret_cast<const unsigned*>(q));
+  } else if (FLAT) {
     const uint4 r = __ldg(reinterpret_cast<const uint4*>(q));
     w[0] = r.x; w[1] = r.y; w[2] = r.z; w[3] = r.w;
   } else {
 #pragma unroll
-    for (int k = 0; k < PER / 4; ++k) w[k] = 0;
-#pragma unroll
-    for (int k = 0; k < PER / V; ++k) {
-      if (k * V >= live) continue;
-      if (V == 8) {
-        const uint2 r = __ldg(reinterpret_cast<const uint2*>(q) + k);
-        w[(2 * k) % (PER / 4)] = r.x;
-        w[(2 * k + 1) % (PER / 4)] = r.y;
-      } else {
-        w[k % (PER / 4)] = __ldg(reinterpret_cast<const unsigned*>(q) + k);
-      }
+    for (int k = 0; k < VECS; ++k) {
+      const uint2 r = k * V < live ? __ldg(reinterpret_cast<const uint2*>(q) + k) : make_uint2(0, 0);
+      w[2 * k] = r.x;
+      w[2 * k + 1] = r.y;
     }
   }
 #pragma unroll
-  for (int k = 0; k < PER / 4; ++k) restore4(w[k], f, v + 4 * k);
+  for (int k = 0; k < VECS * V / 4; ++k) restore4(w[k], f, v + 4 * k);
 }
 
 template <typename T>
-__device__ __forceinline__ void store16(T* x, int live, const float (&v)[PER]) {
+__device__ __forceinline__ void store(T* x, int live, const float (&v)[OUT<T> * Vec16<T>::N]) {
   constexpr int V = Vec16<T>::N;
 #pragma unroll
-  for (int k = 0; k < PER / V; ++k)
+  for (int k = 0; k < OUT<T>; ++k)
     if (k * V < live) Vec16<T>::store(x + k * V, v + k * V);
 }
 
 template <typename T, bool FLAT>
 __global__ void __launch_bounds__(NT) ckpt_unpack_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ scale,
                                                          long long threads, int N, int runs, T* __restrict__ x) {
+  constexpr int PER = OUT<T> * Vec16<T>::N;
   for (long long i = (long long)blockIdx.x * NT + threadIdx.x; i < threads; i += (long long)gridDim.x * NT) {
-    const Place p = place_of<FLAT>(i, N, runs);
+    const Place p = place_of<PER, FLAT>(i, N, runs);
     if (p.live == 0) continue;
     float v[PER];
-    restore16<T, FLAT>(q + p.at, p.live, factor(__ldg(scale + p.run)), v);
-    store16<T>(x + p.at, p.live, v);
+    restore<T, FLAT>(q + p.at, p.live, factor(__ldg(scale + p.run)), v);
+    store<T>(x + p.at, p.live, v);
   }
 }
 
@@ -157,13 +160,13 @@ __device__ __forceinline__ float silu(float g) {
   return __fdividef(g < 0.f ? g * e : g, 1.f + e);
 }
 
-// FLAT (Hp % 32 == 0): 16 columns of g and the same of u; otherwise the columns of one 16-byte
+// FLAT (Hp % 32 == 0): a thread's columns of g and the same of u; otherwise the columns of one 16-byte
 // vector, which lie in one run of g and one of u whatever Hp is
 template <typename T, bool FLAT>
 __global__ void __launch_bounds__(NT) ckpt_swiglu_kernel(const int8_t* __restrict__ q, const uint8_t* __restrict__ scale,
                                                          int rows, int Hp, int runs, int per_row, T* __restrict__ gu,
                                                          T* __restrict__ act) {
-  constexpr int STEP = FLAT ? PER : Vec16<T>::N;
+  constexpr int PER = OUT<T> * Vec16<T>::N, STEP = FLAT ? PER : Vec16<T>::N;
   for (long long i = (long long)blockIdx.x * NT + threadIdx.x; i < (long long)rows * per_row;
        i += (long long)gridDim.x * NT) {
     const long long row = i / per_row;
@@ -171,16 +174,16 @@ __global__ void __launch_bounds__(NT) ckpt_swiglu_kernel(const int8_t* __restric
     const long long at = row * 2 * Hp + c;
     const uint8_t* s = scale + row * runs;
     float g[PER], u[PER];
-    restore16<T, FLAT>(q + at, STEP, factor(__ldg(s + c / RUN)), g);
-    restore16<T, FLAT>(q + at + Hp, STEP, factor(__ldg(s + (Hp + c) / RUN)), u);
+    restore<T, FLAT>(q + at, STEP, factor(__ldg(s + c / RUN)), g);
+    restore<T, FLAT>(q + at + Hp, STEP, factor(__ldg(s + (Hp + c) / RUN)), u);
     if (gu) {
-      store16<T>(gu + at, STEP, g);
-      store16<T>(gu + at + Hp, STEP, u);
+      store<T>(gu + at, STEP, g);
+      store<T>(gu + at + Hp, STEP, u);
     }
     if (act) {
 #pragma unroll
       for (int j = 0; j < PER; ++j) g[j] = silu(g[j]) * u[j];
-      store16<T>(act + row * Hp + c, STEP, g);
+      store<T>(act + row * Hp + c, STEP, g);
     }
   }
 }
@@ -193,7 +196,7 @@ int grid_for(long long threads) {
 template <typename T>
 void pack_t(const void* x, int rows, int N, int8_t* q, uint8_t* scale, cudaStream_t s) {
   const int runs = (N + RUN - 1) / RUN;
-  const long long threads = 2LL * rows * runs;
+  const long long threads = (long long)rows * runs * (RUN / 16);
   if (N % RUN == 0)
     ckpt_pack_kernel<T, true><<<grid_for(threads), NT, 0, s>>>(static_cast<const T*>(x), threads, N, runs, q, scale);
   else
@@ -203,7 +206,7 @@ void pack_t(const void* x, int rows, int N, int8_t* q, uint8_t* scale, cudaStrea
 template <typename T>
 void unpack_t(const int8_t* q, const uint8_t* scale, int rows, int N, void* x, cudaStream_t s) {
   const int runs = (N + RUN - 1) / RUN;
-  const long long threads = 2LL * rows * runs;
+  const long long threads = (long long)rows * runs * (RUN / (OUT<T> * Vec16<T>::N));
   if (N % RUN == 0)
     ckpt_unpack_kernel<T, true><<<grid_for(threads), NT, 0, s>>>(q, scale, threads, N, runs, static_cast<T*>(x));
   else
@@ -214,7 +217,7 @@ template <typename T>
 void swiglu_t(const int8_t* q, const uint8_t* scale, int rows, int Hp, void* gu, void* act, cudaStream_t s) {
   const int runs = (2 * Hp + RUN - 1) / RUN;
   const bool flat = Hp % RUN == 0;
-  const int per_row = Hp / (flat ? PER : Vec16<T>::N);
+  const int per_row = Hp / (flat ? OUT<T> * Vec16<T>::N : Vec16<T>::N);
   const int grid = grid_for((long long)rows * per_row);
   if (flat)
     ckpt_swiglu_kernel<T, true><<<grid, NT, 0, s>>>(q, scale, rows, Hp, runs, per_row, static_cast<T*>(gu), static_cast<T*>(act));
