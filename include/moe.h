@@ -169,7 +169,8 @@ MOE_API int moe_route_ex(const void* x, const void* w_router, const float* logit
  *                    scale * s[t,topk_idx[t,k]] / sum_k' s[t,topk_idx[t,k']]
  *
  *   The choice is that of scores in 64 bits: they are compared in fp32 where they are
- *   further apart than fp32's error and in fp64 where they are not.  Without sel_bias the
+ *   further apart than fp32's error and in fp64 where they are not (ranks that fp64's own
+ *   rounding alone tells apart may go either way).  Without sel_bias the
  *   logits order as the scores do, and they are compared (but for the groups' sums).
  *   A logit of -inf takes an expert out of service: it ranks behind every expert in
  *   service (lower expert first), adds nothing to its group's rank (a group with one

@@ -349,3 +349,16 @@ def test_gate_groups_at_the_lowest_number(E, K, G, KG, low):
         for group_max in (True, False):
             for b in (None, rng.standard_normal(E) * 0.1):
                 check(l, K, G, KG, sigmoid, b, not sigmoid, group_max)
+
+
+@pytest.mark.parametrize("E,K,G,KG", [(64, 6, 8, 3), (384, 8, 8, 4), (96, 9, 12, 11), (24, 3, 4, 3), (256, 8, 1, 1)])
+def test_gate_infinite_biases_and_groups(E, K, G, KG):
+    """Biases of +inf put their experts, and so their groups, first; those of -inf and NaN take theirs out."""
+    rng = np.random.default_rng(E * KG)
+    l = rng.standard_normal((100, E)).astype(np.float32)
+    l[::7, ::3] = -np.inf
+    for values in ([np.inf, 0.1], [-np.inf, 0.1, 0.3], [np.nan, -0.1, 0.2], [np.inf, -np.inf, np.nan, 1e38, 0.5]):
+        b = rng.choice(values, E, p=None if len(values) > 2 else [0.05, 0.95])
+        for sigmoid in (True, False):
+            for group_max in (True, False):
+                check(l, K, G, KG, sigmoid, b, False, group_max)

@@ -275,14 +275,14 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
   };
 
   float b[VMAX], mb = 0.f;
-  bool odd = false;  // a bias that is no number
+  bool odd = false;  // a bias of +inf; one of -inf or NaN takes its expert out of the choice
   if (bias) {
     load(bias, 0.f, b);
 #pragma unroll
     for (int j = 0; j < VMAX; ++j) {
       const bool number = fabsf(b[j]) < INFINITY;
       mb = fmaxf(mb, number ? fabsf(b[j]) : 0.f);
-      odd = odd || !number;
+      odd = odd || b[j] == INFINITY;
       if (b[j] != b[j]) b[j] = -INFINITY;
     }
     mb = warp_max(mb);
@@ -439,7 +439,7 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
       // the lanes at the border know how near the next rank is
       const float border = from_key(kth);
       const bool near = mine == kth && after != INT_MIN && rank != -INFINITY && !(rank - from_key(after) > off);
-      if (kept != p.KG || __any_sync(FULL, near)) {
+      if (kept != p.KG || !usual || __any_sync(FULL, near)) {
         const float bound = (group_max ? a1 : a2) - 2.f * Q * fabsf(group_max ? a1 : a2) - LEAST - margin;
         const float slack = fmaxf(off, from_key(__reduce_max_sync(FULL, mine == kth ? order_key(off) : INT_MIN)));
         // ranks that overflowed have no distance: they are open
