@@ -191,3 +191,34 @@ def test_block_of_one_token_serves():
         assert torch.equal(m.moe.idx[0], big.moe.idx[t])
         assert_close(to64(m.y), to64(big.y[t:t + 1]), TOL["bf16"], "y")
         assert_close(to64(m.xn), to64(big.xn[t:t + 1]), TOL["bf16"], "xn")
+
+
+def test_blocks_that_share_expert_buffers():
+    """Two blocks on one set of expert tensors, through checkpoints: every gradient is the bits of two blocks
+    with tensors of their own; a backward whose activations are gone is refused."""
+    (stored, f, dy, dxn), (stored2, f2, _, _) = inputs(), inputs(9)
+    (d, fd), (d2, fd2) = device(stored, f), device(stored2, f2)
+    dyd, dxnd = dev(dy), dev(dxn)
+    size = (SHAPE.T, SHAPE.H, SHAPE.E, SHAPE.K, SHAPE.Hp, "bf16", DEV)
+
+    def run(share):
+        one = layer.MoEBlockBuffers(*size, train=True)
+        two = layer.MoEBlockBuffers(*size, train=True, experts=one.moe if share else None)
+        cks = [layer.ExpertCheckpoint(one.moe), layer.ExpertCheckpoint(two.moe)]
+        forward(one, d, fd, ckpt=cks[0])
+        forward(two, [one.y] + d2[1:], fd2, x0=one.xn, ckpt=cks[1])
+        if share:
+            assert two.moe.gu is one.moe.gu and two.moe.h is not one.moe.h
+            with pytest.raises(ValueError):
+                layer.MoEBlockBuffers(SHAPE.T - 1, *size[1:], train=True, experts=one.moe)
+            with pytest.raises(ValueError):
+                backward(one, d, fd, dyd, dxnd)
+        backward(two, [one.y] + d2[1:], fd2, dyd, dxnd, x0=one.xn, ckpt=cks[1])
+        backward(one, d, fd, two.d_x, two.moe.dx, ckpt=cks[0])
+        assert L.moe_last_device_error() == L.MOE_OK
+        return [getattr(b.moe, n) for b in (one, two) for n in
+                ("d_gate", "d_logits", "dx", "dw_router", "dw_gate", "dw_up", "dw_down")] + \
+            [getattr(b, n) for b in (one, two) for n in ("y", "xn", "d_x", "dw_post", "d_res_scale", "dw_next")] + \
+            [one.dw_pre]
+    for a, b in zip(run(True), run(False)):
+        assert torch.equal(a, b)

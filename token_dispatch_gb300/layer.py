@@ -32,23 +32,40 @@ def _ws(nbytes: int, device):
 
 
 class MoEBuffers:
-    """Device buffers of one MoE layer call (T tokens, H, E, K, Hp)."""
+    """Device buffers of one MoE layer call (T tokens, H, E, K, Hp).
 
-    def __init__(self, T, H, E, K, Hp, dtype: str, device, backward: bool = True, train: bool = False):
+    ``experts``: buffers of another layer of the same sizes, whose xs, act, gu, dh, dxs and FFN
+    workspaces serve this one too.  Such layers run one after the other on one stream, and a
+    layer's backward needs an ExpertCheckpoint of its forward unless no other ran between."""
+
+    def __init__(self, T, H, E, K, Hp, dtype: str, device, backward: bool = True, train: bool = False,
+                 experts: MoEBuffers | None = None):
         self.T, self.H, self.E, self.K, self.Hp, self.dtype = T, H, E, K, Hp, dtype
         self.cdt = _CDT[dtype]
         tdt = _TDT[dtype]
         R = T * K
         dev = device
         f32, i32 = torch.float32, torch.int32
+        if experts is not None:
+            e = experts
+            if (T, H, E, K, Hp, dtype, train) != (e.T, e.H, e.E, e.K, e.Hp, e.dtype, e.gu is not None) or \
+                    backward and not hasattr(e, "dh") or torch.empty(0, device=dev).device != e.xs.device:
+                raise ValueError("MoEBuffers: the buffers to share are of other sizes or another device, or lack a "
+                                 "backward's")
+        # which of the layers that share them xs, act and gu hold the forward of
+        self.key = object()
+        self.holder = [None] if experts is None else experts.holder
+
+        def rows(name, width):
+            return torch.empty((R, width), dtype=tdt, device=dev) if experts is None else getattr(experts, name)
         self.logits = torch.empty((T, E), dtype=f32, device=dev)
         self.idx = torch.empty((T, K), dtype=i32, device=dev)
         self.gate = torch.empty((T, K), dtype=f32, device=dev)
         self.cu = torch.empty((E + 1,), dtype=i32, device=dev)
         self.dst_row = torch.empty((R,), dtype=i32, device=dev)
         self.src_tok = torch.empty((R,), dtype=i32, device=dev)
-        self.xs = torch.empty((R, H), dtype=tdt, device=dev)
-        self.act = torch.empty((R, Hp), dtype=tdt, device=dev)
+        self.xs = rows("xs", H)
+        self.act = rows("act", Hp)
         self.h = torch.empty((R, H), dtype=tdt, device=dev)
         self.y = torch.empty((T, H), dtype=tdt, device=dev)
         self.ws_dispatch_bytes = L.moe_workspace_bytes(L.MOE_OP_DISPATCH, T, H, E, K, Hp)
@@ -58,9 +75,9 @@ class MoEBuffers:
         # the expert FFN's optional workspace (bf16: the down projection's
         # last round split along K)
         self.ws_ffn_bytes = L.moe_workspace_bytes(L.MOE_OP_EXPERT_FFN, T, H, E, K, Hp) if dtype == "bf16" else 0
-        self.ws_ffn = _ws(self.ws_ffn_bytes, dev)
+        self.ws_ffn = _ws(self.ws_ffn_bytes, dev) if experts is None else experts.ws_ffn
         if backward:
-            self.dh = torch.empty((R, H), dtype=tdt, device=dev)
+            self.dh = rows("dh", H)
             self.d_gate = torch.empty((T, K), dtype=f32, device=dev)
             self.d_logits = torch.empty((T, E), dtype=f32, device=dev)
             self.dw_router = torch.empty((H, E), dtype=f32, device=dev)
@@ -69,13 +86,13 @@ class MoEBuffers:
             self.ws_bwd = _ws(self.ws_bwd_bytes, dev)
         self.gu = None
         if train:  # the expert backward: saved [g | u], dxs, fp32 weight gradients
-            self.gu = torch.empty((R, 2 * Hp), dtype=tdt, device=dev)
-            self.dxs = torch.empty((R, H), dtype=tdt, device=dev)
+            self.gu = rows("gu", 2 * Hp)
+            self.dxs = rows("dxs", H)
             self.dw_gate = torch.empty((E, H, Hp), dtype=f32, device=dev)
             self.dw_up = torch.empty((E, H, Hp), dtype=f32, device=dev)
             self.dw_down = torch.empty((E, H, Hp), dtype=f32, device=dev)
             self.ws_ffn_bwd_bytes = L.moe_workspace_bytes(L.MOE_OP_EXPERT_FFN_BWD, T, H, E, K, Hp)
-            self.ws_ffn_bwd = _ws(self.ws_ffn_bwd_bytes, dev)
+            self.ws_ffn_bwd = _ws(self.ws_ffn_bwd_bytes, dev) if experts is None else experts.ws_ffn_bwd
 
 
 def moe_forward(b: MoEBuffers, x, w_router, logit_bias, w_gate, w_up, w_down, stream=None,
@@ -191,7 +208,8 @@ class GroupGate:
 class ExpertCheckpoint:
     """What the expert FFN's backward reads of the forward, in 8 bits: the dispatched rows and
     [g | u] (moe_ckpt_pack), 1.03 bytes a value instead of 2.  act is computed again.  One for
-    each layer; the layers share one MoEBuffers to save from and restore into."""
+    each layer, so that layers whose buffers share these tensors (MoEBuffers(experts=...)) can
+    save from them and restore into them; what else a backward reads, each layer keeps."""
 
     def __init__(self, b: MoEBuffers):
         if b.gu is None:
@@ -216,11 +234,12 @@ class ExpertCheckpoint:
 class MoEBlockBuffers:
     """Buffers of a MoE block: MoEBuffers of its layer (``moe``), the normed input ``x0``, the
     residual stream ``y`` behind the block and the normed input ``xn`` of the next one; for
-    training the gradients of all of them and of the norm weights."""
+    training the gradients of all of them and of the norm weights.  ``experts``: MoEBuffers
+    whose expert tensors ``moe`` shares."""
 
-    def __init__(self, T, H, E, K, Hp, dtype: str, device, train: bool = False):
+    def __init__(self, T, H, E, K, Hp, dtype: str, device, train: bool = False, experts: MoEBuffers | None = None):
         tdt, f32 = _TDT[dtype], torch.float32
-        self.moe = MoEBuffers(T, H, E, K, Hp, dtype, device, backward=train, train=train)
+        self.moe = MoEBuffers(T, H, E, K, Hp, dtype, device, backward=train, train=train, experts=experts)
         self.x0, self.y, self.xn = (torch.empty((T, H), dtype=tdt, device=device) for _ in range(3))
         if train:
             self.d_x = torch.empty((T, H), dtype=tdt, device=device)
@@ -238,7 +257,7 @@ def moe_block_forward(m: MoEBlockBuffers, x, w_pre, w_router, sel_bias, gate: Gr
     w_pre, w_post, w_next (float [H]): weights of the norms before the block, after it and
     before the next one; w_post and w_next may be None (no such norm).  x0: norm(x) where
     the block before has written it (its m.xn); w_pre is then unused.  ckpt: keep the expert
-    activations there, so that m.moe may serve other layers before the backward."""
+    activations there, so that blocks which share m.moe's may run before the backward."""
     b = m.moe
     T, H, E, K, Hp, dt = b.T, b.H, b.E, b.K, b.Hp, b.cdt
     if x0 is None:
@@ -250,6 +269,7 @@ def moe_block_forward(m: MoEBlockBuffers, x, w_pre, w_router, sel_bias, gate: Gr
                    stream=stream)
     L.moe_expert_ffn_ex(b.xs, b.cu, T * K, w_gate, w_up, w_down, E, H, Hp, dt, b.act, b.gu, b.h, b.ws_ffn,
                         b.ws_ffn_bytes, stream=stream)
+    b.holder[0] = b.key
     if ckpt is not None:
         ckpt.save(b, stream=stream)
     L.moe_combine_norm(b.h, b.gate, b.dst_row, None, x, w_post, res_scale, w_next, eps, T, H, K, dt, m.y,
@@ -265,6 +285,8 @@ def moe_block_backward(m: MoEBlockBuffers, x, w_pre, w_router, gate: GroupGate, 
     given (the norm belongs to the block before) m.d_x holds the residual's share alone and
     m.moe.dx = dL/dx0."""
     b = m.moe
+    if ckpt is None and b.holder[0] is not b.key:
+        raise ValueError("moe_block_backward: without ckpt the block's forward must be the last one in its buffers")
     T, H, E, K, Hp, dt = b.T, b.H, b.E, b.K, b.Hp, b.cdt
     L.moe_combine_norm_bwd(dy, dxn, b.h, b.gate, b.dst_row, None, None if w_next is None else m.y, w_post, res_scale,
                            w_next, eps, T, H, K, dt, m.d_x, b.dh, b.d_gate, None,
@@ -272,6 +294,7 @@ def moe_block_backward(m: MoEBlockBuffers, x, w_pre, w_router, gate: GroupGate, 
                            None if w_next is None else m.dw_next, m.ws_norm, m.ws_norm_bytes, stream=stream)
     if ckpt is not None:
         ckpt.restore(b, stream=stream)
+        b.holder[0] = b.key
     L.moe_expert_ffn_bwd(b.xs, b.cu, T * K, w_gate, w_up, w_down, E, H, Hp, dt, b.gu, b.act, b.dh, b.dxs,
                          b.dw_gate, b.dw_up, b.dw_down, b.ws_ffn_bwd, b.ws_ffn_bwd_bytes, stream=stream)
     L.moe_permute_bwd(None, None, b.gate, b.dst_row, None, None, b.dxs, T, H, K, dt, None, None, None, b.dx,
