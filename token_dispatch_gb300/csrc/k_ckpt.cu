@@ -2,6 +2,10 @@
 // of two, the least that holds the run's largest magnitude in 127 steps.  Powers
 // of two keep every division exact, so the only rounding is the one to integers,
 // and the restored values have at most 8 significant bits: exact in bf16 too.
+//
+// The memory bounds all three.  16384 x 28672 bf16: pack 205 us (6.9 TB/s), unpack 221 (6.4),
+// [g | u] and act 290 (6.5), where a copy runs at 6.8; 16384 x 4096 fp32: 51, 55 and 74 us (6.6,
+// 6.1 and 6.4 TB/s).
 #include <math.h>
 
 #include "moe_internal.cuh"
@@ -22,7 +26,8 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float((unsigned)
 
 // A thread takes VECS 16-byte vectors of neighbours, so a run is 32 / (VECS V) lanes, and whole
 // rows of runs (FLAT: N % 32 == 0) move without an index division for each.  Other widths move
-// the same values in pieces of one vector, the last run of a row in fewer of them.
+// the same values in pieces of one vector, the last run of a row in fewer of them (unpack of
+// 16384 x 28672 bf16 that way: 244 us instead of 221).
 //
 // 16 values a thread, but one vector where fp32 is written: four to a thread left each sector
 // to two stores (16384 x 4096 fp32, unpack 71 -> 55 us, [g | u] and act 102 -> 74).  Reading is the

@@ -9,6 +9,11 @@
 // (cp.async, 16 bytes) and waits for its own copies alone.  No thread reads what
 // another copied, so the ring needs no barrier; the only ones are those of the
 // reductions, while the copies of the rows behind are under way.
+//
+// Of a copy's 6.77 TB/s: forward 8192 x 7168 bf16, K = 8: 194 us, 0.98; 8192 x 4096, K = 2
+// without the norm after the block: 58 us, 0.86 (the launch and the first rows' latency are
+// the rest); backward 16384 x 2048, K = 6: 183 us, 0.87 (issue slots 64%).  Seven tokens
+// take 8 us, most of them the launch.
 #include <math.h>
 
 #include <atomic>
@@ -627,6 +632,8 @@ __global__ void __launch_bounds__(512) combine_norm_bwd_kernel(const BwdArgs a) 
 
 // The column sums: a CTA takes 32 columns of [2][H], its 32 warps the parts w, w + 32, ...
 // in order; the warps' sums are added in warp order and multiplied by their column factors.
+// Latency bounds it; it is set up while the kernel before it runs (16384 x 2048, K = 6: 186 us
+// to 183 for both; 1001 x 1000 fp32: 22.5 to 20).
 __global__ void __launch_bounds__(1024)
 column_sums_kernel(const float* part, int parts, int H, const float* __restrict__ w_post,
                    const float* __restrict__ res_scale, float* dw_post, float* d_res_scale, float* dw_next) {
@@ -691,8 +698,11 @@ template <typename T, int X, int S, int MAXT, int CTAS> int fwd_v(const FwdArgs&
   return launch_status();
 }
 
-// 16 values a thread up to H = 8192, 32 beyond.  Rows of up to 8 KB: three CTAs or more to
-// an SM, 8 rows of ring each, so that some stream while others reduce; wider rows: one CTA
+// 16 values a thread up to H = 8192, where the registers still hold weights beside the row, 32
+// beyond (32 for 8192 x 4096, K = 2: 70 us instead of 60; 4096 x 8192: 72 instead of 66).  Rows
+// of up to 8 KB: three CTAs or more to an SM, 8 rows of ring each, so that some stream while
+// others reduce (with 12 rows and as many CTAs as then fit, 16384 x 4096, K = 1: 111 us instead of
+// 98, 11650 x 2880, K = 2: 78 instead of 59; K = 8 is within 3% either way); wider rows: one CTA
 // with 12 rows of up to 16 KB, 6 of up to 32 KB, 3 beyond.
 template <typename T> int fwd_t(const FwdArgs& a, cudaStream_t s) {
   constexpr bool WIDE = sizeof(T) == 4;
@@ -734,7 +744,7 @@ template <typename T, int X, bool HOLD> int bwd_x(BwdArgs& a, int* grid, cudaStr
   if constexpr (HOLD) {
     // As many teams as there are tokens to an SM, where the GPU holds them all at once: a CTA's
     // one set of column sums instead of one for each token (1001 tokens of 1000 fp32 columns:
-    // 24.5 us without, 21 with).  A ring then holds a token's rows, and the team's 2 H sums.
+    // 24.5 us without, 21 with, both before the second launch overlapped the first).  A ring then holds a token's rows, and the team's 2 H sums.
     const int per_sm = (a.T + sm_count() - 1) / sm_count(), sums = (8 * a.H + row - 1) / row, S = R > sums ? R : sums;
     if (per_sm > 1 && per_sm <= MAX_TEAMS && per_sm * threads <= BWD_THREADS && per_sm * (S * row + beside) <= SM_BYTES) {
       a.teams = per_sm;
@@ -742,7 +752,8 @@ template <typename T, int X, bool HOLD> int bwd_x(BwdArgs& a, int* grid, cudaStr
       return bwd_v<T, X, HOLD, true>(a, a.teams * threads, a.teams * (S * row + beside), grid, s);
     }
     // otherwise as many CTAs as the registers have room for, and behind a token's own rows 8, 4
-    // or 2 of the next ones, what shared memory has room for
+    // or 2 of the next ones, what shared memory has room for (4096 x 7168, K = 8: 214 us, with
+    // 2 alone 220; narrower rows within 1%)
     for (int ctas = BWD_THREADS / threads; ctas > 0; --ctas) {
       const int room = (SM_BYTES / ctas - beside - 1024) / row;
       if (room < R + 2) continue;
@@ -753,8 +764,9 @@ template <typename T, int X, bool HOLD> int bwd_x(BwdArgs& a, int* grid, cudaStr
   return bwd_v<T, X, HOLD, false>(a, threads, a.S * row + beside, grid, s);
 }
 
-// 16 values a thread up to H = 8192, 32 beyond; a token's rows are held where two more fit
-// beside them
+// 16 values a thread up to H = 8192, 32 beyond (32 for 16384 x 2048, K = 6: 291 us instead of
+// 186); a token's rows are held where two more fit beside them (read twice instead: 226 us;
+// 4096 x 7168, K = 8: 290 instead of 214)
 template <typename T> int bwd_t(BwdArgs& a, int* grid, cudaStream_t s) {
   constexpr int VPT = 16 / Vec16<T>::N;
   if (a.H > 8192) return bwd_x<T, 32, false>(a, grid, s);
@@ -796,7 +808,6 @@ int launch_combine_norm_bwd(const void* dy, const void* dxn, const void* h, cons
   int grid = 0;
   const int st = dtype == MOE_BF16 ? bwd_t<bf16>(a, &grid, s) : bwd_t<float>(a, &grid, s);
   if (st != MOE_OK || !sums) return st;
-  // launched while the first kernel runs, so that its own start costs nothing
   cudaLaunchAttribute early{};
   early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early.val.programmaticStreamSerializationAllowed = 1;

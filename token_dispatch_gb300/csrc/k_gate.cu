@@ -16,6 +16,11 @@
 // again in fp64 (GB300 does 1/64 of its fp32 rate there: a whole row in fp64, the
 // simplest form of this kernel, took 1628 us for 32768 x 384 logits).  Without a
 // bias the logits are compared, which order as the scores do.
+//
+// What bounds it is instructions, not the 50 MB that 32768 x 384 logits are (7.8 us at the
+// rate of a copy): 723 a token there, 64% of the issue slots, 35-38 us with 8 groups, K = 8.
+// 16384 x 64 take 12 us (530 a token), one token 7.2 us, of which a launch is 5-6.  A row
+// that needs fp64 takes 2-6 us more of its warp, which shows in calls of one round.
 #include <limits.h>
 #include <math.h>
 
@@ -423,7 +428,10 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
         kth = __reduce_max_sync(FULL, key);
         if (key == kth) key = INT_MIN;
       }
-      if (__popc(__ballot_sync(FULL, mine > kth && lig == 0)) >= p.KG) {
+      int after = __reduce_max_sync(FULL, key);
+      stay = mine >= kth && g < p.G;
+      int kept = __popc(__ballot_sync(FULL, stay && lig == 0));
+      if (kept != p.KG && __popc(__ballot_sync(FULL, mine > kth && lig == 0)) >= p.KG) {
         // equal ranks above put that too low: again, counting them
         key = mine;
         for (int n = 0;;) {
@@ -432,10 +440,10 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
           if (key == kth) key = INT_MIN;
           if (n >= p.KG || kth == INT_MIN) break;
         }
+        after = __reduce_max_sync(FULL, key);
+        stay = mine >= kth && g < p.G;
+        kept = __popc(__ballot_sync(FULL, stay && lig == 0));
       }
-      const int after = __reduce_max_sync(FULL, key);
-      stay = mine >= kth && g < p.G;
-      const int kept = __popc(__ballot_sync(FULL, stay && lig == 0));
       // the lanes at the border know how near the next rank is
       const float border = from_key(kth);
       const bool near = mine == kth && after != INT_MIN && rank != -INFINITY && !(rank - from_key(after) > off);
@@ -630,7 +638,9 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
 // Backward: a warp to a token.  All but the softmax without RENORM have a gradient at the
 // chosen experts alone: the row is filled with zeros while the chosen logits are on their
 // way, then their lanes overwrite K of them.  The softmax's row goes through registers in VQ
-// 16-byte pieces a lane (VQ = 0: rows of any length, one value at a time, read twice).
+// 16-byte pieces a lane (VQ = 0: rows of any length, one value at a time, read twice; 16384
+// x 256 take 10.7 us in pieces and 14.6 so).  The launch bounds it: 8192 x 384, logistic, 7.1 us
+// (2.0 at the rate of a copy); 16384 x 64, softmax, 8.2 us (1.4).
 template <int VQ>
 __global__ void __launch_bounds__(32 * WARPS)
 gate_bwd_kernel(const float* __restrict__ d_gate, const float* __restrict__ logits, const int32_t* __restrict__ idx,
@@ -775,6 +785,7 @@ int launch_gate(float* logits, const float* part, int S, const float* bias, int 
   GateShape p{T, E, K, G, KG, E / G, 32 / G, 0, mode, scale};
   p.vpl = (p.gs + p.lpg - 1) / p.lpg;
   if (p.gs % 4 == 0 && p.vpl > 2) p.vpl = (p.vpl + 3) / 4 * 4;  // 16-byte loads
+  // the least instance that holds a lane's experts (32768 x 384 in 12: 33 us, in 16: 44)
 #define MOE_GATE(V) gate_v<V>(logits, part, S, bias, p, idx, gate, s)
   if (p.vpl <= 2) MOE_GATE(2);
   else if (p.vpl <= 4) MOE_GATE(4);
