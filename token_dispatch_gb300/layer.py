@@ -234,8 +234,8 @@ class ExpertCheckpoint:
 class MoEBlockBuffers:
     """Buffers of a MoE block: MoEBuffers of its layer (``moe``), the normed input ``x0``, the
     residual stream ``y`` behind the block and the normed input ``xn`` of the next one; for
-    training the gradients of all of them and of the norm weights.  ``experts``: MoEBuffers
-    whose expert tensors ``moe`` shares."""
+    training (bf16, as the expert FFN's backward) the gradients of all of them and of the norm
+    weights.  ``experts``: MoEBuffers whose expert tensors ``moe`` shares."""
 
     def __init__(self, T, H, E, K, Hp, dtype: str, device, train: bool = False, experts: MoEBuffers | None = None):
         tdt, f32 = _TDT[dtype], torch.float32
