@@ -159,7 +159,7 @@ struct FwdArgs {
   const float* row_scale;
   const void* residual;
   const float *w_post, *res_scale, *w_next;
-  float eps;
+  float eps, inv_h;  // inv_h: 1 / H
   int T, H, K;
   void *y, *xn;
 };
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(MAXT, CTAS) combine_norm_kernel(const FwdArgs 
       float2 s = both(0.f);
 #pragma unroll
       for (int i = 0; i < P; ++i) s = __ffma2_rn(z[i], z[i], s);
-      f *= 1.f / sqrtf(sum.run(s.x + s.y, turn++) / a.H + a.eps);
+      f *= rsqrtf(sum.run(s.x + s.y, turn++) * a.inv_h + a.eps);
     }
     if (a.residual) copies_wait<S - 1>();
     float2 s = both(0.f);
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(MAXT, CTAS) combine_norm_kernel(const FwdArgs 
     }
     if (a.residual) next_row();
     if (a.w_next) {
-      const float q = 1.f / sqrtf(sum.run(s.x + s.y, turn++) / a.H + a.eps);
+      const float q = rsqrtf(sum.run(s.x + s.y, turn++) * a.inv_h + a.eps);
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
         float2 x[N], p[N], n[N];
@@ -310,7 +310,7 @@ struct BwdArgs {
   const void *dy, *dxn, *h, *y;
   MetaSource meta;
   const float *row_scale, *w_post, *res_scale, *w_next;
-  float eps;
+  float eps, inv_h;  // inv_h: 1 / H
   int T, H, K;
   void *d_res, *dh;
   float *d_gate, *d_scale;
@@ -528,11 +528,11 @@ __global__ void __launch_bounds__(512) combine_norm_bwd_kernel(const BwdArgs a) 
     for (int i = 0; i < 6; ++i) s[i] = s2[i].x + s2[i].y;
     team_sum8(s, sums, turn++, warp, nw, bar);
     if (t != first) write_gates(t - stride, (j & 1) ^ 1);
-    const float inv_h = 1.f / a.H;
-    const float q = next ? 1.f / sqrtf(s[0] * inv_h + a.eps) : 0.f, vm = s[1] * q * inv_h;
-    const float r = a.w_post ? 1.f / sqrtf(s[2] * inv_h + a.eps) : 1.f;
+    const float q = next ? rsqrtf(s[0] * a.inv_h + a.eps) : 0.f, vm = s[1] * q * a.inv_h;
+    const float r = a.w_post ? rsqrtf(s[2] * a.inv_h + a.eps) : 1.f;
     const float sd = r * (s[3] + q * (s[4] - q * vm * s[5]));
-    const float um = a.w_post ? rs * sd * inv_h : 0.f;
+    const float um = a.w_post ? rs * sd * a.inv_h : 0.f;
+    const float2 rsr = both(rs * r), zu = both(-um * r * r), q2 = both(q), qvm = both(-q * vm);
     if (tid == 0 && a.d_scale) a.d_scale[t] = sd;
 
     if (!HOLD) copies_wait<0>();
@@ -550,9 +550,8 @@ __global__ void __launch_bounds__(512) combine_norm_bwd_kernel(const BwdArgs a) 
         Pairs<T>::unpack(ring[by_x + v * NT], x);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const float2 u = __fmul2_rn(y[i], both(q));
-          const float2 e = __ffma2_rn(x[i], n[i], __fmul2_rn(u, both(-vm)));
-          d[i] = __ffma2_rn(both(q), e, d[i]);
+          const float2 u = __fmul2_rn(y[i], q2);
+          d[i] = __ffma2_rn(u, qvm, __ffma2_rn(q2, __fmul2_rn(x[i], n[i]), d[i]));
           M[v * N + i] = __ffma2_rn(x[i], u, M[v * N + i]);
         }
       }
@@ -560,9 +559,9 @@ __global__ void __launch_bounds__(512) combine_norm_bwd_kernel(const BwdArgs a) 
         *reinterpret_cast<uint4*>(static_cast<char*>(a.d_res) + t * row_bytes + offset[v]) = Pairs<T>::pack(d);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float2 u = __fmul2_rn(z[v * N + i], both(r)), e = __fmul2_rn(d[i], both(rs));
-        Q[v * N + i] = __ffma2_rn(e, u, Q[v * N + i]);
-        z[v * N + i] = __fmul2_rn(both(r), __ffma2_rn(e, p[i], __fmul2_rn(u, both(-um))));  // dz
+        const float2 u = __fmul2_rn(z[v * N + i], rsr);
+        Q[v * N + i] = __ffma2_rn(d[i], u, Q[v * N + i]);
+        z[v * N + i] = __ffma2_rn(rsr, __fmul2_rn(d[i], p[i]), __fmul2_rn(z[v * N + i], zu));  // dz
       }
     }
     for (int i = 0; i < A; ++i) next_row();
@@ -788,7 +787,7 @@ int launch_combine_norm(const void* h, const float* gate, const int32_t* dst_row
                         float eps, int T, int H, int K, int dtype, void* y, void* xn, cudaStream_t s) {
   if (T == 0) return MOE_OK;
   const FwdArgs a{h, MetaSource{gate, dst_row, T, (long long)T * K, K, device_error_word()}, row_scale, residual,
-                  w_post, res_scale, w_next, eps, T, H, K, y, xn};
+                  w_post, res_scale, w_next, eps, 1.f / H, T, H, K, y, xn};
   return dtype == MOE_BF16 ? fwd_t<bf16>(a, s) : fwd_t<float>(a, s);
 }
 
@@ -804,7 +803,7 @@ int launch_combine_norm_bwd(const void* dy, const void* dxn, const void* h, cons
     return MOE_OK;
   }
   BwdArgs a{dy, dxn, h, y, MetaSource{gate, dst_row, T, (long long)T * K, K, device_error_word()}, row_scale, w_post,
-            res_scale, w_next, eps, T, H, K, d_res, dh, d_gate, d_scale, sums ? static_cast<float*>(ws) : nullptr, 0, 1};
+            res_scale, w_next, eps, 1.f / H, T, H, K, d_res, dh, d_gate, d_scale, sums ? static_cast<float*>(ws) : nullptr, 0, 1};
   int grid = 0;
   const int st = dtype == MOE_BF16 ? bwd_t<bf16>(a, &grid, s) : bwd_t<float>(a, &grid, s);
   if (st != MOE_OK || !sums) return st;
