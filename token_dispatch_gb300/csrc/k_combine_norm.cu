@@ -12,8 +12,9 @@
 //
 // Of a copy's 6.77 TB/s: forward 8192 x 7168 bf16, K = 8: 194 us, 0.98; 8192 x 4096, K = 2
 // without the norm after the block: 58 us, 0.86 (the launch and the first rows' latency are
-// the rest); backward 16384 x 2048, K = 6: 183 us, 0.87 (issue slots 64%).  Seven tokens
-// take 8 us, most of them the launch.
+// the rest); backward 16384 x 2048, K = 6: 183 us, 0.87; 8192 x 4096, K = 2: 110 us, 0.72,
+// where the norms' instructions are more of a token (issue slots 61%, 16 warps to an SM).  Seven
+// tokens forward take 8 us, most of them the launch.
 #include <math.h>
 
 #include <atomic>
@@ -328,9 +329,8 @@ __host__ __device__ constexpr int beside_gates(int nw, int R) { return beside_sr
 __host__ __device__ constexpr int beside_rows(int nw, int R, int K) { return beside_gates(nw, R) + META * K / 2; }
 __host__ __device__ constexpr int beside_all(int nw, int R, int K) { return beside_rows(nw, R, K) + META * K / 4; }
 
-__device__ __forceinline__ void wait_all_but(int n) {  // n or fewer
-  if (n >= 8) copies_wait<8>();
-  else if (n >= 4) copies_wait<4>();
+__device__ __forceinline__ void wait_all_but(int n) {  // 4, 2 or none
+  if (n >= 4) copies_wait<4>();
   else if (n >= 2) copies_wait<2>();
   else copies_wait<0>();
 }
@@ -348,7 +348,12 @@ __device__ __forceinline__ void wait_all_but(int n) {  // n or fewer
 // One reduction serves both norms.  With D = dy + q (w_next dxn - q vm y):
 //   <aw D, z> = <aw dy, z> + q <aw w_next dxn, z> - q^2 vm <aw y, z>,
 // so its three products are summed along with y^2, w_next dxn y and z^2.
-template <typename T, int X, bool HOLD, bool TEAMS>
+//
+// NEXT, DY: dxn (with w_next and y) and dy are there.  Registers are what a thread runs out of
+// (128, where 170 would take a quarter fewer instructions): the two are no arguments, and
+// w_next is read again for each token, from L1 (8192 x 4096, K = 2: 123 us to 110 for both; in
+// shared memory 106, but without the room for the rows of K = 8: 256 us instead of 230).
+template <typename T, int X, bool HOLD, bool TEAMS, bool NEXT, bool DY>
 __global__ void __launch_bounds__(512) combine_norm_bwd_kernel(const BwdArgs a) {
   extern __shared__ uint4 smem[];
   asm volatile("griddepcontrol.launch_dependents;");  // the column sums may get ready
@@ -361,8 +366,8 @@ __global__ void __launch_bounds__(512) combine_norm_bwd_kernel(const BwdArgs a) 
   uint4* ring = smem + team * S * VPT * NT;
   // T < 2^31: a token's number, and those of the ones ahead, fit in 32 bits without sign
   const unsigned first = blockIdx.x * teams + team, stride = gridDim.x * teams;
-  const bool next = a.w_next != nullptr;
-  const int A = (next ? 2 : 0) + (a.dy ? 1 : 0), R = HOLD ? A + K : 2 * (A + K);
+  constexpr int A = (NEXT ? 2 : 0) + (DY ? 1 : 0);
+  const int R = HOLD ? A + K : 2 * (A + K);
   const int beside = teams * S * VPT * NT + team * beside_all(nw, R, K);
   unsigned long long* src = reinterpret_cast<unsigned long long*>(smem + beside + beside_src(nw));
   float2* gates = reinterpret_cast<float2*>(smem + beside + beside_gates(nw, R));  // twice, as a pair
@@ -386,7 +391,7 @@ __global__ void __launch_bounds__(512) combine_norm_bwd_kernel(const BwdArgs a) 
       rows[j * K + k] = row;
     } else {
       const int x = k - K;
-      p = row_address(next && x < 2 ? (x == 0 ? a.y : a.dxn) : a.dy, t < (unsigned)a.T ? (long long)t : -1ll, row_bytes);
+      p = row_address(NEXT && x < 2 ? (x == 0 ? a.y : a.dxn) : a.dy, t < (unsigned)a.T ? (long long)t : -1ll, row_bytes);
     }
     unsigned long long* q = src + j * R;
     if (HOLD) {
@@ -404,28 +409,25 @@ __global__ void __launch_bounds__(512) combine_norm_bwd_kernel(const BwdArgs a) 
     a.meta.get(t, k, row, g);
     note(j, k, t, row, g);
   }
-  float2 aw[HOLD_W ? P : 1], wn[HOLD_W ? P : 1];
-  auto weights = [&](int v, float2* p, float2* n) {
+  float2 aw[HOLD_W ? P : 1];
+  auto post_weights = [&](int v, float2* p) {
     float2 r[N];
     load_w<N>(a.w_post, offset[v] / 16 * V, live[v], p);
     load_w<N>(a.res_scale, offset[v] / 16 * V, live[v], r);
-    load_w<N>(a.w_next, offset[v] / 16 * V, live[v], n);
 #pragma unroll
     for (int i = 0; i < N; ++i) p[i] = __fmul2_rn(p[i], r[i]);
   };
   if (HOLD_W) {
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) weights(v, aw + v * N, wn + v * N);
+    for (int v = 0; v < VPT; ++v) post_weights(v, aw + v * N);
   }
   auto weights_of = [&](int v, float2* p, float2* n) {
+    if (NEXT) load_w<N>(a.w_next, offset[v] / 16 * V, true, n);  // beside the row dxn is 0
     if (HOLD_W) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        p[i] = aw[(v * N + i) % (HOLD_W ? P : 1)];
-        n[i] = wn[(v * N + i) % (HOLD_W ? P : 1)];
-      }
+      for (int i = 0; i < N; ++i) p[i] = aw[(v * N + i) % (HOLD_W ? P : 1)];
     } else {
-      weights(v, p, n);
+      post_weights(v, p);
     }
   };
   team_sync(bar, nw);
@@ -503,7 +505,7 @@ __global__ void __launch_bounds__(512) combine_norm_bwd_kernel(const BwdArgs a) 
         p[i] = __fmul2_rn(p[i], z[v * N + i]);
         s2[2] = __ffma2_rn(z[v * N + i], z[v * N + i], s2[2]);
       }
-      if (next) {
+      if (NEXT) {
         Pairs<T>::unpack(ring[at_y + v * NT], y);
         Pairs<T>::unpack(ring[at_x + v * NT], x);
 #pragma unroll
@@ -515,7 +517,7 @@ __global__ void __launch_bounds__(512) combine_norm_bwd_kernel(const BwdArgs a) 
           s2[5] = __ffma2_rn(p[i], y[i], s2[5]);
         }
       }
-      if (a.dy) {
+      if (DY) {
         Pairs<T>::unpack(ring[at_d + v * NT], x);
 #pragma unroll
         for (int i = 0; i < N; ++i) s2[3] = __ffma2_rn(p[i], x[i], s2[3]);
@@ -528,7 +530,7 @@ __global__ void __launch_bounds__(512) combine_norm_bwd_kernel(const BwdArgs a) 
     for (int i = 0; i < 6; ++i) s[i] = s2[i].x + s2[i].y;
     team_sum8(s, sums, turn++, warp, nw, bar);
     if (t != first) write_gates(t - stride, (j & 1) ^ 1);
-    const float q = next ? rsqrtf(s[0] * a.inv_h + a.eps) : 0.f, vm = s[1] * q * a.inv_h;
+    const float q = NEXT ? rsqrtf(s[0] * a.inv_h + a.eps) : 0.f, vm = s[1] * q * a.inv_h;
     const float r = a.w_post ? rsqrtf(s[2] * a.inv_h + a.eps) : 1.f;
     const float sd = r * (s[3] + q * (s[4] - q * vm * s[5]));
     const float um = a.w_post ? rs * sd * a.inv_h : 0.f;
@@ -541,10 +543,13 @@ __global__ void __launch_bounds__(512) combine_norm_bwd_kernel(const BwdArgs a) 
     for (int v = 0; v < VPT; ++v) {
       float2 p[N], n[N], d[N];
       weights_of(v, p, n);
+      if (DY) {
+        Pairs<T>::unpack(ring[by_d + v * NT], d);
+      } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) d[i] = both(0.f);
-      if (a.dy) Pairs<T>::unpack(ring[by_d + v * NT], d);
-      if (next) {
+        for (int i = 0; i < N; ++i) d[i] = both(0.f);
+      }
+      if (NEXT) {
         float2 x[N], y[N];
         Pairs<T>::unpack(ring[at + v * NT], y);
         Pairs<T>::unpack(ring[by_x + v * NT], x);
@@ -724,14 +729,21 @@ int bwd_rows(const BwdArgs& a) { return a.K + (a.w_next ? 2 : 0) + (a.dy ? 1 : 0
 // 128 registers leave room for 512 threads to an SM
 constexpr int BWD_THREADS = 512, MAX_TEAMS = 8;
 
-template <typename T, int X, bool HOLD, bool TEAMS> int bwd_v(BwdArgs& a, int threads, int smem, int* grid, cudaStream_t s) {
+template <typename T, int X, bool HOLD, bool TEAMS, bool NEXT, bool DY>
+int bwd_n(BwdArgs& a, int threads, int smem, int* grid, cudaStream_t s) {
   static std::atomic<unsigned long long> known{0};
   const int tokens = (a.T + a.teams - 1) / a.teams;
-  const int st = persistent_grid(combine_norm_bwd_kernel<T, X, HOLD, TEAMS>, known, threads, smem, SM_BYTES,
+  const int st = persistent_grid(combine_norm_bwd_kernel<T, X, HOLD, TEAMS, NEXT, DY>, known, threads, smem, SM_BYTES,
                                  bwd_ctas_per_sm(a.H), tokens, grid);
   if (st != MOE_OK) return st;
-  combine_norm_bwd_kernel<T, X, HOLD, TEAMS><<<*grid, threads, smem, s>>>(a);
+  combine_norm_bwd_kernel<T, X, HOLD, TEAMS, NEXT, DY><<<*grid, threads, smem, s>>>(a);
   return launch_status();
+}
+
+template <typename T, int X, bool HOLD, bool TEAMS> int bwd_v(BwdArgs& a, int threads, int smem, int* grid, cudaStream_t s) {
+  if (!a.w_next) return bwd_n<T, X, HOLD, TEAMS, false, true>(a, threads, smem, grid, s);
+  return a.dy ? bwd_n<T, X, HOLD, TEAMS, true, true>(a, threads, smem, grid, s)
+              : bwd_n<T, X, HOLD, TEAMS, true, false>(a, threads, smem, grid, s);
 }
 
 template <typename T, int X, bool HOLD> int bwd_x(BwdArgs& a, int* grid, cudaStream_t s) {
@@ -739,38 +751,44 @@ template <typename T, int X, bool HOLD> int bwd_x(BwdArgs& a, int* grid, cudaStr
   const int threads = threads_for(a.H / Vec16<T>::N, VPT), row = VPT * threads * 16, R = bwd_rows(a);
   const int beside = 16 * beside_all(threads / 32, HOLD ? R : 2 * R, a.K);
   a.teams = 1;
-  a.S = HOLD ? R + 2 : 3;
+  a.S = 3;
   if constexpr (HOLD) {
     // As many teams as there are tokens to an SM, where the GPU holds them all at once: a CTA's
     // one set of column sums instead of one for each token (1001 tokens of 1000 fp32 columns:
-    // 24.5 us without, 21 with, both before the second launch overlapped the first).  A ring then holds a token's rows, and the team's 2 H sums.
+    // 24.5 us without, 21 with, both before the second launch overlapped the first).  A ring
+    // then holds a token's rows, and the team's 2 H sums.
     const int per_sm = (a.T + sm_count() - 1) / sm_count(), sums = (8 * a.H + row - 1) / row, S = R > sums ? R : sums;
     if (per_sm > 1 && per_sm <= MAX_TEAMS && per_sm * threads <= BWD_THREADS && per_sm * (S * row + beside) <= SM_BYTES) {
       a.teams = per_sm;
       a.S = S;
       return bwd_v<T, X, HOLD, true>(a, a.teams * threads, a.teams * (S * row + beside), grid, s);
     }
-    // otherwise as many CTAs as the registers have room for, and behind a token's own rows 8, 4
-    // or 2 of the next ones, what shared memory has room for (4096 x 7168, K = 8: 214 us, with
-    // 2 alone 220; narrower rows within 1%)
-    for (int ctas = BWD_THREADS / threads; ctas > 0; --ctas) {
-      const int room = (SM_BYTES / ctas - beside - 1024) / row;
-      if (room < R + 2) continue;
-      a.S = R + (room >= R + 8 ? 8 : room >= R + 4 ? 4 : 2);
-      break;
-    }
+    // Otherwise CTAs, as many as the registers have room for, and behind a token's own rows 4, 2 or
+    // none of the next ones, what shared memory has room for (with 8, w_next would lose its place
+    // in L1: 4096 x 7168, K = 2: 119 us instead of 113).  A quarter of the CTAs go for 4 rows where
+    // that is enough (13104 x 2048, K = 8: 3 CTAs 179 us, 4 with 2 rows 194), not more (8192 x
+    // 4096, K = 8: 2 CTAs with 2 rows 225 us, one with 4 264).
+    auto ahead = [&](int ctas) {
+      const int room = (SM_BYTES / ctas - beside - 1024) / row - R;
+      return room >= 4 ? 4 : room >= 2 ? 2 : room >= 0 ? 0 : -1;
+    };
+    int ctas = BWD_THREADS / threads;
+    while (ctas > 1 && ahead(ctas) < 4 && 4 * (ctas - 1) * threads >= 3 * BWD_THREADS) --ctas;
+    if (ahead(ctas) < 4) ctas = BWD_THREADS / threads;
+    while (ctas > 1 && ahead(ctas) < 0) --ctas;
+    a.S = R + ahead(ctas);
   }
   return bwd_v<T, X, HOLD, false>(a, threads, a.S * row + beside, grid, s);
 }
 
 // 16 values a thread up to H = 8192, 32 beyond (32 for 16384 x 2048, K = 6: 291 us instead of
-// 186); a token's rows are held where two more fit beside them (read twice instead: 226 us;
+// 186); a token's rows are held where they fit (read twice instead: 226 us;
 // 4096 x 7168, K = 8: 290 instead of 214)
 template <typename T> int bwd_t(BwdArgs& a, int* grid, cudaStream_t s) {
   constexpr int VPT = 16 / Vec16<T>::N;
   if (a.H > 8192) return bwd_x<T, 32, false>(a, grid, s);
   const long long row = VPT * threads_for(a.H / Vec16<T>::N, VPT) * 16;
-  return (bwd_rows(a) + 2) * row <= RING_BYTES ? bwd_x<T, 16, true>(a, grid, s) : bwd_x<T, 16, false>(a, grid, s);
+  return bwd_rows(a) * row <= RING_BYTES ? bwd_x<T, 16, true>(a, grid, s) : bwd_x<T, 16, false>(a, grid, s);
 }
 
 long long bwd_max_ctas(int T, int H) {
