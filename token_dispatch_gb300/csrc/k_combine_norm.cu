@@ -166,8 +166,10 @@ struct FwdArgs {
 };
 
 // X values of a row for each thread, S rows of ring, CTAS of at most MAXT threads to an SM.
-// Order of a token's rows: its K rows of h, then residual.
-template <typename T, int X, int S, int MAXT, int CTAS>
+// Order of a token's rows: its K rows of h, then residual.  ALL: h, residual, w_post and w_next
+// are there, as in a block (16384 x 512, K = 1 to 3: 19 to 23 us as arguments, 17 to 19 so;
+// 16384 x 1024: 32 to 38, 26 to 37; within 3% from 2048 columns on).
+template <typename T, int X, int S, int MAXT, int CTAS, bool ALL>
 __global__ void __launch_bounds__(MAXT, CTAS) combine_norm_kernel(const FwdArgs a) {
   extern __shared__ uint4 ring[];
   __shared__ unsigned long long src[META * (MAXK + 1)];
@@ -175,7 +177,9 @@ __global__ void __launch_bounds__(MAXT, CTAS) combine_norm_kernel(const FwdArgs 
   __shared__ CtaSum sum;
   constexpr int N = Pairs<T>::N, V = 2 * N, VPT = X / V, P = X / 2;
   constexpr bool HOLD_W = X <= 16;  // the weights fit in registers beside the row
-  const int tid = threadIdx.x, NT = blockDim.x, nvec = a.H / V, K = a.K, R = K + (a.residual ? 1 : 0);
+  const int tid = threadIdx.x, NT = blockDim.x, nvec = a.H / V, K = a.K;
+  const bool residual = ALL || a.residual, post = ALL || a.w_post, next = ALL || a.w_next;
+  const int R = K + (residual ? 1 : 0);
   const long long row_bytes = (long long)a.H * sizeof(T);
   int offset[VPT];
   bool live[VPT];  // columns beside the row read as zeros
@@ -252,13 +256,13 @@ __global__ void __launch_bounds__(MAXT, CTAS) combine_norm_kernel(const FwdArgs 
       }
       next_row();
     }
-    if (a.w_post) {
+    if (post) {
       float2 s = both(0.f);
 #pragma unroll
       for (int i = 0; i < P; ++i) s = __ffma2_rn(z[i], z[i], s);
       f *= rsqrtf(sum.run(s.x + s.y, turn++) * a.inv_h + a.eps);
     }
-    if (a.residual) copies_wait<S - 1>();
+    if (residual) copies_wait<S - 1>();
     float2 s = both(0.f);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
@@ -271,18 +275,18 @@ __global__ void __launch_bounds__(MAXT, CTAS) combine_norm_kernel(const FwdArgs 
       }
 #pragma unroll
       for (int i = 0; i < N; ++i) x[i] = both(0.f);
-      if (a.residual) Pairs<T>::unpack(ring[at + v * NT], x);
+      if (residual) Pairs<T>::unpack(ring[at + v * NT], x);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         x[i] = __ffma2_rn(__fmul2_rn(both(f), z[v * N + i]), p[i], x[i]);
         z[v * N + i] = x[i];
         s = __ffma2_rn(x[i], x[i], s);
       }
-      if (a.y && live[v])
+      if ((ALL || a.y) && live[v])
         *reinterpret_cast<uint4*>(static_cast<char*>(a.y) + t * row_bytes + offset[v]) = Pairs<T>::pack(x);
     }
-    if (a.residual) next_row();
-    if (a.w_next) {
+    if (residual) next_row();
+    if (next) {
       const float q = rsqrtf(sum.run(s.x + s.y, turn++) * a.inv_h + a.eps);
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
@@ -298,7 +302,7 @@ __global__ void __launch_bounds__(MAXT, CTAS) combine_norm_kernel(const FwdArgs 
         if (live[v])
           *reinterpret_cast<uint4*>(static_cast<char*>(a.xn) + t * row_bytes + offset[v]) = Pairs<T>::pack(x);
       }
-    } else if (!a.w_post) {
+    } else if (!post) {
       __syncthreads();  // a token takes one barrier at least: the addresses below are read behind it
     }
     if (tid < R) note(j == 0 ? META - 1 : j - 1, tid, t_ahead, m_row, m_gate);
@@ -691,15 +695,21 @@ template <typename F> int persistent_grid(F kernel, std::atomic<unsigned long lo
   return MOE_OK;
 }
 
-template <typename T, int X, int S, int MAXT, int CTAS> int fwd_v(const FwdArgs& a, cudaStream_t s) {
+template <typename T, int X, int S, int MAXT, int CTAS, bool ALL> int fwd_a(const FwdArgs& a, cudaStream_t s) {
   constexpr int VPT = X / Vec16<T>::N;
   const int threads = threads_for(a.H / Vec16<T>::N, VPT), smem = S * VPT * threads * 16;
   int grid = 0;
   static std::atomic<unsigned long long> known{0};
-  const int st = persistent_grid(combine_norm_kernel<T, X, S, MAXT, CTAS>, known, threads, smem, RING_BYTES, 32, a.T, &grid);
+  const int st = persistent_grid(combine_norm_kernel<T, X, S, MAXT, CTAS, ALL>, known, threads, smem, RING_BYTES, 32, a.T,
+                                 &grid);
   if (st != MOE_OK) return st;
-  combine_norm_kernel<T, X, S, MAXT, CTAS><<<grid, threads, smem, s>>>(a);
+  combine_norm_kernel<T, X, S, MAXT, CTAS, ALL><<<grid, threads, smem, s>>>(a);
   return launch_status();
+}
+
+template <typename T, int X, int S, int MAXT, int CTAS> int fwd_v(const FwdArgs& a, cudaStream_t s) {
+  return a.K > 0 && a.residual && a.w_post && a.w_next ? fwd_a<T, X, S, MAXT, CTAS, true>(a, s)
+                                                       : fwd_a<T, X, S, MAXT, CTAS, false>(a, s);
 }
 
 // 16 values a thread up to H = 8192, where the registers still hold weights beside the row, 32
