@@ -18,8 +18,8 @@
 // bias the logits are compared, which order as the scores do.
 //
 // What bounds it is instructions, not the 50 MB that 32768 x 384 logits are (7.8 us at the
-// rate of a copy): 723 a token there, 64% of the issue slots, 35-38 us with 8 groups, K = 8.
-// 16384 x 64 take 12 us (530 a token), one token 7.2 us, of which a launch is 5-6.  A row
+// rate of a copy): 676 a token there, 63% of the issue slots, 31-36 us with 8 groups, K = 8.
+// 16384 x 64 take 12-13 us (487 a token), one token 7.2 us, of which a launch is 5-6.  A row
 // that needs fp64 takes 2-6 us more of its warp, which shows in calls of one round.
 #include <limits.h>
 #include <math.h>
@@ -246,14 +246,18 @@ __device__ __forceinline__ float gate_value(float l, bool on, bool sigmoid, bool
   return sigmoid || s == 0.f ? s : s * rz;
 }
 
-template <int VMAX>
-__global__ void __launch_bounds__(32 * WARPS, VMAX <= 4 ? 8 : VMAX <= 12 ? 6 : 1)
+// SIGMOID_BIAS: logistic scores with a bias (32768 x 384: 32.9 us with both as arguments, 30.9 so;
+// 16384 x 384: 20.6 and 18.9).  Six CTAs to an SM: 80 registers (131072 x 384 with five 120 us,
+// with six 115; 131072 x 64 with eight 80 us, with six 78).
+template <int VMAX, bool SIGMOID_BIAS>
+__global__ void __launch_bounds__(32 * WARPS, VMAX <= 12 ? 6 : 1)
 gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, const float* __restrict__ bias,
             GateShape p, int32_t* __restrict__ idx, float* __restrict__ gate) {
   __shared__ __align__(16) float cand_c[WARPS][32];
   __shared__ int cand_e[WARPS][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool sigmoid = (p.mode & 0xf) == MOE_GATE_SIGMOID, renorm = p.mode & MOE_GATE_RENORM;
+  const bool sigmoid = SIGMOID_BIAS || (p.mode & 0xf) == MOE_GATE_SIGMOID, renorm = p.mode & MOE_GATE_RENORM;
+  const bool biased = SIGMOID_BIAS || bias;
   const bool group_max = p.mode & MOE_GATE_GROUP_MAX;
   const int g = lane / p.lpg, lig = lane - g * p.lpg;
   const int pos0 = lig * p.vpl;
@@ -281,7 +285,7 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
 
   float b[VMAX], mb = 0.f;
   bool odd = false;  // a bias of +inf; one of -inf or NaN takes its expert out of the choice
-  if (bias) {
+  if (biased) {
     load(bias, 0.f, b);
 #pragma unroll
     for (int j = 0; j < VMAX; ++j) {
@@ -320,9 +324,9 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
     // How far two scores must be apart to be surely in order: the errors of both.  A logistic
     // score s is off by 4u of its exponential and |l| u of that one's argument, both times
     // s (1 - s), and by 3u of the sum and reciprocal: under 6u; then s + b rounds.
-    float margin = bias ? 2.f * U * (8.f + mb) : 0.f;
+    float margin = biased ? 2.f * U * (8.f + mb) : 0.f;
     const bool by_sum = p.KG < p.G && !group_max;
-    if (bias && sigmoid) {
+    if (SIGMOID_BIAS) {
       float zero = 0.f;  // NaN where a score is
 #pragma unroll
       for (int j = 0; j < VMAX; ++j) {
@@ -339,9 +343,9 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
       usual = !__any_sync(FULL, !(m < INFINITY)) && !odd;
       bad = !usual && __any_sync(FULL, m != m);
       // softmax: the row's maximum and sum, where something needs them
-      if (!sigmoid && (bias || !renorm || by_sum)) {
+      if (!sigmoid && (biased || !renorm || by_sum)) {
         m = bad ? __int_as_float(0x7fffffff) : from_key(__reduce_max_sync(FULL, order_key(m)));
-        if (bias || !renorm) {
+        if (biased || !renorm) {
           float z = 0.f;
           if (m > -INFINITY) {
 #pragma unroll
@@ -353,10 +357,10 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
           rz = fast_rcp(z);
         }
       }
-      if (bias) {
+      if (biased) {
         // a softmax score, at most 1/z, by the same of its exponential and quotient and by its sum
         // over vpl values and 5 shuffles
-        if (!sigmoid) margin = 2.f * U * ((22.f + p.vpl) * rz + 1.f + mb);
+        margin = 2.f * U * ((22.f + p.vpl) * rz + 1.f + mb);
 #pragma unroll
         for (int j = 0; j < VMAX; ++j) c[j] = c[j] > -INFINITY && usual ? score(c[j]) + b[j] : -INFINITY;
       } else {
@@ -401,7 +405,7 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
       }
       // a group's rank, and how far two ranks must be apart to be surely in order
       float rank = a1, off = margin + 2.f * Q * fabsf(a1) + LEAST;
-      if (!group_max && bias) {
+      if (!group_max && biased) {
         if (a2 > -INFINITY) {
           rank += a2;
           off += off + 2.f * Q * fabsf(a2) + 4.f * U * fabsf(rank);
@@ -587,7 +591,7 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
         if (in) {
           e = cand_e[warp][lane];
           mine = row[e];
-          v = bias ? score(mine) + __ldg(bias + e) : mine;
+          v = biased ? score(mine) + __ldg(bias + e) : mine;
         }
         cand_c[warp][lane] = v;
         __syncwarp();
@@ -602,7 +606,7 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
         // `close` counts the lane itself and those ahead
         if (__any_sync(FULL, in && ahead < p.K && close > ahead + 1)) {
           double x = mine;
-          if (bias) {
+          if (biased) {
             const Row64 r = row64(row, bias, p.E, sigmoid, m);
             x = in ? r.value(e) : 0.0;
           }
@@ -763,10 +767,11 @@ template <auto KERNEL> int resident_grid(long long T) {
   return (int)(ctas < cap ? ctas : cap);
 }
 
-template <int VMAX>
+template <int VMAX, bool SIGMOID_BIAS>
 void gate_v(float* logits, const float* part, int S, const float* bias, const GateShape& p, int32_t* idx, float* gate,
             cudaStream_t s) {
-  gate_kernel<VMAX><<<resident_grid<gate_kernel<VMAX>>(p.T), 32 * WARPS, 0, s>>>(logits, part, S, bias, p, idx, gate);
+  gate_kernel<VMAX, SIGMOID_BIAS><<<resident_grid<gate_kernel<VMAX, SIGMOID_BIAS>>(p.T), 32 * WARPS, 0, s>>>(
+      logits, part, S, bias, p, idx, gate);
 }
 
 template <int VQ>
@@ -785,8 +790,11 @@ int launch_gate(float* logits, const float* part, int S, const float* bias, int 
   GateShape p{T, E, K, G, KG, E / G, 32 / G, 0, mode, scale};
   p.vpl = (p.gs + p.lpg - 1) / p.lpg;
   if (p.gs % 4 == 0 && p.vpl > 2) p.vpl = (p.vpl + 3) / 4 * 4;  // 16-byte loads
-  // the least instance that holds a lane's experts (32768 x 384 in 12: 33 us, in 16: 44)
-#define MOE_GATE(V) gate_v<V>(logits, part, S, bias, p, idx, gate, s)
+  // the least instance that holds a lane's experts (32768 x 384 in the one of 12: 33 us, of 16: 44)
+  const bool sigmoid_bias = bias && (mode & 0xf) == MOE_GATE_SIGMOID;
+#define MOE_GATE(V)                                                           \
+  (sigmoid_bias ? gate_v<V, true>(logits, part, S, bias, p, idx, gate, s) : \
+                  gate_v<V, false>(logits, part, S, bias, p, idx, gate, s))
   if (p.vpl <= 2) MOE_GATE(2);
   else if (p.vpl <= 4) MOE_GATE(4);
   else if (p.vpl <= 8) MOE_GATE(8);
