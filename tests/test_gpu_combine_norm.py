@@ -338,3 +338,14 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for a, g in zip(alone, got):
         assert torch.equal(a[0], g[0]) and torch.equal(a[1], g[1]) and all(torch.equal(a[2][n], g[2][n]) for n in a[2])
+
+
+@pytest.mark.parametrize("opt", ["all", "post"])
+@pytest.mark.parametrize("size", [("bf16", 1500, 1024, 8), ("bf16", 1000, 2048, 8), ("bf16", 500, 4096, 8), ("bf16", 700, 4096, 2),
+                                  ("bf16", 320, 7168, 11), ("f32", 700, 3000, 5), ("f32", 320, 4096, 6)],
+                         ids=lambda s: "%s_T%d_H%d_K%d" % s if isinstance(s, tuple) else s)
+def test_more_tokens_than_ctas_at_every_depth_of_the_ring(size, opt):
+    """Several tokens to a CTA, with none, 2 and 4 of the next one's rows on their way, and two passes over a token."""
+    c = Case(*size, seed=size[3], **OPTIONS[opt])
+    y, _ = check_forward(c, 1e-5)
+    check_backward(c, 1e-5, y)
