@@ -10,7 +10,7 @@
 // another copied, so the ring needs no barrier; the only ones are those of the
 // reductions, while the copies of the rows behind are under way.
 //
-// Of a copy's 6.77 TB/s: forward 8192 x 7168 bf16, K = 8: 194 us, 0.98; 8192 x 4096, K = 2
+// Of a copy's 6.77 TB/s: forward 8192 x 7168 bf16, K = 8: 195 us, 0.98; 8192 x 4096, K = 2
 // without the norm after the block: 58 us, 0.86 (the launch and the first rows' latency are
 // the rest); backward 16384 x 2048, K = 6: 183 us, 0.87; 8192 x 4096, K = 2: 110 us, 0.72,
 // where the norms' instructions are more of a token (issue slots 61%, 16 warps to an SM).  Seven
@@ -694,7 +694,7 @@ template <typename F> int persistent_grid(F kernel, std::atomic<unsigned long lo
   return MOE_OK;
 }
 
-template <typename T, int X, int S, int MAXT, int CTAS, bool ALL> int fwd_v(const FwdArgs& a, cudaStream_t s) {
+template <typename T, int X, int S, int MAXT, int CTAS, bool ALL> int fwd_a(const FwdArgs& a, cudaStream_t s) {
   constexpr int VPT = X / Vec16<T>::N;
   const int threads = threads_for(a.H / Vec16<T>::N, VPT), smem = S * VPT * threads * 16;
   int grid = 0;
@@ -706,26 +706,30 @@ template <typename T, int X, int S, int MAXT, int CTAS, bool ALL> int fwd_v(cons
   return launch_status();
 }
 
+// A block's whole call has instances of its own: instructions count where K is small (16384 x 512,
+// K = 1 to 3: 17 to 19 us instead of 19 to 23; 16384 x 1024: 26 to 37 instead of 32 to 38; 8192 x
+// 7168, K = 2: 110 instead of 114, K = 8 the same).
+template <typename T, int X, int S, int MAXT, int CTAS> int fwd_v(const FwdArgs& a, cudaStream_t s) {
+  return a.K > 0 && a.residual && a.w_post && a.w_next ? fwd_a<T, X, S, MAXT, CTAS, true>(a, s)
+                                                       : fwd_a<T, X, S, MAXT, CTAS, false>(a, s);
+}
+
 // 16 values a thread up to H = 8192, where the registers still hold weights beside the row, 32
 // beyond (32 for 8192 x 4096, K = 2: 70 us instead of 60; 4096 x 8192: 72 instead of 66).  Rows
 // of up to 8 KB: three CTAs or more to an SM, 8 rows of ring each, so that some stream while
 // others reduce (with 12 rows and as many CTAs as then fit, 16384 x 4096, K = 1: 111 us instead of
 // 98, 11650 x 2880, K = 2: 78 instead of 59; K = 8 is within 3% either way); wider rows: one CTA
-// with 12 rows of up to 16 KB, 6 of up to 32 KB, 3 beyond.  A block's whole call has an instance of
-// its own in the narrow rows, where instructions count (16384 x 512, K = 1 to 3: 17 to 19 us instead
-// of 19 to 23; 16384 x 1024: 26 to 37 instead of 32 to 38; 8192 x 7168, K = 8: 197 instead of 194).
+// with 12 rows of up to 16 KB, 6 of up to 32 KB, 3 beyond.
 template <typename T> int fwd_t(const FwdArgs& a, cudaStream_t s) {
   constexpr bool WIDE = sizeof(T) == 4;
   const int row = a.H * (int)sizeof(T);
-  if (row <= 8192 && a.H <= 4096)
-    return a.K > 0 && a.residual && a.w_post && a.w_next ? fwd_v<T, 16, 8, 256, 3, true>(a, s)
-                                                         : fwd_v<T, 16, 8, 256, 3, false>(a, s);
-  if (row <= 16384 && a.H <= 8192) return fwd_v<T, 16, 12, 512, 1, false>(a, s);
+  if (row <= 8192 && a.H <= 4096) return fwd_v<T, 16, 8, 256, 3>(a, s);
+  if (row <= 16384 && a.H <= 8192) return fwd_v<T, 16, 12, 512, 1>(a, s);
   if constexpr (WIDE) {
-    if (a.H <= 8192) return fwd_v<T, 16, 6, 512, 1, false>(a, s);
-    return fwd_v<T, 32, 3, 512, 1, false>(a, s);
+    if (a.H <= 8192) return fwd_v<T, 16, 6, 512, 1>(a, s);
+    return fwd_v<T, 32, 3, 512, 1>(a, s);
   } else {
-    return fwd_v<T, 32, 6, 512, 1, false>(a, s);
+    return fwd_v<T, 32, 6, 512, 1>(a, s);
   }
 }
 
