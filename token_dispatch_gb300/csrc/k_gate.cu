@@ -448,15 +448,21 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
         stay = mine >= kth && g < p.G;
         kept = __popc(__ballot_sync(FULL, stay && lig == 0));
       }
-      // the lanes at the border know how near the next rank is
+      // Every group tells whether it is as far beyond the border as its own error asks: then each pair
+      // of a kept and a left group is further apart than the larger of its two errors.  Ranks of
+      // -inf, of groups with no expert in service, have none.
       const float border = from_key(kth);
-      const bool near = mine == kth && after != INT_MIN && rank != -INFINITY && !(rank - from_key(after) > off);
+      const bool near = g < p.G && rank != -INFINITY && !(fabsf(rank - (stay ? from_key(after) : border)) > off);
       if (kept != p.KG || !usual || __any_sync(FULL, near)) {
         const float bound = (group_max ? a1 : a2) - 2.f * Q * fabsf(group_max ? a1 : a2) - LEAST - margin;
-        const float slack = fmaxf(off, from_key(__reduce_max_sync(FULL, mine == kth ? order_key(off) : INT_MIN)));
-        // ranks that overflowed have no distance: they are open
-        const bool open = g < p.G && !(fabsf(rank - border) > slack);
-        const bool in = g < p.G && rank - border > slack;
+        // Sure with any group's error: those further above the KG + 1st rank (at most KG can be ahead of
+        // or level with them, themselves among these) and those further below the KG-th (KG are ahead).
+        // Ranks that overflowed have no distance: they are open.
+        const float next = kept > p.KG ? border : from_key(after);
+        const float slack =
+            from_key(__reduce_max_sync(FULL, g < p.G && rank != -INFINITY ? order_key(off) : INT_MIN));
+        const bool in = g < p.G && rank - next > slack;
+        const bool open = g < p.G && !in && !(border - rank > slack);
         // from the values at hand, unless a lane may have more of them
         const bool plain = border > -INFINITY && usual &&
                            !__any_sync(FULL, open && f3 >= bound && f3 > -INFINITY && count > 3);
