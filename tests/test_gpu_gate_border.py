@@ -102,3 +102,22 @@ def test_gate_groups_of_unlike_logits(E, G, KG, sigmoid):
     idx, _ = run_gate(l, 2 * KG, G, KG, sigmoid, None, False, False, 1.0)
     ref = np.sort(np.argsort(-group_ranks(l, None, G, sigmoid), axis=1, kind="stable")[:, :KG], axis=1)
     assert np.array_equal(np.sort(idx // (E // G), axis=1)[:, ::2], ref)
+
+
+@pytest.mark.parametrize("sigmoid", [True, False], ids=["sigmoid", "softmax"])
+@pytest.mark.parametrize("size", SIZES[:6], ids=["E%d_K%d_G%d_%d" % s for s in SIZES[:6]])
+def test_gate_finite_biases_up_to_the_highest_number(size, sigmoid):
+    """Biases that differ far above 1e30 order their groups and experts by what they are."""
+    E, K, G, KG = size
+    rng = np.random.default_rng(E + KG)
+    l = rng.standard_normal((60, E)).astype(np.float32)
+    l[::4, ::3] = -np.inf
+    for values in ([3e30, 0.9e30, 0, 0], [1e29, 2e29, 0.99e30, 1.01e30, -2e30, 0, 0, 0], [3.4e38, 3e38, 2e38, 1e35, -3e38, 0, 0]):
+        for group_max in (False, True):
+            check(l, K, G, KG, sigmoid, rng.choice(values, E), True, group_max)
+    # one expert far above 1e30 in every other group, two below it in the rest
+    b = np.zeros((G, E // G))
+    b[::2, 1] = 3e30
+    b[1::2, :2] = 0.9e30
+    for group_max in (False, True):
+        check(l, K, G, KG, sigmoid, b.ravel(), True, group_max)

@@ -284,14 +284,16 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
   };
 
   float b[VMAX], mb = 0.f;
-  bool odd = false;  // a bias of +inf; one of -inf or NaN takes its expert out of the choice
+  // `odd`: a bias of +inf, or one that the logistic scores' upper bound of 1e30 below would cut; one of
+  // -inf or NaN takes its expert out of the choice
+  bool odd = false;
   if (biased) {
     load(bias, 0.f, b);
 #pragma unroll
     for (int j = 0; j < VMAX; ++j) {
       const bool number = fabsf(b[j]) < INFINITY;
       mb = fmaxf(mb, number ? fabsf(b[j]) : 0.f);
-      odd = odd || b[j] == INFINITY;
+      odd = odd || b[j] >= (SIGMOID_BIAS ? 1e29f : INFINITY);
       if (b[j] != b[j]) b[j] = -INFINITY;
     }
     mb = warp_max(mb);
