@@ -205,7 +205,8 @@ MOE_API int moe_route_group(const void* x, const void* w_router, const float* se
  *   MOE_GATE_SOFTMAX                  d_logits = scale * s (G - <d_gate, s>) over the whole row,
  *                                     G = d_gate at the chosen experts, 0 elsewhere
  *   MOE_GATE_SOFTMAX|MOE_GATE_RENORM  d_logits = scale * q (d_gate - <d_gate, q>)
- *   and 0 elsewhere; an expert listed twice in a row receives the sum of its shares.
+ *   and 0 elsewhere; an expert listed twice in a row receives the sum of its shares.  A NaN logit shows in
+ *   what the formula makes of it: the whole row, or the chosen experts, or its own place alone.
  *   d_gate [T,K], logits [T,E] float; topk_idx [T,K] int32 as moe_gate wrote it (an index
  *   outside [0,E) sets MOE_ERR_DEVICE_BOUNDS and has no share); d_logits [T,E] float out,
  *   apart from logits, every element written.  MOE_GATE_GROUP_MAX is accepted and changes nothing.  Sizes as

@@ -729,7 +729,8 @@ gate_bwd_kernel(const float* __restrict__ d_gate, const float* __restrict__ logi
       }
     }
     const float sum = renorm ? warp_sum(s) : z;
-    const float q = sigmoid && !renorm ? s : sum > 0.f ? s / sum : 0.f;
+    // a sum of 0, where nothing is in service, has no shares; a NaN stays one
+    const float q = sigmoid && !renorm ? s : sum == 0.f ? 0.f : s / sum;
     const float inner = sigmoid && !renorm ? 0.f : warp_sum(dg * q);
     float d = q * (whole ? dg : rest * (dg - inner));
     // an expert listed more than once: its first place takes the sum
@@ -745,7 +746,7 @@ gate_bwd_kernel(const float* __restrict__ d_gate, const float* __restrict__ logi
       first = first && __ffs(same) - 1 == lane;
     }
     if (whole) {
-      const float f = z > 0.f ? -scale * inner / z : 0.f;
+      const float f = z == 0.f ? 0.f : -scale * inner / z;
       if (VQ > 0) {
 #pragma unroll
         for (int q4 = 0; q4 < VQ; ++q4) {
@@ -754,7 +755,7 @@ gate_bwd_kernel(const float* __restrict__ d_gate, const float* __restrict__ logi
             *reinterpret_cast<float4*>(out + i) = make_float4(f * v[q4].x, f * v[q4].y, f * v[q4].z, f * v[q4].w);
         }
       } else {
-        for (int i = lane; i < E; i += 32) out[i] = row[i] == -INFINITY ? 0.f : f * expf(row[i] - m);
+        for (int i = lane; i < E; i += 32) out[i] = f * (row[i] == -INFINITY ? 0.f : expf(row[i] - m));
       }
       d -= q * inner;
     }
