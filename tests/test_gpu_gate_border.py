@@ -3,7 +3,7 @@ scores beside groups of a large and a small one, whose ranks are sums that cance
 import numpy as np
 import pytest
 
-from tests.test_gpu_gate import check, run_gate
+from tests.test_gpu_gate import check, draw, run_gate
 
 pytestmark = pytest.mark.gpu
 
@@ -121,3 +121,12 @@ def test_gate_finite_biases_up_to_the_highest_number(size, sigmoid):
     b[1::2, :2] = 0.9e30
     for group_max in (False, True):
         check(l, K, G, KG, sigmoid, b.ravel(), True, group_max)
+
+
+@pytest.mark.parametrize("kind", ["plain", "ties", "near", "masked"])
+@pytest.mark.parametrize("size", SIZES, ids=["E%d_K%d_G%d_%d" % s for s in SIZES])
+def test_gate_softmax_by_logits_alone(size, kind):
+    """Groups ranked by their largest logit and rescaled gates: nothing asks for the row's maximum or sum, in
+    rows that 64 bits settle neither."""
+    E, K, G, KG = size
+    check(draw(100, E, kind, E + KG), K, G, KG, False, None, True, True)

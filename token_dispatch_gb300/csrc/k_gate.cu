@@ -104,9 +104,11 @@ struct Row64 {  // what a row's 64-bit scores need
   }
 };
 
-__device__ __noinline__ Row64 row64(const float* row, const float* bias, int E, bool sigmoid, float m) {
+// `scored`: scores are asked for, not the logits' order alone (then m is the row's maximum in every lane,
+// and a softmax needs its sum)
+__device__ __noinline__ Row64 row64(const float* row, const float* bias, int E, bool sigmoid, float m, bool scored) {
   Row64 r{row, bias, (double)m, 1.0, sigmoid};
-  if (!sigmoid) {
+  if (!sigmoid && scored) {
     double z = 0;
 #pragma unroll 4
     for (int e = threadIdx.x & 31; e < E; e += 32) z += m == -INFINITY ? 0.0 : exp((double)row[e] - r.m);
@@ -468,7 +470,7 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
         // from the values at hand, unless a lane may have more of them
         const bool plain = border > -INFINITY && usual &&
                            !__any_sync(FULL, open && f3 >= bound && f3 > -INFINITY && count > 3);
-        const Row64 r = row64(row, bias, p.E, sigmoid, m);
+        const Row64 r = row64(row, bias, p.E, sigmoid, m, biased || !group_max);
         stay = plain ? settle_groups64(r, p, g, lig, e0, make_float3(f1, f2, f3), (1u << BITS) - 1, bound, open,
                                        in)
                      : keep_groups64(r, p, g, lig, bound + margin, margin) && g < p.G;
@@ -615,7 +617,7 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
         if (__any_sync(FULL, in && ahead < p.K && close > ahead + 1)) {
           double x = mine;
           if (biased) {
-            const Row64 r = row64(row, bias, p.E, sigmoid, m);
+            const Row64 r = row64(row, bias, p.E, sigmoid, m, true);
             x = in ? r.value(e) : 0.0;
           }
           place = 0;
@@ -630,7 +632,7 @@ gate_kernel(float* __restrict__ logits, const float* __restrict__ part, int S, c
         const unsigned who = __ballot_sync(FULL, stay && lig == 0);
         unsigned keep = 0;
         for (int o = 0; o < p.G; ++o) keep |= ((who >> (o * p.lpg)) & 1u) << o;
-        e = choose64(row64(row, bias, p.E, sigmoid, m), p, keep);
+        e = choose64(row64(row, bias, p.E, sigmoid, m, biased), p, keep);
         if (lane < p.K) {
           place = lane;
           mine = row[e];
