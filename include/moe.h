@@ -470,7 +470,7 @@ MOE_API int moe_combine_norm_bwd(const void* dy, const void* dxn, const void* h,
  *   by where a lies between powers of two).  A run that holds an infinity or a NaN has
  *   scale 255 and q 0, and is restored as NaN.
  *   x [rows,N] dtype; q [rows,N] int8 out; scale [rows, ceil(N/32)] uint8 out.  N a
- *   multiple of 8 (bf16) or 4 (fp32).
+ *   multiple of 8 (bf16) or 4 (fp32), at most 2^31 - 32.
  */
 MOE_API int moe_ckpt_pack(const void* x, int rows, int N, int dtype, int8_t* q, uint8_t* scale, void* stream);
 

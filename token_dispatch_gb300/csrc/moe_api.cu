@@ -226,7 +226,8 @@ static int check_ckpt(const void* q, const void* scale, int rows, int N, int dty
   if (!valid_dtype(dtype) || rows < 0 || N < 1) return MOE_ERR_INVALID_ARG;
   if (rows > 0 && (!q || !scale)) return MOE_ERR_INVALID_ARG;
   if (!all_aligned({q, scale})) return MOE_ERR_MISALIGNED;
-  return N % vec_elems(dtype) != 0 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+  // columns are 32-bit numbers, up to the end of a row's last run of 32
+  return N % vec_elems(dtype) != 0 || N > 0x7fffffe0 ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
 int moe_ckpt_pack(const void* x, int rows, int N, int dtype, int8_t* q, uint8_t* scale, void* stream) {
