@@ -31,12 +31,22 @@ def _ws(nbytes: int, device):
     return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
+class _Holder:
+    """Which forward the expert tensors xs, act and gu hold, of all layers that share them."""
+
+    def __init__(self):
+        self.forward = None  # none that is known, or one that has not come to its end
+        self.shared = False
+
+
 class MoEBuffers:
     """Device buffers of one MoE layer call (T tokens, H, E, K, Hp).
 
     ``experts``: buffers of another layer of the same sizes, whose xs, act, gu, dh, dxs and FFN
     workspaces serve this one too.  Such layers run one after the other on one stream, and a
-    layer's backward needs an ExpertCheckpoint of its forward unless no other ran between."""
+    layer's backward needs an ExpertCheckpoint of its forward (moe_block_backward) unless no
+    other ran between: moe_forward and moe_block_forward note whose tensors they are, and the
+    backward of a forward that is gone is refused."""
 
     def __init__(self, T, H, E, K, Hp, dtype: str, device, backward: bool = True, train: bool = False,
                  experts: MoEBuffers | None = None):
@@ -52,9 +62,9 @@ class MoEBuffers:
                     backward and not hasattr(e, "dh") or torch.empty(0, device=dev).device != e.xs.device:
                 raise ValueError("MoEBuffers: the buffers to share are of other sizes or another device, or lack a "
                                  "backward's")
-        # which of the layers that share them xs, act and gu hold the forward of
-        self.key = object()
-        self.holder = [None] if experts is None else experts.holder
+        self.forward = object()  # this layer's last forward
+        self.holder = _Holder() if experts is None else experts.holder
+        self.holder.shared = experts is not None
 
         def rows(name, width):
             return torch.empty((R, width), dtype=tdt, device=dev) if experts is None else getattr(experts, name)
@@ -95,6 +105,13 @@ class MoEBuffers:
             self.ws_ffn_bwd = _ws(self.ws_ffn_bwd_bytes, dev) if experts is None else experts.ws_ffn_bwd
 
 
+def _forward_begins(b: MoEBuffers):
+    """A forward of b begins: no other's activations are whole from here on, and an older one's
+    routing in b is gone."""
+    b.holder.forward = None
+    b.forward = object()
+
+
 def moe_forward(b: MoEBuffers, x, w_router, logit_bias, w_gate, w_up, w_down, stream=None,
                 row_scale=None, residual=None, out_row=None, y=None, route_flags=0, fused_gather=None):
     """One MoE forward pass into the buffers of ``b`` (y defaults to ``b.y``);
@@ -107,6 +124,7 @@ def moe_forward(b: MoEBuffers, x, w_router, logit_bias, w_gate, w_up, w_down, st
     T, H, E, K, Hp, dt = b.T, b.H, b.E, b.K, b.Hp, b.cdt
     if fused_gather is None or b.gu is not None:
         fused_gather = False
+    _forward_begins(b)
     L.moe_route_ex(x, w_router, logit_bias, T, H, E, K, dt, route_flags, b.logits, b.idx, b.gate, b.ws_route,
                    b.ws_route_bytes, stream=stream)
     L.moe_dispatch(x, b.idx, T, H, E, K, dt, b.cu, b.dst_row, b.src_tok, None if fused_gather else b.xs,
@@ -117,6 +135,7 @@ def moe_forward(b: MoEBuffers, x, w_router, logit_bias, w_gate, w_up, w_down, st
     else:
         L.moe_expert_ffn_ex(b.xs, b.cu, T * K, w_gate, w_up, w_down, E, H, Hp, dt, b.act, b.gu, b.h,
                             b.ws_ffn, b.ws_ffn_bytes, stream=stream)
+    b.holder.forward = b.forward
     L.moe_combine(b.h, b.gate, b.dst_row, row_scale, residual, out_row, T, H, K, dt,
                   b.y if y is None else y, stream=stream)
 
@@ -135,8 +154,11 @@ def moe_backward(b: MoEBuffers, x, w_router, dy, dxs, stream=None, row_scale=Non
 
 def moe_train_backward(b: MoEBuffers, x, w_router, w_gate, w_up, w_down, dy, stream=None, route_flags=0):
     """Full backward of the layer (buffers made with train=True, forward run
-    with them): dh and d_gate, the expert backward (dxs and the three weight
-    gradients), dx = sum_k dxs[row(t,k)] plus the router's share, dw_router."""
+    with them, and the last one in them where layers share expert tensors): dh and
+    d_gate, the expert backward (dxs and the three weight gradients), dx = sum_k
+    dxs[row(t,k)] plus the router's share, dw_router."""
+    if b.holder.shared and b.holder.forward is not b.forward:
+        raise ValueError("moe_train_backward: the layer's forward must be the last one in the expert tensors it shares")
     T, H, E, K, Hp, dt = b.T, b.H, b.E, b.K, b.Hp, b.cdt
     L.moe_permute_bwd(dy, b.h, b.gate, b.dst_row, None, None, None, T, H, K, dt, b.dh, b.d_gate, None, None,
                       stream=stream)
@@ -221,14 +243,18 @@ class ExpertCheckpoint:
         self.xs_scale = torch.empty((R, (b.H + 31) // 32), dtype=torch.uint8, device=dev)
 
     def save(self, b: MoEBuffers, stream=None):
+        if b.holder.shared and b.holder.forward is not b.forward:
+            raise ValueError("ExpertCheckpoint: the expert tensors hold another layer's forward")
         R = b.T * b.K
         L.moe_ckpt_pack(b.gu, R, 2 * b.Hp, b.cdt, self.gu, self.gu_scale, stream=stream)
         L.moe_ckpt_pack(b.xs, R, b.H, b.cdt, self.xs, self.xs_scale, stream=stream)
 
     def restore(self, b: MoEBuffers, stream=None):
         R = b.T * b.K
+        b.holder.forward = None
         L.moe_ckpt_swiglu(self.gu, self.gu_scale, R, b.Hp, b.cdt, b.gu, b.act, stream=stream)
         L.moe_ckpt_unpack(self.xs, self.xs_scale, R, b.H, b.cdt, b.xs, stream=stream)
+        b.holder.forward = b.forward
 
 
 class MoEBlockBuffers:
@@ -240,6 +266,7 @@ class MoEBlockBuffers:
     def __init__(self, T, H, E, K, Hp, dtype: str, device, train: bool = False, experts: MoEBuffers | None = None):
         tdt, f32 = _TDT[dtype], torch.float32
         self.moe = MoEBuffers(T, H, E, K, Hp, dtype, device, backward=train, train=train, experts=experts)
+        self.forward = self.moe.forward  # the block's last forward
         self.x0, self.y, self.xn = (torch.empty((T, H), dtype=tdt, device=device) for _ in range(3))
         if train:
             self.d_x = torch.empty((T, H), dtype=tdt, device=device)
@@ -260,6 +287,8 @@ def moe_block_forward(m: MoEBlockBuffers, x, w_pre, w_router, sel_bias, gate: Gr
     activations there, so that blocks which share m.moe's may run before the backward."""
     b = m.moe
     T, H, E, K, Hp, dt = b.T, b.H, b.E, b.K, b.Hp, b.cdt
+    _forward_begins(b)
+    m.forward = b.forward
     if x0 is None:
         x0 = m.x0
         L.moe_combine_norm(None, None, None, None, x, None, None, w_pre, eps, T, H, 0, dt, None, x0, stream=stream)
@@ -269,7 +298,7 @@ def moe_block_forward(m: MoEBlockBuffers, x, w_pre, w_router, sel_bias, gate: Gr
                    stream=stream)
     L.moe_expert_ffn_ex(b.xs, b.cu, T * K, w_gate, w_up, w_down, E, H, Hp, dt, b.act, b.gu, b.h, b.ws_ffn,
                         b.ws_ffn_bytes, stream=stream)
-    b.holder[0] = b.key
+    b.holder.forward = b.forward
     if ckpt is not None:
         ckpt.save(b, stream=stream)
     L.moe_combine_norm(b.h, b.gate, b.dst_row, None, x, w_post, res_scale, w_next, eps, T, H, K, dt, m.y,
@@ -285,7 +314,9 @@ def moe_block_backward(m: MoEBlockBuffers, x, w_pre, w_router, gate: GroupGate, 
     given (the norm belongs to the block before) m.d_x holds the residual's share alone and
     m.moe.dx = dL/dx0."""
     b = m.moe
-    if ckpt is None and b.holder[0] is not b.key:
+    if m.forward is not b.forward:
+        raise ValueError("moe_block_backward: another forward has run in the block's buffers")
+    if ckpt is None and b.holder.forward is not b.forward:
         raise ValueError("moe_block_backward: without ckpt the block's forward must be the last one in its buffers")
     T, H, E, K, Hp, dt = b.T, b.H, b.E, b.K, b.Hp, b.cdt
     L.moe_combine_norm_bwd(dy, dxn, b.h, b.gate, b.dst_row, None, None if w_next is None else m.y, w_post, res_scale,
@@ -294,7 +325,6 @@ def moe_block_backward(m: MoEBlockBuffers, x, w_pre, w_router, gate: GroupGate, 
                            None if w_next is None else m.dw_next, m.ws_norm, m.ws_norm_bytes, stream=stream)
     if ckpt is not None:
         ckpt.restore(b, stream=stream)
-        b.holder[0] = b.key
     L.moe_expert_ffn_bwd(b.xs, b.cu, T * K, w_gate, w_up, w_down, E, H, Hp, dt, b.gu, b.act, b.dh, b.dxs,
                          b.dw_gate, b.dw_up, b.dw_down, b.ws_ffn_bwd, b.ws_ffn_bwd_bytes, stream=stream)
     L.moe_permute_bwd(None, None, b.gate, b.dst_row, None, None, b.dxs, T, H, K, dt, None, None, None, b.dx,
