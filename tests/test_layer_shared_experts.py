@@ -1,5 +1,5 @@
-"""Whose activations the shared expert tensors hold: a backward of a forward that is gone is refused before anything
-is launched.  The library's calls are stood in for; CPU only."""
+"""Whose activations the shared expert tensors hold: a backward of a forward that is gone, and a checkpoint that
+holds another one or none, are refused before anything is launched.  The library's calls are stood in for; CPU only."""
 import pytest
 
 from token_dispatch_gb300 import _lib as L
@@ -96,6 +96,23 @@ def test_layer_and_block_on_shared_tensors(calls):
     refused(calls, block_backward, block, ckpt=ck)
 
 
+def test_checkpoints_of_nothing_and_of_another_forward(calls):
+    one = layer.MoEBlockBuffers(*SIZE, train=True)
+    two = layer.MoEBlockBuffers(*SIZE, train=True, experts=one.moe)
+    a, b = layer.ExpertCheckpoint(one.moe), layer.ExpertCheckpoint(two.moe)
+    block_forward(one)
+    refused(calls, a.restore, one.moe)  # never saved
+    refused(calls, block_backward, one, ckpt=a)
+    block_forward(one, ckpt=a)
+    block_forward(two, ckpt=b)
+    refused(calls, block_backward, one, ckpt=b)
+    block_backward(two, ckpt=b)
+    block_backward(one, ckpt=a)
+    block_forward(one)  # a second batch, not saved
+    refused(calls, block_backward, one, ckpt=a)
+    block_backward(one)
+
+
 @pytest.mark.parametrize("at", ["moe_route_group", "moe_dispatch", "moe_expert_ffn_ex"])
 def test_a_forward_that_ended_early(calls, at):
     one = layer.MoEBlockBuffers(*SIZE, train=True)
@@ -107,3 +124,21 @@ def test_a_forward_that_ended_early(calls, at):
     calls.fails = None
     refused(calls, block_backward, one)
     refused(calls, block_backward, two)
+
+
+def test_a_checkpoint_that_was_not_finished(calls):
+    one = layer.MoEBlockBuffers(*SIZE, train=True)
+    ck = layer.ExpertCheckpoint(one.moe)
+    block_forward(one, ckpt=ck)
+    calls.fails = "moe_ckpt_pack"
+    with pytest.raises(L.MoEError):
+        block_forward(one, ckpt=ck)
+    calls.fails = None
+    refused(calls, block_backward, one, ckpt=ck)
+    block_forward(one, ckpt=ck)
+    calls.fails = "moe_ckpt_unpack"
+    with pytest.raises(L.MoEError):
+        block_backward(one, ckpt=ck)
+    calls.fails = None
+    refused(calls, block_backward, one)
+    block_backward(one, ckpt=ck)

@@ -231,11 +231,13 @@ class ExpertCheckpoint:
     """What the expert FFN's backward reads of the forward, in 8 bits: the dispatched rows and
     [g | u] (moe_ckpt_pack), 1.03 bytes a value instead of 2.  act is computed again.  One for
     each layer, so that layers whose buffers share these tensors (MoEBuffers(experts=...)) can
-    save from them and restore into them; what else a backward reads, each layer keeps."""
+    save from them and restore into them; what else a backward reads, each layer keeps.  It
+    serves the backward of the forward that it was saved from."""
 
     def __init__(self, b: MoEBuffers):
         if b.gu is None:
             raise ValueError("ExpertCheckpoint: the buffers were made without train=True")
+        self.forward = None  # the forward that it holds
         dev, R = b.gu.device, b.T * b.K
         self.gu = torch.empty((R, 2 * b.Hp), dtype=torch.int8, device=dev)
         self.gu_scale = torch.empty((R, (2 * b.Hp + 31) // 32), dtype=torch.uint8, device=dev)
@@ -246,15 +248,19 @@ class ExpertCheckpoint:
         if b.holder.shared and b.holder.forward is not b.forward:
             raise ValueError("ExpertCheckpoint: the expert tensors hold another layer's forward")
         R = b.T * b.K
+        self.forward = None
         L.moe_ckpt_pack(b.gu, R, 2 * b.Hp, b.cdt, self.gu, self.gu_scale, stream=stream)
         L.moe_ckpt_pack(b.xs, R, b.H, b.cdt, self.xs, self.xs_scale, stream=stream)
+        self.forward = b.forward
 
     def restore(self, b: MoEBuffers, stream=None):
+        if self.forward is None:
+            raise ValueError("ExpertCheckpoint: nothing has been saved")
         R = b.T * b.K
         b.holder.forward = None
         L.moe_ckpt_swiglu(self.gu, self.gu_scale, R, b.Hp, b.cdt, b.gu, b.act, stream=stream)
         L.moe_ckpt_unpack(self.xs, self.xs_scale, R, b.H, b.cdt, b.xs, stream=stream)
-        b.holder.forward = b.forward
+        b.holder.forward = self.forward
 
 
 class MoEBlockBuffers:
@@ -318,6 +324,8 @@ def moe_block_backward(m: MoEBlockBuffers, x, w_pre, w_router, gate: GroupGate, 
         raise ValueError("moe_block_backward: another forward has run in the block's buffers")
     if ckpt is None and b.holder.forward is not b.forward:
         raise ValueError("moe_block_backward: without ckpt the block's forward must be the last one in its buffers")
+    if ckpt is not None and ckpt.forward is not b.forward:
+        raise ValueError("moe_block_backward: ckpt does not hold the block's last forward")
     T, H, E, K, Hp, dt = b.T, b.H, b.E, b.K, b.Hp, b.cdt
     L.moe_combine_norm_bwd(dy, dxn, b.h, b.gate, b.dst_row, None, None if w_next is None else m.y, w_post, res_scale,
                            w_next, eps, T, H, K, dt, m.d_x, b.dh, b.d_gate, None,
