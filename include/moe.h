@@ -466,9 +466,10 @@ MOE_API int moe_combine_norm_bwd(const void* dy, const void* dxn, const void* h,
  *   Every run of 32 neighbours of a row (the last one of a row may be shorter) shares one
  *   power of two: with a = max |x| of the run, e = the least integer >= -126 with
  *   a <= 127 * 2^e, scale[row, run] = e + 127, q = x / 2^e rounded to the nearest integer,
- *   halves to even.  A value is off by at most 2^(e-1), at most a / 127 (a / 254 to a / 127
- *   by where a lies between powers of two).  A run that holds an infinity or a NaN has
- *   scale 255 and q 0, and is restored as NaN.
+ *   halves to even.  A value is off by at most 2^(e-1): where a > 127 * 2^-127, so that e follows
+ *   a, at most a / 127 (a / 254 to a / 127 by where a lies between powers of two); in smaller
+ *   runs 2^-127, whatever a.  A run that holds an infinity or a NaN has scale 255 and q 0, and is
+ *   restored as NaN.
  *   x [rows,N] dtype; q [rows,N] int8 out; scale [rows, ceil(N/32)] uint8 out.  N a
  *   multiple of 8 (bf16) or 4 (fp32), at most 2^31 - 32.
  */
