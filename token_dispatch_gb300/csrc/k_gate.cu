@@ -18,8 +18,9 @@
 // bias the logits are compared, which order as the scores do.
 //
 // What bounds it is instructions, not the 50 MB that 32768 x 384 logits are (7.8 us at the
-// rate of a copy): 676 a token there, 63% of the issue slots, 31-36 us with 8 groups, K = 8.
-// 16384 x 64 take 12-13 us (487 a token), one token 7.2 us, of which a launch is 5-6.  A row
+// rate of a copy): 677 a token there, 63% of the issue slots, 35 us with 8 groups, K = 8 (31 with
+// logits that L2 holds; without groups 29.5, 559 a token).  16384 x 64 take 12.3 us (489 a token;
+// without groups 10.4), one token 7.2 us, of which a launch is 5-6.  A row
 // that needs fp64 takes 2-6 us more of its warp, which shows in calls of one round.
 #include <limits.h>
 #include <math.h>
@@ -248,8 +249,8 @@ __device__ __forceinline__ float gate_value(float l, bool on, bool sigmoid, bool
   return sigmoid || s == 0.f ? s : s * rz;
 }
 
-// SIGMOID_BIAS: logistic scores with a bias (32768 x 384: 32.9 us with both as arguments, 30.9 so;
-// 16384 x 384: 20.6 and 18.9).  Six CTAs to an SM: 80 registers (131072 x 384 with five 120 us,
+// SIGMOID_BIAS: logistic scores with a bias (one set of logits, held by L2: 32768 x 384 32.9 us with both
+// as arguments, 30.9 so; 16384 x 384 20.6 and 18.9).  Six CTAs to an SM: 80 registers (131072 x 384 with five 120 us,
 // with six 115; 131072 x 64 with eight 80 us, with six 78).
 template <int VMAX, bool SIGMOID_BIAS>
 __global__ void __launch_bounds__(32 * WARPS, VMAX <= 12 ? 6 : 1)
@@ -801,7 +802,8 @@ int launch_gate(float* logits, const float* part, int S, const float* bias, int 
   GateShape p{T, E, K, G, KG, E / G, 32 / G, 0, mode, scale};
   p.vpl = (p.gs + p.lpg - 1) / p.lpg;
   if (p.gs % 4 == 0 && p.vpl > 2) p.vpl = (p.vpl + 3) / 4 * 4;  // 16-byte loads
-  // the least instance that holds a lane's experts (32768 x 384 in the one of 12: 33 us, of 16: 44)
+  // the least instance that holds a lane's experts (32768 x 384 in the one of 12: 33 us, of 16: 44).  Lanes
+  // of 17 to 32 share one: 16384 x 640 in 8 groups (20 of a lane) 33 us, x 1024 (32) 36
   const bool sigmoid_bias = bias && (mode & 0xf) == MOE_GATE_SIGMOID;
 #define MOE_GATE(V)                                                           \
   (sigmoid_bias ? gate_v<V, true>(logits, part, S, bias, p, idx, gate, s) : \

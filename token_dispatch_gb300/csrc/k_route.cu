@@ -734,8 +734,10 @@ int launch_router_dx_tc(const void* dl3, const void* w, int T, int H, int E, boo
 
 // The tensor-core router backward serves bf16 layers whose W_r rows are
 // 16-byte multiples (E % 8 == 0) and whose dx rows tile by 64 columns.
-// A given logit gradient of 8 or 16 experts stays on FFMA: the streaming passes
-// that serve these counts form the gradient themselves.
+// A given logit gradient of fewer than 32 experts stays on FFMA: the streaming
+// passes that serve 8 and 16 form the gradient themselves (8192 x 4096: 80 and 138
+// us, where they take 42 and 45), and 24 go with them (191 us; 54 where the
+// gradient is formed here; 32 experts, on the tensor cores: 47).
 static bool route_bwd_on_tensor_cores(int mode, int dtype, int H, int E) {
   if (mode == MOE_ROUTE_LOGIT_GRAD && E < 32) return false;
   return mode != MOE_ROUTE_MOD_LINEAR && dtype == MOE_BF16 && E % 8 == 0 && H % 64 == 0;
