@@ -46,7 +46,8 @@ class MoEBuffers:
     workspaces serve this one too.  Such layers run one after the other on one stream, and a
     layer's backward needs an ExpertCheckpoint of its forward (moe_block_backward) unless no
     other ran between: moe_forward and moe_block_forward note whose tensors they are, and the
-    backward of a forward that is gone is refused."""
+    backward of a forward that is gone is refused.  A captured graph notes that at its capture
+    alone: such graphs are replayed in the order of their captures."""
 
     def __init__(self, T, H, E, K, Hp, dtype: str, device, backward: bool = True, train: bool = False,
                  experts: MoEBuffers | None = None):
