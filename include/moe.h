@@ -65,7 +65,8 @@ typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
 
 /* operation ids for moe_workspace_bytes */
 enum { MOE_OP_ROUTE = 0, MOE_OP_DISPATCH = 1, MOE_OP_EXPERT_FFN = 2, MOE_OP_ROUTE_BWD = 3, MOE_OP_MOD_SELECT = 4,
-       MOE_OP_EXPERT_FFN_BWD = 5, MOE_OP_COMBINE_NORM_BWD = 6 };
+       MOE_OP_EXPERT_FFN_BWD = 5, MOE_OP_COMBINE_NORM_BWD = 6, MOE_OP_EXPERT_FFN_W4 = 7, MOE_OP_ORTHOGONALIZE = 8,
+       MOE_OP_MUON_STEP = 9 };
 
 /* moe_gate modes: the score function, and bits that may be or-ed in */
 enum { MOE_GATE_SOFTMAX = 0, MOE_GATE_SIGMOID = 1, MOE_GATE_RENORM = 0x10, MOE_GATE_GROUP_MAX = 0x20 };
@@ -489,6 +490,95 @@ MOE_API int moe_ckpt_unpack(const int8_t* q, const uint8_t* scale, int rows, int
  */
 MOE_API int moe_ckpt_swiglu(const int8_t* q, const uint8_t* scale, int rows, int Hp, int dtype, void* gu, void* act,
               void* stream);
+
+/*
+ * Expert weights in 4 bits with group scales
+ *
+ *   w [E, rows, cols] dtype, one of the expert tensors.  `axis` is the one that its product
+ *   sums over: 0 (rows; w_gate and w_up, [E, H, H']) or 1 (cols; w_down).  With in = the size
+ *   of that axis, out = the other one's, and B = ceil(in / 128) blocks:
+ *     every `group` (32, 64 or 128) neighbours along `axis` of one output share a scale;
+ *     with a = max |w| of the group, s = the least number of 5 significant bits >= a / 7 (the
+ *     quotient rounded to fp32), at least 2^-126; code = w / s (in fp32) rounded to the nearest
+ *     integer, halves to even: -7..7.  code * s has at most 8 significant bits and is exact in
+ *     bf16.  A value is off by at most s / 2, and s < 17/16 * a / 7 where that is above 2^-126.
+ *     A group that holds a NaN, an infinity or a magnitude of 2^127 or more has the scale NaN
+ *     and is restored as NaN.
+ *   q     [E, out, B * 16] 32-bit words, 8 codes (as code + 8) in each: inputs 128 b + 32 j + 8 v
+ *         .. + 7 (0 <= j, v < 4) are word 16 b + 4 v + j, input i of them in bits 4 (i / 2) + 16 (i % 2)
+ *   scale [E, out, B * 128 / group] bf16
+ *   Inputs past `in` (the last block's rest) are written as zeros.  E * rows * cols may pass
+ *   2^31.  rows and cols multiples of 8 (bf16) or 4 (fp32), at most 2^23; E <= 65535.  q and scale
+ *   of tensors made elsewhere may hold any codes (-8 too) and any finite bf16 scales.
+ */
+MOE_API int moe_w4_pack(const void* w, int E, int rows, int cols, int axis, int group, int dtype, uint32_t* q,
+              void* scale, void* stream);
+
+/* w = code * s: the weights that the packed form stands for (arguments as moe_w4_pack). */
+MOE_API int moe_w4_unpack(const uint32_t* q, const void* scale, int E, int rows, int cols, int axis, int group, int dtype,
+              void* w, void* stream);
+
+/*
+ * Expert FFN with weights of 4 bits
+ *
+ *   act[r,:] = silu(xs[r,:] Wg[e]) * (xs[r,:] Wu[e]),  h[r,:] = act[r,:] Wd[e]^T
+ *   for row r of expert e, as moe_expert_ffn, with the three tensors as moe_w4_pack makes them:
+ *   q_gate, s_gate and q_up, s_up of [E,H,Hp] with axis 0, q_down, s_down of [E,H,Hp] with axis 1,
+ *   all with the same `group`.
+ *   x, src_tok: the routed rows, as in moe_expert_ffn_gather (row r reads x[src_tok[r],:], x [T,H]);
+ *   src_tok NULL: x is xs [rows,H], as in moe_expert_ffn, and T is not used.  An entry of src_tok
+ *   outside [0,T) sets MOE_ERR_DEVICE_BOUNDS and counts as a row of zeros; so does a cu_seqlens that
+ *   does not run from 0 to rows, whose offsets are read as if cut off there (rows of no expert are left).
+ *   act [rows,Hp], h [rows,H] dtype out.  Products are fp32 sums of bf16 rows and exact weights; act
+ *   is rounded to dtype before the second product.  For few rows: each expert with rows has its
+ *   weights read once for up to 64 of them.
+ *   dtype MOE_BF16; H and Hp multiples of 8; E <= 1024.  Workspace:
+ *   moe_workspace_bytes(MOE_OP_EXPERT_FFN_W4, T, H, E, K, Hp) bytes for rows = T * K (0: NULL).  Calls
+ *   that may run at the same time need distinct workspaces.
+ */
+MOE_API int moe_expert_ffn_w4(const void* x, const int32_t* src_tok, int T, const int32_t* cu_seqlens, int rows,
+              const uint32_t* q_gate, const void* s_gate, const uint32_t* q_up, const void* s_up, const uint32_t* q_down,
+              const void* s_down, int E, int H, int Hp, int group, int dtype, void* act, void* h, void* ws,
+              size_t ws_bytes, void* stream);
+
+/*
+ * Orthogonalised matrices by Newton-Schulz products
+ *
+ *   For each of E matrices U = x[e] [M,N]:  X = U / (|U|_F + eps), then `steps` times
+ *     X <- a X + b (X X^T) X + c (X X^T)^2 X
+ *   (computed on the shorter side).  With the Muon optimiser's coefficients (3.4445, -4.7750,
+ *   2.0315) and 5 steps the singular values that are not far below the largest come to about 1.
+ *   x [E,M,N] dtype; out [E,M,N] bf16 (dtype names x's type).  out may not overlap x.
+ *   The products' operands are fp16 (2^10 times X, which is below 2 there for such coefficients)
+ *   with fp32 sums, the diagonals of X X^T and of the polynomial fp32: for matrices of noise with
+ *   some directions that stand out the result is within about 2e-3 of exact arithmetic (2-norm, relative).
+ *   What is far below x's root mean square singular value (some 2^-11 of it) is not resolved: such
+ *   directions come out small, not as in exact arithmetic.
+ *   The norm neither over- nor underflows.  A matrix of zeros gives zeros; one that holds a NaN or
+ *   an infinity gives NaN; the others of the batch are not touched by it.
+ *   1 <= steps <= 64; a, b, c finite; eps >= 0, finite; 1 <= M, N <= 65536; E <= 65535.  Any M and N.
+ *   Workspace: moe_workspace_bytes(MOE_OP_ORTHOGONALIZE, 0, M, E, 0, N) bytes, about 4 to 8 bytes
+ *   for each element of x.  Calls that may run at the same time need distinct workspaces.
+ */
+MOE_API int moe_orthogonalize(const void* x, int E, int M, int N, int dtype, int steps, float a, float b, float c,
+              float eps, void* out, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Momentum step with an orthogonalised update, on an expert tensor
+ *
+ *   m_out = beta m + dw
+ *   u     = m_out, or with nesterov dw + beta m_out
+ *   O     = moe_orthogonalize of u (steps, a, b, c, eps), not rounded
+ *   w_out = (1 - lr weight_decay) w - lr scale O
+ *   w, w_out [E,M,N] dtype; dw, m, m_out [E,M,N] float (dw as moe_expert_ffn_bwd writes it);
+ *   w_low [E,M,N] bf16, nullable: w_out rounded to bf16 (with dtype MOE_F32, for weights kept in
+ *   fp32 that the products read in bf16).  w_out may be w, m_out may be m; no other overlap.
+ *   0 <= beta < 1; lr, weight_decay, scale finite; nesterov 0 or 1; the rest, the workspace
+ *   (MOE_OP_MUON_STEP) and the accuracy of O as moe_orthogonalize.  Sums are fp32.
+ */
+MOE_API int moe_muon_step(const void* w, const float* dw, const float* m, int E, int M, int N, int dtype, float beta,
+              int nesterov, float lr, float weight_decay, float scale, int steps, float a, float b, float c, float eps,
+              void* w_out, void* w_low, float* m_out, void* ws, size_t ws_bytes, void* stream);
 
 /*
  * Mixture-of-Depths capacity router                       [FW, MoD paragraph]

@@ -32,6 +32,9 @@ MOE_OP_ROUTE_BWD = 3
 MOE_OP_MOD_SELECT = 4
 MOE_OP_EXPERT_FFN_BWD = 5
 MOE_OP_COMBINE_NORM_BWD = 6
+MOE_OP_EXPERT_FFN_W4 = 7
+MOE_OP_ORTHOGONALIZE = 8
+MOE_OP_MUON_STEP = 9
 
 MOE_GATE_SOFTMAX = 0
 MOE_GATE_SIGMOID = 1
@@ -52,7 +55,8 @@ EXPORTS = ("moe_status_str", "moe_version", "moe_kernel_launches", "moe_workspac
            "moe_route", "moe_route_ex", "moe_dispatch", "moe_dispatch_noalloc", "moe_expert_ffn",
            "moe_expert_ffn_ex", "moe_expert_ffn_gather", "moe_expert_ffn_bwd", "moe_combine", "moe_route_bwd",
            "moe_permute_bwd", "mod_select", "moe_ep_plan", "moe_gate", "moe_gate_bwd", "moe_route_group",
-           "moe_combine_norm", "moe_combine_norm_bwd", "moe_ckpt_pack", "moe_ckpt_unpack", "moe_ckpt_swiglu")
+           "moe_combine_norm", "moe_combine_norm_bwd", "moe_ckpt_pack", "moe_ckpt_unpack", "moe_ckpt_swiglu",
+           "moe_w4_pack", "moe_w4_unpack", "moe_expert_ffn_w4", "moe_orthogonalize", "moe_muon_step")
 
 
 class MoEError(RuntimeError):
@@ -95,6 +99,11 @@ _SIGS = {
     "moe_ckpt_pack": (_I, [_P, _I, _I, _I, _P, _P, _P]),
     "moe_ckpt_unpack": (_I, [_P, _P, _I, _I, _I, _P, _P]),
     "moe_ckpt_swiglu": (_I, [_P, _P, _I, _I, _I, _P, _P, _P]),
+    "moe_w4_pack": (_I, [_P] + [_I] * 6 + [_P, _P, _P]),
+    "moe_w4_unpack": (_I, [_P, _P] + [_I] * 6 + [_P, _P]),
+    "moe_expert_ffn_w4": (_I, [_P, _P, _I, _P, _I] + [_P] * 6 + [_I] * 5 + [_P, _P, _P, _Z, _P]),
+    "moe_orthogonalize": (_I, [_P] + [_I] * 5 + [_F] * 4 + [_P, _P, _Z, _P]),
+    "moe_muon_step": (_I, [_P] * 3 + [_I] * 4 + [_F, _I, _F, _F, _F, _I] + [_F] * 4 + [_P] * 4 + [_Z, _P]),
     "moe_ep_plan": (_I, [_I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
 }
 
@@ -266,7 +275,7 @@ def mod_select(x, w_mod, B, L, H, C, dtype, score, sel, sel_score, mask, x_sel, 
 
 
 # Tensor arguments of the calls below: names, in the order of the C arguments, and types
-# ("x": the call's dtype).
+# ("x": the call's dtype, "h": bf16, "i": 32-bit words).
 _TENSORS = {
     "moe_gate": "logits:f sel_bias:f topk_idx:i topk_gate:f",
     "moe_gate_bwd": "d_gate:f logits:f topk_idx:i d_logits:f",
@@ -277,6 +286,11 @@ _TENSORS = {
     "moe_ckpt_pack": "x:x q:c scale:b",
     "moe_ckpt_unpack": "q:c scale:b x:x",
     "moe_ckpt_swiglu": "q:c scale:b gu:x act:x",
+    "moe_w4_pack": "w:x q:i scale:h",
+    "moe_w4_unpack": "q:i scale:h w:x",
+    "moe_expert_ffn_w4": "x:x src_tok:i cu_seqlens:i q_gate:i s_gate:h q_up:i s_up:h q_down:i s_down:h act:x h:x ws:b",
+    "moe_orthogonalize": "x:x out:h ws:b",
+    "moe_muon_step": "w:x dw:f m:f w_out:x w_low:h m_out:f ws:b",
 }
 _types = {}  # (call, dtype): the types of its tensors
 _cuda = None
@@ -287,7 +301,7 @@ def _types_of(fn, dtype):
     import torch
     if dtype not in (MOE_F32, MOE_BF16):
         raise MoEError(fn, MOE_ERR_INVALID_ARG, moe_status_str(MOE_ERR_INVALID_ARG))
-    kinds = {"f": torch.float32, "i": torch.int32, "c": torch.int8, "b": torch.uint8,
+    kinds = {"f": torch.float32, "i": torch.int32, "c": torch.int8, "b": torch.uint8, "h": torch.bfloat16,
              "x": torch.bfloat16 if dtype == MOE_BF16 else torch.float32}
     _cuda = torch.cuda
     _types[fn, dtype] = t = tuple(kinds[w.split(":")[1]] for w in _TENSORS[fn].split())
@@ -369,6 +383,51 @@ def moe_ckpt_swiglu(q, scale, rows, Hp, dtype, gu, act, stream=None):
     n, runs = rows * Hp, rows * ((2 * Hp + 31) // 32)
     a = _args("moe_ckpt_swiglu", dtype, (q, scale, gu, act), (2 * n, runs, 2 * n, n))
     _check("moe_ckpt_swiglu", lib().moe_ckpt_swiglu(a[0], a[1], rows, Hp, dtype, a[2], a[3], _stream(stream)))
+
+
+def _w4_sizes(E, out, inp, group):
+    """Words of codes and scales of a packed tensor with `out` outputs of `inp` inputs."""
+    blocks = (inp + 127) // 128
+    return E * out * blocks * 16, E * out * blocks * 128 // group if group > 0 else 0
+
+
+def moe_w4_pack(w, E, rows, cols, axis, group, dtype, q, scale, stream=None):
+    out, inp = (cols, rows) if axis == 0 else (rows, cols)
+    a = _args("moe_w4_pack", dtype, (w, q, scale), (E * rows * cols, *_w4_sizes(E, out, inp, group)))
+    _check("moe_w4_pack", lib().moe_w4_pack(a[0], E, rows, cols, axis, group, dtype, a[1], a[2], _stream(stream)))
+
+
+def moe_w4_unpack(q, scale, E, rows, cols, axis, group, dtype, w, stream=None):
+    out, inp = (cols, rows) if axis == 0 else (rows, cols)
+    a = _args("moe_w4_unpack", dtype, (q, scale, w), (*_w4_sizes(E, out, inp, group), E * rows * cols))
+    _check("moe_w4_unpack", lib().moe_w4_unpack(a[0], a[1], E, rows, cols, axis, group, dtype, a[2], _stream(stream)))
+
+
+def moe_expert_ffn_w4(x, src_tok, T, cu_seqlens, rows, q_gate, s_gate, q_up, s_up, q_down, s_down, E, H, Hp, group,
+                      dtype, act, h, ws=None, ws_bytes=0, stream=None):
+    n_q, n_s = _w4_sizes(E, Hp, H, group)
+    d_q, d_s = _w4_sizes(E, H, Hp, group)
+    a = _args("moe_expert_ffn_w4", dtype,
+              (x, src_tok, cu_seqlens, q_gate, s_gate, q_up, s_up, q_down, s_down, act, h, ws),
+              ((rows if src_tok is None else T) * H, rows, E + 1, n_q, n_s, n_q, n_s, d_q, d_s, rows * Hp, rows * H,
+               ws_bytes))
+    _check("moe_expert_ffn_w4", lib().moe_expert_ffn_w4(a[0], a[1], T, a[2], rows, *a[3:9], E, H, Hp, group, dtype,
+                                                        a[9], a[10], a[11], ws_bytes, _stream(stream)))
+
+
+def moe_orthogonalize(x, E, M, N, dtype, steps, a, b, c, eps, out, ws=None, ws_bytes=0, stream=None):
+    n = E * M * N
+    t = _args("moe_orthogonalize", dtype, (x, out, ws), (n, n, ws_bytes))
+    _check("moe_orthogonalize", lib().moe_orthogonalize(t[0], E, M, N, dtype, steps, a, b, c, eps, t[1], t[2],
+                                                        ws_bytes, _stream(stream)))
+
+
+def moe_muon_step(w, dw, m, E, M, N, dtype, beta, nesterov, lr, weight_decay, scale, steps, a, b, c, eps, w_out, w_low,
+                  m_out, ws=None, ws_bytes=0, stream=None):
+    n = E * M * N
+    t = _args("moe_muon_step", dtype, (w, dw, m, w_out, w_low, m_out, ws), (n, n, n, n, n, n, ws_bytes))
+    _check("moe_muon_step", lib().moe_muon_step(*t[:3], E, M, N, dtype, beta, int(nesterov), lr, weight_decay, scale,
+                                                steps, a, b, c, eps, *t[3:], ws_bytes, _stream(stream)))
 
 
 def moe_ep_plan(R, E, S, K, B, counts):

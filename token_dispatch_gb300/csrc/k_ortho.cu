@@ -1,0 +1,681 @@
+// Orthogonalised updates of weight matrices by Newton-Schulz products, and the
+// momentum step around them.
+//
+// For each matrix U [M, N] of a batch, m = min(M, N), n = max(M, N):
+//   X = U / (|U|_F + eps), transposed where M > N, so that X is [m, n];
+//   `steps` times  A = X X^T,  X <- a X + (b A + c A A) X.
+// A step is three products of matrices on the tensor cores (ns_gemm_kernel):
+//   GRAM   A = X X^T, kept as its diagonal s (fp32) and the rest D
+//   POLY   D D, whose epilogue forms b A + c A A = diag(d) + P:
+//            P_ij = (b + c (s_i + s_j)) D_ij + c (D D)_ij,   i != j
+//            d_i  = a + b s_i + c s_i^2 + c (D D)_ii         (a X taken in)
+//   APPLY  X <- diag(d) X + P X
+// GRAM and POLY are symmetric: the tiles on and above the diagonal are computed, and
+// those above it stored twice.
+//
+// Operands are fp16 with fp32 sums.  Every operand is within a small factor of 1 in size,
+// so fp16's range is enough (X, D and P are held times 2^10: an element of X is about
+// 1 / sqrt(m n) at first) and it keeps 3 bits more than bf16 for the same rate.  What fp16 loses
+// is further made small by keeping the diagonals of A and P in fp32: at the end A is near 1
+// and a + b A + c A A near 0.7 while its terms are near 3.4, -4.8 and 2.0, so a rounding of
+// the diagonal would come back several times larger.  Measured in simulation on noise with a few
+// directions that stand out of it: relative error of the result 0.7 to 1.2e-3, against 1.7 to
+// 2.5e-3 with the diagonals in fp16 and 1.3 to 2.1e-2 in bf16.  Directions of U whose singular
+// value is below some 2^-11 of the root mean square are not resolved (they come out as small noise).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include "tc_ptx.cuh"
+
+namespace moe {
+namespace ns {
+
+using namespace tc;
+
+constexpr int BM = 128;  // rows of a CTA; a pair has 256
+constexpr int BN = 256;
+constexpr int BK = 64;
+constexpr int STAGES = 6;
+constexpr int OPERAND_BYTES = BM * BK * 2;  // A rows of a CTA, and its half of the B columns
+constexpr int STAGE_BYTES = 2 * OPERAND_BYTES;
+constexpr int THREADS = 192;  // producer, MMA issuer, four epilogue warps
+constexpr int STG = 33;       // floats between the rows of an epilogue staging tile
+constexpr float HELD = 1024.f;  // X, D and P are stored times this
+constexpr float INV = 1.f / 1024.f;
+
+enum Mode { GRAM = 0, POLY = 1, APPLY = 2, FINAL = 3 };
+template <int MODE>
+constexpr size_t smem_bytes() {
+  return (size_t)STAGES * STAGE_BYTES + (MODE == FINAL ? 4 * 32 * STG * 4 : 0) + (2 * STAGES + 5) * 8 + 1024;
+}
+
+// Where the last step's result goes: `o` (bf16), or the weights' update
+// w_out = keep * w - step * X (dtype of the weights; w_low: a bf16 copy).
+struct Result {
+  bf16* o = nullptr;
+  const void* w = nullptr;
+  void* w_out = nullptr;
+  bf16* w_low = nullptr;
+  int dtype = MOE_BF16;
+  float keep = 1.f, step = 0.f;
+  bool tall = false;  // X is the transposed matrix
+};
+
+struct Params {
+  int E, m, n;
+  long long ldx, lda;  // elements between rows of X, and of D and P
+  const __half* in;    // POLY: D, APPLY and FINAL: X
+  __half* out;
+  float *s, *d;  // [E][lda]
+  float a, b, c;
+  Result r;
+  unsigned* err;
+  unsigned long long wait_limit;
+};
+
+struct Tile {
+  int e, i, j, row0, n0;
+};
+template <int MODE>
+__host__ __device__ inline int tiles_per_matrix(int m, int n) {
+  const int mt = (m + 255) / 256, nt = (n + 255) / 256;
+  return MODE == GRAM || MODE == POLY ? mt * (mt + 1) / 2 : mt * nt;
+}
+template <int MODE>
+__device__ __forceinline__ Tile tile_of(int t, const Params& p, int per, uint32_t rank) {
+  Tile w;
+  w.e = t / per;
+  const int r = t - w.e * per;
+  if (MODE == GRAM || MODE == POLY) {  // column blocks from the left, i <= j in each
+    int j = (int)((sqrtf(8.f * r + 1.f) - 1.f) * 0.5f);
+    while (j * (j + 1) / 2 > r) --j;
+    while ((j + 1) * (j + 2) / 2 <= r) ++j;
+    w.j = j;
+    w.i = r - j * (j + 1) / 2;
+  } else {
+    const int mt = (p.m + 255) / 256;
+    w.i = r % mt;
+    w.j = r / mt;
+  }
+  w.row0 = w.i * 2 * BM + (int)rank * BM;
+  w.n0 = w.j * BN;
+  return w;
+}
+
+__device__ __forceinline__ void load_row(const __half* src, uint4 (&v)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = reinterpret_cast<const uint4*>(src)[j];
+}
+__device__ __forceinline__ void store_row(__half* dst, const float (&v)[32]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint4 q;
+    __half2* h = reinterpret_cast<__half2*>(&q);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) h[k] = __floats2half2_rn(v[8 * j + 2 * k], v[8 * j + 2 * k + 1]);
+    reinterpret_cast<uint4*>(dst)[j] = q;
+  }
+}
+// 32 columns col0.. of this lane's row as rows of the transposed place: neighbouring lanes swap
+// halves, so that each writes two neighbours of one row
+__device__ __forceinline__ void store_mirrored(__half* plane, long long ld, int row, int col0, int m, int lane,
+                                               const float (&v)[32]) {
+  const int odd = lane & 1, at = row - odd;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const float got = __shfl_xor_sync(0xffffffffu, odd ? v[2 * k] : v[2 * k + 1], 1);
+    const __half2 h = odd ? __floats2half2_rn(got, v[2 * k + 1]) : __floats2half2_rn(v[2 * k], got);
+    const int j = col0 + 2 * k + odd;
+    if (j < m && at < m) *reinterpret_cast<__half2*>(plane + (long long)j * ld + at) = h;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void update_weight(const Result& r, long long at, float y) {
+  const float w = r.keep * to_f32(static_cast<const T*>(r.w)[at]) - r.step * y;
+  static_cast<T*>(r.w_out)[at] = from_f32<T>(w);
+  if (r.w_low) r.w_low[at] = __float2bfloat16_rn(w);
+}
+__device__ __forceinline__ void put_result(const Result& r, long long at, float y) {
+  if (r.o) r.o[at] = __float2bfloat16_rn(y);
+  else if (r.dtype == MOE_BF16) update_weight<bf16>(r, at, y);
+  else update_weight<float>(r, at, y);
+}
+
+// The products on pairs of SMs: 256 x 256 tiles by the two-CTA MMA, TMA operands in a ring of
+// six stages, two accumulators in tensor memory so that the epilogue of a tile runs under the
+// next one's products.  Barriers as in the expert products' pair kernel: `full` the leader's
+// (both CTAs' bytes), `empty` and `accf` each CTA's own, `acce` the leader's.  All waits are bounded.
+template <int MODE>
+__global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
+ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Params p) {
+  constexpr bool SYM = MODE == GRAM || MODE == POLY;
+  constexpr bool B_MN = !SYM;  // X [K = m][N = n] with its columns together
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* stage_out = reinterpret_cast<float*>(smem + STAGES * STAGE_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES + (MODE == FINAL ? 4 * 32 * STG * 4 : 0));
+  __shared__ uint32_t tmem_base_slot;
+  __shared__ int abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+  const int per = tiles_per_matrix<MODE>(p.m, p.n);
+  const int total = p.E * per;
+  const int K = MODE == GRAM ? p.n : p.m;
+  const int cols = SYM ? p.m : p.n;
+  const int kbs = (K + BK - 1) / BK;
+
+  auto full_bar = [&](int s) { return smem_u32(&bars[s]); };
+  auto empty_bar = [&](int s) { return smem_u32(&bars[STAGES + s]); };
+  auto accf_bar = [&](int a) { return smem_u32(&bars[2 * STAGES + a]); };
+  auto acce_bar = [&](int a) { return smem_u32(&bars[2 * STAGES + 2 + a]); };
+  const uint32_t drain_bar = smem_u32(&bars[2 * STAGES + 4]);
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(accf_bar(a), 1);
+      mbar_init(acce_bar(a), 2 * 128);  // the epilogue threads of both CTAs
+    }
+    mbar_init(drain_bar, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    prefetch_tmap(&tmA);
+    prefetch_tmap(&tmB);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base_slot)),
+                 "r"(2u * BN));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the peer's barriers are initialised before anything arrives on them
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_base_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int filled[STAGES];
+      for (int s = 0; s < STAGES; ++s) filled[s] = -1;
+      bool ok = true;
+      for (int t = pair; ok && t < total; t += n_pairs) {
+        const Tile w = tile_of<MODE>(t, p, per, rank);
+        const int b0 = w.n0 + (int)rank * (BN / 2);
+        for (int kb = 0; kb < kbs; ++kb) {
+          if (!wait_bounded(empty_bar(stage), phase ^ 1u, &abort_flag, p)) { ok = false; break; }
+          const uint32_t a_dst = smem_u32(smem + stage * STAGE_BYTES), b_dst = a_dst + OPERAND_BYTES;
+          if (leader) {
+            mbar_expect_tx(full_bar(stage), 2 * STAGE_BYTES);
+            filled[stage] = (int)phase;
+          }
+          const uint32_t fb = cluster_addr(full_bar(stage), 0);
+          tma_load_3d_pair(a_dst, &tmA, fb, kb * BK, w.row0, w.e);
+          if (B_MN) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              tma_load_3d_pair(b_dst + c * (64 * BK * 2), &tmB, fb, b0 + c * 64, kb * BK, w.e);
+          } else {
+            tma_load_3d_pair(b_dst, &tmB, fb, kb * BK, b0, w.e);
+          }
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+      }
+      if (leader) {  // every stage filled must have landed, both CTAs' bytes
+        for (int s = 0; s < STAGES; ++s) {
+          if (filled[s] < 0) continue;
+          const long long t0 = clock64();
+          while (!mbar_try_wait(full_bar(s), (uint32_t)filled[s])) {
+            if ((unsigned long long)(clock64() - t0) > DRAIN_LIMIT) { set_error(p.err, DEV_TIMEOUT); break; }
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------- MMA issuer (leader only)
+    if (leader && lane == 0) {
+      constexpr uint32_t IDESC = instr_desc(2 * BM, BN, false, B_MN, true);
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true, issued = false;
+      int i = 0;
+      for (int t = pair; ok && t < total; t += n_pairs, ++i) {
+        const int acc = i & 1;
+        if (!wait_bounded_cluster(acce_bar(acc), (((uint32_t)i >> 1) & 1u) ^ 1u, &abort_flag, p)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * BN;
+        for (int kb = 0; kb < kbs; ++kb) {
+          if (!wait_bounded(full_bar(stage), phase, &abort_flag, p)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t a_t = smem_u32(smem + stage * STAGE_BYTES), b_t = a_t + OPERAND_BYTES;
+#pragma unroll
+          for (int k = 0; k < BK / 16; ++k) {
+            const uint64_t adesc = smem_desc(a_t + k * 32, 16, 1024);
+            const uint64_t bdesc =
+                B_MN ? smem_desc(b_t + k * 16 * 128, 64 * BK * 2, 1024) : smem_desc(b_t + k * 32, 16, 1024);
+            tc_mma_pair(d_tmem, adesc, bdesc, IDESC, (kb > 0 || k > 0) ? 1u : 0u);
+          }
+          issued = true;
+          tc_commit_pair(empty_bar(stage), 3);
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        }
+        if (ok) tc_commit_pair(accf_bar(acc), 3);
+      }
+      if (issued) {
+        tc_commit_pair(drain_bar, 1);
+        const long long t0 = clock64();
+        while (!mbar_try_wait(drain_bar, 0)) {
+          if ((unsigned long long)(clock64() - t0) > DRAIN_LIMIT) { set_error(p.err, DEV_TIMEOUT); break; }
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;  // TMEM lane quadrant of this warp
+    float* stg = stage_out + q * 32 * STG;
+    int i = 0;
+    for (int t = pair; t < total; t += n_pairs, ++i) {
+      const int acc = i & 1;
+      const Tile w = tile_of<MODE>(t, p, per, rank);
+      const int row = w.row0 + q * 32 + lane;
+      const bool row_ok = row < p.m;
+      const long long ldi = MODE == POLY ? p.lda : p.ldx;
+      const __half* in_row = p.in + ((long long)w.e * p.m + row) * ldi + w.n0;
+      float s_row = 0.f, d_row = 0.f;
+      uint4 xr[4], xn[4];
+      const int chunks = min(BN / 32, (cols - w.n0 + 31) / 32);
+      if (MODE != GRAM && row_ok) {
+        load_row(in_row, xr);
+        if (MODE == POLY) s_row = p.s[(long long)w.e * p.lda + row];
+        else d_row = p.d[(long long)w.e * p.lda + row];
+      }
+      if (!wait_bounded(accf_bar(acc), ((uint32_t)i >> 1) & 1u, &abort_flag, p)) break;
+      tc_fence_after();
+      const uint32_t tbase = tmem_base + acc * BN + ((uint32_t)(q * 32) << 16);
+#pragma unroll 1
+      for (int c = 0; c < chunks; ++c) {
+        if (MODE != GRAM && row_ok && c + 1 < chunks) load_row(in_row + (c + 1) * 32, xn);
+        float v[32];
+        tmem_ld32(tbase + c * 32, v);
+        const int col0 = w.n0 + c * 32;
+        if (MODE == GRAM) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] *= INV;  // A, held times 2^10
+          if (w.i == w.j) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (col0 + j == row) {
+                if (row_ok) p.s[(long long)w.e * p.lda + row] = v[j] * INV;
+                v[j] = 0.f;
+              }
+          }
+        } else if (MODE == POLY) {
+          const float* sc = p.s + (long long)w.e * p.lda + col0;
+          const __half2* h = reinterpret_cast<const __half2*>(xr);
+          const float k0 = p.b + p.c * s_row, k1 = p.c * INV;
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 sj = *reinterpret_cast<const float4*>(sc + j);
+            const float2 x0 = __half22float2(h[j / 2]), x1 = __half22float2(h[j / 2 + 1]);
+            if (w.i == w.j) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (col0 + j + k == row && row_ok)
+                  p.d[(long long)w.e * p.lda + row] = p.a + (p.b + p.c * s_row) * s_row + k1 * INV * v[j + k];
+            }
+            v[j] = fmaf(k1, v[j], fmaf(p.c, sj.x, k0) * x0.x);
+            v[j + 1] = fmaf(k1, v[j + 1], fmaf(p.c, sj.y, k0) * x0.y);
+            v[j + 2] = fmaf(k1, v[j + 2], fmaf(p.c, sj.z, k0) * x1.x);
+            v[j + 3] = fmaf(k1, v[j + 3], fmaf(p.c, sj.w, k0) * x1.y);
+          }
+          if (w.i == w.j) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (col0 + j == row) v[j] = 0.f;
+          }
+        } else {
+          const __half2* h = reinterpret_cast<const __half2*>(xr);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float2 x = __half22float2(h[j]);
+            v[2 * j] = fmaf(d_row, x.x, v[2 * j] * INV);
+            v[2 * j + 1] = fmaf(d_row, x.y, v[2 * j + 1] * INV);
+          }
+        }
+        if (MODE == FINAL) {
+          const long long plane = (long long)w.e * p.m * p.n;
+          if (p.r.tall) {  // a row of X is a column of the result: its lanes' rows lie together
+#pragma unroll 4
+            for (int j = 0; j < 32; ++j)
+              if (row_ok && col0 + j < p.n) put_result(p.r, plane + (long long)(col0 + j) * p.m + row, v[j] * INV);
+          } else {  // turned around in shared memory, so that a warp writes along a row
+#pragma unroll
+            for (int j = 0; j < 32; ++j) stg[lane * STG + j] = v[j] * INV;
+            __syncwarp();
+            const int r0 = w.row0 + q * 32;
+#pragma unroll 4
+            for (int r = 0; r < 32; ++r)
+              if (r0 + r < p.m && col0 + lane < p.n)
+                put_result(p.r, plane + (long long)(r0 + r) * p.n + col0 + lane, stg[r * STG + lane]);
+            __syncwarp();
+          }
+        } else {
+          const long long ldo = SYM ? p.lda : p.ldx;
+          __half* plane = p.out + (long long)w.e * p.m * ldo;
+          if (row_ok) store_row(plane + row * ldo + col0, v);
+          if (SYM && w.i != w.j) store_mirrored(plane, ldo, row, col0, p.m, lane, v);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) xr[j] = xn[j];
+      }
+      tc_fence_before();
+      if (leader) mbar_arrive(acce_bar(acc));
+      else mbar_arrive_remote(cluster_addr(acce_bar(acc), 0));
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs are done with tensor memory and with each other's barriers
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(2u * BN));
+  }
+}
+
+// ------------------------------------------------------- norm and first X ---
+// |U|_F without over- or underflow: the squares are summed in three scales, of u, 2^-80 u and
+// 2^80 u, in fp32 for a thread's values and in fp64 from there on, and the scale that holds the
+// sum is taken at the end.
+constexpr int PARTS = 256;   // most partial sums of a matrix
+constexpr int SUM_NT = 256;
+constexpr float BIG = 1.2089258196146292e24f;  // 2^80
+
+struct Source {
+  const void* x = nullptr;  // the matrices, dtype; or the momentum step's:
+  const float* g = nullptr;
+  const float* m = nullptr;
+  float* m_out = nullptr;
+  float beta = 0.f;
+  bool nesterov = false;
+};
+
+enum From { FROM_F32 = 0, FROM_BF16 = 1, FROM_MOMENTUM = 2 };
+
+// u at `at`, and with FIRST the momentum written
+template <int FROM, bool FIRST>
+__device__ __forceinline__ float u_at(const Source& s, long long at) {
+  if (FROM == FROM_F32) return static_cast<const float*>(s.x)[at];
+  if (FROM == FROM_BF16) return __bfloat162float(static_cast<const bf16*>(s.x)[at]);
+  if (FIRST) {
+    const float g = s.g[at], m = fmaf(s.beta, s.m[at], g);
+    s.m_out[at] = m;
+    return s.nesterov ? fmaf(s.beta, m, g) : m;
+  }
+  const float m = s.m_out[at];
+  return s.nesterov ? fmaf(s.beta, m, s.g[at]) : m;
+}
+// four neighbours, 16-byte aligned (8 for bf16)
+template <int FROM, bool FIRST>
+__device__ __forceinline__ float4 u4_at(const Source& s, long long at) {
+  if (FROM == FROM_F32) return *reinterpret_cast<const float4*>(static_cast<const float*>(s.x) + at);
+  if (FROM == FROM_BF16) {
+    const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(s.x) + at);
+    const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&q.x));
+    const float2 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&q.y));
+    return make_float4(lo.x, lo.y, hi.x, hi.y);
+  }
+  float4 m, g = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (FIRST || s.nesterov) g = *reinterpret_cast<const float4*>(s.g + at);
+  if (FIRST) {
+    m = *reinterpret_cast<const float4*>(s.m + at);
+    m = make_float4(fmaf(s.beta, m.x, g.x), fmaf(s.beta, m.y, g.y), fmaf(s.beta, m.z, g.z), fmaf(s.beta, m.w, g.w));
+    *reinterpret_cast<float4*>(s.m_out + at) = m;
+  } else {
+    m = *reinterpret_cast<const float4*>(s.m_out + at);
+  }
+  if (!s.nesterov) return m;
+  return make_float4(fmaf(s.beta, m.x, g.x), fmaf(s.beta, m.y, g.y), fmaf(s.beta, m.z, g.z), fmaf(s.beta, m.w, g.w));
+}
+
+struct Sums {
+  float mid = 0.f, high = 0.f, low = 0.f;
+  __device__ __forceinline__ void add(float u) {
+    const float h = u * (1.f / BIG), l = u * BIG;
+    mid = fmaf(u, u, mid);
+    high = fmaf(h, h, high);
+    low = fmaf(l, l, low);
+  }
+};
+
+// block `blockIdx.x` of a matrix's `gridDim.x` takes `span` neighbours (a multiple of 4)
+template <int FROM, bool VEC>
+__global__ void __launch_bounds__(SUM_NT) ns_sum_kernel(const Source s, long long size, long long span,
+                                                        double* __restrict__ part) {
+  const long long base = (long long)blockIdx.y * size, lo = blockIdx.x * span, hi = min(size, lo + span);
+  Sums a;
+  if (VEC) {
+#pragma unroll 4
+    for (long long i = lo + 4 * threadIdx.x; i < hi; i += 4 * SUM_NT) {
+      const float4 u = u4_at<FROM, true>(s, base + i);
+      a.add(u.x), a.add(u.y), a.add(u.z), a.add(u.w);
+    }
+  } else {
+#pragma unroll 4
+    for (long long i = lo + threadIdx.x; i < hi; i += SUM_NT) a.add(u_at<FROM, true>(s, base + i));
+  }
+  __shared__ double red[3][SUM_NT / 32];
+  double v[3] = {a.mid, a.high, a.low};
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    if ((threadIdx.x & 31) == 0) red[k][threadIdx.x >> 5] = v[k];
+  }
+  __syncthreads();
+  if (threadIdx.x < 3) {
+    double sum = 0;
+    for (int w = 0; w < SUM_NT / 32; ++w) sum += red[threadIdx.x][w];
+    part[((long long)blockIdx.y * PARTS + blockIdx.x) * 3 + threadIdx.x] = sum;
+  }
+}
+
+// 2^10 / (|U| + eps) as the product of two floats, neither of which leaves the range; NaN for a
+// matrix that holds a NaN or an infinity, 0 for one of zeros
+__device__ __forceinline__ float2 first_factor(const double* part, int parts, double eps, int lane) {
+  double v[3] = {0, 0, 0};
+  for (int i = lane; i < parts; i += 32)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) v[k] += part[i * 3 + k];
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+  double norm = v[0] > 0x1p100 ? sqrt(v[1]) * 0x1p80 : v[0] > 0x1p-60 ? sqrt(v[0]) : sqrt(v[2]) * 0x1p-80;
+  if (!(v[1] < HUGE_VAL)) return make_float2(NAN, NAN);
+  if (norm == 0) return make_float2(0.f, 0.f);
+  int e;
+  const double f = frexp(norm + eps, &e);  // norm + eps = f 2^e
+  return make_float2(ldexpf(1.f, -(e / 2)), (float)ldexp(1024.0 / f, -(e - e / 2)));
+}
+
+// First X (fp16, times 2^10) from U, turned around where M > N: 64 x 64 tiles through shared
+// memory, read along U's rows and written along X's.
+constexpr int LT = 64;
+constexpr int LOAD_NT = 256;
+template <int FROM>
+__global__ void __launch_bounds__(LOAD_NT) ns_load_kernel(const Source s, int M, int N, bool tall, long long ldx,
+                                                          const double* __restrict__ part, int parts, double eps,
+                                                          __half* __restrict__ x) {
+  __shared__ __half tile[LT][LT + 2];
+  __shared__ float2 factor;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.z;
+  const int r0 = blockIdx.y * LT, c0 = blockIdx.x * LT;
+  const long long base = (long long)e * M * N;
+  float u[LT / 8][2];
+#pragma unroll
+  for (int k = 0; k < LT / 8; ++k)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = r0 + warp + 8 * k, c = c0 + lane + 32 * h;
+      u[k][h] = r < M && c < N ? u_at<FROM, false>(s, base + (long long)r * N + c) : 0.f;
+    }
+  if (warp == 0) {
+    const float2 f = first_factor(part + (long long)e * PARTS * 3, parts, eps, lane);
+    if (lane == 0) factor = f;
+  }
+  __syncthreads();
+  const float2 f = factor;
+#pragma unroll
+  for (int k = 0; k < LT / 8; ++k)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) tile[warp + 8 * k][lane + 32 * h] = __float2half_rn(u[k][h] * f.x * f.y);
+  __syncthreads();
+  const int m = tall ? N : M, n = tall ? M : N, xr0 = tall ? c0 : r0, xc0 = tall ? r0 : c0;
+  __half* plane = x + (long long)e * m * ldx;
+#pragma unroll
+  for (int k = 0; k < LT / 8; ++k) {
+    const int r = warp + 8 * k, c = 2 * lane;
+    const __half2 v = tall ? __halves2half2(tile[c][r], tile[c + 1][r]) : __halves2half2(tile[r][c], tile[r][c + 1]);
+    // a column behind the last one lies in the row's padding
+    if (xr0 + r < m && xc0 + c < n) *reinterpret_cast<__half2*>(plane + (long long)(xr0 + r) * ldx + xc0 + c) = v;
+  }
+}
+
+// ------------------------------------------------------------------ host ----
+inline long long up(long long v, long long k) { return (v + k - 1) / k * k; }
+
+struct Layout {
+  long long ldx, lda;
+  size_t x[2], d, p, s, diag, part, bytes;
+};
+Layout layout(int E, int M, int N) {
+  Layout l;
+  const long long m = M < N ? M : N, n = M < N ? N : M;
+  l.ldx = up(n, 64);
+  l.lda = up(m, 64);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  for (int k = 0; k < 2; ++k) l.x[k] = take((size_t)E * m * l.ldx * 2);
+  l.d = take((size_t)E * m * l.lda * 2);
+  l.p = take((size_t)E * m * l.lda * 2);
+  l.s = take((size_t)E * l.lda * 4);
+  l.diag = take((size_t)E * l.lda * 4);
+  l.part = take((size_t)E * PARTS * 3 * 8);
+  l.bytes = at;
+  return l;
+}
+
+bool map_half(CUtensorMap* t, const void* base, long long inner, long long ld, long long rows, long long depth,
+              int box_rows) {
+  cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)depth};
+  cuuint64_t str[2] = {(cuuint64_t)ld * 2, (cuuint64_t)ld * rows * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+  return make_map(t, base, 3, dims, str, box, CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
+}
+
+template <int MODE>
+int launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const Params& p, cudaStream_t s) {
+  auto k = ns_gemm_kernel<MODE>;
+  constexpr size_t smem = smem_bytes<MODE>();
+  static_assert(smem + 1024 <= 227 * 1024, "shared memory");
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  const long long tiles = (long long)p.E * tiles_per_matrix<MODE>(p.m, p.n);
+  long long pairs = sm_count() / 2;
+  if (tiles < pairs) pairs = tiles;
+  k<<<(unsigned)(2 * pairs), THREADS, smem, s>>>(a, b, p);
+  return launch_status();
+}
+
+template <int FROM>
+int run(const Source& src, int E, int M, int N, int steps, float a, float b, float c, float eps, const Result& result,
+        void* ws, cudaStream_t st) {
+  const Layout l = layout(E, M, N);
+  const int m = M < N ? M : N, n = M < N ? N : M;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  double* part = reinterpret_cast<double*>(base + l.part);
+  const long long size = (long long)M * N;
+  // partial sums: enough blocks to fill the GPU, 4096 values or more to a block
+  long long parts = up(8LL * sm_count(), E) / E;
+  if (parts > up(size, 4096) / 4096) parts = up(size, 4096) / 4096;
+  if (parts > PARTS) parts = PARTS;
+  const long long span = up(up(size, parts) / parts, 4);
+  const dim3 sum_grid((unsigned)parts, (unsigned)E);
+  if (size % 4 == 0) ns_sum_kernel<FROM, true><<<sum_grid, SUM_NT, 0, st>>>(src, size, span, part);
+  else ns_sum_kernel<FROM, false><<<sum_grid, SUM_NT, 0, st>>>(src, size, span, part);
+  int r = launch_status();
+  if (r != MOE_OK) return r;
+  __half* x = reinterpret_cast<__half*>(base + l.x[0]);
+  __half* x2 = reinterpret_cast<__half*>(base + l.x[1]);
+  __half* D = reinterpret_cast<__half*>(base + l.d);
+  __half* P = reinterpret_cast<__half*>(base + l.p);
+  const dim3 load_grid((unsigned)((N + LT - 1) / LT), (unsigned)((M + LT - 1) / LT), (unsigned)E);
+  ns_load_kernel<FROM><<<load_grid, LOAD_NT, 0, st>>>(src, M, N, result.tall, l.ldx, part, (int)parts, eps, x);
+  if ((r = launch_status()) != MOE_OK) return r;
+
+  Params p;
+  p.E = E, p.m = m, p.n = n, p.ldx = l.ldx, p.lda = l.lda;
+  p.s = reinterpret_cast<float*>(base + l.s), p.d = reinterpret_cast<float*>(base + l.diag);
+  p.a = a, p.b = b, p.c = c;
+  p.r = result;
+  p.err = device_error_word(), p.wait_limit = g_wait_limit;
+  CUtensorMap mx, mx_cols, md, mp;
+  if (!map_half(&md, D, m, l.lda, m, E, 128) || !map_half(&mp, P, m, l.lda, m, E, 128)) return MOE_ERR_CUDA;
+  for (int k = 0; k < steps; ++k) {
+    if (!map_half(&mx, x, n, l.ldx, m, E, 128) || !map_half(&mx_cols, x, n, l.ldx, m, E, 64)) return MOE_ERR_CUDA;
+    p.in = nullptr, p.out = D;
+    if ((r = launch_gemm<GRAM>(mx, mx, p, st)) != MOE_OK) return r;
+    p.in = D, p.out = P;
+    if ((r = launch_gemm<POLY>(md, md, p, st)) != MOE_OK) return r;
+    p.in = x, p.out = x2;
+    r = k + 1 < steps ? launch_gemm<APPLY>(mp, mx_cols, p, st) : launch_gemm<FINAL>(mp, mx_cols, p, st);
+    if (r != MOE_OK) return r;
+    __half* t = x;
+    x = x2;
+    x2 = t;
+  }
+  return MOE_OK;
+}
+
+}  // namespace ns
+
+size_t orthogonalize_ws_bytes(int E, int M, int N) { return ns::layout(E, M, N).bytes; }
+
+int launch_orthogonalize(const void* x, int E, int M, int N, int dtype, int steps, float a, float b, float c, float eps,
+                         void* out, void* ws, cudaStream_t s) {
+  ns::Source src;
+  src.x = x;
+  ns::Result r;
+  r.o = static_cast<bf16*>(out);
+  r.tall = M > N;
+  return dtype == MOE_BF16 ? ns::run<ns::FROM_BF16>(src, E, M, N, steps, a, b, c, eps, r, ws, s)
+                           : ns::run<ns::FROM_F32>(src, E, M, N, steps, a, b, c, eps, r, ws, s);
+}
+
+int launch_muon_step(const void* w, const float* dw, const float* m, int E, int M, int N, int dtype, float beta,
+                     bool nesterov, float lr, float decay, float scale, int steps, float a, float b, float c, float eps,
+                     void* w_out, void* w_low, float* m_out, void* ws, cudaStream_t s) {
+  ns::Source src;
+  src.g = dw, src.m = m, src.m_out = m_out, src.beta = beta, src.nesterov = nesterov;
+  ns::Result r;
+  r.w = w, r.w_out = w_out, r.w_low = static_cast<bf16*>(w_low), r.dtype = dtype;
+  r.keep = (float)(1.0 - (double)lr * decay), r.step = (float)((double)lr * scale), r.tall = M > N;
+  return ns::run<ns::FROM_MOMENTUM>(src, E, M, N, steps, a, b, c, eps, r, ws, s);
+}
+
+}  // namespace moe

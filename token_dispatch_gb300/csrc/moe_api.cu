@@ -86,6 +86,12 @@ size_t moe_workspace_bytes(int op, int T, int H, int E, int K, int Hp) {
     case MOE_OP_ROUTE_BWD: return (E > 0 && H > 0) ? route_bwd_ws_bytes(T, H, E) : 0;
     case MOE_OP_EXPERT_FFN: return expert_ffn_ws_bytes();
     case MOE_OP_COMBINE_NORM_BWD: return H > 0 ? combine_norm_bwd_ws_bytes(T, H) : 0;
+    case MOE_OP_EXPERT_FFN_W4: {
+      const long long rows = (long long)T * K;
+      return H > 0 && E > 0 && Hp > 0 && rows <= 0x7fffffffll ? expert_ffn_w4_ws_bytes((int)rows, H, E, Hp) : 0;
+    }
+    case MOE_OP_ORTHOGONALIZE:
+    case MOE_OP_MUON_STEP: return H > 0 && E > 0 && Hp > 0 ? orthogonalize_ws_bytes(E, H, Hp) : 0;
     case MOE_OP_EXPERT_FFN_BWD: return Hp > 0 ? expert_ffn_bwd_ws_bytes((int)((long long)T * K), Hp) : 0;
     default: return 0;
   }
@@ -254,6 +260,84 @@ int moe_ckpt_swiglu(const int8_t* q, const uint8_t* scale, int rows, int Hp, int
   if (Hp % vec_elems(dtype) != 0) return MOE_ERR_UNSUPPORTED;
   if (!all_aligned({gu, act})) return MOE_ERR_MISALIGNED;
   return launch_ckpt_swiglu(q, scale, rows, Hp, dtype, gu, act, as_stream(stream));
+}
+
+static int check_w4(const void* q, const void* scale, int E, int rows, int cols, int axis, int group, int dtype) {
+  if (!valid_dtype(dtype) || E < 1 || rows < 1 || cols < 1 || (axis != 0 && axis != 1)) return MOE_ERR_INVALID_ARG;
+  if (group != 32 && group != 64 && group != 128) return MOE_ERR_INVALID_ARG;
+  if (!q || !scale) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned({q, scale})) return MOE_ERR_MISALIGNED;
+  if (rows % vec_elems(dtype) != 0 || cols % vec_elems(dtype) != 0 || rows > (1 << 23) || cols > (1 << 23) || E > 65535)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+int moe_w4_pack(const void* w, int E, int rows, int cols, int axis, int group, int dtype, uint32_t* q, void* scale,
+                void* stream) {
+  int st = check_w4(q, scale, E, rows, cols, axis, group, dtype);
+  if (st != MOE_OK) return st;
+  if (!w) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(w)) return MOE_ERR_MISALIGNED;
+  return launch_w4_pack(w, E, rows, cols, axis, group, dtype, q, scale, as_stream(stream));
+}
+
+int moe_w4_unpack(const uint32_t* q, const void* scale, int E, int rows, int cols, int axis, int group, int dtype,
+                  void* w, void* stream) {
+  int st = check_w4(q, scale, E, rows, cols, axis, group, dtype);
+  if (st != MOE_OK) return st;
+  if (!w) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(w)) return MOE_ERR_MISALIGNED;
+  return launch_w4_unpack(q, scale, E, rows, cols, axis, group, dtype, w, as_stream(stream));
+}
+
+int moe_expert_ffn_w4(const void* x, const int32_t* src_tok, int T, const int32_t* cu_seqlens, int rows,
+                      const uint32_t* q_gate, const void* s_gate, const uint32_t* q_up, const void* s_up,
+                      const uint32_t* q_down, const void* s_down, int E, int H, int Hp, int group, int dtype, void* act,
+                      void* h, void* ws, size_t ws_bytes, void* stream) {
+  if (!valid_dtype(dtype) || rows < 0 || E < 1 || H < 1 || Hp < 1 || T < 0) return MOE_ERR_INVALID_ARG;
+  if (group != 32 && group != 64 && group != 128) return MOE_ERR_INVALID_ARG;
+  if (!cu_seqlens || !q_gate || !s_gate || !q_up || !s_up || !q_down || !s_down) return MOE_ERR_INVALID_ARG;
+  if (rows > 0 && (!x || !act || !h || (src_tok && T < 1))) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned({x, src_tok, cu_seqlens, q_gate, s_gate, q_up, s_up, q_down, s_down, act, h, ws}))
+    return MOE_ERR_MISALIGNED;
+  if (dtype != MOE_BF16 || H % 8 != 0 || Hp % 8 != 0 || E > 1024 || H > (1 << 23) || Hp > (1 << 23))
+    return MOE_ERR_UNSUPPORTED;
+  const size_t need = expert_ffn_w4_ws_bytes(rows, H, E, Hp);
+  if (rows > 0 && need > 0 && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
+  return launch_expert_ffn_w4(x, src_tok, T, cu_seqlens, rows, q_gate, s_gate, q_up, s_up, q_down, s_down, E, H, Hp,
+                              group, act, h, ws, as_stream(stream));
+}
+
+static int check_ortho(int E, int M, int N, int dtype, int steps, float a, float b, float c, float eps, const void* ws,
+                       size_t ws_bytes) {
+  if (!valid_dtype(dtype) || E < 1 || M < 1 || N < 1 || steps < 1 || steps > 64) return MOE_ERR_INVALID_ARG;
+  if (!isfinite(a) || !isfinite(b) || !isfinite(c) || !isfinite(eps) || !(eps >= 0)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(ws)) return MOE_ERR_MISALIGNED;
+  const long long tiles = (long long)E * ((M + 255) / 256) * ((N + 255) / 256);
+  if (E > 65535 || M > 65536 || N > 65536 || tiles > 0x7fffffffll) return MOE_ERR_UNSUPPORTED;
+  return !ws || ws_bytes < orthogonalize_ws_bytes(E, M, N) ? MOE_ERR_WORKSPACE : MOE_OK;
+}
+
+int moe_orthogonalize(const void* x, int E, int M, int N, int dtype, int steps, float a, float b, float c, float eps,
+                      void* out, void* ws, size_t ws_bytes, void* stream) {
+  if (!x || !out) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned({x, out})) return MOE_ERR_MISALIGNED;
+  int st = check_ortho(E, M, N, dtype, steps, a, b, c, eps, ws, ws_bytes);
+  if (st != MOE_OK) return st;
+  return launch_orthogonalize(x, E, M, N, dtype, steps, a, b, c, eps, out, ws, as_stream(stream));
+}
+
+int moe_muon_step(const void* w, const float* dw, const float* m, int E, int M, int N, int dtype, float beta,
+                  int nesterov, float lr, float weight_decay, float scale, int steps, float a, float b, float c,
+                  float eps, void* w_out, void* w_low, float* m_out, void* ws, size_t ws_bytes, void* stream) {
+  if (!w || !dw || !m || !w_out || !m_out || (nesterov != 0 && nesterov != 1)) return MOE_ERR_INVALID_ARG;
+  if (!(beta >= 0 && beta < 1) || !isfinite(lr) || !isfinite(weight_decay) || !isfinite(scale))
+    return MOE_ERR_INVALID_ARG;
+  if (!all_aligned({w, dw, m, w_out, w_low, m_out})) return MOE_ERR_MISALIGNED;
+  int st = check_ortho(E, M, N, dtype, steps, a, b, c, eps, ws, ws_bytes);
+  if (st != MOE_OK) return st;
+  return launch_muon_step(w, dw, m, E, M, N, dtype, beta, nesterov != 0, lr, weight_decay, scale, steps, a, b, c, eps,
+                          w_out, w_low, m_out, ws, as_stream(stream));
 }
 
 int moe_dispatch(const void* x, const int32_t* topk_idx, int T, int H, int E, int K, int dtype,

@@ -165,6 +165,24 @@ int launch_ckpt_unpack(const int8_t* q, const uint8_t* scale, int rows, int N, i
 int launch_ckpt_swiglu(const int8_t* q, const uint8_t* scale, int rows, int Hp, int dtype, void* gu, void* act,
                        cudaStream_t s);
 
+// expert weights in 4 bits
+int launch_w4_pack(const void* w, int E, int rows, int cols, int axis, int group, int dtype, void* q, void* scale,
+                   cudaStream_t s);
+int launch_w4_unpack(const void* q, const void* scale, int E, int rows, int cols, int axis, int group, int dtype,
+                     void* w, cudaStream_t s);
+size_t expert_ffn_w4_ws_bytes(int rows, int H, int E, int Hp);
+int launch_expert_ffn_w4(const void* x, const int32_t* src_tok, int T, const int32_t* cu, int rows, const void* q_gate,
+                         const void* s_gate, const void* q_up, const void* s_up, const void* q_down, const void* s_down,
+                         int E, int H, int Hp, int group, void* act, void* h, void* ws, cudaStream_t s);
+
+// orthogonalised updates
+size_t orthogonalize_ws_bytes(int E, int M, int N);
+int launch_orthogonalize(const void* x, int E, int M, int N, int dtype, int steps, float a, float b, float c, float eps,
+                         void* out, void* ws, cudaStream_t s);
+int launch_muon_step(const void* w, const float* dw, const float* m, int E, int M, int N, int dtype, float beta,
+                     bool nesterov, float lr, float decay, float scale, int steps, float a, float b, float c, float eps,
+                     void* w_out, void* w_low, float* m_out, void* ws, cudaStream_t s);
+
 // dispatch / combine / permute backward
 size_t dispatch_ws_bytes(int T, int E, int K);
 int launch_dispatch(const void* x, const int32_t* idx, int T, int H, int E, int K, int dtype,
