@@ -498,8 +498,8 @@ MOE_API int moe_ckpt_swiglu(const int8_t* q, const uint8_t* scale, int rows, int
  *   sums over: 0 (rows; w_gate and w_up, [E, H, H']) or 1 (cols; w_down).  With in = the size
  *   of that axis, out = the other one's, and B = ceil(in / 128) blocks:
  *     every `group` (32, 64 or 128) neighbours along `axis` of one output share a scale;
- *     with a = max |w| of the group, s = the least number of 5 significant bits >= a / 7 (the
- *     quotient rounded to fp32), at least 2^-126; code = w / s (in fp32) rounded to the nearest
+ *     with a = max |w| of the group, s = the least number of 5 significant bits >= a * (1 / 7) (both
+ *     rounded to fp32), at least 2^-126; code = w / s (in fp32) rounded to the nearest
  *     integer, halves to even: -7..7.  code * s has at most 8 significant bits and is exact in
  *     bf16.  A value is off by at most s / 2, and s < 17/16 * a / 7 where that is above 2^-126.
  *     A group that holds a NaN, an infinity or a magnitude of 2^127 or more has the scale NaN
@@ -532,7 +532,7 @@ MOE_API int moe_w4_unpack(const uint32_t* q, const void* scale, int E, int rows,
  *   act [rows,Hp], h [rows,H] dtype out.  Products are fp32 sums of bf16 rows and exact weights; act
  *   is rounded to dtype before the second product.  For few rows: each expert with rows has its
  *   weights read once for up to 64 of them.
- *   dtype MOE_BF16; H and Hp multiples of 8; E <= 1024.  Workspace:
+ *   dtype MOE_BF16; H and Hp multiples of 8, at most 2^20; E <= 1024.  Workspace:
  *   moe_workspace_bytes(MOE_OP_EXPERT_FFN_W4, T, H, E, K, Hp) bytes for rows = T * K (0: NULL).  Calls
  *   that may run at the same time need distinct workspaces.
  */

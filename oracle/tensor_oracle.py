@@ -21,7 +21,7 @@ def w4_pack(w, axis, group):
     with np.errstate(invalid="ignore", over="ignore"):
         a = np.abs(x).max(axis=3)  # NaN where there is one
         bad = ~(a < 2.0 ** 127)
-        m, e = np.frexp((np.where(bad, 0, a) / np.float32(7)).astype(np.float32).astype(np.float64))
+        m, e = np.frexp((np.where(bad, 0, a) * (np.float32(1) / np.float32(7))).astype(np.float32).astype(np.float64))
         s = np.maximum(np.ldexp(np.ceil(m * 32), e - 5), 2.0 ** -126)
         q = np.rint(np.where(bad[..., None], 0, x) / s[..., None].astype(np.float32))
     s[bad] = np.nan

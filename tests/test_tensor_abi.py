@@ -49,7 +49,7 @@ def test_expert_ffn_w4_refusals(L):
         assert st(**bad) == L.MOE_ERR_INVALID_ARG, bad
     for name in ("x", "src", "cu", "qg", "sg", "qu", "su", "qd", "sd", "act", "h", "ws"):
         assert st(**{name: A + 4}, **({"T": 4} if name == "src" else {})) == L.MOE_ERR_MISALIGNED, name
-    for bad in (dict(dtype=L.MOE_F32), dict(H=60), dict(Hp=68), dict(E=1025), dict(H=(1 << 23) + 8)):
+    for bad in (dict(dtype=L.MOE_F32), dict(H=60), dict(Hp=68), dict(E=1025), dict(H=(1 << 20) + 8)):
         assert st(**bad) == L.MOE_ERR_UNSUPPORTED, bad
     assert st(rows=0, x=None, act=None, h=None) == L.MOE_OK
 

@@ -300,7 +300,7 @@ int moe_expert_ffn_w4(const void* x, const int32_t* src_tok, int T, const int32_
   if (rows > 0 && (!x || !act || !h || (src_tok && T < 1))) return MOE_ERR_INVALID_ARG;
   if (!all_aligned({x, src_tok, cu_seqlens, q_gate, s_gate, q_up, s_up, q_down, s_down, act, h, ws}))
     return MOE_ERR_MISALIGNED;
-  if (dtype != MOE_BF16 || H % 8 != 0 || Hp % 8 != 0 || E > 1024 || H > (1 << 23) || Hp > (1 << 23))
+  if (dtype != MOE_BF16 || H % 8 != 0 || Hp % 8 != 0 || E > 1024 || H > (1 << 20) || Hp > (1 << 20))
     return MOE_ERR_UNSUPPORTED;
   const size_t need = expert_ffn_w4_ws_bytes(rows, H, E, Hp);
   if (rows > 0 && need > 0 && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
