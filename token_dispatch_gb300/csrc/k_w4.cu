@@ -154,6 +154,92 @@ __global__ void __launch_bounds__(128) w4_unpack_rows_kernel(const unsigned* __r
   }
 }
 
+// ------------------------------------------------------------ tiles and items ---
+constexpr int MAX_E = 1024;
+
+struct Args {
+  const bf16* x = nullptr;
+  const int32_t* src_tok;  // row r of x, or nullptr: row r itself
+  int x_rows;
+  const int32_t* cu;
+  int E, R, in, out;  // out: outputs of a tensor
+  int group;
+  const bf16 *s0, *s1;
+  bf16* y;  // [R, out]
+  int wk = 0;  // w4_rows_kernel: warps that share a strip of outputs
+  unsigned* err;
+  unsigned long long wait_limit;
+};
+
+// The tiles of N rows of all experts: before[e] = tiles of the experts before e.  Offsets that
+// do not run upwards from 0 to R are cut off there and reported.
+struct Tiles {
+  int before[MAX_E + 1], row0[MAX_E], row1[MAX_E];
+  int warp_sum[8];
+};
+template <int N>
+__device__ __forceinline__ void count_tiles(Tiles& t, const int32_t* cu, int E, int R, unsigned* err) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int PER = MAX_E / 256;  // experts of a thread; the first 256 threads
+  const int e0 = threadIdx.x * PER;
+  int n[PER], sum = 0, incl = 0;
+  if (threadIdx.x < 256) {
+    int at[PER + 1];
+#pragma unroll
+    for (int k = 0; k <= PER; ++k) at[k] = e0 + k <= E ? __ldg(cu + e0 + k) : R;
+    if (threadIdx.x == 0 && blockIdx.x == 0 && (at[0] != 0 || __ldg(cu + E) != R)) set_error(err, DEV_BOUNDS);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      const int a = min(max(at[k], 0), R), b = min(max(at[k + 1], a), R);
+      n[k] = e0 + k < E ? (b - a + N - 1) / N : 0;
+      sum += n[k];
+      if (e0 + k < E) t.row0[e0 + k] = a, t.row1[e0 + k] = b;
+    }
+    incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) t.warp_sum[warp] = incl;
+  }
+  __syncthreads();
+  if (threadIdx.x < 256) {
+    int run = incl - sum;
+    for (int w = 0; w < warp; ++w) run += t.warp_sum[w];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+      if (e0 + k <= E) t.before[e0 + k] = run;
+      run += n[k];
+    }
+    if (threadIdx.x == 255) t.before[E] = run;
+  }
+  __syncthreads();
+}
+
+struct Item {
+  int e, r0, rows, n0;  // n0: first output; rows 0: no more items
+};
+// item i: experts in order, in each its strips of outputs in order, in each strip its tiles of rows
+template <int N>
+__device__ __forceinline__ Item item_of(const Tiles& t, int E, long long i, int strips, int width) {
+  Item w = {0, 0, 0, 0};
+  if (i >= (long long)t.before[E] * strips) return w;
+  int lo = 0, hi = E - 1;
+  while (lo < hi) {  // the last expert whose items begin at or before i
+    const int mid = (lo + hi + 1) >> 1;
+    if ((long long)t.before[mid] * strips <= i) lo = mid;
+    else hi = mid - 1;
+  }
+  const int tiles = t.before[lo + 1] - t.before[lo], local = (int)(i - (long long)t.before[lo] * strips);
+  const int strip = local / tiles, tile = local - strip * tiles;
+  w.e = lo;
+  w.r0 = t.row0[lo] + tile * N;
+  w.rows = min(N, t.row1[lo] - w.r0);
+  w.n0 = strip * width;
+  return w;
+}
+
 // ------------------------------------------------------ products of few rows ---
 // Weights are the MMA's A operand (16 outputs x 16 inputs), up to 8 NT routed rows its B operand, so a
 // weight is read and turned into bf16 once for all of an expert's rows in the tile.  A pair of codes
@@ -173,112 +259,27 @@ __global__ void __launch_bounds__(128) w4_unpack_rows_kernel(const unsigned* __r
 // group g reads row 4 (g & 1) + g / 2 of each eight, so that the two rows which a quarter
 // of a warp reads together lie in different halves of the banks.
 constexpr int NT_WARPS = 8;
-constexpr int MAX_E = 1024;
 constexpr int STAGES = 2;
 constexpr int STAGE_BYTES = 32 * 128;
 constexpr int AHEAD = 8;  // items that a warp's loads may be ahead, a power of two above STAGES + 1
 
-struct Args {
-  const bf16* x;
-  const int32_t* src_tok;  // row r of x, or nullptr: row r itself
-  int x_rows;
-  const int32_t* cu;
-  int E, R, in, out;       // out: rows of q0
-  const bf16 *s0, *s1;
-  bf16* y;                 // [R, out]
-  int wk;                  // warps that share a strip of outputs: 1, 2, 4 or 8
-  unsigned* err;
-  unsigned long long wait_limit;
-};
-
 // d = a b + c
 __device__ __forceinline__ void mma_bf16(float (&d)[4], const unsigned (&a)[4], unsigned b0, unsigned b1,
                                          const float (&c)[4]) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, "
       "%12, %13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
-// codes of a word's pair t as bf16 numbers 128 + (q + 8), or with SUB as q
-template <bool SUB>
+// codes of a word's pair t as bf16 numbers 128 + (q + 8)
 __device__ __forceinline__ unsigned pair_of(unsigned word, int t) {
   unsigned v;  // (word >> 4 t) & 0x000f000f | 0x43004300
   asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(v) : "r"(word >> (4 * t)), "r"(0x43004300u));
-  if (SUB) {
-    const __nv_bfloat162 q = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), __float2bfloat162_rn(136.f));
-    v = *reinterpret_cast<const unsigned*>(&q);
-  }
   return v;
 }
 __device__ __forceinline__ unsigned word_of(const uint4& v, int j) {
   return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
-}
-
-// The tiles of TT rows of all experts: before[e] = tiles of the experts before e.  Offsets that
-// do not run upwards from 0 to R are cut off there and reported.
-struct Tiles {
-  int before[MAX_E + 1], row0[MAX_E + 1];
-  int warp_sum[NT_WARPS];
-};
-template <int TT>
-__device__ __forceinline__ void count_tiles(Tiles& t, const int32_t* cu, int E, int R, unsigned* err) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int PER = MAX_E / (32 * NT_WARPS);  // experts of a thread
-  const int e0 = threadIdx.x * PER;
-  int at[PER + 1], sum = 0;
-#pragma unroll
-  for (int k = 0; k <= PER; ++k) at[k] = e0 + k <= E ? __ldg(cu + e0 + k) : R;
-  if (threadIdx.x == 0 && blockIdx.x == 0 && (at[0] != 0 || __ldg(cu + E) != R)) set_error(err, DEV_BOUNDS);
-  int n[PER];
-#pragma unroll
-  for (int k = 0; k < PER; ++k) {
-    const int a = min(max(at[k], 0), R), b = min(max(at[k + 1], a), R);
-    n[k] = e0 + k < E ? (b - a + TT - 1) / TT : 0;
-    sum += n[k];
-    if (e0 + k < E) t.row0[e0 + k] = a;
-  }
-  int incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) t.warp_sum[warp] = incl;
-  __syncthreads();
-  int run = incl - sum;
-  for (int w = 0; w < warp; ++w) run += t.warp_sum[w];
-#pragma unroll
-  for (int k = 0; k < PER; ++k) {
-    if (e0 + k <= E) t.before[e0 + k] = run;
-    run += n[k];
-  }
-  if (threadIdx.x == 32 * NT_WARPS - 1) t.before[E] = run;
-  __syncthreads();
-}
-
-struct Item {
-  int e, r0, rows, n0;  // n0: first output; rows 0: no more items
-};
-// item i: experts in order, in each its strips in order, in each strip its tiles
-template <int TT>
-__device__ __forceinline__ Item item_of(const Tiles& t, const int32_t* cu, int E, int R, long long i, int strips,
-                                        int width) {
-  Item w = {0, 0, 0, 0};
-  if (i >= (long long)t.before[E] * strips) return w;
-  int lo = 0, hi = E - 1;
-  while (lo < hi) {  // the last expert whose items begin at or before i
-    const int mid = (lo + hi + 1) >> 1;
-    if ((long long)t.before[mid] * strips <= i) lo = mid;
-    else hi = mid - 1;
-  }
-  const int tiles = t.before[lo + 1] - t.before[lo], local = (int)(i - (long long)t.before[lo] * strips);
-  const int strip = local / tiles, tile = local - strip * tiles;
-  w.e = lo;
-  w.r0 = t.row0[lo] + tile * TT;
-  w.rows = min(TT, min(max(__ldg(cu + lo + 1), t.row0[lo]), R) - w.r0);
-  w.n0 = strip * width;
-  return w;
 }
 
 // The scales of a pair of blocks for one output, 2 SC bf16 numbers in SC registers (a row of scales
@@ -301,21 +302,15 @@ __device__ __forceinline__ void load_scales(unsigned (&v)[SC], const bf16* p, bo
 __device__ const uint4 zero_row[16] = {};  // what a lane without a row reads
 
 constexpr int RESIDENT = 2;  // CTAs of an SM
-// buffers where the warps' sums meet: two in turn save a barrier an item
-template <int NT>
-constexpr int sum_bufs() { return NT <= 2 ? 2 : 1; }
-template <int NT>
-constexpr size_t rows_smem() {  // stages, sums, and room to align the stages
-  return (size_t)NT_WARPS * STAGES * STAGE_BYTES + (size_t)sum_bufs<NT>() * NT_WARPS * 8 * NT * 32 * 4 + 1024;
-}
+constexpr int ROWS = 8;      // rows of a tile
+constexpr int SUMS = 8 * 32;  // a warp's sums: [2 tiles of outputs][4][32 lanes]
+// stages, sums (two places in turn save a barrier an item), and room to align the stages
+constexpr size_t ROWS_SMEM = (size_t)NT_WARPS * STAGES * STAGE_BYTES + 2 * NT_WARPS * SUMS * 4 + 1024;
 
-template <int NT, int G, bool GATE_UP>
+template <int G, bool GATE_UP>
 __global__ void __launch_bounds__(32 * NT_WARPS, RESIDENT)
 w4_rows_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ CUtensorMap tm1, const Args p) {
-  constexpr int STRIP = GATE_UP ? 16 : 32, TT = 8 * NT, SC = BLOCK / G;
-  constexpr int SUMS = 8 * NT * 32;  // floats of a warp: [2 NT 4][32 lanes]
-  constexpr bool ONES = NT == 1;
-  constexpr int XH = NT == 1 ? 2 : 1;
+  constexpr int STRIP = GATE_UP ? 16 : 32, SC = BLOCK / G;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Tiles tiles;
   __shared__ Item coming[NT_WARPS][AHEAD];
@@ -335,7 +330,7 @@ w4_rows_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ 
     for (int s = 0; s < STAGES; ++s) tc::mbar_init(tc::smem_u32(&bars[warp][s]), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  count_tiles<TT>(tiles, p.cu, p.E, p.R, p.err);  // ends with a barrier of the CTA
+  count_tiles<ROWS>(tiles, p.cu, p.E, p.R, p.err);  // ends with a barrier of the CTA
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- the warp's loads: stage `issued` of its sequence of (item, pair of blocks)
@@ -345,7 +340,7 @@ w4_rows_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ 
   bool loading;
   const bf16* load_s = nullptr;  // scales of this lane's row of the stage
   auto next_item = [&]() {
-    const Item w = item_of<TT>(tiles, p.cu, p.E, p.R, load_i, strips, STRIP);
+    const Item w = item_of<ROWS>(tiles, p.E, load_i, strips, STRIP);
     if (lane == 0) coming[warp][load_items % AHEAD] = w;
     load_i += stride;
     ++load_items;
@@ -393,47 +388,38 @@ w4_rows_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ 
   for (int round = 0;; ++round) {
     const Item it = coming[warp][round % AHEAD];
     if (it.rows <= 0) break;
-    const int rows = it.rows, live = (rows + 7) / 8;
-    const uint4* xr[NT];  // of the next pair of blocks
-    int step[NT];
-#pragma unroll
-    for (int r = 0; r < NT; ++r) {
-      xr[r] = zero_row;
-      step[r] = 0;
-      if (r * 8 + g < rows) {
-        long long from = it.r0 + r * 8 + g;
-        if (p.src_tok) from = __ldg(p.src_tok + from);
-        if (from < 0 || from >= p.x_rows) {
-          set_error(p.err, DEV_BOUNDS);
-        } else {
-          xr[r] = reinterpret_cast<const uint4*>(p.x + from * p.in) + tg;
-          step[r] = BLOCK / 8;
-        }
+    const uint4* xr = zero_row;  // this lane's row
+    int step = 0;
+    if (g < it.rows) {
+      long long from = it.r0 + g;
+      if (p.src_tok) from = __ldg(p.src_tok + from);
+      if (from < 0 || from >= p.x_rows) {
+        set_error(p.err, DEV_BOUNDS);
+      } else {
+        xr = reinterpret_cast<const uint4*>(p.x + from * p.in) + tg;
+        step = BLOCK / 8;
       }
     }
-    float acc[2][NT][4] = {};
+    float acc[2][4] = {};
 #pragma unroll 1
     for (int pair = kw; pair < pairs; pair += wk) {
       const int slot = done % STAGES;
-      // a row's values of run j of block b for tile r; lanes past the last input get zeros
-      auto load_x = [&](int r, int b, int j) {
-        const uint4* xp = xr[r] + b * step[r] + 4 * j;
-        return b * BLOCK + 32 * j + 8 * tg < p.in ? *xp : make_uint4(0, 0, 0, 0);
-      };
-      uint4 xv[XH][4];
-      if (NT == 1) {  // one tile of rows: its values are asked for before the weights are waited for
+      // the row's values of the pair, asked for before the weights are waited for; lanes past the last input
+      // get zeros
+      uint4 xv[2][4];
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
+      for (int half = 0; half < 2; ++half)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) xv[half % XH][j] = load_x(0, 2 * pair + half, j);
-      }
+        for (int j = 0; j < 4; ++j) {
+          const int b = 2 * pair + half;
+          xv[half][j] = b * BLOCK + 32 * j + 8 * tg < p.in ? xr[b * step + 4 * j] : make_uint4(0, 0, 0, 0);
+        }
       // a wait that gives up: the warp goes on without loads, so that its barriers are met
       if (ok) ok = tc::wait_bounded(tc::smem_u32(&bars[warp][slot]), (done / STAGES) & 1, &abort_flag, p);
       ok = __all_sync(0xffffffffu, ok);
       if (ok) ++landed;
       const uint8_t* st = ring + slot * STAGE_BYTES + prow * 128;
       auto block = [&](int half) {
-        const int b = 2 * pair + half;
         uint4 w[2][2];
         float sc[2][2][SC];
 #pragma unroll
@@ -451,47 +437,29 @@ w4_rows_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ 
         constexpr int RUNS = 4 / SC;  // runs of 32 inputs in a group
 #pragma unroll
         for (int k = 0; k < SC; ++k) {
-          float c[NT][2][4] = {};
-          if (ONES) {
-            const unsigned minus136[4] = {0xc308c308u, 0xc308c308u, 0xc308c308u, 0xc308c308u};
-#pragma unroll
-            for (int j = k * RUNS; j < (k + 1) * RUNS; ++j) {
-              mma_bf16(c[0][0], minus136, xv[half % XH][j].x, xv[half % XH][j].y, c[0][0]);
-              mma_bf16(c[0][0], minus136, xv[half % XH][j].z, xv[half % XH][j].w, c[0][0]);
-            }
-#pragma unroll
-            for (int m = 0; m < 4; ++m) c[0][1][m] = c[0][0][m];
-          }
+          float c[2][4] = {};
+          const unsigned minus136[4] = {0xc308c308u, 0xc308c308u, 0xc308c308u, 0xc308c308u};
 #pragma unroll
           for (int j = k * RUNS; j < (k + 1) * RUNS; ++j) {
-            // the run's weights, once for all tiles of rows
-            unsigned a[2][2][4];
+            mma_bf16(c[0], minus136, xv[half][j].x, xv[half][j].y, c[0]);
+            mma_bf16(c[0], minus136, xv[half][j].z, xv[half][j].w, c[0]);
+          }
+#pragma unroll
+          for (int m = 0; m < 4; ++m) c[1][m] = c[0][m];
+#pragma unroll
+          for (int j = k * RUNS; j < (k + 1) * RUNS; ++j)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               const unsigned u = word_of(w[t][0], j), v = word_of(w[t][1], j);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                a[t][i / 2][i % 2 * 2] = pair_of<!ONES>(u, i);
-                a[t][i / 2][i % 2 * 2 + 1] = pair_of<!ONES>(v, i);
-              }
+              const unsigned a0[4] = {pair_of(u, 0), pair_of(v, 0), pair_of(u, 1), pair_of(v, 1)};
+              const unsigned a1[4] = {pair_of(u, 2), pair_of(v, 2), pair_of(u, 3), pair_of(v, 3)};
+              mma_bf16(c[t], a0, xv[half][j].x, xv[half][j].y, c[t]);
+              mma_bf16(c[t], a1, xv[half][j].z, xv[half][j].w, c[t]);
             }
 #pragma unroll
-            for (int r = 0; r < NT; ++r) {
-              if (r > 0 && r >= live) break;
-              const uint4 x = NT == 1 ? xv[half % XH][j] : load_x(r, b, j);
+          for (int t = 0; t < 2; ++t)
 #pragma unroll
-              for (int t = 0; t < 2; ++t) {
-                mma_bf16(c[r][t], a[t][0], x.x, x.y, c[r][t]);
-                mma_bf16(c[r][t], a[t][1], x.z, x.w, c[r][t]);
-              }
-            }
-          }
-#pragma unroll
-          for (int r = 0; r < NT; ++r)
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-              for (int m = 0; m < 4; ++m) acc[t][r][m] = fmaf(sc[t][m / 2][k], c[r][t][m], acc[t][r][m]);
+            for (int m = 0; m < 4; ++m) acc[t][m] = fmaf(sc[t][m / 2][k], c[t][m], acc[t][m]);
         }
       };
       block(0);
@@ -502,30 +470,23 @@ w4_rows_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ 
       issue(ok);
     }
 
-    // the strip's warps add up, and each finishes some of the rows
-    auto meet = [&]() {
-      if (wk == 1) __syncwarp();
-      else asm volatile("bar.sync %0, %1;" ::"r"(1 + sub), "r"(32 * wk) : "memory");
-    };
-    float* buf = red + round % sum_bufs<NT>() * (NT_WARPS * SUMS);
+    // the strip's warps add up, and each finishes some of the sums
+    float* buf = red + (round & 1) * (NT_WARPS * SUMS);
     float* mine = buf + warp * SUMS + lane;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int r = 0; r < NT; ++r)
-#pragma unroll
-        for (int m = 0; m < 4; ++m) mine[((t * NT + r) * 4 + m) * 32] = acc[t][r][m];
-    meet();
+      for (int m = 0; m < 4; ++m) mine[(t * 4 + m) * 32] = acc[t][m];
+    if (wk == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(1 + sub), "r"(32 * wk) : "memory");
     const float* strip = buf + (warp - kw) * SUMS + lane;
-    // pieces of 8 rows x 2 outputs a lane, shared out among the strip's warps
-    for (int u = kw; u < live * 4; u += wk) {
-      const int r8 = u >> 2, m = u & 3;
+    for (int m = kw; m < 4; m += wk) {
       float v[2] = {0.f, 0.f};
       for (int k = 0; k < wk; ++k)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) v[t] += strip[k * SUMS + ((t * NT + r8) * 4 + m) * 32];
-      const int r = r8 * 8 + 2 * tg + (m & 1), n = it.n0 + prow + 8 * (m >> 1);
-      if (r >= rows) continue;
+        for (int t = 0; t < 2; ++t) v[t] += strip[k * SUMS + (t * 4 + m) * 32];
+      const int r = 2 * tg + (m & 1), n = it.n0 + prow + 8 * (m >> 1);
+      if (r >= it.rows) continue;
       bf16* dst = p.y + (long long)(it.r0 + r) * p.out;
       if (GATE_UP) {
         if (n < p.out) dst[n] = __float2bfloat16_rn(v[0] / (1.f + expf(-v[0])) * v[1]);
@@ -534,7 +495,6 @@ w4_rows_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ 
         if (n + 16 < p.out) dst[n + 16] = __float2bfloat16_rn(v[1]);
       }
     }
-    if (sum_bufs<NT>() == 1) meet();
   }
   // a warp whose wait gave up leaves nothing under way
   for (; landed < issued; ++landed) {
@@ -545,21 +505,26 @@ w4_rows_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ 
   }
 }
 
-// codes of [rows, in] weights: [rows, words] by pairs of blocks
-bool map_codes(CUtensorMap* m, const void* q, long long rows, int in, int box_rows) {
+// codes of [rows, in] weights, `words` of a row and `box_rows` rows at a time
+bool map_codes(CUtensorMap* m, const void* q, long long rows, int in, int box_words, int box_rows) {
   const long long words = (long long)blocks_of(in) * WORDS;
   cuuint64_t dims[2] = {(cuuint64_t)words, (cuuint64_t)rows};
   cuuint64_t str[1] = {(cuuint64_t)words * 4};
-  cuuint32_t box[2] = {2 * WORDS, (cuuint32_t)box_rows};
-  return tc::make_map(m, q, 2, dims, str, box, CU_TENSOR_MAP_DATA_TYPE_UINT32);
+  cuuint32_t box[2] = {(cuuint32_t)box_words, (cuuint32_t)box_rows};
+  return tc::make_map(m, q, 2, dims, str, box, CU_TENSOR_MAP_DATA_TYPE_UINT32,
+                      box_words == WORDS ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int NT, int G, bool GATE_UP>
-int launch_rows(Args p, const CUtensorMap& tm0, const CUtensorMap& tm1, cudaStream_t s) {
-  constexpr int STRIP = GATE_UP ? 16 : 32, TT = 8 * NT;
-  constexpr size_t smem = rows_smem<NT>();
+template <int G, bool GATE_UP>
+int launch_rows(const void* x, const void* q0, const void* q1, Args p, cudaStream_t s) {
+  constexpr int STRIP = GATE_UP ? 16 : 32;
+  CUtensorMap tm0, tm1;
+  const long long outs = (long long)p.E * p.out;
+  if (!map_codes(&tm0, q0, outs, p.in, 2 * WORDS, STRIP) || !map_codes(&tm1, q1, outs, p.in, 2 * WORDS, STRIP))
+    return MOE_ERR_CUDA;
+  p.x = static_cast<const bf16*>(x);
   const int pairs = (blocks_of(p.in) + 1) / 2, strips = (p.out + STRIP - 1) / STRIP;
-  const long long slots = (p.E < p.R ? p.E : p.R) + (long long)(p.R / TT);  // at most
+  const long long slots = (p.E < p.R ? p.E : p.R) + (long long)(p.R / ROWS);  // at most
   const long long resident = (long long)RESIDENT * sm_count();
   // Warps to a strip: more of them make the items finer, and each item costs its warps a meeting
   // (about as much as 0.7 pairs of blocks).  The least of rounds x time of an item.
@@ -570,13 +535,13 @@ int launch_rows(Args p, const CUtensorMap& tm0, const CUtensorMap& tm1, cudaStre
     if (wk == 1 || cost < best) p.wk = wk, best = cost;
   }
   const long long ctas = (slots * strips * p.wk + NT_WARPS - 1) / NT_WARPS;
-  auto k = w4_rows_kernel<NT, G, GATE_UP>;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+  auto k = w4_rows_kernel<G, GATE_UP>;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ROWS_SMEM) != cudaSuccess)
     return MOE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(ctas < resident ? ctas : resident));
   cfg.blockDim = dim3(32 * NT_WARPS);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = ROWS_SMEM;
   cfg.stream = s;
   // the second product's CTAs start, and fetch their first weights, while the first one's finish
   cudaLaunchAttribute attr[1];
@@ -591,21 +556,502 @@ int launch_rows(Args p, const CUtensorMap& tm0, const CUtensorMap& tm1, cudaStre
   return launch_status();
 }
 
+// ----------------------------------------------------- products of more rows ---
+// A tile is 128 outputs (64 of gate and the same 64 of up, or 128 of down) for up to N routed rows of one
+// expert.  The weights are the MMA's A operand and live in tensor memory: a thread takes one
+// output, turns a block of its codes into 128 bf16 numbers in registers and stores them into its
+// lane's columns, where tcgen05.mma reads them.  Only the codes themselves and the rows x pass
+// through shared memory.  (With the bf16 weights there too, 16 KB written and read for every 4 KB of codes,
+// shared memory would bound the kernel at half the memory's rate; with warp-level MMAs fed from
+// registers the work around them did, measured: T = 1, E = 384 57 us, T = 64, E = 64 177 us.)
+//
+// A pair of codes comes out of its word as 128 + (q + 8) by a shift and a lop3 (bf16 holds whole numbers
+// up to 256), minus 136 is q, times the scale the weight: all exact for scales of 5 significant
+// bits.  These are 17 operations for 8 weights, 7 of them on the half-rate integer pipe, so the conversion
+// needs some 80% of the issue slots at the memory's rate; it takes 16 of the 23 warps.
+//
+// Roles of a CTA, one to an SM: warp 0 loads codes (TMA), warp 1 issues the MMAs, warps 2 to 5 are the
+// epilogue, warps 6 to 21 convert (four sets of four warps, each every fourth block), warp 22 loads
+// the rows x.  All loops run over the same sequence of tiles and blocks, so loads and
+// conversion do not stop between tiles.  Every wait is bounded.
+constexpr int SETS = 4;
+constexpr int THREADS = 32 * (6 + 4 * SETS + 1);
+constexpr int TILE = 128;                     // outputs of a tile
+constexpr int CODE_BYTES = TILE * BLOCK / 2;  // a block of codes of a tile
+constexpr int A_COLS = BLOCK / 2;             // tensor memory columns of a block of bf16 weights
+template <int N>
+struct Cfg {
+  // pairs of blocks that may be converted, and have their rows x loaded, ahead of the MMAs
+  static constexpr int PAIRS = N <= 64 ? 3 : 2;
+  // Pairs of blocks of codes under way.  Two more than the above, so that a converting warp may ask for its next block's
+  // codes by their parity: the load before it in the same place is then known to have landed.
+  static constexpr int CODES = PAIRS + 2;
+  static constexpr int X_BYTES = N * BLOCK * 2;  // a block of the rows: two halves of 64 inputs
+  static constexpr int ACC_COLS = N < 32 ? 32 : N;
+  static constexpr int A_BASE = 2 * ACC_COLS;
+  static constexpr int EX_BYTES = 2 * 4 * 16 * 32 * 4;  // sums of gate and up on their way to each other's warps
+  static constexpr size_t SMEM = (size_t)2 * CODES * CODE_BYTES + (size_t)2 * PAIRS * X_BYTES + EX_BYTES + 1024;
+  static_assert(A_BASE + 2 * PAIRS * A_COLS <= 512, "tensor memory");
+};
+
+__device__ __forceinline__ unsigned bits_of(__nv_bfloat162 v) { return *reinterpret_cast<unsigned*>(&v); }
+__device__ __forceinline__ __nv_bfloat162 pair_from(unsigned v) { return *reinterpret_cast<__nv_bfloat162*>(&v); }
+// the weights of a word's pair t: (q, q') s
+__device__ __forceinline__ unsigned weights_of(unsigned word, int t, __nv_bfloat162 s) {
+  unsigned v;  // (word >> 4 t) & 0x000f000f | 0x43004300
+  asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(v) : "r"(word >> (4 * t)), "r"(0x43004300u));
+  return bits_of(__hmul2(__hsub2(pair_from(v), __float2bfloat162_rn(136.f)), s));
+}
+// 32 lanes x 32 columns of tensor memory
+__device__ __forceinline__ void tmem_st32(uint32_t at, const unsigned (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(at)
+      : "memory");
+}
+// D (+)= A B with A in tensor memory
+__device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// whether a phase has completed, without waiting
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// R rows of one output a lane, `rows` of them there: neighbouring lanes swap, so that each writes two
+// neighbours of every other row.  The number of outputs is even.
+template <int R>
+__device__ __forceinline__ void store_rows(const float (&v)[R], bf16* dst, long long ld, int rows, bool store) {
+  const int odd = threadIdx.x & 1;
+#pragma unroll
+  for (int k = 0; k < R / 2; ++k) {
+    const float got = __shfl_xor_sync(0xffffffffu, odd ? v[2 * k] : v[2 * k + 1], 1);
+    const __nv_bfloat162 h = odd ? __floats2bfloat162_rn(got, v[2 * k + 1]) : __floats2bfloat162_rn(v[2 * k], got);
+    if (store && 2 * k + odd < rows) *reinterpret_cast<__nv_bfloat162*>(dst + (2 * k + odd) * ld - odd) = h;
+  }
+}
+
+// the scale of every run of 32 inputs of a block, as bf16 numbers in pairs: G = 32: four numbers,
+// 64: two, 128: one
+template <int G>
+__device__ __forceinline__ uint2 load_scales(const bf16* p) {
+  uint2 v;
+  if (G == 32) {
+    v = __ldg(reinterpret_cast<const uint2*>(p));
+  } else if (G == 64) {
+    const unsigned a = __ldg(reinterpret_cast<const unsigned*>(p));
+    v = make_uint2(__byte_perm(a, a, 0x1010), __byte_perm(a, a, 0x3232));
+  } else {
+    const unsigned a = __ldg(reinterpret_cast<const unsigned short*>(p));
+    v.x = v.y = a | a << 16;
+  }
+  return v;
+}
+
+template <int N, int G, bool GATE_UP>
+__global__ void __launch_bounds__(THREADS, 1)
+w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ CUtensorMap tm1,
+              const __grid_constant__ CUtensorMap tmx, const Args p) {
+  using C = Cfg<N>;
+  using namespace tc;
+  constexpr int WIDTH = GATE_UP ? TILE / 2 : TILE, SC = BLOCK / G;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* xs = smem + 2 * C::CODES * CODE_BYTES;
+  float* ex = reinterpret_cast<float*>(xs + 2 * C::PAIRS * C::X_BYTES);
+  __shared__ Tiles tiles;
+  __shared__ uint64_t bars[2 * C::CODES + 3 * C::PAIRS + 5];
+  __shared__ uint32_t tmem_base_slot;
+  __shared__ int abort_flag;
+  auto codef = [&](int s) { return smem_u32(&bars[s]); };                       // codes have landed
+  auto codee = [&](int s) { return smem_u32(&bars[C::CODES + s]); };            // and been read
+  auto xf = [&](int b) { return smem_u32(&bars[2 * C::CODES + b]); };           // rows have landed
+  auto af = [&](int b) { return smem_u32(&bars[2 * C::CODES + C::PAIRS + b]); };  // weights are in tensor memory
+  auto done = [&](int b) { return smem_u32(&bars[2 * C::CODES + 2 * C::PAIRS + b]); };  // and have been multiplied
+  auto accf = [&](int a) { return smem_u32(&bars[2 * C::CODES + 3 * C::PAIRS + a]); };
+  auto acce = [&](int a) { return smem_u32(&bars[2 * C::CODES + 3 * C::PAIRS + 2 + a]); };
+  const uint32_t drain = smem_u32(&bars[2 * C::CODES + 3 * C::PAIRS + 4]);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int blocks = blocks_of(p.in), pairs = (blocks + 1) / 2, strips = (p.out + WIDTH - 1) / WIDTH;
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < C::CODES; ++s) {
+      mbar_init(codef(s), 1);
+      mbar_init(codee(s), 8);  // the converting warps of two blocks
+    }
+    for (int b = 0; b < C::PAIRS; ++b) {
+      mbar_init(xf(b), 1);
+      mbar_init(af(b), 8);
+      mbar_init(done(b), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(accf(a), 1);
+      mbar_init(acce(a), 128);
+    }
+    mbar_init(drain, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    prefetch_tmap(&tm0);
+    prefetch_tmap(&tm1);
+    prefetch_tmap(&tmx);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base_slot)),
+                 "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  count_tiles<N>(tiles, p.cu, p.E, p.R, p.err);  // with barriers of the CTA
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_slot;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  auto item = [&](long long i) { return item_of<N>(tiles, p.E, i, strips, WIDTH); };
+  const long long items = (long long)tiles.before[p.E] * strips;
+  // waits for loads under way when a role stops: nothing lands after the CTA has gone
+  auto drain_loads = [&](auto bar, int stages, int issued) {
+    for (int k = max(0, issued - stages); k < issued; ++k) {
+      const long long t0 = clock64();
+      while (!mbar_try_wait(bar(k % stages), (k / stages) & 1)) {
+        if ((unsigned long long)(clock64() - t0) > DRAIN_LIMIT) { set_error(p.err, DEV_TIMEOUT); break; }
+      }
+    }
+  };
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- codes
+    int u = 0;  // pair of the whole sequence
+    bool ok = true;
+    for (long long i = blockIdx.x; ok && i < items; i += gridDim.x) {
+      const Item it = item(i);
+      const int row = it.e * p.out + it.n0;
+      for (int b = 0; b < blocks; b += 2, ++u) {
+        const int s = u % C::CODES;
+        ok = __all_sync(0xffffffffu, wait_bounded(codee(s), (u / C::CODES & 1) ^ 1, &abort_flag, p));
+        if (!ok) break;
+        const uint32_t dst = smem_u32(smem + 2 * s * CODE_BYTES);
+        const bool two = b + 1 < blocks;
+        if (elect_one()) {
+          mbar_expect_tx(codef(s), two ? 2 * CODE_BYTES : CODE_BYTES);
+          tma_load_2d(dst, &tm0, codef(s), b * WORDS, row);
+          if (GATE_UP) tma_load_2d(dst + CODE_BYTES / 2, &tm1, codef(s), b * WORDS, row);
+          if (two) {
+            tma_load_2d(dst + CODE_BYTES, &tm0, codef(s), (b + 1) * WORDS, row);
+            if (GATE_UP) tma_load_2d(dst + CODE_BYTES + CODE_BYTES / 2, &tm1, codef(s), (b + 1) * WORDS, row);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) drain_loads(codef, C::CODES, u);
+  } else if (warp == 6 + 4 * SETS) {
+    // ---------------------------------------------------------------- rows x
+    if (!GATE_UP) asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows that gate and up left
+    int u = 0;
+    bool ok = true;
+    for (long long i = blockIdx.x; ok && i < items; i += gridDim.x) {
+      const Item it = item(i);
+      for (int b = 0; b < blocks; b += 2, ++u) {
+        const int s = u % C::PAIRS;
+        ok = __all_sync(0xffffffffu, wait_bounded(done(s), (u / C::PAIRS & 1) ^ 1, &abort_flag, p));
+        if (!ok) break;
+        const uint32_t dst = smem_u32(xs + 2 * s * C::X_BYTES);
+        const int halves = b + 1 < blocks ? 4 : 2;
+        if (elect_one()) {
+          mbar_expect_tx(xf(s), halves * (N * 128));
+#pragma unroll
+          for (int h = 0; h < 4; ++h)
+            if (h < halves) tma_load_2d(dst + h * (N * 128), &tmx, xf(s), b * BLOCK + 64 * h, it.r0);
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) drain_loads(xf, C::PAIRS, u);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA
+    constexpr uint32_t IDESC = instr_desc(TILE, N, false, false);
+    int u = 0, n = 0;
+    bool ok = true, ready = false;
+    for (long long i = blockIdx.x; ok && i < items; i += gridDim.x, ++n) {
+      const int a = n & 1;
+      ok = __all_sync(0xffffffffu, wait_bounded(acce(a), (n / 2 & 1) ^ 1, &abort_flag, p));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t d = tmem + a * C::ACC_COLS;
+      for (int b = 0; b < blocks; b += 2, ++u) {
+        const int buf = u % C::PAIRS, next = (u + 1) % C::PAIRS;
+        if (!ready) {
+          ok = wait_bounded(xf(buf), u / C::PAIRS & 1, &abort_flag, p) &&
+               wait_bounded(af(buf), u / C::PAIRS & 1, &abort_flag, p);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
+        tc_fence_after();
+        // asked here, the answers for the next pair are there once this one's MMAs have been issued
+        const bool next_x = mbar_test_wait(xf(next), (u + 1) / C::PAIRS & 1);
+        const bool next_a = mbar_test_wait(af(next), (u + 1) / C::PAIRS & 1);
+        const uint32_t x = smem_u32(xs + 2 * buf * C::X_BYTES), w = tmem + C::A_BASE + 2 * buf * A_COLS;
+        const bool two = b + 1 < blocks;
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 2 * BLOCK / 16; ++k)
+            if (k < BLOCK / 16 || two)
+              mma_tmem_a(d, w + k * 8, smem_desc(x + k / 4 * (N * 128) + k % 4 * 32, 16, 1024), IDESC, b > 0 || k > 0);
+          tc_commit(done(buf));
+        }
+        ready = __all_sync(0xffffffffu, next_x && next_a);
+      }
+      if (ok && elect_one()) tc_commit(accf(a));
+      __syncwarp();
+    }
+    if (u > 0) {
+      if (elect_one()) tc_commit(drain);
+      __syncwarp();
+      const long long t0 = clock64();
+      while (!mbar_try_wait(drain, 0)) {
+        if ((unsigned long long)(clock64() - t0) > DRAIN_LIMIT) { set_error(p.err, DEV_TIMEOUT); break; }
+      }
+    }
+  } else if (warp >= 6) {
+    // ------------------------------------------------------------ conversion
+    const int set = (warp - 6) >> 2, q = warp & 3;
+    const int row = q * 32 + lane;  // of the tile, and lane of tensor memory
+    const uint32_t lanes = (uint32_t)(q * 32) << 16;
+    // The set's blocks are set, set + SETS, .. of the whole sequence, in which every item has an even number of
+    // blocks: the second one of its last pair may not exist, and is then met without being converted.  So the
+    // set's place in a pair stays the same, and its pairs are SETS / 2 apart.
+    constexpr int STEP = SETS / 2;
+    static_assert(SETS % 2 == 0 && STEP <= C::PAIRS && STEP <= C::CODES, "places advance by less than a round");
+    const int half = set & 1;
+    // places and phases of codes and of buffers
+    int s = (set >> 1) % C::CODES, buf = (set >> 1) % C::PAIRS;
+    uint32_t s_phase = 0, buf_phase = 1;
+    if ((set >> 1) >= C::PAIRS) buf_phase ^= 1;
+    // the scales of this thread's output in an item (outputs behind the last one: the last one's)
+    auto scales_of = [&](const Item& it) {
+      const int n = min(it.n0 + (GATE_UP ? row & 63 : row), p.out - 1);
+      return (GATE_UP && row >= 64 ? p.s1 : p.s0) + ((long long)it.e * p.out + n) * blocks * SC;
+    };
+    // the set's next block in its item, counted on into the following ones
+    long long i = blockIdx.x, i_next = i;
+    int b = set;
+    Item it = item(i);
+    const bf16 *sp = scales_of(it), *sp_next = sp;
+    auto settle = [&](long long& i, int& b, const bf16*& sp) {  // over to the item that holds block b
+      while (i < items && b >= 2 * pairs) {
+        b -= 2 * pairs;
+        i += gridDim.x;
+        if (i < items) sp = scales_of(item(i));
+      }
+    };
+    settle(i, b, sp);
+    uint2 sc = make_uint2(0, 0);
+    if (i < items && b < blocks) sc = load_scales<G>(sp + b * SC);
+    bool landed = false;
+    const uint32_t from = (uint32_t)(half * CODE_BYTES + row * 64);
+    while (i < items) {
+      // the scales of the block after this one
+      const uint2 now = sc;
+      i_next = i, sp_next = sp;
+      int b_next = b + SETS;
+      settle(i_next, b_next, sp_next);
+      if (i_next < items && b_next < blocks) sc = load_scales<G>(sp_next + b_next * SC);
+      const bool real = b < blocks;
+      uint4 w[4];
+      auto read = [&]() {
+        // 64 bytes of the row, in four pieces whose places are exchanged by the row's bits 1 and 2
+        const uint8_t* src = smem + 2 * s * CODE_BYTES + from;
+        if (real) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) w[v] = *reinterpret_cast<const uint4*>(src + ((v ^ (row >> 1 & 3)) << 4));
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(codee(s));
+      };
+      const bool early = landed;
+      if (early) read();
+      if (!__all_sync(0xffffffffu, wait_bounded(done(buf), buf_phase, &abort_flag, p))) break;
+      if (!early) {
+        if (!__all_sync(0xffffffffu, wait_bounded(codef(s), s_phase, &abort_flag, p))) break;
+        read();
+      }
+      s += STEP;
+      if (s >= C::CODES) s -= C::CODES, s_phase ^= 1;
+      landed = mbar_test_wait(codef(s), s_phase);  // the answer is there after the conversion
+      if (real) {
+        tc_fence_after();
+        const uint32_t dst = tmem + lanes + C::A_BASE + (2 * buf + half) * A_COLS;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          unsigned r[32];
+#pragma unroll
+          for (int jj = 0; jj < 2; ++jj) {
+            const int j = 2 * h + jj;  // run of 32 inputs
+            const unsigned two = j < 2 ? now.x : now.y;
+            const __nv_bfloat162 sj = pair_from(__byte_perm(two, two, j & 1 ? 0x3232 : 0x1010));
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const unsigned word = j == 0 ? w[v].x : j == 1 ? w[v].y : j == 2 ? w[v].z : w[v].w;
+#pragma unroll
+              for (int t = 0; t < 4; ++t) r[jj * 16 + v * 4 + t] = weights_of(word, t, sj);
+            }
+          }
+          tmem_st32(dst + h * 32, r);
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(af(buf));
+      buf += STEP;
+      if (buf >= C::PAIRS) buf -= C::PAIRS, buf_phase ^= 1;
+      landed = __all_sync(0xffffffffu, landed);
+      i = i_next, b = b_next, sp = sp_next;
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue
+    const int q = warp & 3;
+    int n = 0;
+    bool ok = true;  // after a wait that gave up the barriers between warps are still met
+    for (long long i = blockIdx.x; i < items; i += gridDim.x, ++n) {
+      const Item it = item(i);
+      const int a = n & 1;
+      if (ok) ok = wait_bounded(accf(a), n / 2 & 1, &abort_flag, p);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+      const uint32_t src = tmem + a * C::ACC_COLS + ((uint32_t)(q * 32) << 16);
+      const int out = it.n0 + (GATE_UP ? q & 1 : q) * 32 + lane;
+      bf16* dst = p.y + (long long)it.r0 * p.out + out;
+      const bool store = ok && out < p.out;
+#pragma unroll 1
+      for (int r0 = 0; r0 < it.rows; r0 += 32) {
+        float v[32];
+        tmem_ld32(src + r0, v);
+        if (GATE_UP) {
+          // gate's warp and up's give each other half of the rows, and each finishes the other half; two
+          // places in turn save a barrier
+          float* ex_at = ex + ((r0 >> 5) & 1) * (4 * 512) + lane;
+          float y[16];
+#pragma unroll
+          for (int r = 0; r < 16; ++r) ex_at[q * 512 + r * 32] = q < 2 ? v[16 + r] : v[r];
+          asm volatile("bar.sync %0, 64;" ::"r"(1 + (q & 1)) : "memory");
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const float other = ex_at[(q ^ 2) * 512 + r * 32];
+            const float g = q < 2 ? v[r] : other, u = q < 2 ? other : v[16 + r];
+            y[r] = __fdividef(g, 1.f + __expf(-g)) * u;
+          }
+          const int at = r0 + (q < 2 ? 0 : 16);
+          store_rows<16>(y, dst + (long long)at * p.out, p.out, it.rows - at, store);
+        } else {
+          store_rows<32>(v, dst + (long long)r0 * p.out, p.out, it.rows - r0, store);
+        }
+      }
+      // a tile of one round fills the first place again
+      if (GATE_UP) asm volatile("bar.sync %0, 64;" ::"r"(1 + (q & 1)) : "memory");
+      tc_fence_before();
+      mbar_arrive(acce(a));
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+  }
+}
+
+bool map_rows(CUtensorMap* m, const void* x, long long rows, int in, int box_rows) {
+  cuuint64_t dims[2] = {(cuuint64_t)in, (cuuint64_t)rows};
+  cuuint64_t str[1] = {(cuuint64_t)in * 2};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  return tc::make_map(m, x, 2, dims, str, box);
+}
+
+template <int N, int G, bool GATE_UP>
+int launch_ffn(const void* x, const void* q0, const void* q1, const Args& p, cudaStream_t s) {
+  using C = Cfg<N>;
+  constexpr int WIDTH = GATE_UP ? TILE / 2 : TILE;
+  static_assert(C::SMEM + sizeof(Tiles) + 512 <= 227 * 1024, "shared memory");
+  CUtensorMap tm0, tm1, tmx;
+  const long long rows = (long long)p.E * p.out;
+  if (!map_codes(&tm0, q0, rows, p.in, WORDS, WIDTH) || !map_codes(&tm1, q1, rows, p.in, WORDS, WIDTH) ||
+      !map_rows(&tmx, x, p.x_rows, p.in, N))
+    return MOE_ERR_CUDA;
+  const long long strips = (p.out + WIDTH - 1) / WIDTH;
+  const long long items = ((long long)(p.E < p.R ? p.E : p.R) + p.R / N) * strips;  // at most
+  const long long sms = sm_count();
+  auto k = w4_ffn_kernel<N, G, GATE_UP>;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(items < sms ? items : sms));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  // the second product's CTAs start, and convert their first weights, while the first one's finish
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = GATE_UP ? 0 : 1;
+  if (cudaLaunchKernelEx(&cfg, k, tm0, tm1, tmx, p) != cudaSuccess) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  return launch_status();
+}
+
+// rows of a tile, by the mean of an expert's: the conversion of a weight costs the same for any number
+inline int tile_rows(int R, int E) {
+  const int mean = R / E;
+  return mean <= 4 ? ROWS : mean <= 8 ? 16 : mean <= 20 ? 32 : mean <= 48 ? 64 : 128;
+}
 template <int G, bool GATE_UP>
-int launch_rows_nt(const Args& p, const CUtensorMap& tm0, const CUtensorMap& tm1, cudaStream_t s) {
-  const int mean = p.R / p.E;  // rows of an expert
-  if (mean <= 4) return launch_rows<1, G, GATE_UP>(p, tm0, tm1, s);
-  if (mean <= 12) return launch_rows<2, G, GATE_UP>(p, tm0, tm1, s);
-  return launch_rows<4, G, GATE_UP>(p, tm0, tm1, s);
+int launch_ffn_n(const void* x, const void* q0, const void* q1, const Args& p, cudaStream_t s) {
+  switch (tile_rows(p.R, p.E)) {
+    case ROWS: return launch_rows<G, GATE_UP>(x, q0, q1, p, s);
+    case 16: return launch_ffn<16, G, GATE_UP>(x, q0, q1, p, s);
+    case 32: return launch_ffn<32, G, GATE_UP>(x, q0, q1, p, s);
+    case 64: return launch_ffn<64, G, GATE_UP>(x, q0, q1, p, s);
+    default: return launch_ffn<128, G, GATE_UP>(x, q0, q1, p, s);
+  }
 }
 template <bool GATE_UP>
-int launch_rows_g(const Args& p, int G, const void* q0, const void* q1, cudaStream_t s) {
-  CUtensorMap tm0, tm1;
-  const long long rows = (long long)p.E * p.out;
-  if (!map_codes(&tm0, q0, rows, p.in, GATE_UP ? 16 : 32) || !map_codes(&tm1, q1, rows, p.in, GATE_UP ? 16 : 32))
-    return MOE_ERR_CUDA;
-  return G == 32 ? launch_rows_nt<32, GATE_UP>(p, tm0, tm1, s)
-                 : G == 64 ? launch_rows_nt<64, GATE_UP>(p, tm0, tm1, s) : launch_rows_nt<128, GATE_UP>(p, tm0, tm1, s);
+int launch_ffn_g(const void* x, const void* q0, const void* q1, const Args& p, cudaStream_t s) {
+  return p.group == 32 ? launch_ffn_n<32, GATE_UP>(x, q0, q1, p, s)
+                       : p.group == 64 ? launch_ffn_n<64, GATE_UP>(x, q0, q1, p, s)
+                                       : launch_ffn_n<128, GATE_UP>(x, q0, q1, p, s);
+}
+
+// the routed rows side by side, for tiles of rows that are loaded as a whole; a row that does not exist is zeros
+__global__ void __launch_bounds__(256) w4_gather_kernel(const uint4* __restrict__ x, const int32_t* __restrict__ src_tok,
+                                                        int T, int vecs, uint4* __restrict__ xs, unsigned* err) {
+  const long long r = blockIdx.x;
+  const int from = __ldg(src_tok + r);
+  const bool ok = from >= 0 && from < T;
+  if (!ok && threadIdx.x == 0) set_error(err, DEV_BOUNDS);
+  for (int i = threadIdx.x; i < vecs; i += 256)
+    xs[r * vecs + i] = ok ? __ldg(x + (long long)from * vecs + i) : make_uint4(0, 0, 0, 0);
 }
 
 unsigned grid_of(long long threads, int nt) {
@@ -662,25 +1108,35 @@ int launch_w4_unpack(const void* q, const void* scale, int E, int rows, int cols
                            : w4::unpack<float>(q, scale, E, rows, cols, axis, group, w, s);
 }
 
-size_t expert_ffn_w4_ws_bytes(int R, int H, int E, int Hp) { return 0; }
+size_t expert_ffn_w4_ws_bytes(int rows, int H, int E) {
+  return w4::tile_rows(rows, E) >= 16 ? (size_t)rows * H * sizeof(bf16) : 0;
+}
 
 int launch_expert_ffn_w4(const void* x, const int32_t* src_tok, int T, const int32_t* cu, int rows, const void* q_gate,
                          const void* s_gate, const void* q_up, const void* s_up, const void* q_down, const void* s_down,
                          int E, int H, int Hp, int group, void* act, void* h, void* ws, cudaStream_t s) {
   if (rows == 0) return MOE_OK;
+  if (src_tok && w4::tile_rows(rows, E) >= 16) {
+    w4::w4_gather_kernel<<<rows, 256, 0, s>>>(static_cast<const uint4*>(x), src_tok, T, H / 8, static_cast<uint4*>(ws),
+                                              device_error_word());
+    const int st = launch_status();
+    if (st != MOE_OK) return st;
+    x = ws;
+    src_tok = nullptr;
+  }
   w4::Args a;
-  a.x = static_cast<const bf16*>(x), a.src_tok = src_tok, a.x_rows = src_tok ? T : rows;
-  a.cu = cu, a.E = E, a.R = rows, a.in = H, a.out = Hp, a.wk = 0;
+  a.src_tok = src_tok, a.x_rows = src_tok ? T : rows;
+  a.cu = cu, a.E = E, a.R = rows, a.in = H, a.out = Hp, a.group = group;
   a.err = device_error_word(), a.wait_limit = tc::g_wait_limit;
   a.s0 = static_cast<const bf16*>(s_gate), a.s1 = static_cast<const bf16*>(s_up);
   a.y = static_cast<bf16*>(act);
-  const int st = w4::launch_rows_g<true>(a, group, q_gate, q_up, s);
+  const int st = w4::launch_ffn_g<true>(x, q_gate, q_up, a, s);
   if (st != MOE_OK) return st;
-  a.x = static_cast<const bf16*>(act), a.src_tok = nullptr, a.x_rows = rows;
+  a.src_tok = nullptr, a.x_rows = rows;
   a.in = Hp, a.out = H;
   a.s0 = a.s1 = static_cast<const bf16*>(s_down);
   a.y = static_cast<bf16*>(h);
-  return w4::launch_rows_g<false>(a, group, q_down, q_down, s);
+  return w4::launch_ffn_g<false>(act, q_down, q_down, a, s);
 }
 
 }  // namespace moe
