@@ -26,6 +26,8 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "tc_ptx.cuh"
 
 namespace moe {
@@ -36,19 +38,24 @@ using namespace tc;
 constexpr int BM = 128;  // rows of a CTA; a pair has 256
 constexpr int BN = 256;
 constexpr int BK = 64;
-constexpr int STAGES = 6;
 constexpr int OPERAND_BYTES = BM * BK * 2;  // A rows of a CTA, and its half of the B columns
 constexpr int STAGE_BYTES = 2 * OPERAND_BYTES;
-constexpr int THREADS = 192;  // producer, MMA issuer, four epilogue warps
+constexpr int EPI_WARPS = 8;  // two for each quarter of tensor memory's lanes, half of the columns each
+constexpr int THREADS = 32 * (2 + EPI_WARPS);
 constexpr int STG = 33;       // floats between the rows of an epilogue staging tile
 constexpr float HELD = 1024.f;  // X, D and P are stored times this
 constexpr float INV = 1.f / 1024.f;
 
 enum Mode { GRAM = 0, POLY = 1, APPLY = 2, FINAL = 3 };
+enum Kind { ORTHO = 0, MUON_BF16 = 1, MUON_F32 = 2 };  // what FINAL writes
 template <int MODE>
-constexpr size_t smem_bytes() {
-  return (size_t)STAGES * STAGE_BYTES + (MODE == FINAL ? 4 * 32 * STG * 4 : 0) + (2 * STAGES + 5) * 8 + 1024;
-}
+struct Cfg {
+  static constexpr int STAGES = MODE == FINAL ? 5 : 6;
+  // FINAL: a tile to turn around, POLY: the diagonal at its columns, for each epilogue warp
+  static constexpr int OUT_BYTES = MODE == FINAL ? EPI_WARPS * 32 * STG * 4 : MODE == POLY ? EPI_WARPS * 128 * 4 : 0;
+  static constexpr size_t SMEM = (size_t)STAGES * STAGE_BYTES + OUT_BYTES + (2 * STAGES + 5) * 8 + 1024;
+  static_assert(SMEM + 1024 <= 227 * 1024, "shared memory");
+};
 
 // Where the last step's result goes: `o` (bf16), or the weights' update
 // w_out = keep * w - step * X (dtype of the weights; w_low: a bf16 copy).
@@ -57,9 +64,9 @@ struct Result {
   const void* w = nullptr;
   void* w_out = nullptr;
   bf16* w_low = nullptr;
-  int dtype = MOE_BF16;
   float keep = 1.f, step = 0.f;
   bool tall = false;  // X is the transposed matrix
+  bool vec = false;   // rows of the result begin at 16 bytes (tall: at a pair of elements)
 };
 
 struct Params {
@@ -131,31 +138,122 @@ __device__ __forceinline__ void store_mirrored(__half* plane, long long ld, int 
   }
 }
 
-template <typename T>
-__device__ __forceinline__ void update_weight(const Result& r, long long at, float y) {
-  const float w = r.keep * to_f32(static_cast<const T*>(r.w)[at]) - r.step * y;
-  static_cast<T*>(r.w_out)[at] = from_f32<T>(w);
-  if (r.w_low) r.w_low[at] = __float2bfloat16_rn(w);
+// ---- the result: a lane's 32 values y of row `row` of X, columns col0.. ; `at` is the first one's place
+template <int KIND>
+__device__ __forceinline__ void put_one(const Result& r, long long at, float y) {
+  if (KIND == ORTHO) {
+    r.o[at] = __float2bfloat16_rn(y);
+  } else {
+    using T = typename std::conditional<KIND == MUON_F32, float, bf16>::type;
+    const float w = r.keep * to_f32(static_cast<const T*>(r.w)[at]) - r.step * y;
+    static_cast<T*>(r.w_out)[at] = from_f32<T>(w);
+    if (r.w_low) r.w_low[at] = __float2bfloat16_rn(w);
+  }
 }
-__device__ __forceinline__ void put_result(const Result& r, long long at, float y) {
-  if (r.o) r.o[at] = __float2bfloat16_rn(y);
-  else if (r.dtype == MOE_BF16) update_weight<bf16>(r, at, y);
-  else update_weight<float>(r, at, y);
+// The old weights of a chunk, asked for a chunk ahead: of a row's 32 columns as 16-byte vectors, or
+// (tall) of pairs of X's rows, as store_mirrored's lanes hold them.
+template <int KIND>
+struct Old {
+  static constexpr int N = KIND == ORTHO ? 1 : KIND == MUON_BF16 ? 16 : 32;
+  unsigned v[N];
+  __device__ __forceinline__ void load(const Result& r, long long plane, int row, int col0, int m, int n, int lane) {
+    if (KIND == ORTHO || !r.vec) return;
+    constexpr int S = KIND == MUON_F32 ? 4 : 2;  // bytes of an element
+    const char* w = static_cast<const char*>(r.w);
+    if (r.tall) {
+      const int odd = lane & 1;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const int j = col0 + 2 * k + odd;
+        if (j < n && row - odd < m) {
+          const char* src = w + (plane + (long long)j * m + row - odd) * S;
+          if (KIND == MUON_F32) {
+            const float2 f = *reinterpret_cast<const float2*>(src);
+            v[2 * k % N] = __float_as_uint(f.x), v[(2 * k + 1) % N] = __float_as_uint(f.y);
+          } else {
+            v[k % N] = *reinterpret_cast<const unsigned*>(src);
+          }
+        }
+      }
+    } else if (row < m) {
+#pragma unroll
+      for (int k = 0; k < N / 4; ++k)
+        if (col0 + k * (16 / S) < n) {
+          const uint4 q = *reinterpret_cast<const uint4*>(w + (plane + (long long)row * n + col0) * S + 16 * k);
+          v[4 * k % N] = q.x, v[(4 * k + 1) % N] = q.y, v[(4 * k + 2) % N] = q.z, v[(4 * k + 3) % N] = q.w;
+        }
+    }
+  }
+  __device__ __forceinline__ float at(int i) const {  // element i of this lane
+    if (KIND == MUON_F32) return __uint_as_float(v[i % N]);
+    return __uint_as_float(i & 1 ? v[i / 2 % N] & 0xffff0000u : v[i / 2 % N] << 16);
+  }
+};
+template <int KIND>
+__device__ __forceinline__ float new_weight(const Result& r, const Old<KIND>& old, int i, float y) {
+  return KIND == ORTHO ? y : r.keep * old.at(i) - r.step * y;
+}
+__device__ __forceinline__ unsigned pack2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const unsigned*>(&h);
+}
+// a lane's row: 16-byte vectors
+template <int KIND>
+__device__ __forceinline__ void put_row(const Result& r, const Old<KIND>& old, long long plane, int row, int col0, int m,
+                                        int n, const float (&y)[32]) {
+  if (row >= m) return;
+  const long long at = plane + (long long)row * n + col0;
+  bf16* low = KIND == ORTHO ? r.o : KIND == MUON_BF16 ? static_cast<bf16*>(r.w_out) : r.w_low;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (col0 + 8 * k >= n) break;
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = new_weight<KIND>(r, old, 8 * k + i, y[8 * k + i]);
+    const uint4 q = make_uint4(pack2(w[0], w[1]), pack2(w[2], w[3]), pack2(w[4], w[5]), pack2(w[6], w[7]));
+    if (KIND == MUON_F32) {
+      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(r.w_out) + at + 8 * k);
+      dst[0] = make_float4(w[0], w[1], w[2], w[3]);
+      dst[1] = make_float4(w[4], w[5], w[6], w[7]);
+    }
+    if (KIND != MUON_F32 || low) *reinterpret_cast<uint4*>(low + at + 8 * k) = q;
+    if (KIND == MUON_BF16 && r.w_low) *reinterpret_cast<uint4*>(r.w_low + at + 8 * k) = q;
+  }
+}
+// tall: neighbouring lanes swap, so that each writes a pair of every other row of the result
+template <int KIND>
+__device__ __forceinline__ void put_mirrored(const Result& r, const Old<KIND>& old, long long plane, int row, int col0,
+                                             int m, int n, int lane, const float (&y)[32]) {
+  const int odd = lane & 1;
+  bf16* low = KIND == ORTHO ? r.o : KIND == MUON_BF16 ? static_cast<bf16*>(r.w_out) : r.w_low;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const float got = __shfl_xor_sync(0xffffffffu, odd ? y[2 * k] : y[2 * k + 1], 1);
+    const int j = col0 + 2 * k + odd;
+    if (j >= n || row - odd >= m) continue;
+    const float a = new_weight<KIND>(r, old, 2 * k, odd ? got : y[2 * k]);
+    const float b = new_weight<KIND>(r, old, 2 * k + 1, odd ? y[2 * k + 1] : got);
+    const long long at = plane + (long long)j * m + row - odd;
+    if (KIND == MUON_F32) *reinterpret_cast<float2*>(static_cast<float*>(r.w_out) + at) = make_float2(a, b);
+    if (KIND != MUON_F32 || low) *reinterpret_cast<unsigned*>(low + at) = pack2(a, b);
+    if (KIND == MUON_BF16 && r.w_low) *reinterpret_cast<unsigned*>(r.w_low + at) = pack2(a, b);
+  }
 }
 
 // The products on pairs of SMs: 256 x 256 tiles by the two-CTA MMA, TMA operands in a ring of
 // six stages, two accumulators in tensor memory so that the epilogue of a tile runs under the
 // next one's products.  Barriers as in the expert products' pair kernel: `full` the leader's
 // (both CTAs' bytes), `empty` and `accf` each CTA's own, `acce` the leader's.  All waits are bounded.
-template <int MODE>
+template <int MODE, int KIND = ORTHO>
 __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
 ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Params p) {
   constexpr bool SYM = MODE == GRAM || MODE == POLY;
+  constexpr int STAGES = Cfg<MODE>::STAGES;
   constexpr bool B_MN = !SYM;  // X [K = m][N = n] with its columns together
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* stage_out = reinterpret_cast<float*>(smem + STAGES * STAGE_BYTES);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES + (MODE == FINAL ? 4 * 32 * STG * 4 : 0));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES + Cfg<MODE>::OUT_BYTES);
   __shared__ uint32_t tmem_base_slot;
   __shared__ int abort_flag;
 
@@ -183,7 +281,7 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(accf_bar(a), 1);
-      mbar_init(acce_bar(a), 2 * 128);  // the epilogue threads of both CTAs
+      mbar_init(acce_bar(a), 2 * 32 * EPI_WARPS);  // the epilogue threads of both CTAs
     }
     mbar_init(drain_bar, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -200,10 +298,12 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   cluster_sync();  // the peer's barriers are initialised before anything arrives on them
   tc_fence_after();
   const uint32_t tmem_base = tmem_base_slot;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
       int stage = 0;
       uint32_t phase = 0;
       int filled[STAGES];
@@ -243,7 +343,7 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     }
   } else if (warp == 1) {
     // ---------------------------------------------- MMA issuer (leader only)
-    if (leader && lane == 0) {
+    if (leader) {
       constexpr uint32_t IDESC = instr_desc(2 * BM, BN, false, B_MN, true);
       int stage = 0;
       uint32_t phase = 0;
@@ -251,28 +351,36 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       int i = 0;
       for (int t = pair; ok && t < total; t += n_pairs, ++i) {
         const int acc = i & 1;
-        if (!wait_bounded_cluster(acce_bar(acc), (((uint32_t)i >> 1) & 1u) ^ 1u, &abort_flag, p)) break;
+        ok = __all_sync(0xffffffffu,
+                        wait_bounded_cluster(acce_bar(acc), (((uint32_t)i >> 1) & 1u) ^ 1u, &abort_flag, p));
+        if (!ok) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BN;
         for (int kb = 0; kb < kbs; ++kb) {
-          if (!wait_bounded(full_bar(stage), phase, &abort_flag, p)) { ok = false; break; }
+          ok = __all_sync(0xffffffffu, wait_bounded(full_bar(stage), phase, &abort_flag, p));
+          if (!ok) break;
           tc_fence_after();
           const uint32_t a_t = smem_u32(smem + stage * STAGE_BYTES), b_t = a_t + OPERAND_BYTES;
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < BK / 16; ++k) {
-            const uint64_t adesc = smem_desc(a_t + k * 32, 16, 1024);
-            const uint64_t bdesc =
-                B_MN ? smem_desc(b_t + k * 16 * 128, 64 * BK * 2, 1024) : smem_desc(b_t + k * 32, 16, 1024);
-            tc_mma_pair(d_tmem, adesc, bdesc, IDESC, (kb > 0 || k > 0) ? 1u : 0u);
+            for (int k = 0; k < BK / 16; ++k) {
+              const uint64_t adesc = smem_desc(a_t + k * 32, 16, 1024);
+              const uint64_t bdesc =
+                  B_MN ? smem_desc(b_t + k * 16 * 128, 64 * BK * 2, 1024) : smem_desc(b_t + k * 32, 16, 1024);
+              tc_mma_pair(d_tmem, adesc, bdesc, IDESC, (kb > 0 || k > 0) ? 1u : 0u);
+            }
+            tc_commit_pair(empty_bar(stage), 3);
           }
+          __syncwarp();
           issued = true;
-          tc_commit_pair(empty_bar(stage), 3);
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
-        if (ok) tc_commit_pair(accf_bar(acc), 3);
+        if (ok && elect_one()) tc_commit_pair(accf_bar(acc), 3);
+        __syncwarp();
       }
       if (issued) {
-        tc_commit_pair(drain_bar, 1);
+        if (elect_one()) tc_commit_pair(drain_bar, 1);
+        __syncwarp();
         const long long t0 = clock64();
         while (!mbar_try_wait(drain_bar, 0)) {
           if ((unsigned long long)(clock64() - t0) > DRAIN_LIMIT) { set_error(p.err, DEV_TIMEOUT); break; }
@@ -281,33 +389,52 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     }
   } else {
     // ------------------------------------------------------------ epilogue
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int CHUNKS = BN / 32 / 2;  // of 32 columns, of a warp
     const int q = warp & 3;  // TMEM lane quadrant of this warp
-    float* stg = stage_out + q * 32 * STG;
+    const int c_begin = ((warp - 2) >> 2) * CHUNKS;
+    float* stg = stage_out + (warp - 2) * (MODE == POLY ? 128 : 32 * STG);
     int i = 0;
     for (int t = pair; t < total; t += n_pairs, ++i) {
       const int acc = i & 1;
       const Tile w = tile_of<MODE>(t, p, per, rank);
       const int row = w.row0 + q * 32 + lane;
       const bool row_ok = row < p.m;
+      const int c_end = min(c_begin + CHUNKS, (cols - w.n0 + 31) / 32);
+      // What the epilogue reads is asked for before the sums are waited for.
       const long long ldi = MODE == POLY ? p.lda : p.ldx;
       const __half* in_row = p.in + ((long long)w.e * p.m + row) * ldi + w.n0;
+      uint4 xr[MODE == GRAM ? 1 : CHUNKS][4];
       float s_row = 0.f, d_row = 0.f;
-      uint4 xr[4], xn[4];
-      const int chunks = min(BN / 32, (cols - w.n0 + 31) / 32);
       if (MODE != GRAM && row_ok) {
-        load_row(in_row, xr);
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c)
+          if (c_begin + c < c_end) load_row(in_row + (c_begin + c) * 32, xr[MODE == GRAM ? 0 : c]);
         if (MODE == POLY) s_row = p.s[(long long)w.e * p.lda + row];
         else d_row = p.d[(long long)w.e * p.lda + row];
       }
+      if (MODE == POLY) {  // the diagonal at the warp's columns (lda is a multiple of 64)
+        const float* sc = p.s + (long long)w.e * p.lda + w.n0 + c_begin * 32;
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) stg[c * 32 + lane] = c_begin + c < c_end ? sc[c * 32 + lane] : 0.f;
+        __syncwarp();
+      }
+      const long long result = (long long)w.e * p.m * p.n;  // of FINAL's matrix
+      Old<KIND> old, old_n;
+      if (MODE == FINAL && c_begin < c_end) old.load(p.r, result, row, w.n0 + c_begin * 32, p.m, p.n, lane);
       if (!wait_bounded(accf_bar(acc), ((uint32_t)i >> 1) & 1u, &abort_flag, p)) break;
       tc_fence_after();
       const uint32_t tbase = tmem_base + acc * BN + ((uint32_t)(q * 32) << 16);
-#pragma unroll 1
-      for (int c = 0; c < chunks; ++c) {
-        if (MODE != GRAM && row_ok && c + 1 < chunks) load_row(in_row + (c + 1) * 32, xn);
+#pragma unroll
+      for (int cc = 0; cc < CHUNKS; ++cc) {
+        const int c = c_begin + cc;
+        if (c >= c_end) break;
+        if (MODE == FINAL && c + 1 < c_end) old_n.load(p.r, result, row, w.n0 + (c + 1) * 32, p.m, p.n, lane);
         float v[32];
         tmem_ld32(tbase + c * 32, v);
         const int col0 = w.n0 + c * 32;
+        const __half2* h = reinterpret_cast<const __half2*>(xr[MODE == GRAM ? 0 : cc]);
         if (MODE == GRAM) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] *= INV;  // A, held times 2^10
@@ -320,31 +447,29 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
               }
           }
         } else if (MODE == POLY) {
-          const float* sc = p.s + (long long)w.e * p.lda + col0;
-          const __half2* h = reinterpret_cast<const __half2*>(xr);
           const float k0 = p.b + p.c * s_row, k1 = p.c * INV;
+          float own = 0.f;  // (D D)_ii
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
-            const float4 sj = *reinterpret_cast<const float4*>(sc + j);
+            const float4 sj = *reinterpret_cast<const float4*>(stg + cc * 32 + j);
             const float2 x0 = __half22float2(h[j / 2]), x1 = __half22float2(h[j / 2 + 1]);
             if (w.i == w.j) {
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                if (col0 + j + k == row && row_ok)
-                  p.d[(long long)w.e * p.lda + row] = p.a + (p.b + p.c * s_row) * s_row + k1 * INV * v[j + k];
+                if (col0 + j + k == row) own = v[j + k];
             }
             v[j] = fmaf(k1, v[j], fmaf(p.c, sj.x, k0) * x0.x);
             v[j + 1] = fmaf(k1, v[j + 1], fmaf(p.c, sj.y, k0) * x0.y);
             v[j + 2] = fmaf(k1, v[j + 2], fmaf(p.c, sj.z, k0) * x1.x);
             v[j + 3] = fmaf(k1, v[j + 3], fmaf(p.c, sj.w, k0) * x1.y);
           }
-          if (w.i == w.j) {
+          if (w.i == w.j && row_ok && row >= col0 && row < col0 + 32) {
+            p.d[(long long)w.e * p.lda + row] = p.a + (p.b + p.c * s_row) * s_row + k1 * INV * own;
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               if (col0 + j == row) v[j] = 0.f;
           }
         } else {
-          const __half2* h = reinterpret_cast<const __half2*>(xr);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const float2 x = __half22float2(h[j]);
@@ -353,30 +478,34 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           }
         }
         if (MODE == FINAL) {
-          const long long plane = (long long)w.e * p.m * p.n;
-          if (p.r.tall) {  // a row of X is a column of the result: its lanes' rows lie together
-#pragma unroll 4
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] *= INV;
+          if (p.r.vec && p.r.tall) {
+            put_mirrored<KIND>(p.r, old, result, row, col0, p.m, p.n, lane, v);
+          } else if (p.r.vec) {
+            put_row<KIND>(p.r, old, result, row, col0, p.m, p.n, v);
+          } else if (p.r.tall) {  // a row of X is a column of the result: its lanes' rows lie together
+#pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (row_ok && col0 + j < p.n) put_result(p.r, plane + (long long)(col0 + j) * p.m + row, v[j] * INV);
+              if (row_ok && col0 + j < p.n) put_one<KIND>(p.r, result + (long long)(col0 + j) * p.m + row, v[j]);
           } else {  // turned around in shared memory, so that a warp writes along a row
 #pragma unroll
-            for (int j = 0; j < 32; ++j) stg[lane * STG + j] = v[j] * INV;
+            for (int j = 0; j < 32; ++j) stg[lane * STG + j] = v[j];
             __syncwarp();
             const int r0 = w.row0 + q * 32;
 #pragma unroll 4
             for (int r = 0; r < 32; ++r)
               if (r0 + r < p.m && col0 + lane < p.n)
-                put_result(p.r, plane + (long long)(r0 + r) * p.n + col0 + lane, stg[r * STG + lane]);
+                put_one<KIND>(p.r, result + (long long)(r0 + r) * p.n + col0 + lane, stg[r * STG + lane]);
             __syncwarp();
           }
+          old = old_n;
         } else {
           const long long ldo = SYM ? p.lda : p.ldx;
           __half* plane = p.out + (long long)w.e * p.m * ldo;
           if (row_ok) store_row(plane + row * ldo + col0, v);
           if (SYM && w.i != w.j) store_mirrored(plane, ldo, row, col0, p.m, lane, v);
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) xr[j] = xn[j];
       }
       tc_fence_before();
       if (leader) mbar_arrive(acce_bar(acc));
@@ -462,6 +591,7 @@ struct Sums {
 template <int FROM, bool VEC>
 __global__ void __launch_bounds__(SUM_NT) ns_sum_kernel(const Source s, long long size, long long span,
                                                         double* __restrict__ part) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const long long base = (long long)blockIdx.y * size, lo = blockIdx.x * span, hi = min(size, lo + span);
   Sums a;
   if (VEC) {
@@ -490,9 +620,14 @@ __global__ void __launch_bounds__(SUM_NT) ns_sum_kernel(const Source s, long lon
   }
 }
 
-// 2^10 / (|U| + eps) as the product of two floats, neither of which leaves the range; NaN for a
-// matrix that holds a NaN or an infinity, 0 for one of zeros
-__device__ __forceinline__ float2 first_factor(const double* part, int parts, double eps, int lane) {
+// 2^10 / (|U| + eps) of each matrix as the product of two floats, neither of which leaves the range; NaN for
+// one that holds a NaN or an infinity, 0 for one of zeros.  A warp a matrix.
+__global__ void __launch_bounds__(32) ns_factor_kernel(const double* __restrict__ part, int parts, double eps,
+                                                       float2* __restrict__ factor) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x;
+  part += (long long)blockIdx.x * PARTS * 3;
   double v[3] = {0, 0, 0};
   for (int i = lane; i < parts; i += 32)
 #pragma unroll
@@ -501,45 +636,61 @@ __device__ __forceinline__ float2 first_factor(const double* part, int parts, do
   for (int k = 0; k < 3; ++k)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-  double norm = v[0] > 0x1p100 ? sqrt(v[1]) * 0x1p80 : v[0] > 0x1p-60 ? sqrt(v[0]) : sqrt(v[2]) * 0x1p-80;
-  if (!(v[1] < HUGE_VAL)) return make_float2(NAN, NAN);
-  if (norm == 0) return make_float2(0.f, 0.f);
-  int e;
-  const double f = frexp(norm + eps, &e);  // norm + eps = f 2^e
-  return make_float2(ldexpf(1.f, -(e / 2)), (float)ldexp(1024.0 / f, -(e - e / 2)));
+  if (lane != 0) return;
+  const double norm = v[0] > 0x1p100 ? sqrt(v[1]) * 0x1p80 : v[0] > 0x1p-60 ? sqrt(v[0]) : sqrt(v[2]) * 0x1p-80;
+  float2 f = make_float2(0.f, 0.f);
+  if (!(v[1] < HUGE_VAL)) {
+    f = make_float2(NAN, NAN);
+  } else if (norm != 0) {
+    int e;
+    const double x = frexp(norm + eps, &e);  // norm + eps = x 2^e
+    f = make_float2(ldexpf(1.f, -(e / 2)), (float)ldexp(1024.0 / x, -(e - e / 2)));
+  }
+  factor[blockIdx.x] = f;
 }
 
 // First X (fp16, times 2^10) from U, turned around where M > N: 64 x 64 tiles through shared
-// memory, read along U's rows and written along X's.
+// memory, read along U's rows and written along X's.  VEC: N is a multiple of 4.
 constexpr int LT = 64;
 constexpr int LOAD_NT = 256;
-template <int FROM>
+template <int FROM, bool VEC>
 __global__ void __launch_bounds__(LOAD_NT) ns_load_kernel(const Source s, int M, int N, bool tall, long long ldx,
-                                                          const double* __restrict__ part, int parts, double eps,
-                                                          __half* __restrict__ x) {
-  __shared__ __half tile[LT][LT + 2];
-  __shared__ float2 factor;
+                                                          const float2* __restrict__ factor, __half* __restrict__ x) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ __align__(16) __half tile[LT][LT + 4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.z;
   const int r0 = blockIdx.y * LT, c0 = blockIdx.x * LT;
   const long long base = (long long)e * M * N;
-  float u[LT / 8][2];
+  const float2 f = __ldg(factor + e);
+  if (VEC) {
+    const int rr = threadIdx.x >> 4, cc = (threadIdx.x & 15) * 4;
+    float4 u[LT / 16];
 #pragma unroll
-  for (int k = 0; k < LT / 8; ++k)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = r0 + warp + 8 * k, c = c0 + lane + 32 * h;
-      u[k][h] = r < M && c < N ? u_at<FROM, false>(s, base + (long long)r * N + c) : 0.f;
+    for (int k = 0; k < LT / 16; ++k) {
+      const int r = r0 + rr + 16 * k, c = c0 + cc;
+      u[k] = r < M && c < N ? u4_at<FROM, false>(s, base + (long long)r * N + c) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-  if (warp == 0) {
-    const float2 f = first_factor(part + (long long)e * PARTS * 3, parts, eps, lane);
-    if (lane == 0) factor = f;
+#pragma unroll
+    for (int k = 0; k < LT / 16; ++k) {
+      __half2* dst = reinterpret_cast<__half2*>(&tile[rr + 16 * k][cc]);
+      dst[0] = __floats2half2_rn(u[k].x * f.x * f.y, u[k].y * f.x * f.y);
+      dst[1] = __floats2half2_rn(u[k].z * f.x * f.y, u[k].w * f.x * f.y);
+    }
+  } else {
+    float u[LT / 8][2];
+#pragma unroll
+    for (int k = 0; k < LT / 8; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = r0 + warp + 8 * k, c = c0 + lane + 32 * h;
+        u[k][h] = r < M && c < N ? u_at<FROM, false>(s, base + (long long)r * N + c) : 0.f;
+      }
+#pragma unroll
+    for (int k = 0; k < LT / 8; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) tile[warp + 8 * k][lane + 32 * h] = __float2half_rn(u[k][h] * f.x * f.y);
   }
-  __syncthreads();
-  const float2 f = factor;
-#pragma unroll
-  for (int k = 0; k < LT / 8; ++k)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) tile[warp + 8 * k][lane + 32 * h] = __float2half_rn(u[k][h] * f.x * f.y);
   __syncthreads();
   const int m = tall ? N : M, n = tall ? M : N, xr0 = tall ? c0 : r0, xc0 = tall ? r0 : c0;
   __half* plane = x + (long long)e * m * ldx;
@@ -557,7 +708,7 @@ inline long long up(long long v, long long k) { return (v + k - 1) / k * k; }
 
 struct Layout {
   long long ldx, lda;
-  size_t x[2], d, p, s, diag, part, bytes;
+  size_t x[2], d, p, s, diag, part, factor, bytes;
 };
 Layout layout(int E, int M, int N) {
   Layout l;
@@ -576,6 +727,7 @@ Layout layout(int E, int M, int N) {
   l.s = take((size_t)E * l.lda * 4);
   l.diag = take((size_t)E * l.lda * 4);
   l.part = take((size_t)E * PARTS * 3 * 8);
+  l.factor = take((size_t)E * 8);
   l.bytes = at;
   return l;
 }
@@ -588,21 +740,40 @@ bool map_half(CUtensorMap* t, const void* base, long long inner, long long ld, l
   return make_map(t, base, 3, dims, str, box, CU_TENSOR_MAP_DATA_TYPE_FLOAT16);
 }
 
-template <int MODE>
+// Each kernel of the chain is set up while the one before it finishes, and waits for that one's end before it
+// touches memory (griddepcontrol).
+template <typename... P, typename... A>
+int launch_next(void (*k)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, k, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  return launch_status();
+}
+
+template <int MODE, int KIND = ORTHO>
 int launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const Params& p, cudaStream_t s) {
-  auto k = ns_gemm_kernel<MODE>;
-  constexpr size_t smem = smem_bytes<MODE>();
-  static_assert(smem + 1024 <= 227 * 1024, "shared memory");
+  auto k = ns_gemm_kernel<MODE, KIND>;
+  constexpr size_t smem = Cfg<MODE>::SMEM;
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return MOE_ERR_CUDA;
   const long long tiles = (long long)p.E * tiles_per_matrix<MODE>(p.m, p.n);
   long long pairs = sm_count() / 2;
   if (tiles < pairs) pairs = tiles;
-  k<<<(unsigned)(2 * pairs), THREADS, smem, s>>>(a, b, p);
-  return launch_status();
+  return launch_next(k, dim3((unsigned)(2 * pairs)), THREADS, smem, s, a, b, p);
 }
 
-template <int FROM>
+template <int FROM, int KIND>
 int run(const Source& src, int E, int M, int N, int steps, float a, float b, float c, float eps, const Result& result,
         void* ws, cudaStream_t st) {
   const Layout l = layout(E, M, N);
@@ -625,8 +796,12 @@ int run(const Source& src, int E, int M, int N, int steps, float a, float b, flo
   __half* D = reinterpret_cast<__half*>(base + l.d);
   __half* P = reinterpret_cast<__half*>(base + l.p);
   const dim3 load_grid((unsigned)((N + LT - 1) / LT), (unsigned)((M + LT - 1) / LT), (unsigned)E);
-  ns_load_kernel<FROM><<<load_grid, LOAD_NT, 0, st>>>(src, M, N, result.tall, l.ldx, part, (int)parts, eps, x);
-  if ((r = launch_status()) != MOE_OK) return r;
+  float2* factor = reinterpret_cast<float2*>(base + l.factor);
+  r = launch_next(ns_factor_kernel, dim3((unsigned)E), 32, 0, st, part, (int)parts, (double)eps, factor);
+  if (r != MOE_OK) return r;
+  r = launch_next(N % 4 == 0 ? ns_load_kernel<FROM, true> : ns_load_kernel<FROM, false>, load_grid, LOAD_NT, 0, st, src,
+                  M, N, result.tall, l.ldx, factor, x);
+  if (r != MOE_OK) return r;
 
   Params p;
   p.E = E, p.m = m, p.n = n, p.ldx = l.ldx, p.lda = l.lda;
@@ -643,7 +818,8 @@ int run(const Source& src, int E, int M, int N, int steps, float a, float b, flo
     p.in = D, p.out = P;
     if ((r = launch_gemm<POLY>(md, md, p, st)) != MOE_OK) return r;
     p.in = x, p.out = x2;
-    r = k + 1 < steps ? launch_gemm<APPLY>(mp, mx_cols, p, st) : launch_gemm<FINAL>(mp, mx_cols, p, st);
+    r = k + 1 < steps ? launch_gemm<APPLY>(mp, mx_cols, p, st)
+                      : launch_gemm<FINAL, KIND>(mp, mx_cols, p, st);
     if (r != MOE_OK) return r;
     __half* t = x;
     x = x2;
@@ -662,9 +838,9 @@ int launch_orthogonalize(const void* x, int E, int M, int N, int dtype, int step
   src.x = x;
   ns::Result r;
   r.o = static_cast<bf16*>(out);
-  r.tall = M > N;
-  return dtype == MOE_BF16 ? ns::run<ns::FROM_BF16>(src, E, M, N, steps, a, b, c, eps, r, ws, s)
-                           : ns::run<ns::FROM_F32>(src, E, M, N, steps, a, b, c, eps, r, ws, s);
+  r.tall = M > N, r.vec = N % (r.tall ? 2 : 8) == 0;
+  return dtype == MOE_BF16 ? ns::run<ns::FROM_BF16, ns::ORTHO>(src, E, M, N, steps, a, b, c, eps, r, ws, s)
+                           : ns::run<ns::FROM_F32, ns::ORTHO>(src, E, M, N, steps, a, b, c, eps, r, ws, s);
 }
 
 int launch_muon_step(const void* w, const float* dw, const float* m, int E, int M, int N, int dtype, float beta,
@@ -673,9 +849,11 @@ int launch_muon_step(const void* w, const float* dw, const float* m, int E, int 
   ns::Source src;
   src.g = dw, src.m = m, src.m_out = m_out, src.beta = beta, src.nesterov = nesterov;
   ns::Result r;
-  r.w = w, r.w_out = w_out, r.w_low = static_cast<bf16*>(w_low), r.dtype = dtype;
-  r.keep = (float)(1.0 - (double)lr * decay), r.step = (float)((double)lr * scale), r.tall = M > N;
-  return ns::run<ns::FROM_MOMENTUM>(src, E, M, N, steps, a, b, c, eps, r, ws, s);
+  r.w = w, r.w_out = w_out, r.w_low = static_cast<bf16*>(w_low);
+  r.keep = (float)(1.0 - (double)lr * decay), r.step = (float)((double)lr * scale);
+  r.tall = M > N, r.vec = N % (r.tall ? 2 : 8) == 0;
+  return dtype == MOE_BF16 ? ns::run<ns::FROM_MOMENTUM, ns::MUON_BF16>(src, E, M, N, steps, a, b, c, eps, r, ws, s)
+                           : ns::run<ns::FROM_MOMENTUM, ns::MUON_F32>(src, E, M, N, steps, a, b, c, eps, r, ws, s);
 }
 
 }  // namespace moe
