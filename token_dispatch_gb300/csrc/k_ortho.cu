@@ -10,8 +10,8 @@
 //            P_ij = (b + c (s_i + s_j)) D_ij + c (D D)_ij,   i != j
 //            d_i  = a + b s_i + c s_i^2 + c (D D)_ii         (a X taken in)
 //   APPLY  X <- diag(d) X + P X
-// GRAM and POLY are symmetric: the tiles on and above the diagonal are computed, and
-// those above it stored twice.
+// GRAM and POLY are symmetric: the 256 x 256 tiles on and above the diagonal are computed and kept, and
+// a tile below it is read as the transposed one above (the tensor core takes either order).
 //
 // Operands are fp16 with fp32 sums.  Every operand is within a small factor of 1 in size,
 // so fp16's range is enough (X, D and P are held times 2^10: an element of X is about
@@ -42,7 +42,7 @@ constexpr int OPERAND_BYTES = BM * BK * 2;  // A rows of a CTA, and its half of 
 constexpr int STAGE_BYTES = 2 * OPERAND_BYTES;
 constexpr int EPI_WARPS = 8;  // two for each quarter of tensor memory's lanes, half of the columns each
 constexpr int THREADS = 32 * (2 + EPI_WARPS);
-constexpr int STG = 33;       // floats between the rows of an epilogue staging tile
+constexpr int STG = 36;       // floats between the rows of FINAL's staging tiles
 constexpr float HELD = 1024.f;  // X, D and P are stored times this
 constexpr float INV = 1.f / 1024.f;
 
@@ -51,9 +51,10 @@ enum Kind { ORTHO = 0, MUON_BF16 = 1, MUON_F32 = 2 };  // what FINAL writes
 template <int MODE>
 struct Cfg {
   static constexpr int STAGES = MODE == FINAL ? 5 : 6;
-  // FINAL: a tile to turn around, POLY: the diagonal at its columns, for each epilogue warp
-  static constexpr int OUT_BYTES = MODE == FINAL ? EPI_WARPS * 32 * STG * 4 : MODE == POLY ? EPI_WARPS * 128 * 4 : 0;
-  static constexpr size_t SMEM = (size_t)STAGES * STAGE_BYTES + OUT_BYTES + (2 * STAGES + 5) * 8 + 1024;
+  // an epilogue warp's tile of 32 x 32 on its way between rows a lane and whole row pieces, and the
+  // diagonal at its columns
+  static constexpr int WARP_BYTES = (MODE == FINAL ? 32 * STG * 4 : 2048) + (MODE == POLY ? 512 : 0);
+  static constexpr size_t SMEM = (size_t)STAGES * STAGE_BYTES + EPI_WARPS * WARP_BYTES + (2 * STAGES + 5) * 8 + 1024;
   static_assert(SMEM + 1024 <= 227 * 1024, "shared memory");
 };
 
@@ -66,7 +67,7 @@ struct Result {
   bf16* w_low = nullptr;
   float keep = 1.f, step = 0.f;
   bool tall = false;  // X is the transposed matrix
-  bool vec = false;   // rows of the result begin at 16 bytes (tall: at a pair of elements)
+  bool vec = false;   // rows of the result are multiples of four elements
 };
 
 struct Params {
@@ -110,133 +111,122 @@ __device__ __forceinline__ Tile tile_of(int t, const Params& p, int per, uint32_
   return w;
 }
 
-__device__ __forceinline__ void load_row(const __half* src, uint4 (&v)[4]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) v[j] = reinterpret_cast<const uint4*>(src)[j];
+// A warp's tile of 32 rows x 32 columns of fp16 is read and written in whole pieces of 64 bytes of a row, four
+// lanes to a piece; a lane's own row comes and goes through 2 KB of shared memory, where the four 16-byte
+// parts of a row are exchanged by the row's bits 1 and 2 (no bank conflicts).  (With a row to a lane in global
+// memory too, each access touched 32 lines, and the L1's tag stage took as long as the products: POLY at
+// 64 x 1408 x 1408 210 us.)
+struct Piece {
+  uint4 v[4];
+};
+__device__ __forceinline__ uint4* part_of(uint8_t* stg, int row, int part) {
+  return reinterpret_cast<uint4*>(stg + row * 64 + ((part ^ (row >> 1 & 3)) << 4));
 }
-__device__ __forceinline__ void store_row(__half* dst, const float (&v)[32]) {
+// rows row0 + lane / 4 + 8 k, columns col0 + 8 (lane % 4) .. of a matrix with `rows` rows (columns up to the row's padding)
+__device__ __forceinline__ void load_piece(Piece& q, const __half* plane, long long ld, int row0, int col0, int rows,
+                                           int lane) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
+  for (int k = 0; k < 4; ++k) {
+    const int r = row0 + (lane >> 2) + 8 * k;
+    if (r < rows) q.v[k] = *reinterpret_cast<const uint4*>(plane + r * ld + col0 + 8 * (lane & 3));
+  }
+}
+__device__ __forceinline__ void own_row(const Piece& q, uint8_t* stg, int lane, uint4 (&row)[4]) {
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) *part_of(stg, (lane >> 2) + 8 * k, lane & 3) = q.v[k];
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) row[k] = *part_of(stg, lane, k);
+}
+__device__ __forceinline__ void store_tile(__half* plane, long long ld, int row0, int col0, int rows, uint8_t* stg,
+                                           int lane, const float (&v)[32]) {
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
     uint4 q;
     __half2* h = reinterpret_cast<__half2*>(&q);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) h[k] = __floats2half2_rn(v[8 * j + 2 * k], v[8 * j + 2 * k + 1]);
-    reinterpret_cast<uint4*>(dst)[j] = q;
+    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(v[8 * k + 2 * i], v[8 * k + 2 * i + 1]);
+    *part_of(stg, lane, k) = q;
   }
-}
-// 32 columns col0.. of this lane's row as rows of the transposed place: neighbouring lanes swap
-// halves, so that each writes two neighbours of one row
-__device__ __forceinline__ void store_mirrored(__half* plane, long long ld, int row, int col0, int m, int lane,
-                                               const float (&v)[32]) {
-  const int odd = lane & 1, at = row - odd;
+  __syncwarp();
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const float got = __shfl_xor_sync(0xffffffffu, odd ? v[2 * k] : v[2 * k + 1], 1);
-    const __half2 h = odd ? __floats2half2_rn(got, v[2 * k + 1]) : __floats2half2_rn(v[2 * k], got);
-    const int j = col0 + 2 * k + odd;
-    if (j < m && at < m) *reinterpret_cast<__half2*>(plane + (long long)j * ld + at) = h;
+  for (int k = 0; k < 4; ++k) {
+    const int r = row0 + (lane >> 2) + 8 * k;
+    if (r < rows)
+      *reinterpret_cast<uint4*>(plane + r * ld + col0 + 8 * (lane & 3)) = *part_of(stg, (lane >> 2) + 8 * k, lane & 3);
   }
 }
 
-// ---- the result: a lane's 32 values y of row `row` of X, columns col0.. ; `at` is the first one's place
-template <int KIND>
-__device__ __forceinline__ void put_one(const Result& r, long long at, float y) {
-  if (KIND == ORTHO) {
-    r.o[at] = __float2bfloat16_rn(y);
-  } else {
-    using T = typename std::conditional<KIND == MUON_F32, float, bf16>::type;
-    const float w = r.keep * to_f32(static_cast<const T*>(r.w)[at]) - r.step * y;
-    static_cast<T*>(r.w_out)[at] = from_f32<T>(w);
-    if (r.w_low) r.w_low[at] = __float2bfloat16_rn(w);
-  }
-}
-// The old weights of a chunk, asked for a chunk ahead: of a row's 32 columns as 16-byte vectors, or
-// (tall) of pairs of X's rows, as store_mirrored's lanes hold them.
-template <int KIND>
-struct Old {
-  static constexpr int N = KIND == ORTHO ? 1 : KIND == MUON_BF16 ? 16 : 32;
-  unsigned v[N];
-  __device__ __forceinline__ void load(const Result& r, long long plane, int row, int col0, int m, int n, int lane) {
-    if (KIND == ORTHO || !r.vec) return;
-    constexpr int S = KIND == MUON_F32 ? 4 : 2;  // bytes of an element
-    const char* w = static_cast<const char*>(r.w);
-    if (r.tall) {
-      const int odd = lane & 1;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int j = col0 + 2 * k + odd;
-        if (j < n && row - odd < m) {
-          const char* src = w + (plane + (long long)j * m + row - odd) * S;
-          if (KIND == MUON_F32) {
-            const float2 f = *reinterpret_cast<const float2*>(src);
-            v[2 * k % N] = __float_as_uint(f.x), v[(2 * k + 1) % N] = __float_as_uint(f.y);
-          } else {
-            v[k % N] = *reinterpret_cast<const unsigned*>(src);
-          }
-        }
-      }
-    } else if (row < m) {
-#pragma unroll
-      for (int k = 0; k < N / 4; ++k)
-        if (col0 + k * (16 / S) < n) {
-          const uint4 q = *reinterpret_cast<const uint4*>(w + (plane + (long long)row * n + col0) * S + 16 * k);
-          v[4 * k % N] = q.x, v[(4 * k + 1) % N] = q.y, v[(4 * k + 2) % N] = q.z, v[(4 * k + 3) % N] = q.w;
-        }
-    }
-  }
-  __device__ __forceinline__ float at(int i) const {  // element i of this lane
-    if (KIND == MUON_F32) return __uint_as_float(v[i % N]);
-    return __uint_as_float(i & 1 ? v[i / 2 % N] & 0xffff0000u : v[i / 2 % N] << 16);
-  }
+// ---- the result.  A warp's tile lies in shared memory by rows of the result (turned around for a tall one); in round
+// k a lane has four neighbours of row lane / 8 + 4 k.
+struct Place {  // the tile's corner in a matrix of `rows` rows of `len`, which begins at `plane`
+  long long plane;
+  int row0, col0, rows, len;
 };
 template <int KIND>
-__device__ __forceinline__ float new_weight(const Result& r, const Old<KIND>& old, int i, float y) {
-  return KIND == ORTHO ? y : r.keep * old.at(i) - r.step * y;
-}
+struct Old {  // the old weights of a tile, asked for a tile ahead
+  static constexpr int N = KIND == ORTHO ? 1 : KIND == MUON_BF16 ? 2 : 4;
+  unsigned v[8][N];
+  __device__ __forceinline__ void load(const Result& r, const Place& p, int lane) {
+    if (KIND == ORTHO || !r.vec) return;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int row = p.row0 + (lane >> 3) + 4 * k, col = p.col0 + 4 * (lane & 7);
+      if (row >= p.rows || col >= p.len) continue;
+      const long long at = p.plane + (long long)row * p.len + col;
+      if (KIND == MUON_BF16) {
+        const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const bf16*>(r.w) + at);
+        v[k][0] = q.x, v[k][1 % N] = q.y;
+      } else {
+        const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const float*>(r.w) + at);
+        v[k][0] = q.x, v[k][1 % N] = q.y, v[k][2 % N] = q.z, v[k][3 % N] = q.w;
+      }
+    }
+  }
+  __device__ __forceinline__ float at(int k, int i) const {
+    if (KIND == MUON_F32) return __uint_as_float(v[k][i % N]);
+    return __uint_as_float(i & 1 ? v[k][i / 2 % N] & 0xffff0000u : v[k][i / 2 % N] << 16);
+  }
+};
 __device__ __forceinline__ unsigned pack2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const unsigned*>(&h);
 }
-// a lane's row: 16-byte vectors
 template <int KIND>
-__device__ __forceinline__ void put_row(const Result& r, const Old<KIND>& old, long long plane, int row, int col0, int m,
-                                        int n, const float (&y)[32]) {
-  if (row >= m) return;
-  const long long at = plane + (long long)row * n + col0;
+__device__ __forceinline__ void put_tile(const Result& r, const Place& p, const Old<KIND>& old, const float* stg, int lane) {
+  using T = typename std::conditional<KIND == MUON_F32, float, bf16>::type;
   bf16* low = KIND == ORTHO ? r.o : KIND == MUON_BF16 ? static_cast<bf16*>(r.w_out) : r.w_low;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if (col0 + 8 * k >= n) break;
-    float w[8];
+  for (int k = 0; k < 8; ++k) {
+    const int row = p.row0 + (lane >> 3) + 4 * k, col = p.col0 + 4 * (lane & 7);
+    if (row >= p.rows || col >= p.len) continue;
+    const float4 q = *reinterpret_cast<const float4*>(stg + ((lane >> 3) + 4 * k) * STG + 4 * (lane & 7));
+    float y[4] = {q.x, q.y, q.z, q.w};
+    const long long at = p.plane + (long long)row * p.len + col;
+    if (r.vec) {
+      if (KIND != ORTHO)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = new_weight<KIND>(r, old, 8 * k + i, y[8 * k + i]);
-    const uint4 q = make_uint4(pack2(w[0], w[1]), pack2(w[2], w[3]), pack2(w[4], w[5]), pack2(w[6], w[7]));
-    if (KIND == MUON_F32) {
-      float4* dst = reinterpret_cast<float4*>(static_cast<float*>(r.w_out) + at + 8 * k);
-      dst[0] = make_float4(w[0], w[1], w[2], w[3]);
-      dst[1] = make_float4(w[4], w[5], w[6], w[7]);
+        for (int i = 0; i < 4; ++i) y[i] = r.keep * old.at(k, i) - r.step * y[i];
+      const uint2 h = make_uint2(pack2(y[0], y[1]), pack2(y[2], y[3]));
+      if (KIND == MUON_F32)
+        *reinterpret_cast<float4*>(static_cast<float*>(r.w_out) + at) = make_float4(y[0], y[1], y[2], y[3]);
+      if (KIND != MUON_F32 || low) *reinterpret_cast<uint2*>(low + at) = h;
+      if (KIND == MUON_BF16 && r.w_low) *reinterpret_cast<uint2*>(r.w_low + at) = h;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (col + i >= p.len) break;
+        if (KIND == ORTHO) {
+          r.o[at + i] = __float2bfloat16_rn(y[i]);
+        } else {
+          const float w = r.keep * to_f32(static_cast<const T*>(r.w)[at + i]) - r.step * y[i];
+          static_cast<T*>(r.w_out)[at + i] = from_f32<T>(w);
+          if (r.w_low) r.w_low[at + i] = __float2bfloat16_rn(w);
+        }
+      }
     }
-    if (KIND != MUON_F32 || low) *reinterpret_cast<uint4*>(low + at + 8 * k) = q;
-    if (KIND == MUON_BF16 && r.w_low) *reinterpret_cast<uint4*>(r.w_low + at + 8 * k) = q;
-  }
-}
-// tall: neighbouring lanes swap, so that each writes a pair of every other row of the result
-template <int KIND>
-__device__ __forceinline__ void put_mirrored(const Result& r, const Old<KIND>& old, long long plane, int row, int col0,
-                                             int m, int n, int lane, const float (&y)[32]) {
-  const int odd = lane & 1;
-  bf16* low = KIND == ORTHO ? r.o : KIND == MUON_BF16 ? static_cast<bf16*>(r.w_out) : r.w_low;
-#pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    const float got = __shfl_xor_sync(0xffffffffu, odd ? y[2 * k] : y[2 * k + 1], 1);
-    const int j = col0 + 2 * k + odd;
-    if (j >= n || row - odd >= m) continue;
-    const float a = new_weight<KIND>(r, old, 2 * k, odd ? got : y[2 * k]);
-    const float b = new_weight<KIND>(r, old, 2 * k + 1, odd ? y[2 * k + 1] : got);
-    const long long at = plane + (long long)j * m + row - odd;
-    if (KIND == MUON_F32) *reinterpret_cast<float2*>(static_cast<float*>(r.w_out) + at) = make_float2(a, b);
-    if (KIND != MUON_F32 || low) *reinterpret_cast<unsigned*>(low + at) = pack2(a, b);
-    if (KIND == MUON_BF16 && r.w_low) *reinterpret_cast<unsigned*>(r.w_low + at) = pack2(a, b);
   }
 }
 
@@ -246,14 +236,14 @@ __device__ __forceinline__ void put_mirrored(const Result& r, const Old<KIND>& o
 // (both CTAs' bytes), `empty` and `accf` each CTA's own, `acce` the leader's.  All waits are bounded.
 template <int MODE, int KIND = ORTHO>
 __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
-ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Params p) {
+ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmT,
+               const __grid_constant__ CUtensorMap tmA2, const Params p) {
   constexpr bool SYM = MODE == GRAM || MODE == POLY;
   constexpr int STAGES = Cfg<MODE>::STAGES;
-  constexpr bool B_MN = !SYM;  // X [K = m][N = n] with its columns together
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* stage_out = reinterpret_cast<float*>(smem + STAGES * STAGE_BYTES);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES + Cfg<MODE>::OUT_BYTES);
+  uint8_t* stage_out = smem + STAGES * STAGE_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * STAGE_BYTES + EPI_WARPS * Cfg<MODE>::WARP_BYTES);
   __shared__ uint32_t tmem_base_slot;
   __shared__ int abort_flag;
 
@@ -266,6 +256,10 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   const int K = MODE == GRAM ? p.n : p.m;
   const int cols = SYM ? p.m : p.n;
   const int kbs = (K + BK - 1) / BK;
+  // Whether a block of the first operand (rows of tile row i) or of the second is read as it lies in the transposed
+  // place, [64 of K][rows] in two boxes of 64 rows: D and P below the diagonal, and X as APPLY's second operand.
+  auto a_turned = [&](int i, int kb) { return MODE != GRAM && kb / 4 < i; };
+  auto b_turned = [&](int j, int kb) { return MODE == POLY ? kb / 4 < j : !SYM; };
 
   auto full_bar = [&](int s) { return smem_u32(&bars[s]); };
   auto empty_bar = [&](int s) { return smem_u32(&bars[STAGES + s]); };
@@ -281,12 +275,13 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(accf_bar(a), 1);
-      mbar_init(acce_bar(a), 2 * 32 * EPI_WARPS);  // the epilogue threads of both CTAs
+      mbar_init(acce_bar(a), 2 * EPI_WARPS);  // the epilogue warps of both CTAs
     }
     mbar_init(drain_bar, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     prefetch_tmap(&tmA);
-    prefetch_tmap(&tmB);
+    prefetch_tmap(&tmT);
+    if (!SYM) prefetch_tmap(&tmA2);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base_slot)),
@@ -320,13 +315,20 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             filled[stage] = (int)phase;
           }
           const uint32_t fb = cluster_addr(full_bar(stage), 0);
-          tma_load_3d_pair(a_dst, &tmA, fb, kb * BK, w.row0, w.e);
-          if (B_MN) {
+          // the maps of the turned boxes: of D (POLY), of P and of X (APPLY: P's is tmA2)
+          if (a_turned(w.i, kb)) {
 #pragma unroll
             for (int c = 0; c < 2; ++c)
-              tma_load_3d_pair(b_dst + c * (64 * BK * 2), &tmB, fb, b0 + c * 64, kb * BK, w.e);
+              tma_load_3d_pair(a_dst + c * (64 * BK * 2), SYM ? &tmT : &tmA2, fb, w.row0 + c * 64, kb * BK, w.e);
           } else {
-            tma_load_3d_pair(b_dst, &tmB, fb, kb * BK, b0, w.e);
+            tma_load_3d_pair(a_dst, &tmA, fb, kb * BK, w.row0, w.e);
+          }
+          if (b_turned(w.j, kb)) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+              tma_load_3d_pair(b_dst + c * (64 * BK * 2), &tmT, fb, b0 + c * 64, kb * BK, w.e);
+          } else {
+            tma_load_3d_pair(b_dst, &tmA, fb, kb * BK, b0, w.e);
           }
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
@@ -344,7 +346,6 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   } else if (warp == 1) {
     // ---------------------------------------------- MMA issuer (leader only)
     if (leader) {
-      constexpr uint32_t IDESC = instr_desc(2 * BM, BN, false, B_MN, true);
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true, issued = false;
@@ -356,7 +357,10 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         if (!ok) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BN;
+        const Tile w = tile_of<MODE>(t, p, per, 0);
         for (int kb = 0; kb < kbs; ++kb) {
+          const bool at = a_turned(w.i, kb), bt = b_turned(w.j, kb);
+          const uint32_t idesc = instr_desc(2 * BM, BN, false, false, true) | (at ? 1u << 15 : 0u) | (bt ? 1u << 16 : 0u);
           ok = __all_sync(0xffffffffu, wait_bounded(full_bar(stage), phase, &abort_flag, p));
           if (!ok) break;
           tc_fence_after();
@@ -364,10 +368,10 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           if (elect_one()) {
 #pragma unroll
             for (int k = 0; k < BK / 16; ++k) {
-              const uint64_t adesc = smem_desc(a_t + k * 32, 16, 1024);
-              const uint64_t bdesc =
-                  B_MN ? smem_desc(b_t + k * 16 * 128, 64 * BK * 2, 1024) : smem_desc(b_t + k * 32, 16, 1024);
-              tc_mma_pair(d_tmem, adesc, bdesc, IDESC, (kb > 0 || k > 0) ? 1u : 0u);
+              // as it lies: +32 bytes for 16 of K in the 128-byte row; turned: +16 rows, 64-wide boxes 8 KB apart
+              const uint64_t adesc = at ? smem_desc(a_t + k * 16 * 128, 64 * BK * 2, 1024) : smem_desc(a_t + k * 32, 16, 1024);
+              const uint64_t bdesc = bt ? smem_desc(b_t + k * 16 * 128, 64 * BK * 2, 1024) : smem_desc(b_t + k * 32, 16, 1024);
+              tc_mma_pair(d_tmem, adesc, bdesc, idesc, (kb > 0 || k > 0) ? 1u : 0u);
             }
             tc_commit_pair(empty_bar(stage), 3);
           }
@@ -393,36 +397,46 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     constexpr int CHUNKS = BN / 32 / 2;  // of 32 columns, of a warp
     const int q = warp & 3;  // TMEM lane quadrant of this warp
     const int c_begin = ((warp - 2) >> 2) * CHUNKS;
-    float* stg = stage_out + (warp - 2) * (MODE == POLY ? 128 : 32 * STG);
+    uint8_t* stg = stage_out + (warp - 2) * Cfg<MODE>::WARP_BYTES;
+    float* diag = reinterpret_cast<float*>(stg + 2048);  // POLY
+    float* wide = reinterpret_cast<float*>(stg);         // FINAL
+    constexpr bool ALL = MODE == POLY || MODE == APPLY;  // all that the epilogue reads is asked for at once
     int i = 0;
     for (int t = pair; t < total; t += n_pairs, ++i) {
       const int acc = i & 1;
       const Tile w = tile_of<MODE>(t, p, per, rank);
-      const int row = w.row0 + q * 32 + lane;
+      const int row0 = w.row0 + q * 32, row = row0 + lane;
       const bool row_ok = row < p.m;
       const int c_end = min(c_begin + CHUNKS, (cols - w.n0 + 31) / 32);
       // What the epilogue reads is asked for before the sums are waited for.
       const long long ldi = MODE == POLY ? p.lda : p.ldx;
-      const __half* in_row = p.in + ((long long)w.e * p.m + row) * ldi + w.n0;
-      uint4 xr[MODE == GRAM ? 1 : CHUNKS][4];
+      const __half* in = p.in + (long long)w.e * p.m * ldi;
+      Piece piece[ALL ? CHUNKS : 2];
       float s_row = 0.f, d_row = 0.f;
-      if (MODE != GRAM && row_ok) {
+      if (MODE != GRAM) {
 #pragma unroll
-        for (int c = 0; c < CHUNKS; ++c)
-          if (c_begin + c < c_end) load_row(in_row + (c_begin + c) * 32, xr[MODE == GRAM ? 0 : c]);
-        if (MODE == POLY) s_row = p.s[(long long)w.e * p.lda + row];
-        else d_row = p.d[(long long)w.e * p.lda + row];
+        for (int c = 0; c < (ALL ? CHUNKS : 1); ++c)
+          if (c_begin + c < c_end) load_piece(piece[c], in, ldi, row0, w.n0 + (c_begin + c) * 32, p.m, lane);
+        if (row_ok) {
+          if (MODE == POLY) s_row = p.s[(long long)w.e * p.lda + row];
+          else d_row = p.d[(long long)w.e * p.lda + row];
+        }
       }
       if (MODE == POLY) {  // the diagonal at the warp's columns (lda is a multiple of 64)
         const float* sc = p.s + (long long)w.e * p.lda + w.n0 + c_begin * 32;
         __syncwarp();
 #pragma unroll
-        for (int c = 0; c < CHUNKS; ++c) stg[c * 32 + lane] = c_begin + c < c_end ? sc[c * 32 + lane] : 0.f;
+        for (int c = 0; c < CHUNKS; ++c) diag[c * 32 + lane] = c_begin + c < c_end ? sc[c * 32 + lane] : 0.f;
         __syncwarp();
       }
-      const long long result = (long long)w.e * p.m * p.n;  // of FINAL's matrix
-      Old<KIND> old, old_n;
-      if (MODE == FINAL && c_begin < c_end) old.load(p.r, result, row, w.n0 + c_begin * 32, p.m, p.n, lane);
+      // FINAL: where the result of chunk c lies
+      auto place = [&](int c) {
+        const int col0 = w.n0 + c * 32;
+        const long long plane = (long long)w.e * p.m * p.n;
+        return p.r.tall ? Place{plane, col0, row0, p.n, p.m} : Place{plane, row0, col0, p.m, p.n};
+      };
+      Old<KIND> old[2];
+      if (MODE == FINAL && c_begin < c_end) old[0].load(p.r, place(c_begin), lane);
       if (!wait_bounded(accf_bar(acc), ((uint32_t)i >> 1) & 1u, &abort_flag, p)) break;
       tc_fence_after();
       const uint32_t tbase = tmem_base + acc * BN + ((uint32_t)(q * 32) << 16);
@@ -430,11 +444,16 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       for (int cc = 0; cc < CHUNKS; ++cc) {
         const int c = c_begin + cc;
         if (c >= c_end) break;
-        if (MODE == FINAL && c + 1 < c_end) old_n.load(p.r, result, row, w.n0 + (c + 1) * 32, p.m, p.n, lane);
+        if (MODE == FINAL && c + 1 < c_end) {
+          load_piece(piece[(cc + 1) % 2], in, ldi, row0, w.n0 + (c + 1) * 32, p.m, lane);
+          old[(cc + 1) % 2].load(p.r, place(c + 1), lane);
+        }
+        const int col0 = w.n0 + c * 32;
+        uint4 mine[4];
+        if (MODE != GRAM) own_row(piece[ALL ? cc : cc % 2], stg, lane, mine);
+        const __half2* h = reinterpret_cast<const __half2*>(mine);
         float v[32];
         tmem_ld32(tbase + c * 32, v);
-        const int col0 = w.n0 + c * 32;
-        const __half2* h = reinterpret_cast<const __half2*>(xr[MODE == GRAM ? 0 : cc]);
         if (MODE == GRAM) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] *= INV;  // A, held times 2^10
@@ -451,7 +470,7 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           float own = 0.f;  // (D D)_ii
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
-            const float4 sj = *reinterpret_cast<const float4*>(stg + cc * 32 + j);
+            const float4 sj = *reinterpret_cast<const float4*>(diag + cc * 32 + j);
             const float2 x0 = __half22float2(h[j / 2]), x1 = __half22float2(h[j / 2 + 1]);
             if (w.i == w.j) {
 #pragma unroll
@@ -478,38 +497,29 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           }
         }
         if (MODE == FINAL) {
+          __syncwarp();
+          if (p.r.tall) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] *= INV;
-          if (p.r.vec && p.r.tall) {
-            put_mirrored<KIND>(p.r, old, result, row, col0, p.m, p.n, lane, v);
-          } else if (p.r.vec) {
-            put_row<KIND>(p.r, old, result, row, col0, p.m, p.n, v);
-          } else if (p.r.tall) {  // a row of X is a column of the result: its lanes' rows lie together
+            for (int j = 0; j < 32; ++j) wide[j * STG + lane] = v[j] * INV;
+          } else {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (row_ok && col0 + j < p.n) put_one<KIND>(p.r, result + (long long)(col0 + j) * p.m + row, v[j]);
-          } else {  // turned around in shared memory, so that a warp writes along a row
-#pragma unroll
-            for (int j = 0; j < 32; ++j) stg[lane * STG + j] = v[j];
-            __syncwarp();
-            const int r0 = w.row0 + q * 32;
-#pragma unroll 4
-            for (int r = 0; r < 32; ++r)
-              if (r0 + r < p.m && col0 + lane < p.n)
-                put_one<KIND>(p.r, result + (long long)(r0 + r) * p.n + col0 + lane, stg[r * STG + lane]);
-            __syncwarp();
+            for (int j = 0; j < 32; j += 4)
+              *reinterpret_cast<float4*>(wide + lane * STG + j) =
+                  make_float4(v[j] * INV, v[j + 1] * INV, v[j + 2] * INV, v[j + 3] * INV);
           }
-          old = old_n;
+          __syncwarp();
+          put_tile<KIND>(p.r, place(c), old[cc % 2], wide, lane);
         } else {
           const long long ldo = SYM ? p.lda : p.ldx;
-          __half* plane = p.out + (long long)w.e * p.m * ldo;
-          if (row_ok) store_row(plane + row * ldo + col0, v);
-          if (SYM && w.i != w.j) store_mirrored(plane, ldo, row, col0, p.m, lane, v);
+          store_tile(p.out + (long long)w.e * p.m * ldo, ldo, row0, col0, p.m, stg, lane, v);
         }
       }
       tc_fence_before();
-      if (leader) mbar_arrive(acce_bar(acc));
-      else mbar_arrive_remote(cluster_addr(acce_bar(acc), 0));
+      __syncwarp();
+      if (lane == 0) {
+        if (leader) mbar_arrive(acce_bar(acc));
+        else mbar_arrive_remote(cluster_addr(acce_bar(acc), 0));
+      }
     }
   }
 
@@ -762,7 +772,7 @@ int launch_next(void (*k)(P...), dim3 grid, int threads, size_t smem, cudaStream
 }
 
 template <int MODE, int KIND = ORTHO>
-int launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const Params& p, cudaStream_t s) {
+int launch_gemm(const CUtensorMap& a, const CUtensorMap& t, const CUtensorMap& a2, const Params& p, cudaStream_t s) {
   auto k = ns_gemm_kernel<MODE, KIND>;
   constexpr size_t smem = Cfg<MODE>::SMEM;
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
@@ -770,7 +780,7 @@ int launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const Params& p, cud
   const long long tiles = (long long)p.E * tiles_per_matrix<MODE>(p.m, p.n);
   long long pairs = sm_count() / 2;
   if (tiles < pairs) pairs = tiles;
-  return launch_next(k, dim3((unsigned)(2 * pairs)), THREADS, smem, s, a, b, p);
+  return launch_next(k, dim3((unsigned)(2 * pairs)), THREADS, smem, s, a, t, a2, p);
 }
 
 template <int FROM, int KIND>
@@ -809,17 +819,20 @@ int run(const Source& src, int E, int M, int N, int steps, float a, float b, flo
   p.a = a, p.b = b, p.c = c;
   p.r = result;
   p.err = device_error_word(), p.wait_limit = g_wait_limit;
-  CUtensorMap mx, mx_cols, md, mp;
-  if (!map_half(&md, D, m, l.lda, m, E, 128) || !map_half(&mp, P, m, l.lda, m, E, 128)) return MOE_ERR_CUDA;
+  // by 128 rows of 64 of K, and (_t) turned: by 64 of K
+  CUtensorMap mx, mx_t, md, md_t, mp, mp_t;
+  if (!map_half(&md, D, m, l.lda, m, E, 128) || !map_half(&md_t, D, m, l.lda, m, E, 64) ||
+      !map_half(&mp, P, m, l.lda, m, E, 128) || !map_half(&mp_t, P, m, l.lda, m, E, 64))
+    return MOE_ERR_CUDA;
   for (int k = 0; k < steps; ++k) {
-    if (!map_half(&mx, x, n, l.ldx, m, E, 128) || !map_half(&mx_cols, x, n, l.ldx, m, E, 64)) return MOE_ERR_CUDA;
+    if (!map_half(&mx, x, n, l.ldx, m, E, 128) || !map_half(&mx_t, x, n, l.ldx, m, E, 64)) return MOE_ERR_CUDA;
     p.in = nullptr, p.out = D;
-    if ((r = launch_gemm<GRAM>(mx, mx, p, st)) != MOE_OK) return r;
+    if ((r = launch_gemm<GRAM>(mx, mx_t, mx, p, st)) != MOE_OK) return r;
     p.in = D, p.out = P;
-    if ((r = launch_gemm<POLY>(md, md, p, st)) != MOE_OK) return r;
+    if ((r = launch_gemm<POLY>(md, md_t, md, p, st)) != MOE_OK) return r;
     p.in = x, p.out = x2;
-    r = k + 1 < steps ? launch_gemm<APPLY>(mp, mx_cols, p, st)
-                      : launch_gemm<FINAL, KIND>(mp, mx_cols, p, st);
+    r = k + 1 < steps ? launch_gemm<APPLY>(mp, mx_t, mp_t, p, st)
+                      : launch_gemm<FINAL, KIND>(mp, mx_t, mp_t, p, st);
     if (r != MOE_OK) return r;
     __half* t = x;
     x = x2;
@@ -838,7 +851,7 @@ int launch_orthogonalize(const void* x, int E, int M, int N, int dtype, int step
   src.x = x;
   ns::Result r;
   r.o = static_cast<bf16*>(out);
-  r.tall = M > N, r.vec = N % (r.tall ? 2 : 8) == 0;
+  r.tall = M > N, r.vec = N % 4 == 0;
   return dtype == MOE_BF16 ? ns::run<ns::FROM_BF16, ns::ORTHO>(src, E, M, N, steps, a, b, c, eps, r, ws, s)
                            : ns::run<ns::FROM_F32, ns::ORTHO>(src, E, M, N, steps, a, b, c, eps, r, ws, s);
 }
@@ -851,7 +864,7 @@ int launch_muon_step(const void* w, const float* dw, const float* m, int E, int 
   ns::Result r;
   r.w = w, r.w_out = w_out, r.w_low = static_cast<bf16*>(w_low);
   r.keep = (float)(1.0 - (double)lr * decay), r.step = (float)((double)lr * scale);
-  r.tall = M > N, r.vec = N % (r.tall ? 2 : 8) == 0;
+  r.tall = M > N, r.vec = N % 4 == 0;
   return dtype == MOE_BF16 ? ns::run<ns::FROM_MOMENTUM, ns::MUON_BF16>(src, E, M, N, steps, a, b, c, eps, r, ws, s)
                            : ns::run<ns::FROM_MOMENTUM, ns::MUON_F32>(src, E, M, N, steps, a, b, c, eps, r, ws, s);
 }
