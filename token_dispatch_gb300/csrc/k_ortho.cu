@@ -122,7 +122,8 @@ struct Piece {
 __device__ __forceinline__ uint4* part_of(uint8_t* stg, int row, int part) {
   return reinterpret_cast<uint4*>(stg + row * 64 + ((part ^ (row >> 1 & 3)) << 4));
 }
-// rows row0 + lane / 4 + 8 k, columns col0 + 8 (lane % 4) .. of a matrix with `rows` rows (columns up to the row's padding)
+// rows row0 + lane / 4 + 8 k, columns col0 + 8 (lane % 4) .. of a matrix with `rows` rows (columns up to the row's
+// padding)
 __device__ __forceinline__ void load_piece(Piece& q, const __half* plane, long long ld, int row0, int col0, int rows,
                                            int lane) {
 #pragma unroll
@@ -195,7 +196,8 @@ __device__ __forceinline__ unsigned pack2(float a, float b) {
   return *reinterpret_cast<const unsigned*>(&h);
 }
 template <int KIND>
-__device__ __forceinline__ void put_tile(const Result& r, const Place& p, const Old<KIND>& old, const float* stg, int lane) {
+__device__ __forceinline__ void put_tile(const Result& r, const Place& p, const Old<KIND>& old, const float* stg,
+                                         int lane) {
   using T = typename std::conditional<KIND == MUON_F32, float, bf16>::type;
   bf16* low = KIND == ORTHO ? r.o : KIND == MUON_BF16 ? static_cast<bf16*>(r.w_out) : r.w_low;
 #pragma unroll
@@ -256,6 +258,8 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   const int K = MODE == GRAM ? p.n : p.m;
   const int cols = SYM ? p.m : p.n;
   const int kbs = (K + BK - 1) / BK;
+  // a tile with no more than 128 columns takes MMAs of half the width (and no use of half of its second operand)
+  auto narrow = [&](const Tile& w) { return cols - w.n0 <= BN / 2; };
   // Whether a block of the first operand (rows of tile row i) or of the second is read as it lies in the transposed
   // place, [64 of K][rows] in two boxes of 64 rows: D and P below the diagonal, and X as APPLY's second operand.
   auto a_turned = [&](int i, int kb) { return MODE != GRAM && kb / 4 < i; };
@@ -306,7 +310,7 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       bool ok = true;
       for (int t = pair; ok && t < total; t += n_pairs) {
         const Tile w = tile_of<MODE>(t, p, per, rank);
-        const int b0 = w.n0 + (int)rank * (BN / 2);
+        const int b0 = w.n0 + (int)rank * (narrow(w) ? BN / 4 : BN / 2);
         for (int kb = 0; kb < kbs; ++kb) {
           if (!wait_bounded(empty_bar(stage), phase ^ 1u, &abort_flag, p)) { ok = false; break; }
           const uint32_t a_dst = smem_u32(smem + stage * STAGE_BYTES), b_dst = a_dst + OPERAND_BYTES;
@@ -360,7 +364,8 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         const Tile w = tile_of<MODE>(t, p, per, 0);
         for (int kb = 0; kb < kbs; ++kb) {
           const bool at = a_turned(w.i, kb), bt = b_turned(w.j, kb);
-          const uint32_t idesc = instr_desc(2 * BM, BN, false, false, true) | (at ? 1u << 15 : 0u) | (bt ? 1u << 16 : 0u);
+          const uint32_t idesc = instr_desc(2 * BM, narrow(w) ? BN / 2 : BN, false, false, true) |
+                                 (at ? 1u << 15 : 0u) | (bt ? 1u << 16 : 0u);
           ok = __all_sync(0xffffffffu, wait_bounded(full_bar(stage), phase, &abort_flag, p));
           if (!ok) break;
           tc_fence_after();
@@ -369,8 +374,10 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 #pragma unroll
             for (int k = 0; k < BK / 16; ++k) {
               // as it lies: +32 bytes for 16 of K in the 128-byte row; turned: +16 rows, 64-wide boxes 8 KB apart
-              const uint64_t adesc = at ? smem_desc(a_t + k * 16 * 128, 64 * BK * 2, 1024) : smem_desc(a_t + k * 32, 16, 1024);
-              const uint64_t bdesc = bt ? smem_desc(b_t + k * 16 * 128, 64 * BK * 2, 1024) : smem_desc(b_t + k * 32, 16, 1024);
+              const uint64_t adesc =
+                  at ? smem_desc(a_t + k * 16 * 128, 64 * BK * 2, 1024) : smem_desc(a_t + k * 32, 16, 1024);
+              const uint64_t bdesc =
+                  bt ? smem_desc(b_t + k * 16 * 128, 64 * BK * 2, 1024) : smem_desc(b_t + k * 32, 16, 1024);
               tc_mma_pair(d_tmem, adesc, bdesc, idesc, (kb > 0 || k > 0) ? 1u : 0u);
             }
             tc_commit_pair(empty_bar(stage), 3);
@@ -630,8 +637,18 @@ __global__ void __launch_bounds__(SUM_NT) ns_sum_kernel(const Source s, long lon
   }
 }
 
-// 2^10 / (|U| + eps) of each matrix as the product of two floats, neither of which leaves the range; NaN for
-// one that holds a NaN or an infinity, 0 for one of zeros.  A warp a matrix.
+// 2^10 / (|U| + eps) as the product of two floats, neither of which leaves the range, from the three sums; NaN for
+// a matrix that holds a NaN or an infinity, 0 for one of zeros
+__device__ __forceinline__ float2 factor_of(const double (&v)[3], double eps) {
+  const double norm = v[0] > 0x1p100 ? sqrt(v[1]) * 0x1p80 : v[0] > 0x1p-60 ? sqrt(v[0]) : sqrt(v[2]) * 0x1p-80;
+  if (!(v[1] < HUGE_VAL)) return make_float2(NAN, NAN);
+  if (norm == 0) return make_float2(0.f, 0.f);
+  int e;
+  const double x = frexp(norm + eps, &e);  // norm + eps = x 2^e
+  return make_float2(ldexpf(1.f, -(e / 2)), (float)ldexp(1024.0 / x, -(e - e / 2)));
+}
+
+// The factor of each matrix, a warp a matrix.
 __global__ void __launch_bounds__(32) ns_factor_kernel(const double* __restrict__ part, int parts, double eps,
                                                        float2* __restrict__ factor) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -646,17 +663,7 @@ __global__ void __launch_bounds__(32) ns_factor_kernel(const double* __restrict_
   for (int k = 0; k < 3; ++k)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-  if (lane != 0) return;
-  const double norm = v[0] > 0x1p100 ? sqrt(v[1]) * 0x1p80 : v[0] > 0x1p-60 ? sqrt(v[0]) : sqrt(v[2]) * 0x1p-80;
-  float2 f = make_float2(0.f, 0.f);
-  if (!(v[1] < HUGE_VAL)) {
-    f = make_float2(NAN, NAN);
-  } else if (norm != 0) {
-    int e;
-    const double x = frexp(norm + eps, &e);  // norm + eps = x 2^e
-    f = make_float2(ldexpf(1.f, -(e / 2)), (float)ldexp(1024.0 / x, -(e - e / 2)));
-  }
-  factor[blockIdx.x] = f;
+  if (lane == 0) factor[blockIdx.x] = factor_of(v, eps);
 }
 
 // First X (fp16, times 2^10) from U, turned around where M > N: 64 x 64 tiles through shared
@@ -710,6 +717,268 @@ __global__ void __launch_bounds__(LOAD_NT) ns_load_kernel(const Source s, int M,
     const __half2 v = tall ? __halves2half2(tile[c][r], tile[c + 1][r]) : __halves2half2(tile[r][c], tile[r][c + 1]);
     // a column behind the last one lies in the row's padding
     if (xr0 + r < m && xc0 + c < n) *reinterpret_cast<__half2*>(plane + (long long)(xr0 + r) * ldx + xc0 + c) = v;
+  }
+}
+
+// ------------------------------------------------------- small matrices ---
+// m <= 128 and n <= 512: a CTA takes a matrix from U to the result, X and D (then P) in shared memory and the sums in
+// tensor memory.  A step is a few thousand cycles of products and epilogues one after the other, where the chain of
+// kernels above costs three launches (8 x 128 x 256: 128 us in 18 launches).  X lies as 64-column blocks of 128 rows of 128
+// bytes, 16-byte parts exchanged by the row's low bits: the tensor core reads such a block along its rows (GRAM) and
+// down its columns (APPLY).
+constexpr int SM_ROWS = 128, SM_COLS = 512;
+constexpr int SM_WARPS = 16;
+constexpr int SM_NT = 32 * SM_WARPS;
+constexpr int SM_BLOCK = SM_ROWS * 128;  // bytes of 64 columns
+constexpr size_t small_smem(int n) {     // X, D, and the result's staging tiles over and behind D
+  return (size_t)(n + 63) / 64 * SM_BLOCK + SM_WARPS * 32 * STG * 4 + 1024;
+}
+
+struct SmallParams {
+  Source src;
+  int M, N, steps;
+  float a, b, c;
+  double eps;
+  Result r;
+  unsigned* err;
+  unsigned long long wait_limit;
+};
+
+// 16-byte part of a row
+__device__ __forceinline__ uint4* small_part(uint8_t* base, int row, int part) {
+  return reinterpret_cast<uint4*>(base + (part >> 3) * SM_BLOCK + row * 128 + (((part & 7) ^ (row & 7)) << 4));
+}
+__device__ __forceinline__ void small_row(uint8_t* base, int row, int col0, uint4 (&q)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) q[k] = *small_part(base, row, col0 / 8 + k);
+}
+__device__ __forceinline__ void small_store(uint8_t* base, int row, int col0, const float (&v)[32]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint4 q;
+    __half2* h = reinterpret_cast<__half2*>(&q);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = __floats2half2_rn(v[8 * k + 2 * i], v[8 * k + 2 * i + 1]);
+    *small_part(base, row, col0 / 8 + k) = q;
+  }
+}
+
+template <int FROM, int KIND>
+__global__ void __launch_bounds__(SM_NT, 1) ns_small_kernel(const SmallParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* X = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t bar;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag;
+  __shared__ float s_of[SM_ROWS], d_of[SM_ROWS];
+  __shared__ double red[3][SM_WARPS];
+  __shared__ float2 factor;
+  const bool tall = p.M > p.N;
+  const int m = tall ? p.N : p.M, n = tall ? p.M : p.N, blocks = (n + 63) / 64;
+  uint8_t* D = X + blocks * SM_BLOCK;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int q = warp & 3, part = warp >> 2, row = q * 32 + lane;
+  const long long size = (long long)p.M * p.N, base = blockIdx.x * size;
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    mbar_init(smem_u32(&bar), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                 "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  // ---- norm (and the momentum)
+  const bool vec = p.N % 4 == 0;
+  Sums sums;
+  if (vec) {
+#pragma unroll 4
+    for (int i = 4 * threadIdx.x; i < size; i += 4 * SM_NT) {
+      const float4 u = u4_at<FROM, true>(p.src, base + i);
+      sums.add(u.x), sums.add(u.y), sums.add(u.z), sums.add(u.w);
+    }
+  } else {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < size; i += SM_NT) sums.add(u_at<FROM, true>(p.src, base + i));
+  }
+  double v3[3] = {sums.mid, sums.high, sums.low};
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v3[k] += __shfl_xor_sync(0xffffffffu, v3[k], o);
+    if (lane == 0) red[k][warp] = v3[k];
+  }
+  // X's padding takes part in the products: zeros
+  for (int i = threadIdx.x; i < blocks * SM_BLOCK / 16; i += SM_NT)
+    reinterpret_cast<uint4*>(X)[i] = make_uint4(0, 0, 0, 0);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (threadIdx.x == 0) {
+    double sum[3] = {0, 0, 0};
+    for (int w = 0; w < SM_WARPS; ++w)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) sum[k] += red[k][w];
+    factor = factor_of(sum, p.eps);
+  }
+  __syncthreads();
+  // ---- first X
+  {
+    const float2 f = factor;
+    auto put = [&](int r, int c, float u) {
+      const int i = tall ? c : r, j = tall ? r : c;
+      reinterpret_cast<__half*>(small_part(X, i, j / 8))[j % 8] = __float2half_rn(u * f.x * f.y);
+    };
+    if (vec) {
+#pragma unroll 4
+      for (int i = 4 * threadIdx.x; i < size; i += 4 * SM_NT) {
+        const float4 u = u4_at<FROM, false>(p.src, base + i);
+        const int r = i / p.N, c = i - r * p.N;
+        put(r, c, u.x), put(r, c + 1, u.y), put(r, c + 2, u.z), put(r, c + 3, u.w);
+      }
+    } else {
+#pragma unroll 4
+      for (int i = threadIdx.x; i < size; i += SM_NT) {
+        const int r = i / p.N;
+        put(r, i - r * p.N, u_at<FROM, false>(p.src, base + i));
+      }
+    }
+  }
+  const uint32_t tmem = tmem_slot, lanes = tmem + ((uint32_t)(q * 32) << 16);
+  const uint32_t xa = smem_u32(X), da = smem_u32(D);
+  uint32_t phase = 0;
+  // what the threads have written is the tensor core's to read; its sums, once they are there, the threads'
+  auto publish = [&]() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  };
+  auto summed = [&]() {
+    const bool ok = wait_bounded(smem_u32(&bar), phase, &abort_flag, p);
+    phase ^= 1u;
+    tc_fence_after();
+    return __syncthreads_and(ok) != 0;
+  };
+  const int ks = (m + 15) / 16;  // steps of 16 of K = m
+  bool ok = true;
+  for (int step = 0; step < p.steps && ok; ++step) {
+    publish();
+    if (warp == 0) {  // A = X X^T
+      constexpr uint32_t ID = instr_desc(SM_ROWS, SM_ROWS, false, false, true);
+      if (elect_one()) {
+        for (int k = 0; k < (n + 15) / 16; ++k) {
+          const uint64_t x = smem_desc(xa + k / 4 * SM_BLOCK + k % 4 * 32, 16, 1024);
+          tc_mma(tmem, x, x, ID, k > 0);
+        }
+        tc_commit(smem_u32(&bar));
+      }
+      __syncwarp();
+    }
+    ok = summed();
+    if (!ok) break;
+    float v[32];
+    const int col0 = part * 32;
+    tmem_ld32(lanes + col0, v);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] *= INV;
+    if (part == q) {  // the diagonal
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j == lane) {
+          s_of[row] = v[j] * INV;
+          v[j] = 0.f;
+        }
+    }
+    small_store(D, row, col0, v);
+    publish();
+    if (warp == 0) {  // D D
+      constexpr uint32_t ID = instr_desc(SM_ROWS, SM_ROWS, false, false, true);
+      if (elect_one()) {
+        for (int k = 0; k < ks; ++k) {
+          const uint64_t d = smem_desc(da + k / 4 * SM_BLOCK + k % 4 * 32, 16, 1024);
+          tc_mma(tmem, d, d, ID, k > 0);
+        }
+        tc_commit(smem_u32(&bar));
+      }
+      __syncwarp();
+    }
+    ok = summed();
+    if (!ok) break;
+    {
+      uint4 mine[4];
+      small_row(D, row, col0, mine);
+      const __half2* h = reinterpret_cast<const __half2*>(mine);
+      const float s_row = s_of[row], k0 = p.b + p.c * s_row, k1 = p.c * INV;
+      tmem_ld32(lanes + col0, v);
+      if (part == q) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (j == lane) d_of[row] = p.a + (p.b + p.c * s_row) * s_row + k1 * INV * v[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        const float2 x = __half22float2(h[j / 2]);
+        v[j] = fmaf(k1, v[j], fmaf(p.c, s_of[col0 + j], k0) * x.x);
+        v[j + 1] = fmaf(k1, v[j + 1], fmaf(p.c, s_of[col0 + j + 1], k0) * x.y);
+      }
+      if (part == q) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          if (j == lane) v[j] = 0.f;
+      }
+      small_store(D, row, col0, v);
+    }
+    publish();
+    if (warp == 0) {  // P X, up to 256 columns an MMA
+      if (elect_one()) {
+        for (int c = 0; c < n; c += 256) {
+          const uint32_t ID = instr_desc(SM_ROWS, min(256, (n - c + 15) / 16 * 16), false, true, true);
+          for (int k = 0; k < ks; ++k)
+            tc_mma(tmem + c, smem_desc(da + k / 4 * SM_BLOCK + k % 4 * 32, 16, 1024),
+                   smem_desc(xa + c / 64 * SM_BLOCK + k * 16 * 128, SM_BLOCK, 1024), ID, k > 0);
+        }
+        tc_commit(smem_u32(&bar));
+      }
+      __syncwarp();
+    }
+    ok = summed();
+    if (!ok) break;
+    const float d_row = d_of[row];
+    const bool last = step + 1 == p.steps;
+    for (int c0 = part * 32; c0 < n; c0 += 32 * (SM_WARPS / 4)) {
+      uint4 mine[4];
+      small_row(X, row, c0, mine);
+      const __half2* h = reinterpret_cast<const __half2*>(mine);
+      tmem_ld32(lanes + c0, v);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float2 x = __half22float2(h[j]);
+        // a column behind the last one has no sums
+        v[2 * j] = c0 + 2 * j < n ? fmaf(d_row, x.x, v[2 * j] * INV) : 0.f;
+        v[2 * j + 1] = c0 + 2 * j + 1 < n ? fmaf(d_row, x.y, v[2 * j + 1] * INV) : 0.f;
+      }
+      if (!last) {
+        small_store(X, row, c0, v);
+        continue;
+      }
+      float* wide = reinterpret_cast<float*>(D) + warp * 32 * STG;
+      const Place place = tall ? Place{base, c0, q * 32, n, m} : Place{base, q * 32, c0, m, n};
+      Old<KIND> old;
+      old.load(p.r, place, lane);
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 32; ++j) wide[tall ? j * STG + lane : lane * STG + j] = v[j] * INV;
+      __syncwarp();
+      put_tile<KIND>(p.r, place, old, wide, lane);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
   }
 }
 
@@ -786,8 +1055,19 @@ int launch_gemm(const CUtensorMap& a, const CUtensorMap& t, const CUtensorMap& a
 template <int FROM, int KIND>
 int run(const Source& src, int E, int M, int N, int steps, float a, float b, float c, float eps, const Result& result,
         void* ws, cudaStream_t st) {
-  const Layout l = layout(E, M, N);
   const int m = M < N ? M : N, n = M < N ? N : M;
+  if (m <= SM_ROWS && n <= SM_COLS) {
+    SmallParams sp;
+    sp.src = src, sp.M = M, sp.N = N, sp.steps = steps, sp.a = a, sp.b = b, sp.c = c, sp.eps = eps, sp.r = result;
+    sp.err = device_error_word(), sp.wait_limit = g_wait_limit;
+    auto k = ns_small_kernel<FROM, KIND>;
+    static_assert(small_smem(SM_COLS) + 2048 <= 227 * 1024, "shared memory");
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)small_smem(SM_COLS)) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    k<<<E, SM_NT, small_smem(n), st>>>(sp);
+    return launch_status();
+  }
+  const Layout l = layout(E, M, N);
   uint8_t* base = static_cast<uint8_t*>(ws);
   double* part = reinterpret_cast<double*>(base + l.part);
   const long long size = (long long)M * N;
