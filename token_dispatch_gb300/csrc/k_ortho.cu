@@ -160,6 +160,17 @@ __device__ __forceinline__ void store_tile(__half* plane, long long ld, int row0
   }
 }
 
+// v[at], which becomes 0; nothing where `at` is outside 0..31
+__device__ __forceinline__ float take_diagonal(float (&v)[32], int at) {
+  float own = 0.f;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    own = j == at ? v[j] : own;
+    v[j] = j == at ? 0.f : v[j];
+  }
+  return own;
+}
+
 // ---- the result.  A warp's tile lies in shared memory by rows of the result (turned around for a tall one); in round
 // k a lane has four neighbours of row lane / 8 + 4 k.
 struct Place {  // the tile's corner in a matrix of `rows` rows of `len`, which begins at `plane`
@@ -301,49 +312,49 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      asm volatile("griddepcontrol.wait;" ::: "memory");
-      int stage = 0;
-      uint32_t phase = 0;
-      int filled[STAGES];
-      for (int s = 0; s < STAGES; ++s) filled[s] = -1;
-      bool ok = true;
-      for (int t = pair; ok && t < total; t += n_pairs) {
-        const Tile w = tile_of<MODE>(t, p, per, rank);
-        const int b0 = w.n0 + (int)rank * (narrow(w) ? BN / 4 : BN / 2);
-        for (int kb = 0; kb < kbs; ++kb) {
-          if (!wait_bounded(empty_bar(stage), phase ^ 1u, &abort_flag, p)) { ok = false; break; }
-          const uint32_t a_dst = smem_u32(smem + stage * STAGE_BYTES), b_dst = a_dst + OPERAND_BYTES;
-          if (leader) {
-            mbar_expect_tx(full_bar(stage), 2 * STAGE_BYTES);
-            filled[stage] = (int)phase;
-          }
-          const uint32_t fb = cluster_addr(full_bar(stage), 0);
+    // one thread issues, but the warp walks along: see elect_one
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int stage = 0, filled = 0;  // stages filled so far
+    uint32_t phase = 0;
+    bool ok = true;
+    const uint32_t full0 = cluster_addr(full_bar(0), 0);  // the leader's, 8 bytes apart
+    for (int t = pair; ok && t < total; t += n_pairs) {
+      const Tile w = tile_of<MODE>(t, p, per, rank);
+      const int b0 = w.n0 + (int)rank * (narrow(w) ? BN / 4 : BN / 2);
+      for (int kb = 0; kb < kbs; ++kb) {
+        ok = __all_sync(0xffffffffu, wait_bounded(empty_bar(stage), phase ^ 1u, &abort_flag, p));
+        if (!ok) break;
+        const uint32_t a_dst = smem_u32(smem + stage * STAGE_BYTES), b_dst = a_dst + OPERAND_BYTES;
+        const uint32_t fb = full0 + 8 * stage;
+        const bool at = a_turned(w.i, kb), bt = b_turned(w.j, kb);
+        if (elect_one()) {
+          if (leader) mbar_expect_tx(full_bar(stage), 2 * STAGE_BYTES);
           // the maps of the turned boxes: of D (POLY), of P and of X (APPLY: P's is tmA2)
-          if (a_turned(w.i, kb)) {
+          if (at) {
 #pragma unroll
             for (int c = 0; c < 2; ++c)
               tma_load_3d_pair(a_dst + c * (64 * BK * 2), SYM ? &tmT : &tmA2, fb, w.row0 + c * 64, kb * BK, w.e);
           } else {
             tma_load_3d_pair(a_dst, &tmA, fb, kb * BK, w.row0, w.e);
           }
-          if (b_turned(w.j, kb)) {
+          if (bt) {
 #pragma unroll
             for (int c = 0; c < 2; ++c)
               tma_load_3d_pair(b_dst + c * (64 * BK * 2), &tmT, fb, b0 + c * 64, kb * BK, w.e);
           } else {
             tma_load_3d_pair(b_dst, &tmA, fb, kb * BK, b0, w.e);
           }
-          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
+        __syncwarp();
+        ++filled;
+        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
       }
-      if (leader) {  // every stage filled must have landed, both CTAs' bytes
-        for (int s = 0; s < STAGES; ++s) {
-          if (filled[s] < 0) continue;
-          const long long t0 = clock64();
-          while (!mbar_try_wait(full_bar(s), (uint32_t)filled[s])) {
-            if ((unsigned long long)(clock64() - t0) > DRAIN_LIMIT) { set_error(p.err, DEV_TIMEOUT); break; }
-          }
+    }
+    if (leader && lane == 0) {  // every stage filled must have landed, both CTAs' bytes
+      for (int k = max(0, filled - STAGES); k < filled; ++k) {
+        const long long t0 = clock64();
+        while (!mbar_try_wait(full_bar(k % STAGES), (uint32_t)(k / STAGES) & 1u)) {
+          if ((unsigned long long)(clock64() - t0) > DRAIN_LIMIT) { set_error(p.err, DEV_TIMEOUT); break; }
         }
       }
     }
@@ -465,35 +476,24 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] *= INV;  // A, held times 2^10
           if (w.i == w.j) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (col0 + j == row) {
-                if (row_ok) p.s[(long long)w.e * p.lda + row] = v[j] * INV;
-                v[j] = 0.f;
-              }
+            const float own = take_diagonal(v, row - col0);
+            if (row_ok && row >= col0 && row < col0 + 32) p.s[(long long)w.e * p.lda + row] = own * INV;
           }
         } else if (MODE == POLY) {
           const float k0 = p.b + p.c * s_row, k1 = p.c * INV;
-          float own = 0.f;  // (D D)_ii
+          if (w.i == w.j) {
+            const float own = take_diagonal(v, row - col0);  // (D D)_ii; D_ii is 0, and so is P_ii then
+            if (row_ok && row >= col0 && row < col0 + 32)
+              p.d[(long long)w.e * p.lda + row] = p.a + (p.b + p.c * s_row) * s_row + k1 * INV * own;
+          }
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
             const float4 sj = *reinterpret_cast<const float4*>(diag + cc * 32 + j);
             const float2 x0 = __half22float2(h[j / 2]), x1 = __half22float2(h[j / 2 + 1]);
-            if (w.i == w.j) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                if (col0 + j + k == row) own = v[j + k];
-            }
             v[j] = fmaf(k1, v[j], fmaf(p.c, sj.x, k0) * x0.x);
             v[j + 1] = fmaf(k1, v[j + 1], fmaf(p.c, sj.y, k0) * x0.y);
             v[j + 2] = fmaf(k1, v[j + 2], fmaf(p.c, sj.z, k0) * x1.x);
             v[j + 3] = fmaf(k1, v[j + 3], fmaf(p.c, sj.w, k0) * x1.y);
-          }
-          if (w.i == w.j && row_ok && row >= col0 && row < col0 + 32) {
-            p.d[(long long)w.e * p.lda + row] = p.a + (p.b + p.c * s_row) * s_row + k1 * INV * own;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (col0 + j == row) v[j] = 0.f;
           }
         } else {
 #pragma unroll
@@ -770,8 +770,8 @@ __global__ void __launch_bounds__(SM_NT, 1) ns_small_kernel(const SmallParams p)
   __shared__ uint64_t bar;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
-  __shared__ float s_of[SM_ROWS], d_of[SM_ROWS];
-  __shared__ double red[3][SM_WARPS];
+  __shared__ __align__(16) float s_of[SM_ROWS], d_of[SM_ROWS];
+  __shared__ float red[3][SM_WARPS];
   __shared__ float2 factor;
   const bool tall = p.M > p.N;
   const int m = tall ? p.N : p.M, n = tall ? p.M : p.N, blocks = (n + 63) / 64;
@@ -789,25 +789,26 @@ __global__ void __launch_bounds__(SM_NT, 1) ns_small_kernel(const SmallParams p)
                  "r"(512u));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  // ---- norm (and the momentum)
+  // ---- norm (and the momentum): a warp takes every SM_WARPS-th row.  fp32 sums of at most 65536 squares: their
+  // rounding moves X by a common factor alone.
   const bool vec = p.N % 4 == 0;
   Sums sums;
-  if (vec) {
+  for (int r = warp; r < p.M; r += SM_WARPS) {
+    const long long at = base + (long long)r * p.N;
+    if (vec) {
 #pragma unroll 4
-    for (int i = 4 * threadIdx.x; i < size; i += 4 * SM_NT) {
-      const float4 u = u4_at<FROM, true>(p.src, base + i);
-      sums.add(u.x), sums.add(u.y), sums.add(u.z), sums.add(u.w);
+      for (int c = 4 * lane; c < p.N; c += 128) {
+        const float4 u = u4_at<FROM, true>(p.src, at + c);
+        sums.add(u.x), sums.add(u.y), sums.add(u.z), sums.add(u.w);
+      }
+    } else {
+#pragma unroll 4
+      for (int c = lane; c < p.N; c += 32) sums.add(u_at<FROM, true>(p.src, at + c));
     }
-  } else {
-#pragma unroll 4
-    for (int i = threadIdx.x; i < size; i += SM_NT) sums.add(u_at<FROM, true>(p.src, base + i));
   }
-  double v3[3] = {sums.mid, sums.high, sums.low};
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v3[k] += __shfl_xor_sync(0xffffffffu, v3[k], o);
-    if (lane == 0) red[k][warp] = v3[k];
+  {
+    const float v3[3] = {warp_sum(sums.mid), warp_sum(sums.high), warp_sum(sums.low)};
+    if (lane < 3) red[lane][warp] = lane == 0 ? v3[0] : lane == 1 ? v3[1] : v3[2];
   }
   // X's padding takes part in the products: zeros
   for (int i = threadIdx.x; i < blocks * SM_BLOCK / 16; i += SM_NT)
@@ -816,32 +817,39 @@ __global__ void __launch_bounds__(SM_NT, 1) ns_small_kernel(const SmallParams p)
   __syncthreads();
   tc_fence_after();
   if (threadIdx.x == 0) {
-    double sum[3] = {0, 0, 0};
+    float sum[3] = {0.f, 0.f, 0.f};
+#pragma unroll
     for (int w = 0; w < SM_WARPS; ++w)
 #pragma unroll
       for (int k = 0; k < 3; ++k) sum[k] += red[k][w];
-    factor = factor_of(sum, p.eps);
+    const double v3[3] = {sum[0], sum[1], sum[2]};
+    factor = factor_of(v3, p.eps);
   }
   __syncthreads();
   // ---- first X
   {
     const float2 f = factor;
-    auto put = [&](int r, int c, float u) {
-      const int i = tall ? c : r, j = tall ? r : c;
-      reinterpret_cast<__half*>(small_part(X, i, j / 8))[j % 8] = __float2half_rn(u * f.x * f.y);
-    };
-    if (vec) {
+    auto place = [&](int i, int j) { return reinterpret_cast<__half*>(small_part(X, i, j / 8)) + j % 8; };
+    for (int r = warp; r < p.M; r += SM_WARPS) {
+      const long long at = base + (long long)r * p.N;
+      if (vec) {
 #pragma unroll 4
-      for (int i = 4 * threadIdx.x; i < size; i += 4 * SM_NT) {
-        const float4 u = u4_at<FROM, false>(p.src, base + i);
-        const int r = i / p.N, c = i - r * p.N;
-        put(r, c, u.x), put(r, c + 1, u.y), put(r, c + 2, u.z), put(r, c + 3, u.w);
-      }
-    } else {
+        for (int c = 4 * lane; c < p.N; c += 128) {
+          const float4 u = u4_at<FROM, false>(p.src, at + c);
+          const __half2 lo = __floats2half2_rn(u.x * f.x * f.y, u.y * f.x * f.y);
+          const __half2 hi = __floats2half2_rn(u.z * f.x * f.y, u.w * f.x * f.y);
+          if (tall) {
+            *place(c, r) = __low2half(lo), *place(c + 1, r) = __high2half(lo);
+            *place(c + 2, r) = __low2half(hi), *place(c + 3, r) = __high2half(hi);
+          } else {
+            __half2* dst = reinterpret_cast<__half2*>(place(r, c));
+            dst[0] = lo, dst[1] = hi;
+          }
+        }
+      } else {
 #pragma unroll 4
-      for (int i = threadIdx.x; i < size; i += SM_NT) {
-        const int r = i / p.N;
-        put(r, i - r * p.N, u_at<FROM, false>(p.src, base + i));
+        for (int c = lane; c < p.N; c += 32)
+          *(tall ? place(c, r) : place(r, c)) = __float2half_rn(u_at<FROM, false>(p.src, at + c) * f.x * f.y);
       }
     }
   }
@@ -883,14 +891,7 @@ __global__ void __launch_bounds__(SM_NT, 1) ns_small_kernel(const SmallParams p)
     tmem_ld32(lanes + col0, v);
 #pragma unroll
     for (int j = 0; j < 32; ++j) v[j] *= INV;
-    if (part == q) {  // the diagonal
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j == lane) {
-          s_of[row] = v[j] * INV;
-          v[j] = 0.f;
-        }
-    }
+    if (part == q) s_of[row] = take_diagonal(v, lane) * INV;
     small_store(D, row, col0, v);
     publish();
     if (warp == 0) {  // D D
@@ -912,21 +913,16 @@ __global__ void __launch_bounds__(SM_NT, 1) ns_small_kernel(const SmallParams p)
       const __half2* h = reinterpret_cast<const __half2*>(mine);
       const float s_row = s_of[row], k0 = p.b + p.c * s_row, k1 = p.c * INV;
       tmem_ld32(lanes + col0, v);
-      if (part == q) {
+      // D_ii is 0, so P_ii comes out 0 once (D D)_ii has been taken
+      if (part == q) d_of[row] = p.a + (p.b + p.c * s_row) * s_row + k1 * INV * take_diagonal(v, lane);
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (j == lane) d_of[row] = p.a + (p.b + p.c * s_row) * s_row + k1 * INV * v[j];
-      }
-#pragma unroll
-      for (int j = 0; j < 32; j += 2) {
-        const float2 x = __half22float2(h[j / 2]);
-        v[j] = fmaf(k1, v[j], fmaf(p.c, s_of[col0 + j], k0) * x.x);
-        v[j + 1] = fmaf(k1, v[j + 1], fmaf(p.c, s_of[col0 + j + 1], k0) * x.y);
-      }
-      if (part == q) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (j == lane) v[j] = 0.f;
+      for (int j = 0; j < 32; j += 4) {
+        const float4 sj = *reinterpret_cast<const float4*>(s_of + col0 + j);
+        const float2 x0 = __half22float2(h[j / 2]), x1 = __half22float2(h[j / 2 + 1]);
+        v[j] = fmaf(k1, v[j], fmaf(p.c, sj.x, k0) * x0.x);
+        v[j + 1] = fmaf(k1, v[j + 1], fmaf(p.c, sj.y, k0) * x0.y);
+        v[j + 2] = fmaf(k1, v[j + 2], fmaf(p.c, sj.z, k0) * x1.x);
+        v[j + 3] = fmaf(k1, v[j + 3], fmaf(p.c, sj.w, k0) * x1.y);
       }
       small_store(D, row, col0, v);
     }
