@@ -67,7 +67,7 @@ def run(x, dtype, steps=5, coef=COEF, eps=EPS, stream=None):
 
 SHAPES = [(1, 1, 1), (2, 1, 9), (3, 16, 24), (2, 40, 17), (5, 64, 64), (2, 130, 300), (1, 257, 255), (3, 300, 33),
           (2, 512, 256), (1, 384, 1000), (1, 777, 601), (70, 8, 8), (2, 128, 512), (1, 512, 97), (1, 128, 513),
-          (2, 129, 140), (1, 520, 384), (3, 64, 450)]
+          (2, 129, 140), (1, 520, 384), (3, 64, 450), (1, 300, 2500), (2, 2100, 260)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])

@@ -46,7 +46,8 @@ constexpr int STG = 36;       // floats between the rows of FINAL's staging tile
 constexpr float HELD = 1024.f;  // X, D and P are stored times this
 constexpr float INV = 1.f / 1024.f;
 
-enum Mode { GRAM = 0, POLY = 1, APPLY = 2, FINAL = 3 };
+// PART: GRAM's sums over a part of K
+enum Mode { GRAM = 0, POLY = 1, APPLY = 2, FINAL = 3, PART = 4 };
 enum Kind { ORTHO = 0, MUON_BF16 = 1, MUON_F32 = 2 };  // what FINAL writes
 template <int MODE>
 struct Cfg {
@@ -80,22 +81,32 @@ struct Params {
   Result r;
   unsigned* err;
   unsigned long long wait_limit;
+  int splits = 1;          // PART: parts of K
+  float4* part = nullptr;  // their sums, [part][tile][256 / 128 rows][64 quads of columns][128 rows]
 };
 
 struct Tile {
   int e, i, j, row0, n0;
+  int split, index;  // PART: part of K, and tile of all matrices
 };
 template <int MODE>
 __host__ __device__ inline int tiles_per_matrix(int m, int n) {
   const int mt = (m + 255) / 256, nt = (n + 255) / 256;
-  return MODE == GRAM || MODE == POLY ? mt * (mt + 1) / 2 : mt * nt;
+  return MODE == GRAM || MODE == POLY || MODE == PART ? mt * (mt + 1) / 2 : mt * nt;
 }
 template <int MODE>
 __device__ __forceinline__ Tile tile_of(int t, const Params& p, int per, uint32_t rank) {
   Tile w;
+  w.split = 0;
+  if (MODE == PART) {
+    const int tiles = p.E * per;
+    w.split = t / tiles;
+    t -= w.split * tiles;
+  }
+  w.index = t;
   w.e = t / per;
   const int r = t - w.e * per;
-  if (MODE == GRAM || MODE == POLY) {  // column blocks from the left, i <= j in each
+  if (MODE == GRAM || MODE == POLY || MODE == PART) {  // column blocks from the left, i <= j in each
     int j = (int)((sqrtf(8.f * r + 1.f) - 1.f) * 0.5f);
     while (j * (j + 1) / 2 > r) --j;
     while ((j + 1) * (j + 2) / 2 <= r) ++j;
@@ -251,7 +262,8 @@ template <int MODE, int KIND = ORTHO>
 __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
 ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmT,
                const __grid_constant__ CUtensorMap tmA2, const Params p) {
-  constexpr bool SYM = MODE == GRAM || MODE == POLY;
+  constexpr bool SYM = MODE == GRAM || MODE == POLY || MODE == PART;
+  constexpr bool FIRST = MODE == GRAM || MODE == PART;  // X X^T
   constexpr int STAGES = Cfg<MODE>::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -265,15 +277,18 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   const bool leader = rank == 0;
   const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
   const int per = tiles_per_matrix<MODE>(p.m, p.n);
-  const int total = p.E * per;
-  const int K = MODE == GRAM ? p.n : p.m;
+  const int total = p.E * per * (MODE == PART ? p.splits : 1);
+  const int K = FIRST ? p.n : p.m;
   const int cols = SYM ? p.m : p.n;
   const int kbs = (K + BK - 1) / BK;
+  // the blocks of K that a tile sums over
+  auto k_begin = [&](const Tile& w) { return MODE == PART ? (int)((long long)kbs * w.split / p.splits) : 0; };
+  auto k_end = [&](const Tile& w) { return MODE == PART ? (int)((long long)kbs * (w.split + 1) / p.splits) : kbs; };
   // a tile with no more than 128 columns takes MMAs of half the width (and no use of half of its second operand)
   auto narrow = [&](const Tile& w) { return cols - w.n0 <= BN / 2; };
   // Whether a block of the first operand (rows of tile row i) or of the second is read as it lies in the transposed
   // place, [64 of K][rows] in two boxes of 64 rows: D and P below the diagonal, and X as APPLY's second operand.
-  auto a_turned = [&](int i, int kb) { return MODE != GRAM && kb / 4 < i; };
+  auto a_turned = [&](int i, int kb) { return !FIRST && kb / 4 < i; };
   auto b_turned = [&](int j, int kb) { return MODE == POLY ? kb / 4 < j : !SYM; };
 
   auto full_bar = [&](int s) { return smem_u32(&bars[s]); };
@@ -321,7 +336,7 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     for (int t = pair; ok && t < total; t += n_pairs) {
       const Tile w = tile_of<MODE>(t, p, per, rank);
       const int b0 = w.n0 + (int)rank * (narrow(w) ? BN / 4 : BN / 2);
-      for (int kb = 0; kb < kbs; ++kb) {
+      for (int kb = k_begin(w); kb < k_end(w); ++kb) {
         ok = __all_sync(0xffffffffu, wait_bounded(empty_bar(stage), phase ^ 1u, &abort_flag, p));
         if (!ok) break;
         const uint32_t a_dst = smem_u32(smem + stage * STAGE_BYTES), b_dst = a_dst + OPERAND_BYTES;
@@ -373,7 +388,8 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BN;
         const Tile w = tile_of<MODE>(t, p, per, 0);
-        for (int kb = 0; kb < kbs; ++kb) {
+        const int kb0 = k_begin(w);
+        for (int kb = kb0; kb < k_end(w); ++kb) {
           const bool at = a_turned(w.i, kb), bt = b_turned(w.j, kb);
           const uint32_t idesc = instr_desc(2 * BM, narrow(w) ? BN / 2 : BN, false, false, true) |
                                  (at ? 1u << 15 : 0u) | (bt ? 1u << 16 : 0u);
@@ -389,7 +405,7 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                   at ? smem_desc(a_t + k * 16 * 128, 64 * BK * 2, 1024) : smem_desc(a_t + k * 32, 16, 1024);
               const uint64_t bdesc =
                   bt ? smem_desc(b_t + k * 16 * 128, 64 * BK * 2, 1024) : smem_desc(b_t + k * 32, 16, 1024);
-              tc_mma_pair(d_tmem, adesc, bdesc, idesc, (kb > 0 || k > 0) ? 1u : 0u);
+              tc_mma_pair(d_tmem, adesc, bdesc, idesc, (kb > kb0 || k > 0) ? 1u : 0u);
             }
             tc_commit_pair(empty_bar(stage), 3);
           }
@@ -429,9 +445,9 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       // What the epilogue reads is asked for before the sums are waited for.
       const long long ldi = MODE == POLY ? p.lda : p.ldx;
       const __half* in = p.in + (long long)w.e * p.m * ldi;
-      Piece piece[ALL ? CHUNKS : 2];
+      Piece piece[ALL ? CHUNKS : FIRST ? 1 : 2];
       float s_row = 0.f, d_row = 0.f;
-      if (MODE != GRAM) {
+      if (!FIRST) {
 #pragma unroll
         for (int c = 0; c < (ALL ? CHUNKS : 1); ++c)
           if (c_begin + c < c_end) load_piece(piece[c], in, ldi, row0, w.n0 + (c_begin + c) * 32, p.m, lane);
@@ -468,11 +484,16 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         }
         const int col0 = w.n0 + c * 32;
         uint4 mine[4];
-        if (MODE != GRAM) own_row(piece[ALL ? cc : cc % 2], stg, lane, mine);
+        if (!FIRST) own_row(piece[ALL ? cc : FIRST ? 0 : cc % 2], stg, lane, mine);
         const __half2* h = reinterpret_cast<const __half2*>(mine);
         float v[32];
         tmem_ld32(tbase + c * 32, v);
-        if (MODE == GRAM) {
+        if (MODE == PART) {
+          float4* dst = p.part + (((long long)w.split * (p.E * per) + w.index) * 2 + rank) * (64 * BM) + q * 32 + lane;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            dst[(c * 8 + j) * BM] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+        } else if (MODE == GRAM) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] *= INV;  // A, held times 2^10
           if (w.i == w.j) {
@@ -516,7 +537,7 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           }
           __syncwarp();
           put_tile<KIND>(p.r, place(c), old[cc % 2], wide, lane);
-        } else {
+        } else if (MODE != PART) {
           const long long ldo = SYM ? p.lda : p.ldx;
           store_tile(p.out + (long long)w.e * p.m * ldo, ldo, row0, col0, p.m, stg, lane, v);
         }
@@ -537,6 +558,33 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(2u * BN));
   }
+}
+
+// GRAM's parts added in order, and its epilogue: a block takes 4 columns x 128 rows of a tile, a thread a row of them.
+__global__ void __launch_bounds__(BM) ns_join_kernel(const Params p, int per) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int quad = blockIdx.x, rank = blockIdx.y, tiles = p.E * per;
+  const Tile w = tile_of<GRAM>(blockIdx.z, p, per, rank);
+  const int row = w.row0 + threadIdx.x, col = w.n0 + 4 * quad;
+  if (row >= p.m || col >= p.m) return;
+  const float4* src = p.part + ((long long)w.index * 2 + rank) * (64 * BM) + quad * BM + threadIdx.x;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = 0; k < p.splits; ++k) {
+    const float4 x = src[(long long)k * tiles * (2 * 64 * BM)];
+    v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+  }
+  float a[4] = {v.x * INV, v.y * INV, v.z * INV, v.w * INV};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (col + j == row) {
+      p.s[(long long)w.e * p.lda + row] = a[j] * INV;
+      a[j] = 0.f;
+    }
+  uint2 q;
+  reinterpret_cast<__half2*>(&q)[0] = __floats2half2_rn(a[0], a[1]);
+  reinterpret_cast<__half2*>(&q)[1] = __floats2half2_rn(a[2], a[3]);
+  *reinterpret_cast<uint2*>(p.out + ((long long)w.e * p.m + row) * p.lda + col) = q;
 }
 
 // ------------------------------------------------------- norm and first X ---
@@ -983,7 +1031,8 @@ inline long long up(long long v, long long k) { return (v + k - 1) / k * k; }
 
 struct Layout {
   long long ldx, lda;
-  size_t x[2], d, p, s, diag, part, factor, bytes;
+  size_t x[2], d, p, s, diag, part, factor, grams, bytes;
+  int splits;
 };
 Layout layout(int E, int M, int N) {
   Layout l;
@@ -1003,6 +1052,13 @@ Layout layout(int E, int M, int N) {
   l.diag = take((size_t)E * l.lda * 4);
   l.part = take((size_t)E * PARTS * 3 * 8);
   l.factor = take((size_t)E * 8);
+  // Few and long sums X X^T are shared out along K where at least three pairs of SMs can take one, eight blocks of
+  // 64 or more each: 1 x 7168 x 384 281 -> FIGURE us.  With two to a sum the parts' way through memory eats the gain.
+  const long long tiles = (long long)E * tiles_per_matrix<GRAM>((int)m, (int)n);
+  const long long by_sms = sm_count() / 2 / tiles, by_k = up(n, BK) / BK / 8;
+  l.splits = (int)(by_sms < by_k ? by_sms : by_k);
+  if (l.splits < 3) l.splits = 1;
+  l.grams = take(l.splits > 1 ? (size_t)l.splits * tiles * (2 * 64 * BM) * sizeof(float4) : 0);
   l.bytes = at;
   return l;
 }
@@ -1042,7 +1098,7 @@ int launch_gemm(const CUtensorMap& a, const CUtensorMap& t, const CUtensorMap& a
   constexpr size_t smem = Cfg<MODE>::SMEM;
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return MOE_ERR_CUDA;
-  const long long tiles = (long long)p.E * tiles_per_matrix<MODE>(p.m, p.n);
+  const long long tiles = (long long)p.E * tiles_per_matrix<MODE>(p.m, p.n) * (MODE == PART ? p.splits : 1);
   long long pairs = sm_count() / 2;
   if (tiles < pairs) pairs = tiles;
   return launch_next(k, dim3((unsigned)(2 * pairs)), THREADS, smem, s, a, t, a2, p);
@@ -1095,6 +1151,7 @@ int run(const Source& src, int E, int M, int N, int steps, float a, float b, flo
   p.a = a, p.b = b, p.c = c;
   p.r = result;
   p.err = device_error_word(), p.wait_limit = g_wait_limit;
+  p.splits = l.splits, p.part = reinterpret_cast<float4*>(base + l.grams);
   // by 128 rows of 64 of K, and (_t) turned: by 64 of K
   CUtensorMap mx, mx_t, md, md_t, mp, mp_t;
   if (!map_half(&md, D, m, l.lda, m, E, 128) || !map_half(&md_t, D, m, l.lda, m, E, 64) ||
@@ -1103,7 +1160,14 @@ int run(const Source& src, int E, int M, int N, int steps, float a, float b, flo
   for (int k = 0; k < steps; ++k) {
     if (!map_half(&mx, x, n, l.ldx, m, E, 128) || !map_half(&mx_t, x, n, l.ldx, m, E, 64)) return MOE_ERR_CUDA;
     p.in = nullptr, p.out = D;
-    if ((r = launch_gemm<GRAM>(mx, mx_t, mx, p, st)) != MOE_OK) return r;
+    if (l.splits > 1) {
+      if ((r = launch_gemm<PART>(mx, mx_t, mx, p, st)) != MOE_OK) return r;
+      const int per = tiles_per_matrix<GRAM>(m, n);
+      r = launch_next(ns_join_kernel, dim3(64, 2, (unsigned)(E * per)), BM, 0, st, p, per);
+    } else {
+      r = launch_gemm<GRAM>(mx, mx_t, mx, p, st);
+    }
+    if (r != MOE_OK) return r;
     p.in = D, p.out = P;
     if ((r = launch_gemm<POLY>(md, md_t, md, p, st)) != MOE_OK) return r;
     p.in = x, p.out = x2;

@@ -30,127 +30,229 @@ __device__ __forceinline__ float scale_of(float amax) {
   const float s = __uint_as_float((__float_as_uint(amax * (1.f / 7.f)) + 0x7ffffu) & ~0x7ffffu);
   return fmaxf(s, 1.1754943508222875e-38f);
 }
-__device__ __forceinline__ unsigned code_of(float w, float s) {
-  const float q = rintf(w / s);
-  return isnan(q) ? 8u : (unsigned)((int)q + 8);
-}
 __device__ __forceinline__ int shift_of(int i) { return 4 * (i >> 1) + 16 * (i & 1); }
-__device__ __forceinline__ float max_abs(float a, float v) {  // keeps a NaN
-  v = fabsf(v);
-  return v > a || v != v ? v : a;
+// A word of 8 codes.  w / s is the quotient rounded to fp32, and then to the nearest integer, halves to even.  It is
+// formed by Markstein's theorem (IBM J. Res. Dev. 34, 1990): with y = 1 / s rounded, q = w y and r = w - q s exact,
+// q + r y rounded once is w / s rounded once (but where s has a significand of ones alone; it has 5 bits).  Where r might
+// fall below the least number the division itself is made.  Adding 1.5 * 2^23 + 8 rounds to an integer and leaves
+// code + 8 in the low bits.  (With a division, a rounding and a conversion for each value their pipes took three
+// times as long as the memory: 248 us for 64 x 2048 x 1408 bf16, axis 1.)
+__device__ __forceinline__ unsigned word_of_codes(const float (&v)[8], float s) {
+  if (isnan(s)) return 0x88888888u;
+  unsigned x = 0;
+  if (s < 1e-28f) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x |= (__float_as_uint(v[k] / s + 12582920.f) & 15u) << shift_of(k);
+    return x;
+  }
+  const float y = 1.f / s;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float q = v[k] * y;
+    x |= (__float_as_uint(fmaf(fmaf(-q, s, v[k]), y, q) + 12582920.f) & 15u) << shift_of(k);
+  }
+  return x;
 }
+// magnitudes as integers: they order as the numbers do, with infinity and NaN above
+__device__ __forceinline__ unsigned max_abs(unsigned a, float v) { return max(a, __float_as_uint(v) & 0x7fffffffu); }
 
-// w [E, out, in]: a thread takes the 8 inputs of a word, the G / 8 lanes of a group share its largest
+// w [E, out, in]: a thread takes the 8 inputs of a word, the G / 8 lanes of a group share its largest; a CTA takes
+// COL_WORDS neighbours of all words.
+constexpr int COL_NT = 256;
+constexpr int COL_ITEMS = 4;
+constexpr int COL_WORDS = COL_NT * COL_ITEMS;
+struct Spot {
+  long long row;
+  int word;
+};
+// number `at` of a CTA's words: one division of 64 bits for the CTA's first, of 32 from there
+__device__ __forceinline__ Spot spot_of(long long first_row, int first_word, int at, int words) {
+  const unsigned off = (unsigned)(first_word + at), rows = off / (unsigned)words;
+  return {first_row + rows, (int)(off - rows * (unsigned)words)};
+}
 template <typename T, int G>
-__global__ void __launch_bounds__(256) w4_pack_cols_kernel(const T* __restrict__ w, long long rows, int in, int blocks,
-                                                           unsigned* __restrict__ q, bf16* __restrict__ scale) {
-  const long long words = rows * blocks * WORDS, last = (words + 31) / 32 * 32;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < last; i += (long long)gridDim.x * 256) {
-    const long long row = i / (blocks * WORDS);
-    const int word = (int)(i - row * (blocks * WORDS)), c = word * 8;
-    float v[8], amax = 0.f;
+__global__ void __launch_bounds__(COL_NT) w4_pack_cols_kernel(const T* __restrict__ w, long long rows, int in, int blocks,
+                                                              unsigned* __restrict__ q, bf16* __restrict__ scale) {
+  const int words = blocks * WORDS;
+  const long long begin = (long long)blockIdx.x * COL_WORDS, first_row = begin / words;
+  const int first_word = (int)(begin - first_row * words);
+  float v[COL_ITEMS][8];
+  Spot at[COL_ITEMS];
+#pragma unroll
+  for (int i = 0; i < COL_ITEMS; ++i) {
+    at[i] = spot_of(first_row, first_word, i * COL_NT + threadIdx.x, words);
+    const int c = at[i].word * 8;
 #pragma unroll
     for (int k = 0; k < 8; k += Vec16<T>::N) {
-      if (i < words && c + k < in) {
-        Vec16<T>::load(w + row * in + c + k, v + k);
+      if (at[i].row < rows && c + k < in) {
+        Vec16<T>::load(w + at[i].row * in + c + k, v[i] + k);
       } else {
 #pragma unroll
-        for (int u = 0; u < Vec16<T>::N; ++u) v[k + u] = 0.f;
+        for (int u = 0; u < Vec16<T>::N; ++u) v[i][k + u] = 0.f;
       }
     }
+  }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) amax = max_abs(amax, v[k]);
+  for (int i = 0; i < COL_ITEMS; ++i) {
+    unsigned top = 0;
 #pragma unroll
-    for (int o = 1; o < G / 8; o <<= 1) amax = max_abs(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if (i >= words) continue;
-    const float s = scale_of(amax);
-    unsigned x = 0;
+    for (int k = 0; k < 8; ++k) top = max_abs(top, v[i][k]);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x |= code_of(v[k], s) << shift_of(k);
-    const int at = word % WORDS;
-    q[(row * blocks + word / WORDS) * WORDS + at % 4 * 4 + at / 4] = x;
-    if (c % G == 0) scale[row * (blocks * BLOCK / G) + c / G] = __float2bfloat16_rn(s);
+    for (int o = 1; o < G / 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (at[i].row >= rows) continue;
+    const float s = scale_of(__uint_as_float(top));
+    const int word = at[i].word, place = word % WORDS;
+    q[(at[i].row * blocks + word / WORDS) * WORDS + place % 4 * 4 + place / 4] = word_of_codes(v[i], s);
+    if (word % (G / 8) == 0) scale[at[i].row * (blocks * BLOCK / G) + word / (G / 8)] = __float2bfloat16_rn(s);
   }
 }
 
-// w [E, in, out]: a thread takes the block of 128 inputs of one output
+// w [E, in, out]: a CTA takes 64 V outputs (V in 4 bytes) of up to ROW_BLOCKS blocks; a thread V of them over a run of 32
+// inputs, read down the rows in whole lines.  The runs of a group share its largest magnitude, and the words and
+// scales, which lie along an output, go out through shared memory (a thread to an output's whole block: 299 us for
+// 64 x 2048 x 1408 bf16, where memory allows 66).
+constexpr int ROW_NT = 256;
+constexpr int ROW_BLOCKS = 4;
+template <typename T> constexpr int PER4 = 4 / sizeof(T);
+template <typename T> __device__ __forceinline__ float of4(unsigned raw, int c);
+template <> __device__ __forceinline__ float of4<float>(unsigned raw, int) { return __uint_as_float(raw); }
+template <> __device__ __forceinline__ float of4<bf16>(unsigned raw, int c) {
+  return __uint_as_float(c ? raw & 0xffff0000u : raw << 16);
+}
+
 template <typename T, int G>
-__global__ void __launch_bounds__(128) w4_pack_rows_kernel(const T* __restrict__ w, int in, int out, int blocks,
-                                                           unsigned* __restrict__ q, bf16* __restrict__ scale) {
-  const int o = blockIdx.x * 128 + threadIdx.x, b = blockIdx.y, e = blockIdx.z;
-  if (o >= out) return;
-  const T* src = w + ((long long)e * in + b * BLOCK) * out + o;
-  const long long row = (long long)e * out + o;
-  unsigned x[WORDS];
+__global__ void __launch_bounds__(ROW_NT) w4_pack_rows_kernel(const T* __restrict__ w, int in, int out, int blocks,
+                                                              unsigned* __restrict__ q, bf16* __restrict__ scale) {
+  constexpr int V = PER4<T>, COLS = 64 * V, SC = BLOCK / G;
+  __shared__ unsigned words[COLS][WORDS + 1];
+  __shared__ unsigned top[4][COLS];
+  __shared__ bf16 scales[COLS][ROW_BLOCKS * SC];
+  const int tx = threadIdx.x & 63, run = threadIdx.x >> 6, e = blockIdx.z;
+  const int o0 = blockIdx.x * COLS, o = o0 + tx * V, b0 = blockIdx.y * ROW_BLOCKS;
+  const int n_blocks = min(ROW_BLOCKS, blocks - b0);
+  for (int bb = 0; bb < n_blocks; ++bb) {
+    const int b = b0 + bb, k0 = b * BLOCK + run * 32;
+    const T* src = w + ((long long)e * in + k0) * out + o;
+    unsigned raw[32];
 #pragma unroll
-  for (int g = 0; g < BLOCK / G; ++g) {
-    float v[G], amax = 0.f;
+    for (int k = 0; k < 32; ++k)
+      raw[k] = o < out && k0 + k < in ? __ldg(reinterpret_cast<const unsigned*>(src + (long long)k * out)) : 0u;
 #pragma unroll
-    for (int k = 0; k < G; ++k) v[k] = b * BLOCK + g * G + k < in ? to_f32(src[(long long)(g * G + k) * out]) : 0.f;
+    for (int c = 0; c < V; ++c) {
+      unsigned a = 0;
 #pragma unroll
-    for (int k = 0; k < G; ++k) amax = max_abs(amax, v[k]);
-    const float s = scale_of(amax);
-#pragma unroll
-    for (int n = 0; n < G / 8; ++n) {
-      unsigned y = 0;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) y |= code_of(v[8 * n + k], s) << shift_of(k);
-      const int at = g * (G / 8) + n;
-      x[at % 4 * 4 + at / 4] = y;
+      for (int k = 0; k < 32; ++k) a = max_abs(a, of4<T>(raw[k], c));
+      top[run][tx * V + c] = a;
     }
-    scale[row * (blocks * BLOCK / G) + b * (BLOCK / G) + g] = __float2bfloat16_rn(s);
-  }
-  uint4* dst = reinterpret_cast<uint4*>(q + (row * blocks + b) * WORDS);
+    __syncthreads();  // and the words of the block before have been written
 #pragma unroll
-  for (int k = 0; k < 4; ++k) dst[k] = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+    for (int c = 0; c < V; ++c) {
+      constexpr int RUNS = G / 32;
+      const int r0 = run / RUNS * RUNS;
+      unsigned a = top[r0][tx * V + c];
+#pragma unroll
+      for (int r = 1; r < RUNS; ++r) a = max(a, top[r0 + r][tx * V + c]);
+      const float s = scale_of(__uint_as_float(a));
+      if (run == r0) scales[tx * V + c][bb * SC + run / RUNS] = __float2bfloat16_rn(s);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = of4<T>(raw[8 * v + k], c);
+        words[tx * V + c][v * 4 + run] = word_of_codes(x, s);
+      }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < COLS * WORDS; i += ROW_NT) {
+      const int col = i / WORDS, at = i % WORDS;
+      if (o0 + col < out) q[(((long long)e * out + o0 + col) * blocks + b) * WORDS + at] = words[col][at];
+    }
+  }
+  for (int i = threadIdx.x; i < COLS * n_blocks * SC; i += ROW_NT) {
+    const int col = i / (n_blocks * SC), at = i - col * (n_blocks * SC);
+    if (o0 + col < out) scale[((long long)e * out + o0 + col) * (blocks * SC) + b0 * SC + at] = scales[col][at];
+  }
 }
 
+// code + 8 under the exponent of 2^23 is the number 2^23 + code + 8
 __device__ __forceinline__ float value_of(unsigned word, int i, float s) {
-  return (float)((int)((word >> shift_of(i)) & 15u) - 8) * s;
+  return (__uint_as_float(((word >> shift_of(i)) & 15u) | 0x4b000000u) - 8388616.f) * s;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256) w4_unpack_cols_kernel(const unsigned* __restrict__ q, const bf16* __restrict__ scale,
-                                                             long long rows, int in, int blocks, int G,
-                                                             T* __restrict__ w) {
-  const long long words = rows * blocks * WORDS;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < words; i += (long long)gridDim.x * 256) {
-    const long long row = i / (blocks * WORDS);
-    const int word = (int)(i - row * (blocks * WORDS)), c = word * 8, at = word % WORDS;
-    if (c >= in) continue;
-    const unsigned x = q[(row * blocks + word / WORDS) * WORDS + at % 4 * 4 + at / 4];
-    const float s = to_f32(scale[row * (blocks * BLOCK / G) + c / G]);
+__global__ void __launch_bounds__(COL_NT)
+w4_unpack_cols_kernel(const unsigned* __restrict__ q, const bf16* __restrict__ scale, long long rows, int in, int blocks,
+                      int G, T* __restrict__ w) {
+  const int words = blocks * WORDS;
+  const long long begin = (long long)blockIdx.x * COL_WORDS, first_row = begin / words;
+  const int first_word = (int)(begin - first_row * words);
+  unsigned x[COL_ITEMS];
+  bf16 s[COL_ITEMS];
+  Spot at[COL_ITEMS];
+#pragma unroll
+  for (int i = 0; i < COL_ITEMS; ++i) {
+    at[i] = spot_of(first_row, first_word, i * COL_NT + threadIdx.x, words);
+    if (at[i].row >= rows) continue;
+    const int word = at[i].word, place = word % WORDS;
+    x[i] = __ldg(q + (at[i].row * blocks + word / WORDS) * WORDS + place % 4 * 4 + place / 4);
+    s[i] = scale[at[i].row * (blocks * BLOCK / G) + word * 8 / G];
+  }
+#pragma unroll
+  for (int i = 0; i < COL_ITEMS; ++i) {
+    const int c = at[i].word * 8;
+    if (at[i].row >= rows || c >= in) continue;
     float v[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = value_of(x, k, s);
+    for (int k = 0; k < 8; ++k) v[k] = value_of(x[i], k, to_f32(s[i]));
 #pragma unroll
     for (int k = 0; k < 8; k += Vec16<T>::N)
-      if (c + k < in) Vec16<T>::store(w + row * in + c + k, v + k);
+      if (c + k < in) Vec16<T>::store(w + at[i].row * in + c + k, v + k);
   }
 }
 
+// the same way round as w4_pack_rows_kernel
 template <typename T>
-__global__ void __launch_bounds__(128) w4_unpack_rows_kernel(const unsigned* __restrict__ q, const bf16* __restrict__ scale,
-                                                             int in, int out, int blocks, int G, T* __restrict__ w) {
-  const int o = blockIdx.x * 128 + threadIdx.x, b = blockIdx.y, e = blockIdx.z;
-  if (o >= out) return;
-  T* dst = w + ((long long)e * in + b * BLOCK) * out + o;
-  const long long row = (long long)e * out + o;
-  const uint4* src = reinterpret_cast<const uint4*>(q + (row * blocks + b) * WORDS);
-  unsigned x[WORDS];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint4 v = __ldg(src + k);
-    x[4 * k] = v.x, x[4 * k + 1] = v.y, x[4 * k + 2] = v.z, x[4 * k + 3] = v.w;
+__global__ void __launch_bounds__(ROW_NT)
+w4_unpack_rows_kernel(const unsigned* __restrict__ q, const bf16* __restrict__ scale, int in, int out, int blocks, int G,
+                      T* __restrict__ w) {
+  constexpr int V = PER4<T>, COLS = 64 * V;
+  __shared__ unsigned words[COLS][WORDS + 1];
+  __shared__ bf16 scales[COLS][ROW_BLOCKS * 4];
+  const int tx = threadIdx.x & 63, run = threadIdx.x >> 6, e = blockIdx.z, sc = BLOCK / G;
+  const int o0 = blockIdx.x * COLS, o = o0 + tx * V, b0 = blockIdx.y * ROW_BLOCKS;
+  const int n_blocks = min(ROW_BLOCKS, blocks - b0);
+  for (int i = threadIdx.x; i < COLS * n_blocks * sc; i += ROW_NT) {
+    const int col = i / (n_blocks * sc), at = i - col * (n_blocks * sc);
+    if (o0 + col < out) scales[col][at] = scale[((long long)e * out + o0 + col) * (blocks * sc) + b0 * sc + at];
   }
-  const bf16* sc = scale + row * (blocks * BLOCK / G) + b * (BLOCK / G);
+  for (int bb = 0; bb < n_blocks; ++bb) {
+    const int b = b0 + bb, k0 = b * BLOCK + run * 32;
+    __syncthreads();
+    for (int i = threadIdx.x; i < COLS * WORDS; i += ROW_NT) {
+      const int col = i / WORDS, at = i % WORDS;
+      if (o0 + col < out) words[col][at] = __ldg(q + (((long long)e * out + o0 + col) * blocks + b) * WORDS + at);
+    }
+    __syncthreads();
+    if (o >= out) continue;
+    unsigned mine[V][4];
+    float sv[V];
 #pragma unroll
-  for (int at = 0; at < WORDS; ++at) {
-    const float s = to_f32(sc[at * 8 / G]);
+    for (int c = 0; c < V; ++c) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (b * BLOCK + at * 8 + k < in)
-        dst[(long long)(at * 8 + k) * out] = from_f32<T>(value_of(x[at % 4 * 4 + at / 4], k, s));
+      for (int v = 0; v < 4; ++v) mine[c][v] = words[tx * V + c][v * 4 + run];
+      sv[c] = to_f32(scales[tx * V + c][bb * sc + run * 32 / G]);
+    }
+    T* dst = w + ((long long)e * in + k0) * out + o;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      if (k0 + k >= in) break;
+      if (V == 2) {
+        *reinterpret_cast<__nv_bfloat162*>(dst + (long long)k * out) = __floats2bfloat162_rn(
+            value_of(mine[0][k / 8], k % 8, sv[0]), value_of(mine[V - 1][k / 8], k % 8, sv[V - 1]));
+      } else {
+        dst[(long long)k * out] = from_f32<T>(value_of(mine[0][k / 8], k % 8, sv[0]));
+      }
+    }
   }
 }
 
@@ -1054,9 +1156,8 @@ __global__ void __launch_bounds__(256) w4_gather_kernel(const uint4* __restrict_
     xs[r * vecs + i] = ok ? __ldg(x + (long long)from * vecs + i) : make_uint4(0, 0, 0, 0);
 }
 
-unsigned grid_of(long long threads, int nt) {
-  const long long want = (threads + nt - 1) / nt, most = 8LL * sm_count();
-  return (unsigned)(want < most ? want : most);
+unsigned col_grid(long long rows, int blocks) {
+  return (unsigned)((rows * blocks * WORDS + COL_WORDS - 1) / COL_WORDS);
 }
 
 template <typename T, int G>
@@ -1064,12 +1165,15 @@ int pack(const void* w, int E, int rows, int cols, int axis, void* q, void* scal
   if (axis == 1) {
     const int blocks = blocks_of(cols);
     const long long n = (long long)E * rows;
-    w4_pack_cols_kernel<T, G><<<grid_of(n * blocks * WORDS, 256), 256, 0, s>>>(
+    if (n * blocks * WORDS / COL_WORDS >= 0x7fffffffll) return MOE_ERR_UNSUPPORTED;
+    w4_pack_cols_kernel<T, G><<<col_grid(n, blocks), COL_NT, 0, s>>>(
         static_cast<const T*>(w), n, cols, blocks, static_cast<unsigned*>(q), static_cast<bf16*>(scale));
   } else {
     const int blocks = blocks_of(rows);
-    w4_pack_rows_kernel<T, G><<<dim3((cols + 127) / 128, blocks, E), 128, 0, s>>>(
-        static_cast<const T*>(w), rows, cols, blocks, static_cast<unsigned*>(q), static_cast<bf16*>(scale));
+    constexpr int COLS = 64 * PER4<T>;
+    w4_pack_rows_kernel<T, G>
+        <<<dim3((cols + COLS - 1) / COLS, (blocks + ROW_BLOCKS - 1) / ROW_BLOCKS, E), ROW_NT, 0, s>>>(
+            static_cast<const T*>(w), rows, cols, blocks, static_cast<unsigned*>(q), static_cast<bf16*>(scale));
   }
   return launch_status();
 }
@@ -1079,11 +1183,13 @@ int unpack(const void* q, const void* scale, int E, int rows, int cols, int axis
   if (axis == 1) {
     const int blocks = blocks_of(cols);
     const long long n = (long long)E * rows;
-    w4_unpack_cols_kernel<T><<<grid_of(n * blocks * WORDS, 256), 256, 0, s>>>(
+    if (n * blocks * WORDS / COL_WORDS >= 0x7fffffffll) return MOE_ERR_UNSUPPORTED;
+    w4_unpack_cols_kernel<T><<<col_grid(n, blocks), COL_NT, 0, s>>>(
         static_cast<const unsigned*>(q), static_cast<const bf16*>(scale), n, cols, blocks, G, static_cast<T*>(w));
   } else {
     const int blocks = blocks_of(rows);
-    w4_unpack_rows_kernel<T><<<dim3((cols + 127) / 128, blocks, E), 128, 0, s>>>(
+    constexpr int COLS = 64 * PER4<T>;
+    w4_unpack_rows_kernel<T><<<dim3((cols + COLS - 1) / COLS, (blocks + ROW_BLOCKS - 1) / ROW_BLOCKS, E), ROW_NT, 0, s>>>(
         static_cast<const unsigned*>(q), static_cast<const bf16*>(scale), rows, cols, blocks, G, static_cast<T*>(w));
   }
   return launch_status();
