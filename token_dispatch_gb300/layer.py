@@ -16,8 +16,12 @@ device: the row split per expert stays on the device (cu_seqlens).
                   moe_expert_ffn -> moe_combine_norm (combine, norm after the block, gate and
                   residual scale, residual, norm before the next block); backward in the
                   reverse order, its expert activations kept in 8 bits where asked.
+    expert tensors: ExpertMuon updates them with the gradients of a backward (moe_muon_step);
+                  ExpertsW4 holds them in 4 bits, for the forwards' w_gate (moe_expert_ffn_w4).
 """
 from __future__ import annotations
+
+import math
 
 import torch
 
@@ -106,6 +110,108 @@ class MoEBuffers:
             self.ws_ffn_bwd = _ws(self.ws_ffn_bwd_bytes, dev) if experts is None else experts.ws_ffn_bwd
 
 
+def _dtype_of(w):
+    if w.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"expert tensors are bf16 or fp32, not {w.dtype}")
+    return L.MOE_F32 if w.dtype == torch.float32 else L.MOE_BF16
+
+
+class ExpertsW4:
+    """The experts' three tensors [E, H, Hp] in 4 bits (moe_w4_pack), in the place of w_gate, w_up and
+    w_down of moe_forward, mod_forward and moe_block_forward (as w_gate; w_up and w_down are then None).
+    For serving: such a forward keeps nothing that a backward could use."""
+
+    def __init__(self, E, H, Hp, device, group=64):
+        if group not in (32, 64, 128):
+            raise ValueError("ExpertsW4: groups of 32, 64 or 128 weights share a scale")
+        self.E, self.H, self.Hp, self.group = E, H, Hp, group
+
+        def packed(out, inp):
+            blocks = -(-inp // 128)
+            return (torch.empty((E, out, blocks * 16), dtype=torch.int32, device=device),
+                    torch.empty((E, out, blocks * 128 // group), dtype=torch.bfloat16, device=device))
+        self.q_gate, self.s_gate = packed(Hp, H)
+        self.q_up, self.s_up = packed(Hp, H)
+        self.q_down, self.s_down = packed(H, Hp)
+
+    def _each(self, w_gate, w_up, w_down):
+        return ((w_gate, 0, self.q_gate, self.s_gate), (w_up, 0, self.q_up, self.s_up),
+                (w_down, 1, self.q_down, self.s_down))
+
+    def pack(self, w_gate, w_up, w_down, stream=None):
+        """From bf16 or fp32 tensors; returns self."""
+        for w, axis, q, s in self._each(w_gate, w_up, w_down):
+            L.moe_w4_pack(w, self.E, self.H, self.Hp, axis, self.group, _dtype_of(w), q, s, stream=stream)
+        return self
+
+    def unpack(self, w_gate, w_up, w_down, stream=None):
+        """The weights that the packed form stands for, into bf16 or fp32 tensors."""
+        for w, axis, q, s in self._each(w_gate, w_up, w_down):
+            L.moe_w4_unpack(q, s, self.E, self.H, self.Hp, axis, self.group, _dtype_of(w), w, stream=stream)
+
+
+class ExpertMuon:
+    """The momentum of a layer's three expert tensors and their orthogonalised update (moe_muon_step)
+    from the gradients that a backward left in ``b`` (train=True)."""
+
+    def __init__(self, b: MoEBuffers, beta=0.95, nesterov=True, steps=5, coef=(3.4445, -4.7750, 2.0315), eps=1e-7):
+        if b.gu is None:
+            raise ValueError("ExpertMuon: the buffers were made without train=True")
+        self.E, self.H, self.Hp = b.E, b.H, b.Hp
+        self.beta, self.nesterov, self.steps, self.coef, self.eps = beta, nesterov, steps, coef, eps
+        self.m_gate, self.m_up, self.m_down = (torch.zeros_like(b.dw_gate) for _ in range(3))
+        self.ws_bytes = L.moe_workspace_bytes(L.MOE_OP_MUON_STEP, 0, b.H, b.E, 0, b.Hp)
+        self.ws = _ws(self.ws_bytes, b.dw_gate.device)
+
+    def step(self, b: MoEBuffers, w_gate, w_up, w_down, lr, weight_decay=0.0, scale=None, low=(None, None, None),
+             stream=None):
+        """w <- (1 - lr weight_decay) w - lr scale O for the three tensors, in place.  scale: 0.2 sqrt(max(H, Hp))
+        unless given, which makes the update's elements about 0.2 lr in size.  low: for fp32 weights, the bf16
+        tensors that the forward reads, written too."""
+        if (b.E, b.H, b.Hp) != (self.E, self.H, self.Hp):
+            raise ValueError("ExpertMuon: the buffers are of another layer's sizes")
+        if scale is None:
+            scale = 0.2 * math.sqrt(max(self.H, self.Hp))
+        for w, dw, m, lo in ((w_gate, b.dw_gate, self.m_gate, low[0]), (w_up, b.dw_up, self.m_up, low[1]),
+                             (w_down, b.dw_down, self.m_down, low[2])):
+            L.moe_muon_step(w, dw, m, self.E, self.H, self.Hp, _dtype_of(w), self.beta, self.nesterov, lr, weight_decay,
+                            scale, self.steps, *self.coef, self.eps, w, lo, m, self.ws, self.ws_bytes, stream=stream)
+
+
+def _check_w4(b: MoEBuffers, w_gate, w_up, w_down):
+    """The ExpertsW4 that a forward was given for its expert tensors, or None."""
+    if not isinstance(w_gate, ExpertsW4):
+        return None
+    if b.gu is not None or b.dtype != "bf16":
+        raise ValueError("ExpertsW4: 4-bit experts serve bf16 forwards alone (buffers without train=True)")
+    if w_up is not None or w_down is not None:
+        raise ValueError("ExpertsW4: it stands for all three tensors, w_up and w_down are None")
+    if (w_gate.E, w_gate.H, w_gate.Hp) != (b.E, b.H, b.Hp):
+        raise ValueError("ExpertsW4: of another layer's sizes")
+    return w_gate
+
+
+def _dispatch_and_experts(b: MoEBuffers, x, w_gate, w_up, w_down, fused_gather, stream):
+    """From the routing in b to the expert outputs b.h, with the tensors as they are or in 4 bits."""
+    T, H, E, K, Hp, dt = b.T, b.H, b.E, b.K, b.Hp, b.cdt
+    w4 = _check_w4(b, w_gate, w_up, w_down)
+    if w4 is not None:
+        # where the products want the rows side by side, dispatch lays them there
+        fused_gather = L.moe_workspace_bytes(L.MOE_OP_EXPERT_FFN_W4, T, H, E, K, Hp) == 0
+    L.moe_dispatch(x, b.idx, T, H, E, K, dt, b.cu, b.dst_row, b.src_tok, None if fused_gather else b.xs,
+                   b.ws_dispatch, b.ws_dispatch_bytes, stream=stream)
+    if w4 is not None:
+        L.moe_expert_ffn_w4(x if fused_gather else b.xs, b.src_tok if fused_gather else None, T, b.cu, T * K, w4.q_gate,
+                            w4.s_gate, w4.q_up, w4.s_up, w4.q_down, w4.s_down, E, H, Hp, w4.group, dt, b.act, b.h,
+                            stream=stream)
+    elif fused_gather:
+        L.moe_expert_ffn_gather(x, b.src_tok, T, b.cu, T * K, w_gate, w_up, w_down, E, H, Hp, dt, b.act, b.gu, b.h,
+                                b.ws_ffn, b.ws_ffn_bytes, stream=stream)
+    else:
+        L.moe_expert_ffn_ex(b.xs, b.cu, T * K, w_gate, w_up, w_down, E, H, Hp, dt, b.act, b.gu, b.h,
+                            b.ws_ffn, b.ws_ffn_bytes, stream=stream)
+
+
 def _forward_begins(b: MoEBuffers):
     """A forward of b begins: no other's activations are whole from here on, and an older one's
     routing in b is gone."""
@@ -117,6 +223,7 @@ def moe_forward(b: MoEBuffers, x, w_router, logit_bias, w_gate, w_up, w_down, st
                 row_scale=None, residual=None, out_row=None, y=None, route_flags=0, fused_gather=None):
     """One MoE forward pass into the buffers of ``b`` (y defaults to ``b.y``);
     ``route_flags``: MOE_ROUTE_RENORM / MOE_ROUTE_BIAS_SELECT gate options.
+    ``w_gate`` may be ExpertsW4 (and w_up, w_down None).
     ``fused_gather``: dispatch writes only the index maps and the expert FFN
     reads the rows of x itself (moe_expert_ffn_gather); off by default (the
     row-by-row operand fetch measured 7-11% slower than the gather kernel plus
@@ -125,17 +232,11 @@ def moe_forward(b: MoEBuffers, x, w_router, logit_bias, w_gate, w_up, w_down, st
     T, H, E, K, Hp, dt = b.T, b.H, b.E, b.K, b.Hp, b.cdt
     if fused_gather is None or b.gu is not None:
         fused_gather = False
+    _check_w4(b, w_gate, w_up, w_down)
     _forward_begins(b)
     L.moe_route_ex(x, w_router, logit_bias, T, H, E, K, dt, route_flags, b.logits, b.idx, b.gate, b.ws_route,
                    b.ws_route_bytes, stream=stream)
-    L.moe_dispatch(x, b.idx, T, H, E, K, dt, b.cu, b.dst_row, b.src_tok, None if fused_gather else b.xs,
-                   b.ws_dispatch, b.ws_dispatch_bytes, stream=stream)
-    if fused_gather:
-        L.moe_expert_ffn_gather(x, b.src_tok, T, b.cu, T * K, w_gate, w_up, w_down, E, H, Hp, dt, b.act, b.gu, b.h,
-                                b.ws_ffn, b.ws_ffn_bytes, stream=stream)
-    else:
-        L.moe_expert_ffn_ex(b.xs, b.cu, T * K, w_gate, w_up, w_down, E, H, Hp, dt, b.act, b.gu, b.h,
-                            b.ws_ffn, b.ws_ffn_bytes, stream=stream)
+    _dispatch_and_experts(b, x, w_gate, w_up, w_down, fused_gather, stream)
     b.holder.forward = b.forward
     L.moe_combine(b.h, b.gate, b.dst_row, row_scale, residual, out_row, T, H, K, dt,
                   b.y if y is None else y, stream=stream)
@@ -291,9 +392,11 @@ def moe_block_forward(m: MoEBlockBuffers, x, w_pre, w_router, sel_bias, gate: Gr
     w_pre, w_post, w_next (float [H]): weights of the norms before the block, after it and
     before the next one; w_post and w_next may be None (no such norm).  x0: norm(x) where
     the block before has written it (its m.xn); w_pre is then unused.  ckpt: keep the expert
-    activations there, so that blocks which share m.moe's may run before the backward."""
+    activations there, so that blocks which share m.moe's may run before the backward.  w_gate
+    may be ExpertsW4 (and w_up, w_down None)."""
     b = m.moe
     T, H, E, K, Hp, dt = b.T, b.H, b.E, b.K, b.Hp, b.cdt
+    _check_w4(b, w_gate, w_up, w_down)
     _forward_begins(b)
     m.forward = b.forward
     if x0 is None:
@@ -301,10 +404,7 @@ def moe_block_forward(m: MoEBlockBuffers, x, w_pre, w_router, sel_bias, gate: Gr
         L.moe_combine_norm(None, None, None, None, x, None, None, w_pre, eps, T, H, 0, dt, None, x0, stream=stream)
     L.moe_route_group(x0, w_router, sel_bias, T, H, E, K, dt, gate.groups, gate.topk_groups, gate.mode, gate.scale,
                       b.logits, b.idx, b.gate, b.ws_route, b.ws_route_bytes, stream=stream)
-    L.moe_dispatch(x0, b.idx, T, H, E, K, dt, b.cu, b.dst_row, b.src_tok, b.xs, b.ws_dispatch, b.ws_dispatch_bytes,
-                   stream=stream)
-    L.moe_expert_ffn_ex(b.xs, b.cu, T * K, w_gate, w_up, w_down, E, H, Hp, dt, b.act, b.gu, b.h, b.ws_ffn,
-                        b.ws_ffn_bytes, stream=stream)
+    _dispatch_and_experts(b, x0, w_gate, w_up, w_down, False, stream)
     b.holder.forward = b.forward
     if ckpt is not None:
         ckpt.save(b, stream=stream)
