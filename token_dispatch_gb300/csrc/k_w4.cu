@@ -847,7 +847,7 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
       const int row = it.e * p.out + it.n0;
       for (int b = 0; b < blocks; b += 2, ++u) {
         const int s = u % C::CODES;
-        ok = __all_sync(0xffffffffu, wait_bounded(codee(s), (u / C::CODES & 1) ^ 1, &abort_flag, p));
+        ok = __all_sync(0xffffffffu, wait_lazily(codee(s), (u / C::CODES & 1) ^ 1, &abort_flag, p));
         if (!ok) break;
         const uint32_t dst = smem_u32(smem + 2 * s * CODE_BYTES);
         const bool two = b + 1 < blocks;
@@ -873,7 +873,7 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
       const Item it = item(i);
       for (int b = 0; b < blocks; b += 2, ++u) {
         const int s = u % C::PAIRS;
-        ok = __all_sync(0xffffffffu, wait_bounded(done(s), (u / C::PAIRS & 1) ^ 1, &abort_flag, p));
+        ok = __all_sync(0xffffffffu, wait_lazily(done(s), (u / C::PAIRS & 1) ^ 1, &abort_flag, p));
         if (!ok) break;
         const uint32_t dst = smem_u32(xs + 2 * s * C::X_BYTES);
         const int halves = b + 1 < blocks ? 4 : 2;
@@ -952,30 +952,23 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
       const int n = min(it.n0 + (GATE_UP ? row & 63 : row), p.out - 1);
       return (GATE_UP && row >= 64 ? p.s1 : p.s0) + ((long long)it.e * p.out + n) * blocks * SC;
     };
-    // the set's next block in its item, counted on into the following ones
-    long long i = blockIdx.x, i_next = i;
-    int b = set;
-    Item it = item(i);
-    const bf16 *sp = scales_of(it), *sp_next = sp;
-    auto settle = [&](long long& i, int& b, const bf16*& sp) {  // over to the item that holds block b
-      while (i < items && b >= 2 * pairs) {
-        b -= 2 * pairs;
-        i += gridDim.x;
-        if (i < items) sp = scales_of(item(i));
-      }
-    };
-    settle(i, b, sp);
+    // the set's next block in the CTA's item number `k`
+    const int mine = (int)((items - blockIdx.x + gridDim.x - 1) / gridDim.x), span = 2 * pairs;
+    auto scales_at = [&](int k) { return scales_of(item(blockIdx.x + (long long)k * gridDim.x)); };
+    int k = 0, b = set;
+    while (b >= span) b -= span, ++k;
+    const bf16* sp = k < mine ? scales_at(k) : nullptr;
     uint2 sc = make_uint2(0, 0);
-    if (i < items && b < blocks) sc = load_scales<G>(sp + b * SC);
+    if (k < mine && b < blocks) sc = load_scales<G>(sp + b * SC);
     bool landed = false;
     const uint32_t from = (uint32_t)(half * CODE_BYTES + row * 64);
-    while (i < items) {
+    while (k < mine) {
       // the scales of the block after this one
       const uint2 now = sc;
-      i_next = i, sp_next = sp;
-      int b_next = b + SETS;
-      settle(i_next, b_next, sp_next);
-      if (i_next < items && b_next < blocks) sc = load_scales<G>(sp_next + b_next * SC);
+      int k_next = k, b_next = b + SETS;
+      while (b_next >= span) b_next -= span, ++k_next;
+      const bf16* sp_next = k_next == k ? sp : k_next < mine ? scales_at(k_next) : nullptr;
+      if (sp_next && b_next < blocks) sc = load_scales<G>(sp_next + b_next * SC);
       const bool real = b < blocks;
       uint4 w[4];
       auto read = [&]() {
@@ -1026,7 +1019,7 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
       buf += STEP;
       if (buf >= C::PAIRS) buf -= C::PAIRS, buf_phase ^= 1;
       landed = __all_sync(0xffffffffu, landed);
-      i = i_next, b = b_next, sp = sp_next;
+      k = k_next, b = b_next, sp = sp_next;
     }
   } else {
     // -------------------------------------------------------------- epilogue
@@ -1036,7 +1029,7 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
     for (long long i = blockIdx.x; i < items; i += gridDim.x, ++n) {
       const Item it = item(i);
       const int a = n & 1;
-      if (ok) ok = wait_bounded(accf(a), n / 2 & 1, &abort_flag, p);
+      if (ok) ok = wait_lazily(accf(a), n / 2 & 1, &abort_flag, p);
       ok = __all_sync(0xffffffffu, ok);
       tc_fence_after();
       const uint32_t src = tmem + a * C::ACC_COLS + ((uint32_t)(q * 32) << 16);
@@ -1102,6 +1095,7 @@ int launch_ffn(const void* x, const void* q0, const void* q1, const Args& p, cud
   const long long strips = (p.out + WIDTH - 1) / WIDTH;
   const long long items = ((long long)(p.E < p.R ? p.E : p.R) + p.R / N) * strips;  // at most
   const long long sms = sm_count();
+  if (items > 0x3fffffffll) return MOE_ERR_UNSUPPORTED;
   auto k = w4_ffn_kernel<N, G, GATE_UP>;
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM) != cudaSuccess)
     return MOE_ERR_CUDA;

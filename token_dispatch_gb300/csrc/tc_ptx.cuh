@@ -61,6 +61,24 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, vola
   }
 }
 
+// The same for a role that others are well ahead of: it sleeps between its looks, so that it leaves its scheduler's
+// issue slots to the busy warps (a polling loop is some ten instructions a look).
+template <class P>
+__device__ __forceinline__ bool wait_lazily(uint32_t bar, uint32_t parity, volatile int* abort_flag, const P& p) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (;;) {
+    __nanosleep(100);
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if ((unsigned long long)(clock64() - t0) > p.wait_limit) {
+      *abort_flag = 1;
+      set_error(p.err, DEV_TIMEOUT);
+      return false;
+    }
+  }
+}
+
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
