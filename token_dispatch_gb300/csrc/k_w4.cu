@@ -322,25 +322,32 @@ __device__ __forceinline__ void count_tiles(Tiles& t, const int32_t* cu, int E, 
 struct Item {
   int e, r0, rows, n0;  // n0: first output; rows 0: no more items
 };
-// item i: experts in order, in each its strips of outputs in order, in each strip its tiles of rows
-template <int N>
-__device__ __forceinline__ Item item_of(const Tiles& t, int E, long long i, int strips, int width) {
-  Item w = {0, 0, 0, 0};
-  if (i >= (long long)t.before[E] * strips) return w;
-  int lo = 0, hi = E - 1;
-  while (lo < hi) {  // the last expert whose items begin at or before i
-    const int mid = (lo + hi + 1) >> 1;
-    if ((long long)t.before[mid] * strips <= i) lo = mid;
-    else hi = mid - 1;
+// Item i: experts in order, in each its strips of outputs in order, in each strip its tiles of rows.  A whole warp
+// calls it, and with growing i: the experts from the last call's on are looked at 32 at a time.  (By
+// bisection, with 64-bit quotients, an item cost each warp some 300 cycles, 10% of the time of T = 16.)
+struct ItemSearch {
+  int e = 0;
+  template <int N>
+  __device__ __forceinline__ Item at(const Tiles& t, int E, int i, int strips, int width) {
+    Item w = {0, 0, 0, 0};
+    const int tile_no = (int)((unsigned)i / (unsigned)strips);
+    if (tile_no >= t.before[E]) return w;
+    const int lane = threadIdx.x & 31;
+    for (;;) {  // to the last expert whose tiles begin at or before this one
+      const int next = e + 1 + lane;
+      const int n = __popc(__ballot_sync(0xffffffffu, next <= E && t.before[next] <= tile_no));
+      e += n;
+      if (n < 32) break;
+    }
+    const int first = t.before[e], tiles = t.before[e + 1] - first, local = i - first * strips;
+    const int strip = tiles == 1 ? local : (int)((unsigned)local / (unsigned)tiles), tile = local - strip * tiles;
+    w.e = e;
+    w.r0 = t.row0[e] + tile * N;
+    w.rows = min(N, t.row1[e] - w.r0);
+    w.n0 = strip * width;
+    return w;
   }
-  const int tiles = t.before[lo + 1] - t.before[lo], local = (int)(i - (long long)t.before[lo] * strips);
-  const int strip = local / tiles, tile = local - strip * tiles;
-  w.e = lo;
-  w.r0 = t.row0[lo] + tile * N;
-  w.rows = min(N, t.row1[lo] - w.r0);
-  w.n0 = strip * width;
-  return w;
-}
+};
 
 // ------------------------------------------------------ products of few rows ---
 // Weights are the MMA's A operand (16 outputs x 16 inputs), up to 8 NT routed rows its B operand, so a
@@ -436,13 +443,14 @@ w4_rows_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // ---- the warp's loads: stage `issued` of its sequence of (item, pair of blocks)
-  const long long stride = (long long)gridDim.x * (NT_WARPS / wk);
-  long long load_i = (long long)blockIdx.x * (NT_WARPS / wk) + sub;
+  const int stride = gridDim.x * (NT_WARPS / wk);
+  int load_i = blockIdx.x * (NT_WARPS / wk) + sub;
+  ItemSearch search;
   int load_items = 0, load_pair = kw, issued = 0, load_row = 0;
   bool loading;
   const bf16* load_s = nullptr;  // scales of this lane's row of the stage
   auto next_item = [&]() {
-    const Item w = item_of<ROWS>(tiles, p.E, load_i, strips, STRIP);
+    const Item w = search.at<ROWS>(tiles, p.E, load_i, strips, STRIP);
     if (lane == 0) coming[warp][load_items % AHEAD] = w;
     load_i += stride;
     ++load_items;
@@ -628,6 +636,7 @@ int launch_rows(const void* x, const void* q0, const void* q1, Args p, cudaStrea
   const int pairs = (blocks_of(p.in) + 1) / 2, strips = (p.out + STRIP - 1) / STRIP;
   const long long slots = (p.E < p.R ? p.E : p.R) + (long long)(p.R / ROWS);  // at most
   const long long resident = (long long)RESIDENT * sm_count();
+  if (slots * strips > 0x3fffffffll) return MOE_ERR_UNSUPPORTED;
   // Warps to a strip: more of them make the items finer, and each item costs its warps a meeting
   // (about as much as 0.7 pairs of blocks).  The least of rounds x time of an item.
   double best = 0;
@@ -667,10 +676,11 @@ int launch_rows(const void* x, const void* q0, const void* q1, Args p, cudaStrea
 // shared memory would bound the kernel at half the memory's rate; with warp-level MMAs fed from
 // registers the work around them did, measured: T = 1, E = 384 57 us, T = 64, E = 64 177 us.)
 //
-// A pair of codes comes out of its word as 128 + (q + 8) by a shift and a lop3 (bf16 holds whole numbers
-// up to 256), minus 136 is q, times the scale the weight: all exact for scales of 5 significant
-// bits.  These are 17 operations for 8 weights, 7 of them on the half-rate integer pipe, so the conversion
-// needs some 80% of the issue slots at the memory's rate; it takes 16 of the 23 warps.
+// A pair of codes comes out of its word as 16 + (q + 8) by a shift and a lop3 (the codes at the top of bf16's
+// mantissa), and  fma(16 + code, s, -24 s)  is the weight q s, rounded once: its two products are exact
+// within the fma, provided that 24 s is a bf16 number, as it is for every scale of 5 significant bits below 2^123.
+// A warp that meets other scales subtracts 24 and multiplies, with the same results, bit for bit, in more time.
+// That is 12 operations for 8 weights, all on half-rate pipes, 8 on the integer one.
 //
 // Roles of a CTA, one to an SM: warp 0 loads codes (TMA), warp 1 issues the MMAs, warps 2 to 5 are the
 // epilogue, warps 6 to 21 convert (four sets of four warps, each every fourth block), warp 22 loads
@@ -698,11 +708,31 @@ struct Cfg {
 
 __device__ __forceinline__ unsigned bits_of(__nv_bfloat162 v) { return *reinterpret_cast<unsigned*>(&v); }
 __device__ __forceinline__ __nv_bfloat162 pair_from(unsigned v) { return *reinterpret_cast<__nv_bfloat162*>(&v); }
-// the weights of a word's pair t: (q, q') s
-__device__ __forceinline__ unsigned weights_of(unsigned word, int t, __nv_bfloat162 s) {
-  unsigned v;  // (word >> 4 t) & 0x000f000f | 0x43004300
-  asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(v) : "r"(word >> (4 * t)), "r"(0x43004300u));
-  return bits_of(__hmul2(__hsub2(pair_from(v), __float2bfloat162_rn(136.f)), s));
+// the weights of a word's pair t, (q, q') s; minus24 = -24 s, EXACT: that is what it is, unrounded
+template <bool EXACT>
+__device__ __forceinline__ unsigned weights_of(unsigned word, int t, __nv_bfloat162 s, __nv_bfloat162 minus24) {
+  const unsigned at3 = t == 0 ? word << 3 : word >> (4 * t - 3);
+  unsigned v;  // at3 & 0x00780078 | 0x41804180
+  asm("lop3.b32 %0, %1, 0x00780078, %2, 0xea;" : "=r"(v) : "r"(at3), "r"(0x41804180u));
+  if (EXACT) return bits_of(__hfma2(pair_from(v), s, minus24));
+  return bits_of(__hmul2(__hsub2(pair_from(v), __float2bfloat162_rn(24.f)), s));
+}
+// 32 words of 64 inputs' weights, of which those of run j are w[v]'s component j
+template <bool EXACT>
+__device__ __forceinline__ void convert_half(const uint4 (&w)[4], int h, unsigned scales, unsigned minus24,
+                                             unsigned (&r)[32]) {
+#pragma unroll
+  for (int jj = 0; jj < 2; ++jj) {
+    const int j = 2 * h + jj;
+    const __nv_bfloat162 sj = pair_from(__byte_perm(scales, scales, jj ? 0x3232 : 0x1010));
+    const __nv_bfloat162 mj = pair_from(__byte_perm(minus24, minus24, jj ? 0x3232 : 0x1010));
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const unsigned word = j == 0 ? w[v].x : j == 1 ? w[v].y : j == 2 ? w[v].z : w[v].w;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) r[jj * 16 + v * 4 + t] = weights_of<EXACT>(word, t, sj, mj);
+    }
+  }
 }
 // 32 lanes x 32 columns of tensor memory
 __device__ __forceinline__ void tmem_st32(uint32_t at, const unsigned (&r)[32]) {
@@ -752,21 +782,20 @@ __device__ __forceinline__ void store_rows(const float (&v)[R], bf16* dst, long 
   }
 }
 
-// the scale of every run of 32 inputs of a block, as bf16 numbers in pairs: G = 32: four numbers,
-// 64: two, 128: one
+// the scales of a block: four, two or one bf16 number
 template <int G>
 __device__ __forceinline__ uint2 load_scales(const bf16* p) {
-  uint2 v;
-  if (G == 32) {
-    v = __ldg(reinterpret_cast<const uint2*>(p));
-  } else if (G == 64) {
-    const unsigned a = __ldg(reinterpret_cast<const unsigned*>(p));
-    v = make_uint2(__byte_perm(a, a, 0x1010), __byte_perm(a, a, 0x3232));
-  } else {
-    const unsigned a = __ldg(reinterpret_cast<const unsigned short*>(p));
-    v.x = v.y = a | a << 16;
-  }
-  return v;
+  if (G == 32) return __ldg(reinterpret_cast<const uint2*>(p));
+  if (G == 64) return make_uint2(__ldg(reinterpret_cast<const unsigned*>(p)), 0u);
+  return make_uint2(__ldg(reinterpret_cast<const unsigned short*>(p)), 0u);
+}
+// and one for each of its runs of 32 inputs, once they are needed
+template <int G>
+__device__ __forceinline__ uint2 spread_scales(uint2 v) {
+  if (G == 32) return v;
+  if (G == 64) return make_uint2(__byte_perm(v.x, v.x, 0x1010), __byte_perm(v.x, v.x, 0x3232));
+  const unsigned two = v.x | v.x << 16;
+  return make_uint2(two, two);
 }
 
 template <int N, int G, bool GATE_UP>
@@ -826,8 +855,9 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
   tc_fence_after();
   const uint32_t tmem = tmem_base_slot;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  auto item = [&](long long i) { return item_of<N>(tiles, p.E, i, strips, WIDTH); };
-  const long long items = (long long)tiles.before[p.E] * strips;
+  ItemSearch search;
+  auto item = [&](int i) { return search.at<N>(tiles, p.E, i, strips, WIDTH); };
+  const int items = tiles.before[p.E] * strips;
   // waits for loads under way when a role stops: nothing lands after the CTA has gone
   auto drain_loads = [&](auto bar, int stages, int issued) {
     for (int k = max(0, issued - stages); k < issued; ++k) {
@@ -842,7 +872,7 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
     // ---------------------------------------------------------------- codes
     int u = 0;  // pair of the whole sequence
     bool ok = true;
-    for (long long i = blockIdx.x; ok && i < items; i += gridDim.x) {
+    for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
       const Item it = item(i);
       const int row = it.e * p.out + it.n0;
       for (int b = 0; b < blocks; b += 2, ++u) {
@@ -869,7 +899,7 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
     if (!GATE_UP) asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows that gate and up left
     int u = 0;
     bool ok = true;
-    for (long long i = blockIdx.x; ok && i < items; i += gridDim.x) {
+    for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
       const Item it = item(i);
       for (int b = 0; b < blocks; b += 2, ++u) {
         const int s = u % C::PAIRS;
@@ -892,7 +922,7 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
     constexpr uint32_t IDESC = instr_desc(TILE, N, false, false);
     int u = 0, n = 0;
     bool ok = true, ready = false;
-    for (long long i = blockIdx.x; ok && i < items; i += gridDim.x, ++n) {
+    for (int i = blockIdx.x; ok && i < items; i += gridDim.x, ++n) {
       const int a = n & 1;
       ok = __all_sync(0xffffffffu, wait_bounded(acce(a), (n / 2 & 1) ^ 1, &abort_flag, p));
       if (!ok) break;
@@ -953,8 +983,8 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
       return (GATE_UP && row >= 64 ? p.s1 : p.s0) + ((long long)it.e * p.out + n) * blocks * SC;
     };
     // the set's next block in the CTA's item number `k`
-    const int mine = (int)((items - blockIdx.x + gridDim.x - 1) / gridDim.x), span = 2 * pairs;
-    auto scales_at = [&](int k) { return scales_of(item(blockIdx.x + (long long)k * gridDim.x)); };
+    const int mine = (items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x, span = 2 * pairs;
+    auto scales_at = [&](int k) { return scales_of(item(blockIdx.x + k * gridDim.x)); };
     int k = 0, b = set;
     while (b >= span) b -= span, ++k;
     const bf16* sp = k < mine ? scales_at(k) : nullptr;
@@ -964,7 +994,7 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
     const uint32_t from = (uint32_t)(half * CODE_BYTES + row * 64);
     while (k < mine) {
       // the scales of the block after this one
-      const uint2 now = sc;
+      const uint2 raw = sc;
       int k_next = k, b_next = b + SETS;
       while (b_next >= span) b_next -= span, ++k_next;
       const bf16* sp_next = k_next == k ? sp : k_next < mine ? scales_at(k_next) : nullptr;
@@ -994,21 +1024,18 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
       if (real) {
         tc_fence_after();
         const uint32_t dst = tmem + lanes + C::A_BASE + (2 * buf + half) * A_COLS;
+        const uint2 now = spread_scales<G>(raw);
+        // -24 s of every run, and whether those are bf16 numbers themselves (an overflow is a NaN here)
+        const __nv_bfloat162 m24 = __float2bfloat162_rn(-24.f), zero = __float2bfloat162_rn(0.f);
+        const __nv_bfloat162 mx = __hmul2(pair_from(now.x), m24), my = __hmul2(pair_from(now.y), m24);
+        const bool exact = __hbeq2(__hfma2(pair_from(now.x), m24, __hneg2(mx)), zero) &&
+                           __hbeq2(__hfma2(pair_from(now.y), m24, __hneg2(my)), zero);
+        const bool all_exact = __all_sync(0xffffffffu, exact);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           unsigned r[32];
-#pragma unroll
-          for (int jj = 0; jj < 2; ++jj) {
-            const int j = 2 * h + jj;  // run of 32 inputs
-            const unsigned two = j < 2 ? now.x : now.y;
-            const __nv_bfloat162 sj = pair_from(__byte_perm(two, two, j & 1 ? 0x3232 : 0x1010));
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              const unsigned word = j == 0 ? w[v].x : j == 1 ? w[v].y : j == 2 ? w[v].z : w[v].w;
-#pragma unroll
-              for (int t = 0; t < 4; ++t) r[jj * 16 + v * 4 + t] = weights_of(word, t, sj);
-            }
-          }
+          if (all_exact) convert_half<true>(w, h, h ? now.y : now.x, bits_of(h ? my : mx), r);
+          else convert_half<false>(w, h, h ? now.y : now.x, 0, r);
           tmem_st32(dst + h * 32, r);
         }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -1026,7 +1053,7 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
     const int q = warp & 3;
     int n = 0;
     bool ok = true;  // after a wait that gave up the barriers between warps are still met
-    for (long long i = blockIdx.x; i < items; i += gridDim.x, ++n) {
+    for (int i = blockIdx.x; i < items; i += gridDim.x, ++n) {
       const Item it = item(i);
       const int a = n & 1;
       if (ok) ok = wait_lazily(accf(a), n / 2 & 1, &abort_flag, p);
