@@ -466,7 +466,7 @@ w4_rows_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ 
     if (!loading) return;
     if (load) {
       const int slot = issued % STAGES;
-      if (lane == 0) {
+      if (tc::elect_one()) {
         const uint32_t bar = tc::smem_u32(&bars[warp][slot]), dst = tc::smem_u32(ring + slot * STAGE_BYTES);
         tc::mbar_expect_tx(bar, STAGE_BYTES);
         tc::tma_load_2d(dst, &tm0, bar, load_pair * 2 * WORDS, load_row);
