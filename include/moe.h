@@ -501,7 +501,8 @@ MOE_API int moe_ckpt_swiglu(const int8_t* q, const uint8_t* scale, int rows, int
  *     with a = max |w| of the group, s = the least number of 5 significant bits >= a * (1 / 7) (both
  *     rounded to fp32), at least 2^-126; code = w / s (in fp32) rounded to the nearest
  *     integer, halves to even: -7..7.  code * s has at most 8 significant bits and is exact in
- *     bf16.  A value is off by at most s / 2, and s < 17/16 * a / 7 where that is above 2^-126.
+ *     bf16.  A value is off by at most s / 2 (1 + 2^-20), and s <= 17/16 * a / 7 * (1 + 2^-20) where that
+ *     is above 2^-126.
  *     A group that holds a NaN, an infinity or a magnitude of 2^127 or more has the scale NaN
  *     and is restored as NaN.
  *   q     [E, out, B * 16] 32-bit words, 8 codes (as code + 8) in each: inputs 128 b + 32 j + 8 v
@@ -509,7 +510,9 @@ MOE_API int moe_ckpt_swiglu(const int8_t* q, const uint8_t* scale, int rows, int
  *   scale [E, out, B * 128 / group] bf16
  *   Inputs past `in` (the last block's rest) are written as zeros.  E * rows * cols may pass
  *   2^31.  rows and cols multiples of 8 (bf16) or 4 (fp32), at most 2^23; E <= 65535.  q and scale
- *   of tensors made elsewhere may hold any codes (-8 too) and any finite bf16 scales.
+ *   of tensors made elsewhere may hold any codes (-8 too) and any bf16 scales below 2^125 in
+ *   magnitude (whose 8-fold is finite): where a scale has more than 5 significant bits, code * s is
+ *   rounded to bf16 by moe_w4_unpack to bf16 and by moe_expert_ffn_w4 with more than four rows an expert.
  */
 MOE_API int moe_w4_pack(const void* w, int E, int rows, int cols, int axis, int group, int dtype, uint32_t* q,
               void* scale, void* stream);
@@ -527,14 +530,16 @@ MOE_API int moe_w4_unpack(const uint32_t* q, const void* scale, int E, int rows,
  *   all with the same `group`.
  *   x, src_tok: the routed rows, as in moe_expert_ffn_gather (row r reads x[src_tok[r],:], x [T,H]);
  *   src_tok NULL: x is xs [rows,H], as in moe_expert_ffn, and T is not used.  An entry of src_tok
- *   outside [0,T) sets MOE_ERR_DEVICE_BOUNDS and counts as a row of zeros; so does a cu_seqlens that
- *   does not run from 0 to rows, whose offsets are read as if cut off there (rows of no expert are left).
+ *   outside [0,T) sets MOE_ERR_DEVICE_BOUNDS and counts as a row of zeros.  So does a cu_seqlens that
+ *   does not run from 0 to rows: offsets outside are read as if cut off there, and with one below the one before
+ *   it nothing is computed.  Rows of no expert are left as they are.
  *   act [rows,Hp], h [rows,H] dtype out.  Products are fp32 sums of bf16 rows and exact weights; act
- *   is rounded to dtype before the second product.  For few rows: each expert with rows has its
- *   weights read once for up to 64 of them.
+ *   is rounded to dtype before the second product.  For serving, from one row to a few hundred an
+ *   expert: the weights are read in 4 bits once for each 8 to 128 rows of an expert.
  *   dtype MOE_BF16; H and Hp multiples of 8, at most 2^20; E <= 1024.  Workspace:
- *   moe_workspace_bytes(MOE_OP_EXPERT_FFN_W4, T, H, E, K, Hp) bytes for rows = T * K (0: NULL).  Calls
- *   that may run at the same time need distinct workspaces.
+ *   moe_workspace_bytes(MOE_OP_EXPERT_FFN_W4, T, H, E, K, Hp) bytes for rows = T * K, with src_tok alone
+ *   (without it, or where it is 0: NULL).  Calls that may run at the same time need distinct
+ *   workspaces.  act and h overlap no other tensor of the call.
  */
 MOE_API int moe_expert_ffn_w4(const void* x, const int32_t* src_tok, int T, const int32_t* cu_seqlens, int rows,
               const uint32_t* q_gate, const void* s_gate, const uint32_t* q_up, const void* s_up, const uint32_t* q_down,
@@ -553,7 +558,8 @@ MOE_API int moe_expert_ffn_w4(const void* x, const int32_t* src_tok, int T, cons
  *   with fp32 sums, the diagonals of X X^T and of the polynomial fp32: for matrices of noise with
  *   some directions that stand out the result is within about 2e-3 of exact arithmetic (2-norm, relative).
  *   What is far below x's root mean square singular value (some 2^-11 of it) is not resolved: such
- *   directions come out small, not as in exact arithmetic.
+ *   directions come out small, not as in exact arithmetic.  With coefficients that let an element of X
+ *   pass 63 on the way that element is infinite.
  *   The norm neither over- nor underflows.  A matrix of zeros gives zeros; one that holds a NaN or
  *   an infinity gives NaN; the others of the batch are not touched by it.
  *   1 <= steps <= 64; a, b, c finite; eps >= 0, finite; 1 <= M, N <= 65536; E <= 65535.  Any M and N.

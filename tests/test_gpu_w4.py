@@ -204,6 +204,49 @@ def test_bad_indices_are_reported_and_the_rest_holds():
     check_ffn(x, src, short, ws, act[:15], h[:15], group)
 
 
+@pytest.mark.parametrize("T,E", [(3000, 700), (6000, 700)])
+def test_offsets_that_run_up_and_down_give_nothing(T, E):
+    """Every other expert would have all rows: 350 times as many as there are."""
+    H, Hp, group = 64, 32, 32
+    rng = np.random.default_rng(4)
+    ws = weights(E, H, Hp, group, rng)
+    x = synth.store(rng.standard_normal((T, H)), "bf16").host.to(DEV)
+    cu = np.where(np.arange(E + 1) % 2 == 1, T, 0).astype(np.int32)
+    cu[E] = T
+    act, h = ffn(x, None, torch.from_numpy(cu).to(DEV), T, ws, E, H, Hp, group)
+    assert L.moe_last_device_error() == L.MOE_ERR_DEVICE_BOUNDS
+    assert (act == 55).all() and (h == 55).all()
+
+
+@pytest.mark.parametrize("T", [3, 40, 100])
+@pytest.mark.parametrize("size", ["fine", "huge", "tiny"])
+def test_scales_of_any_bits(T, size):
+    """Scales made elsewhere, of 8 significant bits: around 1, just below 2^125 (their 8-fold is finite, their 24-fold
+    is not), and down to subnormal ones.  Rows with one entry make each sum one weight times that entry."""
+    E, H, Hp, group = 1, 128, 64, 32
+    rng = np.random.default_rng(T)
+    ws = weights(E, H, Hp, group, rng)
+    lo, hi, entry = {"fine": (0x3f00, 0x4000, 2.0 ** 6), "huge": (0x7d80, 0x7e00, 2.0 ** -94),
+                     "tiny": (0x0011, 0x0180, 2.0 ** 94)}[size]
+    scale = torch.from_numpy(rng.integers(lo, hi, tuple(ws[1][1].shape)).astype(np.int16)).view(torch.bfloat16)
+    ws[1][1].copy_(scale)
+    ws[0][0].fill_(-1)  # gate: all codes 15, that is 7, and every product 7 * 8
+    ws[0][1].fill_(8 / entry)
+    at = rng.integers(0, H, T)
+    x = torch.zeros((T, H), dtype=torch.bfloat16)
+    x[torch.arange(T), torch.from_numpy(at)] = entry
+    cu = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+    act, _ = ffn(x.to(DEV), None, cu, T, ws, E, H, Hp, group)
+    assert L.moe_last_device_error() == L.MOE_OK
+    words = ws[1][0].cpu().numpy().astype(np.int64) & 0xffffffff
+    j, v, i = at // 32, at % 32 // 8, at % 8
+    code = (words[0][:, 4 * v + j] >> (4 * (i // 2) + 16 * (i % 2)) & 15) - 8
+    want = (56 / (1 + np.exp(-56.0)) * code * scale.double().numpy()[0][:, at // group] * entry).T
+    # the weight and act are rounded to bf16 (the form for few rows rounds act alone), fp32 in between
+    err = np.abs(act.double().cpu().numpy() - want)
+    assert (err <= np.abs(want) * (2 * 2.0 ** -8 + 2.0 ** -15)).all()
+
+
 def test_nan_scales_and_infinite_rows_stay_where_they_are():
     T, E, H, Hp, group = 6, 3, 128, 64, 32
     rng = np.random.default_rng(3)

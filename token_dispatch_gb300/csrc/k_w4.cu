@@ -273,8 +273,12 @@ struct Args {
   unsigned long long wait_limit;
 };
 
-// The tiles of N rows of all experts: before[e] = tiles of the experts before e.  Offsets that
-// do not run upwards from 0 to R are cut off there and reported.
+// Tiles of N rows that R rows of E experts make at most.
+inline long long most_tiles(int R, int E, int N) { return (long long)(E < R ? E : R) + R / N; }
+
+// The tiles of N rows of all experts: before[e] = tiles of the experts before e.  Offsets that do not begin with 0 and
+// end with R, or lie outside, are cut off there and reported.  Where they run downwards, experts would share rows
+// and make more tiles than most_tiles: there are none then.
 struct Tiles {
   int before[MAX_E + 1], row0[MAX_E], row1[MAX_E];
   int warp_sum[8];
@@ -285,6 +289,7 @@ __device__ __forceinline__ void count_tiles(Tiles& t, const int32_t* cu, int E, 
   constexpr int PER = MAX_E / 256;  // experts of a thread; the first 256 threads
   const int e0 = threadIdx.x * PER;
   int n[PER], sum = 0, incl = 0;
+  bool down = false;
   if (threadIdx.x < 256) {
     int at[PER + 1];
 #pragma unroll
@@ -293,7 +298,8 @@ __device__ __forceinline__ void count_tiles(Tiles& t, const int32_t* cu, int E, 
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
       const int a = min(max(at[k], 0), R), b = min(max(at[k + 1], a), R);
-      n[k] = e0 + k < E ? (b - a + N - 1) / N : 0;
+      n[k] = e0 + k < E && b > a ? (b - a - 1) / N + 1 : 0;
+      down |= e0 + k < E && at[k + 1] < at[k];
       sum += n[k];
       if (e0 + k < E) t.row0[e0 + k] = a, t.row1[e0 + k] = b;
     }
@@ -305,14 +311,15 @@ __device__ __forceinline__ void count_tiles(Tiles& t, const int32_t* cu, int E, 
     }
     if (lane == 31) t.warp_sum[warp] = incl;
   }
-  __syncthreads();
+  const bool none = __syncthreads_or(down) != 0;
+  if (none && threadIdx.x == 0 && blockIdx.x == 0) set_error(err, DEV_BOUNDS);
   if (threadIdx.x < 256) {
-    int run = incl - sum;
-    for (int w = 0; w < warp; ++w) run += t.warp_sum[w];
+    int run = none ? 0 : incl - sum;
+    for (int w = 0; w < warp && !none; ++w) run += t.warp_sum[w];
 #pragma unroll
     for (int k = 0; k < PER; ++k) {
       if (e0 + k <= E) t.before[e0 + k] = run;
-      run += n[k];
+      if (!none) run += n[k];
     }
     if (threadIdx.x == 255) t.before[E] = run;
   }
@@ -634,7 +641,7 @@ int launch_rows(const void* x, const void* q0, const void* q1, Args p, cudaStrea
     return MOE_ERR_CUDA;
   p.x = static_cast<const bf16*>(x);
   const int pairs = (blocks_of(p.in) + 1) / 2, strips = (p.out + STRIP - 1) / STRIP;
-  const long long slots = (p.E < p.R ? p.E : p.R) + (long long)(p.R / ROWS);  // at most
+  const long long slots = most_tiles(p.R, p.E, ROWS);
   const long long resident = (long long)RESIDENT * sm_count();
   if (slots * strips > 0x3fffffffll) return MOE_ERR_UNSUPPORTED;
   // Warps to a strip: more of them make the items finer, and each item costs its warps a meeting
@@ -1120,7 +1127,7 @@ int launch_ffn(const void* x, const void* q0, const void* q1, const Args& p, cud
       !map_rows(&tmx, x, p.x_rows, p.in, N))
     return MOE_ERR_CUDA;
   const long long strips = (p.out + WIDTH - 1) / WIDTH;
-  const long long items = ((long long)(p.E < p.R ? p.E : p.R) + p.R / N) * strips;  // at most
+  const long long items = most_tiles(p.R, p.E, N) * strips;
   const long long sms = sm_count();
   if (items > 0x3fffffffll) return MOE_ERR_UNSUPPORTED;
   auto k = w4_ffn_kernel<N, G, GATE_UP>;
