@@ -776,6 +776,18 @@ __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// whether all 128 threads of the epilogue say yes
+__device__ __forceinline__ bool all_of_epilogue(bool yes) {
+  unsigned ok = yes;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %0, 0;\n\t"
+      "barrier.cta.red.and.pred q, 3, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "+r"(ok)::"memory");
+  return ok != 0;
+}
+
 // R rows of one output a lane, `rows` of them there: neighbouring lanes swap, so that each writes two
 // neighbours of every other row.  The number of outputs is even.
 template <int R>
@@ -1041,9 +1053,13 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           unsigned r[32];
-          if (all_exact) convert_half<true>(w, h, h ? now.y : now.x, bits_of(h ? my : mx), r);
-          else convert_half<false>(w, h, h ? now.y : now.x, 0, r);
-          tmem_st32(dst + h * 32, r);
+          if (all_exact) {
+            convert_half<true>(w, h, h ? now.y : now.x, bits_of(h ? my : mx), r);
+            tmem_st32(dst + h * 32, r);
+          } else {
+            convert_half<false>(w, h, h ? now.y : now.x, 0, r);
+            tmem_st32(dst + h * 32, r);
+          }
         }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
@@ -1063,8 +1079,9 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
     for (int i = blockIdx.x; i < items; i += gridDim.x, ++n) {
       const Item it = item(i);
       const int a = n & 1;
-      if (ok) ok = wait_lazily(accf(a), n / 2 & 1, &abort_flag, p);
-      ok = __all_sync(0xffffffffu, ok);
+      // one warp looks, the others are woken by a barrier of the four
+      if (ok && warp == 2) ok = __all_sync(0xffffffffu, wait_lazily(accf(a), n / 2 & 1, &abort_flag, p));
+      ok = all_of_epilogue(ok);
       tc_fence_after();
       const uint32_t src = tmem + a * C::ACC_COLS + ((uint32_t)(q * 32) << 16);
       const int out = it.n0 + (GATE_UP ? q & 1 : q) * 32 + lane;

@@ -62,19 +62,21 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, vola
 }
 
 // The same for a role that others are well ahead of: it sleeps between its looks, so that it leaves its scheduler's
-// issue slots to the busy warps (a polling loop is some ten instructions a look).
+// issue slots to the busy warps.
 template <class P>
 __device__ __forceinline__ bool wait_lazily(uint32_t bar, uint32_t parity, volatile int* abort_flag, const P& p) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
-  for (;;) {
-    __nanosleep(100);
+  for (uint32_t it = 1;; ++it) {
+    __nanosleep(200);
     if (mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if ((unsigned long long)(clock64() - t0) > p.wait_limit) {
-      *abort_flag = 1;
-      set_error(p.err, DEV_TIMEOUT);
-      return false;
+    if ((it & 7u) == 0) {
+      if (*abort_flag) return false;
+      if ((unsigned long long)(clock64() - t0) > p.wait_limit) {
+        *abort_flag = 1;
+        set_error(p.err, DEV_TIMEOUT);
+        return false;
+      }
     }
   }
 }
