@@ -357,19 +357,23 @@ struct ItemSearch {
 };
 
 // ------------------------------------------------------ products of few rows ---
-// Weights are the MMA's A operand (16 outputs x 16 inputs), up to 8 NT routed rows its B operand, so a
-// weight is read and turned into bf16 once for all of an expert's rows in the tile.  A pair of codes
-// comes out of its word as w' = 128 + (q + 8) by a shift, a mask and an or (bf16 holds whole numbers up to 256).
-// For one tile of 8 rows  sum q x = sum w' x - 136 sum x,  the last term by an MMA whose A is -136 throughout and
-// that the others add to, saves the subtraction of each weight; for more rows that MMA would cost more
-// than subtracting once.  The group's scale is applied to its fp32 sums.
+// Weights are the MMA's A operand (16 outputs x 16 inputs), up to 8 routed rows its B operand, so a
+// weight is read and turned into bf16 once for the tile's rows.  A pair of codes comes out of its word as
+// w' = 128 + (q + 8) by a shift and a lop3 (bf16 holds whole numbers up to 256);
+// sum q x = sum w' x - 136 sum x,  and the last term, by an MMA whose A is -136 throughout and that the others add to,
+// saves the subtraction of each weight.  The group's scale is applied to its fp32 sums.
 //
 // An item is a strip of outputs (16 of gate and the same of up, or 32 of down) for one tile of rows.  WK
 // warps share its inputs, each every WK-th pair of blocks; their sums meet in shared memory in a
-// fixed order.  What bounds the kernel is the weights' way from memory, so each warp keeps a ring of
-// STAGES pairs of blocks in flight by TMA, across items.  (Loads into registers met two limits
-// before that one: the 64-byte pieces of 8 rows took the L1's tag stage, and too few of them were under way.)
+// fixed order.  The weights' way from memory comes first: each warp keeps a ring of STAGES pairs of blocks in
+// flight by TMA, across items.  (Loads into registers met two limits before that one: the 64-byte
+// pieces of 8 rows took the L1's tag stage, and too few of them were under way.)
 // The rows x are read through L1, where the strips of an expert find them again.
+//
+// Measured, with the second product: 1 row to each of 8 of 384 experts of 7168 x 2048, groups of 128, 56 us (3.2 TB/s of
+// codes and scales); 4 rows to each of 8 experts of 4096 x 14336, groups of 64, 188 us (4.0 TB/s).  The integer
+// pipe (55%) and the warp-level MMAs (33%) take turns in too few warps to hide each other; two or four tiles of rows a
+// weight, more warps with fewer registers (spills) and asking L2 for the weights ahead brought nothing.
 //
 // A stage holds 32 rows of 128 bytes, swizzled: 16-byte piece c of row r lies at c ^ (r & 7).  Lane
 // group g reads row 4 (g & 1) + g / 2 of each eight, so that the two rows which a quarter
@@ -680,8 +684,7 @@ int launch_rows(const void* x, const void* q0, const void* q1, Args p, cudaStrea
 // output, turns a block of its codes into 128 bf16 numbers in registers and stores them into its
 // lane's columns, where tcgen05.mma reads them.  Only the codes themselves and the rows x pass
 // through shared memory.  (With the bf16 weights there too, 16 KB written and read for every 4 KB of codes,
-// shared memory would bound the kernel at half the memory's rate; with warp-level MMAs fed from
-// registers the work around them did, measured: T = 1, E = 384 57 us, T = 64, E = 64 177 us.)
+// shared memory would bound the kernel at half the memory's rate.)
 //
 // A pair of codes comes out of its word as 16 + (q + 8) by a shift and a lop3 (the codes at the top of bf16's
 // mantissa), and  fma(16 + code, s, -24 s)  is the weight q s, rounded once: its two products are exact
@@ -690,11 +693,16 @@ int launch_rows(const void* x, const void* q0, const void* q1, Args p, cudaStrea
 // That is 12 operations for 8 weights, all on half-rate pipes, 8 on the integer one.
 //
 // Roles of a CTA, one to an SM: warp 0 loads codes (TMA), warp 1 issues the MMAs, warps 2 to 5 are the
-// epilogue, warps 6 to 21 convert (four sets of four warps, each every fourth block), warp 22 loads
+// epilogue, then SETS x 4 warps convert (each set every SETS-th block), and the last warp loads
 // the rows x.  All loops run over the same sequence of tiles and blocks, so loads and
 // conversion do not stop between tiles.  Every wait is bounded.
-constexpr int SETS = 4;
-constexpr int THREADS = 32 * (6 + 4 * SETS + 1);
+//
+// Measured, with the second product: 6 rows to each of 64 experts of 2048 x 1408, groups of 32, 90 us (3.5 TB/s of codes
+// and scales); 384 rows to each, groups of 128, 415 us (1.0 PFLOP/s).  A block of 128 x 128 weights takes some 650
+// cycles where memory would allow 370: the integer pipe is busy two thirds of the time (a third of that are items,
+// places and waits), and the scheduler that also has the MMA warp four fifths.  Six sets for N <= 64 (99 -> 97 us
+// against four; for 128 rows tensor memory has no room for what they would have ahead); shifts as products on
+// the other pipe 104 us; the scales asked for earlier, or through L2, nothing.
 constexpr int TILE = 128;                     // outputs of a tile
 constexpr int CODE_BYTES = TILE * BLOCK / 2;  // a block of codes of a tile
 constexpr int A_COLS = BLOCK / 2;             // tensor memory columns of a block of bf16 weights
@@ -702,9 +710,11 @@ template <int N>
 struct Cfg {
   // pairs of blocks that may be converted, and have their rows x loaded, ahead of the MMAs
   static constexpr int PAIRS = N <= 64 ? 3 : 2;
-  // Pairs of blocks of codes under way.  Two more than the above, so that a converting warp may ask for its next block's
-  // codes by their parity: the load before it in the same place is then known to have landed.
-  static constexpr int CODES = PAIRS + 2;
+  static constexpr int SETS = N <= 64 ? 6 : 4;
+  static constexpr int THREADS = 32 * (6 + 4 * SETS + 1);
+  // Pairs of blocks of codes under way.  As many more than the above as a converting warp's pairs are apart: it asks
+  // for its next block's codes by their parity, and the load before it in the same place is then known to have landed.
+  static constexpr int CODES = PAIRS + SETS / 2;
   static constexpr int X_BYTES = N * BLOCK * 2;  // a block of the rows: two halves of 64 inputs
   static constexpr int ACC_COLS = N < 32 ? 32 : N;
   static constexpr int A_BASE = 2 * ACC_COLS;
@@ -724,33 +734,26 @@ __device__ __forceinline__ unsigned weights_of(unsigned word, int t, __nv_bfloat
   if (EXACT) return bits_of(__hfma2(pair_from(v), s, minus24));
   return bits_of(__hmul2(__hsub2(pair_from(v), __float2bfloat162_rn(24.f)), s));
 }
-// 32 words of 64 inputs' weights, of which those of run j are w[v]'s component j
+// the 16 words of run j's weights, of which the codes are w[v]'s component j
 template <bool EXACT>
-__device__ __forceinline__ void convert_half(const uint4 (&w)[4], int h, unsigned scales, unsigned minus24,
-                                             unsigned (&r)[32]) {
+__device__ __forceinline__ void convert_run(const uint4 (&w)[4], int j, unsigned scales, unsigned minus24,
+                                            unsigned (&r)[16]) {
+  const __nv_bfloat162 s = pair_from(__byte_perm(scales, scales, j & 1 ? 0x3232 : 0x1010));
+  const __nv_bfloat162 m = pair_from(__byte_perm(minus24, minus24, j & 1 ? 0x3232 : 0x1010));
 #pragma unroll
-  for (int jj = 0; jj < 2; ++jj) {
-    const int j = 2 * h + jj;
-    const __nv_bfloat162 sj = pair_from(__byte_perm(scales, scales, jj ? 0x3232 : 0x1010));
-    const __nv_bfloat162 mj = pair_from(__byte_perm(minus24, minus24, jj ? 0x3232 : 0x1010));
+  for (int v = 0; v < 4; ++v) {
+    const unsigned word = j == 0 ? w[v].x : j == 1 ? w[v].y : j == 2 ? w[v].z : w[v].w;
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const unsigned word = j == 0 ? w[v].x : j == 1 ? w[v].y : j == 2 ? w[v].z : w[v].w;
-#pragma unroll
-      for (int t = 0; t < 4; ++t) r[jj * 16 + v * 4 + t] = weights_of<EXACT>(word, t, sj, mj);
-    }
+    for (int t = 0; t < 4; ++t) r[v * 4 + t] = weights_of<EXACT>(word, t, s, m);
   }
 }
-// 32 lanes x 32 columns of tensor memory
-__device__ __forceinline__ void tmem_st32(uint32_t at, const unsigned (&r)[32]) {
+// 32 lanes x 16 columns of tensor memory
+__device__ __forceinline__ void tmem_st16(uint32_t at, const unsigned (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(at)
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
       : "memory");
 }
 // D (+)= A B with A in tensor memory
@@ -818,12 +821,12 @@ __device__ __forceinline__ uint2 spread_scales(uint2 v) {
 }
 
 template <int N, int G, bool GATE_UP>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(Cfg<N>::THREADS, 1)
 w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ CUtensorMap tm1,
               const __grid_constant__ CUtensorMap tmx, const Args p) {
   using C = Cfg<N>;
   using namespace tc;
-  constexpr int WIDTH = GATE_UP ? TILE / 2 : TILE, SC = BLOCK / G;
+  constexpr int WIDTH = GATE_UP ? TILE / 2 : TILE, SC = BLOCK / G, SETS = C::SETS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* xs = smem + 2 * C::CODES * CODE_BYTES;
@@ -872,7 +875,8 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
   tc_fence_before();
   count_tiles<N>(tiles, p.cu, p.E, p.R, p.err);  // with barriers of the CTA
   tc_fence_after();
-  const uint32_t tmem = tmem_base_slot;
+  // All of tensor memory, which begins at 0: known here, its addresses stay in uniform registers.
+  constexpr uint32_t tmem = 0;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   ItemSearch search;
   auto item = [&](int i) { return search.at<N>(tiles, p.E, i, strips, WIDTH); };
@@ -959,13 +963,15 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
         // asked here, the answers for the next pair are there once this one's MMAs have been issued
         const bool next_x = mbar_test_wait(xf(next), (u + 1) / C::PAIRS & 1);
         const bool next_a = mbar_test_wait(af(next), (u + 1) / C::PAIRS & 1);
-        const uint32_t x = smem_u32(xs + 2 * buf * C::X_BYTES), w = tmem + C::A_BASE + 2 * buf * A_COLS;
+        // a descriptor holds its address in units of 16 bytes, in its low bits
+        const uint64_t x = smem_desc(smem_u32(xs + 2 * buf * C::X_BYTES), 16, 1024);
+        const uint32_t w = tmem + C::A_BASE + 2 * buf * A_COLS;
         const bool two = b + 1 < blocks;
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 2 * BLOCK / 16; ++k)
             if (k < BLOCK / 16 || two)
-              mma_tmem_a(d, w + k * 8, smem_desc(x + k / 4 * (N * 128) + k % 4 * 32, 16, 1024), IDESC, b > 0 || k > 0);
+              mma_tmem_a(d, w + k * 8, x + (k / 4 * (N * 128) + k % 4 * 32) / 16, IDESC, b > 0 || k > 0);
           tc_commit(done(buf));
         }
         ready = __all_sync(0xffffffffu, next_x && next_a);
@@ -1051,14 +1057,14 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
                            __hbeq2(__hfma2(pair_from(now.y), m24, __hneg2(my)), zero);
         const bool all_exact = __all_sync(0xffffffffu, exact);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          unsigned r[32];
+        for (int j = 0; j < 4; ++j) {
+          unsigned r[16];
           if (all_exact) {
-            convert_half<true>(w, h, h ? now.y : now.x, bits_of(h ? my : mx), r);
-            tmem_st32(dst + h * 32, r);
+            convert_run<true>(w, j, j < 2 ? now.x : now.y, bits_of(j < 2 ? mx : my), r);
+            tmem_st16(dst + j * 16, r);
           } else {
-            convert_half<false>(w, h, h ? now.y : now.x, 0, r);
-            tmem_st32(dst + h * 32, r);
+            convert_run<false>(w, j, j < 2 ? now.x : now.y, 0, r);
+            tmem_st16(dst + j * 16, r);
           }
         }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -1152,7 +1158,7 @@ int launch_ffn(const void* x, const void* q0, const void* q1, const Args& p, cud
     return MOE_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items < sms ? items : sms));
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = s;
   // the second product's CTAs start, and convert their first weights, while the first one's finish
@@ -1168,7 +1174,17 @@ int launch_ffn(const void* x, const void* q0, const void* q1, const Args& p, cud
   return launch_status();
 }
 
-// rows of a tile, by the mean of an expert's: the conversion of a weight costs the same for any number
+// Rows of a tile, by the mean of an expert's: the conversion of a weight costs the same for any number of rows, so a
+// tile should hold nearly all of an expert's, but its MMAs take the longer the wider it is.  Measured, in us, for
+// routings at random to 8 experts of 2048 x 5632, by the rows of a tile (ROWS: the warp-level form):
+//   mean   2   3   4   6   8  12  16  20  24  32  48  64  96
+//   ROWS  44  58  60  58  74  89  97
+//   16    50  56  60  60  60  64  79  89  93
+//   32    52  58  60  60  62  60  60  62  60  83  95
+//   64            64  64  64  64  64  64  64  64  67  89 103
+//   128           70  70  70  70  72  72  72  72  72  74  76
+// and for 6 rows to each of 64 experts of 2048 x 1408 113 (ROWS) against 97; 4 to each of 8 experts of
+// 4096 x 14336 188 against 202; one to 8 of 384 experts of 7168 x 2048 56 against 66.
 inline int tile_rows(int R, int E) {
   const int mean = R / E;
   return mean <= 4 ? ROWS : mean <= 8 ? 16 : mean <= 20 ? 32 : mean <= 48 ? 64 : 128;
