@@ -686,23 +686,23 @@ int launch_rows(const void* x, const void* q0, const void* q1, Args p, cudaStrea
 // through shared memory.  (With the bf16 weights there too, 16 KB written and read for every 4 KB of codes,
 // shared memory would bound the kernel at half the memory's rate.)
 //
-// A pair of codes comes out of its word as 16 + (q + 8) by a shift and a lop3 (the codes at the top of bf16's
-// mantissa), and  fma(16 + code, s, -24 s)  is the weight q s, rounded once: its two products are exact
-// within the fma, provided that 24 s is a bf16 number, as it is for every scale of 5 significant bits below 2^123.
-// A warp that meets other scales subtracts 24 and multiplies, with the same results, bit for bit, in more time.
-// That is 12 operations for 8 weights, all on half-rate pipes, 8 on the integer one.
+// The least bf16 numbers, subnormal ones and the first normal ones, are the multiples k 2^-133 for k < 256, with k as
+// their bits.  So a word masked to a pair of codes is a pair of numbers already, of code 2^-133 or (4 bits up)
+// code 2^-129, and  fma(code 2^-133, 2^133 s, -8 s)  is the weight q s, rounded once (not at all where s has 5
+// significant bits).  That is 9 operations for 8 weights, 5 of them on the integer pipe.  2^133 s is finite for |s| < 2^-5;
+// a warp that meets other scales makes 128 + code, subtracts 136 and multiplies, with the same result in 15 operations.
 //
 // Roles of a CTA, one to an SM: warp 0 loads codes (TMA), warp 1 issues the MMAs, warps 2 to 5 are the
 // epilogue, then SETS x 4 warps convert (each set every SETS-th block), and the last warp loads
 // the rows x.  All loops run over the same sequence of tiles and blocks, so loads and
 // conversion do not stop between tiles.  Every wait is bounded.
 //
-// Measured, with the second product: 6 rows to each of 64 experts of 2048 x 1408, groups of 32, 90 us (3.5 TB/s of codes
-// and scales); 384 rows to each, groups of 128, 415 us (1.0 PFLOP/s).  A block of 128 x 128 weights takes some 650
-// cycles where memory would allow 370: the integer pipe is busy two thirds of the time (a third of that are items,
-// places and waits), and the scheduler that also has the MMA warp four fifths.  Six sets for N <= 64 (99 -> 97 us
-// against four; for 128 rows tensor memory has no room for what they would have ahead); shifts as products on
-// the other pipe 104 us; the scales asked for earlier, or through L2, nothing.
+// Measured, with the second product: 6 rows to each of 64 experts of 2048 x 1408, groups of 32, 82 us (3.8 TB/s of codes
+// and scales); 384 rows to each, groups of 128, 404 us (1.05 PFLOP/s).  What bounds it for few rows are issue slots:
+// 73% of all and 84% of the scheduler's that also has the MMA warp, start and end of the launches included.  (With
+// 16 + code and fma(., s, -24 s), three more shifts a word, 90 us; with a subtraction and a product 92.)  Six sets
+// for N <= 64 (82 us against 85 with four; for 128 rows tensor memory has no room for what they would have ahead);
+// shifts as products on the other pipe, the scales asked for earlier or through L2, waits that sleep: nothing.
 constexpr int TILE = 128;                     // outputs of a tile
 constexpr int CODE_BYTES = TILE * BLOCK / 2;  // a block of codes of a tile
 constexpr int A_COLS = BLOCK / 2;             // tensor memory columns of a block of bf16 weights
@@ -725,26 +725,28 @@ struct Cfg {
 
 __device__ __forceinline__ unsigned bits_of(__nv_bfloat162 v) { return *reinterpret_cast<unsigned*>(&v); }
 __device__ __forceinline__ __nv_bfloat162 pair_from(unsigned v) { return *reinterpret_cast<__nv_bfloat162*>(&v); }
-// the weights of a word's pair t, (q, q') s; minus24 = -24 s, EXACT: that is what it is, unrounded
-template <bool EXACT>
-__device__ __forceinline__ unsigned weights_of(unsigned word, int t, __nv_bfloat162 s, __nv_bfloat162 minus24) {
-  const unsigned at3 = t == 0 ? word << 3 : word >> (4 * t - 3);
-  unsigned v;  // at3 & 0x00780078 | 0x41804180
-  asm("lop3.b32 %0, %1, 0x00780078, %2, 0xea;" : "=r"(v) : "r"(at3), "r"(0x41804180u));
-  if (EXACT) return bits_of(__hfma2(pair_from(v), s, minus24));
-  return bits_of(__hmul2(__hsub2(pair_from(v), __float2bfloat162_rn(24.f)), s));
-}
-// the 16 words of run j's weights, of which the codes are w[v]'s component j
-template <bool EXACT>
-__device__ __forceinline__ void convert_run(const uint4 (&w)[4], int j, unsigned scales, unsigned minus24,
-                                            unsigned (&r)[16]) {
+__device__ __forceinline__ __nv_bfloat162 times(__nv_bfloat162 v, float by) { return __hmul2(v, __float2bfloat162_rn(by)); }
+// The 16 words of run j's weights, of which the codes are w[v]'s component j and the scale is one of `scales`.
+// SMALL: |s| < 2^-5.
+template <bool SMALL>
+__device__ __forceinline__ void convert_run(const uint4 (&w)[4], int j, unsigned scales, unsigned (&r)[16]) {
   const __nv_bfloat162 s = pair_from(__byte_perm(scales, scales, j & 1 ? 0x3232 : 0x1010));
-  const __nv_bfloat162 m = pair_from(__byte_perm(minus24, minus24, j & 1 ? 0x3232 : 0x1010));
+  const __nv_bfloat162 s133 = times(times(s, 0x1p100f), 0x1p33f), s129 = times(s133, 0x1p-4f), minus8 = times(s, -8.f);
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
     const unsigned word = j == 0 ? w[v].x : j == 1 ? w[v].y : j == 2 ? w[v].z : w[v].w;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) r[v * 4 + t] = weights_of<EXACT>(word, t, s, m);
+    for (int t = 0; t < 4; ++t) {
+      unsigned x;
+      if (SMALL) {
+        x = (t < 2 ? word : word >> 8) & (t & 1 ? 0x00f000f0u : 0x000f000fu);
+        x = bits_of(__hfma2(pair_from(x), t & 1 ? s129 : s133, minus8));
+      } else {
+        x = ((word >> (4 * t)) & 0x000f000fu) | 0x43004300u;
+        x = bits_of(__hmul2(__hsub2(pair_from(x), __float2bfloat162_rn(136.f)), s));
+      }
+      r[v * 4 + t] = x;
+    }
   }
 }
 // 32 lanes x 16 columns of tensor memory
@@ -1050,20 +1052,17 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
         tc_fence_after();
         const uint32_t dst = tmem + lanes + C::A_BASE + (2 * buf + half) * A_COLS;
         const uint2 now = spread_scales<G>(raw);
-        // -24 s of every run, and whether those are bf16 numbers themselves (an overflow is a NaN here)
-        const __nv_bfloat162 m24 = __float2bfloat162_rn(-24.f), zero = __float2bfloat162_rn(0.f);
-        const __nv_bfloat162 mx = __hmul2(pair_from(now.x), m24), my = __hmul2(pair_from(now.y), m24);
-        const bool exact = __hbeq2(__hfma2(pair_from(now.x), m24, __hneg2(mx)), zero) &&
-                           __hbeq2(__hfma2(pair_from(now.y), m24, __hneg2(my)), zero);
-        const bool all_exact = __all_sync(0xffffffffu, exact);
+        const __nv_bfloat162 border = __float2bfloat162_rn(0x1p-5f);
+        const bool small = __hblt2(__habs2(pair_from(now.x)), border) && __hblt2(__habs2(pair_from(now.y)), border);
+        const bool all_small = __all_sync(0xffffffffu, small);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           unsigned r[16];
-          if (all_exact) {
-            convert_run<true>(w, j, j < 2 ? now.x : now.y, bits_of(j < 2 ? mx : my), r);
+          if (all_small) {
+            convert_run<true>(w, j, j < 2 ? now.x : now.y, r);
             tmem_st16(dst + j * 16, r);
           } else {
-            convert_run<false>(w, j, j < 2 ? now.x : now.y, 0, r);
+            convert_run<false>(w, j, j < 2 ? now.x : now.y, r);
             tmem_st16(dst + j * 16, r);
           }
         }
