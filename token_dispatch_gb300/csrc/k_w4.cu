@@ -758,6 +758,21 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const unsigned (&r)[16]) 
       "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
       : "memory");
 }
+// 32 lanes x 32 or 16 columns of sums
+__device__ __forceinline__ void sums_of(uint32_t at, float (&v)[32]) { tc::tmem_ld32(at, v); }
+__device__ __forceinline__ void sums_of(uint32_t at, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at)
+      : "memory");
+#pragma unroll
+  for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]);
+}
 // D (+)= A B with A in tensor memory
 __device__ __forceinline__ void mma_tmem_a(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -1078,6 +1093,7 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
     }
   } else {
     // -------------------------------------------------------------- epilogue
+    constexpr int R = N < 32 ? N : 32;  // rows of a round
     const int q = warp & 3;
     int n = 0;
     bool ok = true;  // after a wait that gave up the barriers between warps are still met
@@ -1093,27 +1109,28 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
       bf16* dst = p.y + (long long)it.r0 * p.out + out;
       const bool store = ok && out < p.out;
 #pragma unroll 1
-      for (int r0 = 0; r0 < it.rows; r0 += 32) {
-        float v[32];
-        tmem_ld32(src + r0, v);
+      for (int r0 = 0; r0 < it.rows; r0 += R) {
+        float v[R];
+        sums_of(src + r0, v);
         if (GATE_UP) {
           // gate's warp and up's give each other half of the rows, and each finishes the other half; two
           // places in turn save a barrier
+          constexpr int HALF = R / 2;
           float* ex_at = ex + ((r0 >> 5) & 1) * (4 * 512) + lane;
-          float y[16];
+          float y[HALF];
 #pragma unroll
-          for (int r = 0; r < 16; ++r) ex_at[q * 512 + r * 32] = q < 2 ? v[16 + r] : v[r];
+          for (int r = 0; r < HALF; ++r) ex_at[q * 512 + r * 32] = q < 2 ? v[HALF + r] : v[r];
           asm volatile("bar.sync %0, 64;" ::"r"(1 + (q & 1)) : "memory");
 #pragma unroll
-          for (int r = 0; r < 16; ++r) {
+          for (int r = 0; r < HALF; ++r) {
             const float other = ex_at[(q ^ 2) * 512 + r * 32];
-            const float g = q < 2 ? v[r] : other, u = q < 2 ? other : v[16 + r];
+            const float g = q < 2 ? v[r] : other, u = q < 2 ? other : v[HALF + r];
             y[r] = __fdividef(g, 1.f + __expf(-g)) * u;
           }
-          const int at = r0 + (q < 2 ? 0 : 16);
-          store_rows<16>(y, dst + (long long)at * p.out, p.out, it.rows - at, store);
+          const int at = r0 + (q < 2 ? 0 : HALF);
+          store_rows<HALF>(y, dst + (long long)at * p.out, p.out, it.rows - at, store);
         } else {
-          store_rows<32>(v, dst + (long long)r0 * p.out, p.out, it.rows - r0, store);
+          store_rows<R>(v, dst + (long long)r0 * p.out, p.out, it.rows - r0, store);
         }
       }
       // a tile of one round fills the first place again
