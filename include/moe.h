@@ -512,7 +512,7 @@ MOE_API int moe_ckpt_swiglu(const int8_t* q, const uint8_t* scale, int rows, int
  *   2^31.  rows and cols multiples of 8 (bf16) or 4 (fp32), at most 2^23; E <= 65535.  q and scale
  *   of tensors made elsewhere may hold any codes (-8 too) and any bf16 scales below 2^125 in
  *   magnitude (whose 8-fold is finite): where a scale has more than 5 significant bits, code * s is
- *   rounded to bf16 by moe_w4_unpack to bf16 and by moe_expert_ffn_w4 with more than four rows an expert.
+ *   rounded to bf16 by moe_w4_unpack to bf16, and by moe_expert_ffn_w4 but in its form for the fewest rows.
  */
 MOE_API int moe_w4_pack(const void* w, int E, int rows, int cols, int axis, int group, int dtype, uint32_t* q,
               void* scale, void* stream);

@@ -168,6 +168,29 @@ def test_ffn_matches_oracle(case, gather):
     assert torch.equal(act, again[0]) and torch.equal(h, again[1])
 
 
+@pytest.mark.parametrize("T", [1, 16])
+def test_few_rows_of_many_experts(T):
+    """One row to each of four experts, and about one to each of 64: either side of the rule that chooses the form
+    for up to four rows.  Against the restored weights (exact in fp32), in 64 bits."""
+    E, K, H, Hp, group = 64, 4, 1024, 1408, 32
+    rng = np.random.default_rng(50 + T)
+    assert (L.moe_workspace_bytes(L.MOE_OP_EXPERT_FFN_W4, T, H, E, K, Hp) > 0) == (T > 1)
+    cu, src = routed(T, E, K, rng)
+    gen = torch.Generator(device=DEV).manual_seed(T)
+    ws = []
+    for axis in (0, 0, 1):
+        w = torch.randn((E, H, Hp), generator=gen, device=DEV) / (Hp if axis else H) ** 0.5
+        q, s = pack(w, axis, group, "f32")
+        L.moe_w4_unpack(q, s, E, H, Hp, axis, group, L.MOE_F32, w)
+        ws.append((q, s, w))
+    x = torch.randn((T, H), generator=gen, device=DEV).bfloat16()
+    act, h = ffn(x, torch.from_numpy(src).to(DEV), torch.from_numpy(cu).to(DEV), T * K, ws, E, H, Hp, group)
+    assert L.moe_last_device_error() == L.MOE_OK
+    live = [e for e in range(E) if cu[e] < cu[e + 1]]
+    host = [(None, None, {e: to64(w[2][e]) for e in live}) for w in ws]
+    check_ffn(x, src, cu, host, act, h, group)
+
+
 def test_all_rows_on_one_expert():
     T, E, H, Hp, group = 300, 16, 256, 128, 64
     rng = np.random.default_rng(1)

@@ -265,7 +265,7 @@ struct Args {
   int x_rows;
   const int32_t* cu;
   int E, R, in, out;  // out: outputs of a tensor
-  int group;
+  int group, tile;  // tile: its rows
   const bf16 *s0, *s1;
   bf16* y;  // [R, out]
   int wk = 0;  // w4_rows_kernel: warps that share a strip of outputs
@@ -370,10 +370,10 @@ struct ItemSearch {
 // pieces of 8 rows took the L1's tag stage, and too few of them were under way.)
 // The rows x are read through L1, where the strips of an expert find them again.
 //
-// Measured, with the second product: 1 row to each of 8 of 384 experts of 7168 x 2048, groups of 128, 56 us (3.2 TB/s of
-// codes and scales); 4 rows to each of 8 experts of 4096 x 14336, groups of 64, 188 us (4.0 TB/s).  The integer
-// pipe (55%) and the warp-level MMAs (33%) take turns in too few warps to hide each other; two or four tiles of rows a
-// weight, more warps with fewer registers (spills) and asking L2 for the weights ahead brought nothing.
+// Measured, with the second product: one row to 8 of 384 experts of 7168 x 2048, groups of 128, 56 us (3.2 TB/s of
+// codes and scales).  The integer pipe (55%) and the warp-level MMAs (33%) take turns in too few warps to hide
+// each other; two or four tiles of rows a weight, more warps with fewer registers (spills) and asking L2 for the
+// weights ahead brought nothing.
 //
 // A stage holds 32 rows of 128 bytes, swizzled: 16-byte piece c of row r lies at c ^ (r & 7).  Lane
 // group g reads row 4 (g & 1) + g / 2 of each eight, so that the two rows which a quarter
@@ -693,16 +693,18 @@ int launch_rows(const void* x, const void* q0, const void* q1, Args p, cudaStrea
 // a warp that meets other scales makes 128 + code, subtracts 136 and multiplies, with the same result in 15 operations.
 //
 // Roles of a CTA, one to an SM: warp 0 loads codes (TMA), warp 1 issues the MMAs, warps 2 to 5 are the
-// epilogue, then SETS x 4 warps convert (each set every SETS-th block), and the last warp loads
-// the rows x.  All loops run over the same sequence of tiles and blocks, so loads and
+// epilogue, then SETS x 8 warps convert (a set takes every SETS-th pair of blocks, four warps a block), and the last
+// warp loads the rows x.  All loops run over the same sequence of tiles and blocks, so loads and
 // conversion do not stop between tiles.  Every wait is bounded.
 //
-// Measured, with the second product: 6 rows to each of 64 experts of 2048 x 1408, groups of 32, 82 us (3.8 TB/s of codes
-// and scales); 384 rows to each, groups of 128, 404 us (1.05 PFLOP/s).  What bounds it for few rows are issue slots:
-// 73% of all and 84% of the scheduler's that also has the MMA warp, start and end of the launches included.  (With
-// 16 + code and fma(., s, -24 s), three more shifts a word, 90 us; with a subtraction and a product 92.)  Six sets
-// for N <= 64 (82 us against 85 with four; for 128 rows tensor memory has no room for what they would have ahead);
-// shifts as products on the other pipe, the scales asked for earlier or through L2, waits that sleep: nothing.
+// Measured, with the second product: 4 rows to each of 8 experts of 4096 x 14336, groups of 64, 163 us (4.6 TB/s of codes
+// and scales); 6 to each of 64 experts of 2048 x 1408, groups of 32, 80 us (3.9); 384 to each, groups of 128, 406 us
+// (1.05 PFLOP/s).  What bounds it for few rows are issue slots: 72% of all and 83% of the scheduler's that also has the
+// MMA warp, start and end of the launches included.  (6 rows: with 16 + code and fma(., s, -24 s), three more shifts
+// a word, 90 us; with a subtraction and a product 92; a set of four warps for a whole pair 82 us for 54% of the
+// slots, as fewer warps wait longer.)  For 128 rows MMAs and conversion take turns: tensor memory has no room for a
+// third pair of blocks.  Shifts as products on the other pipe, the scales asked for earlier or through L2,
+// waits that sleep: nothing.
 constexpr int TILE = 128;                     // outputs of a tile
 constexpr int CODE_BYTES = TILE * BLOCK / 2;  // a block of codes of a tile
 constexpr int A_COLS = BLOCK / 2;             // tensor memory columns of a block of bf16 weights
@@ -710,11 +712,11 @@ template <int N>
 struct Cfg {
   // pairs of blocks that may be converted, and have their rows x loaded, ahead of the MMAs
   static constexpr int PAIRS = N <= 64 ? 3 : 2;
-  static constexpr int SETS = N <= 64 ? 6 : 4;
-  static constexpr int THREADS = 32 * (6 + 4 * SETS + 1);
-  // Pairs of blocks of codes under way.  As many more than the above as a converting warp's pairs are apart: it asks
-  // for its next block's codes by their parity, and the load before it in the same place is then known to have landed.
-  static constexpr int CODES = PAIRS + SETS / 2;
+  static constexpr int SETS = PAIRS;
+  static constexpr int THREADS = 32 * (6 + 8 * SETS + 1);
+  // Pairs of blocks of codes under way: two places for each set's, so that what lay in a place before is known to have
+  // been read when a set asks for its next codes by their parity.
+  static constexpr int CODES = 2 * SETS;
   static constexpr int X_BYTES = N * BLOCK * 2;  // a block of the rows: two halves of 64 inputs
   static constexpr int ACC_COLS = N < 32 ? 32 : N;
   static constexpr int A_BASE = 2 * ACC_COLS;
@@ -867,7 +869,7 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
     abort_flag = 0;
     for (int s = 0; s < C::CODES; ++s) {
       mbar_init(codef(s), 1);
-      mbar_init(codee(s), 8);  // the converting warps of two blocks
+      mbar_init(codee(s), 8);  // the warps of a set
     }
     for (int b = 0; b < C::PAIRS; ++b) {
       mbar_init(xf(b), 1);
@@ -934,7 +936,7 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
       }
     }
     if (lane == 0) drain_loads(codef, C::CODES, u);
-  } else if (warp == 6 + 4 * SETS) {
+  } else if (warp == 6 + 8 * SETS) {
     // ---------------------------------------------------------------- rows x
     if (!GATE_UP) asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows that gate and up left
     int u = 0;
@@ -1006,66 +1008,53 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
     }
   } else if (warp >= 6) {
     // ------------------------------------------------------------ conversion
-    const int set = (warp - 6) >> 2, q = warp & 3;
+    const int set = (warp - 6) >> 3, half = (warp - 6) >> 2 & 1, q = warp & 3;
     const int row = q * 32 + lane;  // of the tile, and lane of tensor memory
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
-    // The set's blocks are set, set + SETS, .. of the whole sequence, in which every item has an even number of
-    // blocks: the second one of its last pair may not exist, and is then met without being converted.  So the
-    // set's place in a pair stays the same, and its pairs are SETS / 2 apart.
-    constexpr int STEP = SETS / 2;
-    static_assert(SETS % 2 == 0 && STEP <= C::PAIRS && STEP <= C::CODES, "places advance by less than a round");
-    const int half = set & 1;
-    // places and phases of codes and of buffers
-    int s = (set >> 1) % C::CODES, buf = (set >> 1) % C::PAIRS;
-    uint32_t s_phase = 0, buf_phase = 1;
-    if ((set >> 1) >= C::PAIRS) buf_phase ^= 1;
+    // The set's pairs of blocks are set, set + SETS, .. of the whole sequence: always in the same place of tensor
+    // memory, and in one of two places of codes.  Four warps take a pair's first block, four its second one (if any).
+    static_assert(SETS == C::PAIRS && C::CODES == 2 * SETS, "a set's places");
+    const uint32_t at = tmem + lanes + C::A_BASE + (2 * set + half) * A_COLS;
+    const uint8_t* from = smem + (2 * set + half) * CODE_BYTES + row * 64;
     // the scales of this thread's output in an item (outputs behind the last one: the last one's)
     auto scales_of = [&](const Item& it) {
       const int n = min(it.n0 + (GATE_UP ? row & 63 : row), p.out - 1);
       return (GATE_UP && row >= 64 ? p.s1 : p.s0) + ((long long)it.e * p.out + n) * blocks * SC;
     };
-    // the set's next block in the CTA's item number `k`
-    const int mine = (items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x, span = 2 * pairs;
-    auto scales_at = [&](int k) { return scales_of(item(blockIdx.x + k * gridDim.x)); };
+    const int mine = (items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+    auto scales_at = [&](int k) { return k < mine ? scales_of(item(blockIdx.x + k * gridDim.x)) : nullptr; };
+    // the next pair of the set is number b of the CTA's item k
     int k = 0, b = set;
-    while (b >= span) b -= span, ++k;
-    const bf16* sp = k < mine ? scales_at(k) : nullptr;
+    while (b >= pairs) b -= pairs, ++k;
+    const bf16* sp = scales_at(k);
     uint2 sc = make_uint2(0, 0);
-    if (k < mine && b < blocks) sc = load_scales<G>(sp + b * SC);
-    bool landed = false;
-    const uint32_t from = (uint32_t)(half * CODE_BYTES + row * 64);
-    while (k < mine) {
-      // the scales of the block after this one
+    auto next_scales = [&]() {
+      if (sp && 2 * b + half < blocks) sc = load_scales<G>(sp + (2 * b + half) * SC);
+    };
+    next_scales();
+    for (int round = 0; k < mine; ++round) {
       const uint2 raw = sc;
-      int k_next = k, b_next = b + SETS;
-      while (b_next >= span) b_next -= span, ++k_next;
-      const bf16* sp_next = k_next == k ? sp : k_next < mine ? scales_at(k_next) : nullptr;
-      if (sp_next && b_next < blocks) sc = load_scales<G>(sp_next + b_next * SC);
-      const bool real = b < blocks;
-      uint4 w[4];
-      auto read = [&]() {
-        // 64 bytes of the row, in four pieces whose places are exchanged by the row's bits 1 and 2
-        const uint8_t* src = smem + 2 * s * CODE_BYTES + from;
-        if (real) {
-#pragma unroll
-          for (int v = 0; v < 4; ++v) w[v] = *reinterpret_cast<const uint4*>(src + ((v ^ (row >> 1 & 3)) << 4));
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(codee(s));
-      };
-      const bool early = landed;
-      if (early) read();
-      if (!__all_sync(0xffffffffu, wait_bounded(done(buf), buf_phase, &abort_flag, p))) break;
-      if (!early) {
-        if (!__all_sync(0xffffffffu, wait_bounded(codef(s), s_phase, &abort_flag, p))) break;
-        read();
+      const bool real = 2 * b + half < blocks;
+      b += SETS;
+      if (b >= pairs) {
+        do b -= pairs, ++k;
+        while (b >= pairs);
+        sp = scales_at(k);
       }
-      s += STEP;
-      if (s >= C::CODES) s -= C::CODES, s_phase ^= 1;
-      landed = mbar_test_wait(codef(s), s_phase);  // the answer is there after the conversion
+      next_scales();
+      const int second = round & 1, s = set + SETS * second;
+      if (!__all_sync(0xffffffffu, wait_bounded(codef(s), round >> 1 & 1, &abort_flag, p))) break;
+      // 64 bytes of the row, in four pieces whose places are exchanged by the row's bits 1 and 2
+      uint4 w[4];
+      if (real)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          w[v] = *reinterpret_cast<const uint4*>(from + 2 * SETS * second * CODE_BYTES + ((v ^ (row >> 1 & 3)) << 4));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(codee(s));
+      if (!__all_sync(0xffffffffu, wait_bounded(done(set), (round & 1) ^ 1, &abort_flag, p))) break;
+      tc_fence_after();
       if (real) {
-        tc_fence_after();
-        const uint32_t dst = tmem + lanes + C::A_BASE + (2 * buf + half) * A_COLS;
         const uint2 now = spread_scales<G>(raw);
         const __nv_bfloat162 border = __float2bfloat162_rn(0x1p-5f);
         const bool small = __hblt2(__habs2(pair_from(now.x)), border) && __hblt2(__habs2(pair_from(now.y)), border);
@@ -1075,21 +1064,17 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
           unsigned r[16];
           if (all_small) {
             convert_run<true>(w, j, j < 2 ? now.x : now.y, r);
-            tmem_st16(dst + j * 16, r);
+            tmem_st16(at + j * 16, r);
           } else {
             convert_run<false>(w, j, j < 2 ? now.x : now.y, r);
-            tmem_st16(dst + j * 16, r);
+            tmem_st16(at + j * 16, r);
           }
         }
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        tc_fence_before();
       }
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(af(buf));
-      buf += STEP;
-      if (buf >= C::PAIRS) buf -= C::PAIRS, buf_phase ^= 1;
-      landed = __all_sync(0xffffffffu, landed);
-      k = k_next, b = b_next, sp = sp_next;
+      if (lane == 0) mbar_arrive(af(set));
     }
   } else {
     // -------------------------------------------------------------- epilogue
@@ -1192,22 +1177,38 @@ int launch_ffn(const void* x, const void* q0, const void* q1, const Args& p, cud
 
 // Rows of a tile, by the mean of an expert's: the conversion of a weight costs the same for any number of rows, so a
 // tile should hold nearly all of an expert's, but its MMAs take the longer the wider it is.  Measured, in us, for
-// routings at random to 8 experts of 2048 x 5632, by the rows of a tile (ROWS: the warp-level form):
-//   mean   2   3   4   6   8  12  16  20  24  32  48  64  96
-//   ROWS  44  58  60  58  74  89  97
-//   16    50  56  60  60  60  64  79  89  93
-//   32    52  58  60  60  62  60  60  62  60  83  95
-//   64            64  64  64  64  64  64  64  64  67  89 103
-//   128           70  70  70  70  72  72  72  72  72  74  76
-// and for 6 rows to each of 64 experts of 2048 x 1408 113 (ROWS) against 97; 4 to each of 8 experts of
-// 4096 x 14336 188 against 202; one to 8 of 384 experts of 7168 x 2048 56 against 66.
-inline int tile_rows(int R, int E) {
+// routings at random to 8 experts of 2048 x 5632, by the rows of a tile:
+//   mean   5   6   8  12  16  20  24  32  48  64  96
+//   16    60  60  60  64  79  89  93
+//   32    62  60  62  60  60  62  60  83  95
+//   64    64  64  64  64  64  64  64  64  67  89 103
+//   128   70  70  70  70  72  72  72  72  72  74  76
+// Up to 4 rows the warp-level form (ROWS) finishes sooner what is small, as its items are finer and its start is
+// shorter; the other one does more in the same time.  Measured (ROWS, the other one):
+//   experts, T, K               items an SM  blocks an SM
+//   8 of 2048 x 5632, 8, 2              4.7            96     44   46
+//   12, 2                               5.2           106     59   53
+//   8 of 4096 x 14336, 1, 2             3.0           125     60   73
+//   2, 2                                5.3           223     94   88
+//   8, 2                               11.6           488    134  140
+//   16, 2                              13.2           556    212  173
+//   64 of 2048 x 1408, 2, 6             2.7            38     32   33
+//   4, 6                                5.0            69     50   44
+//   16, 6                              12.4           173     91   74
+//   384 of 7168 x 2048, 1, 8            4.6           140     61   64
+//   2, 8                                9.0           277    110  103
+//   48 of 1000 x 712, 64, 3             6.2            45     32   36
+inline int tile_rows(int R, int E, int H, int Hp) {
   const int mean = R / E;
-  return mean <= 4 ? ROWS : mean <= 8 ? 16 : mean <= 20 ? 32 : mean <= 48 ? 64 : 128;
+  if (mean > 4) return mean <= 8 ? 16 : mean <= 20 ? 32 : mean <= 48 ? 64 : 128;
+  const double active = E * (1 - exp(-(double)R / E));  // experts with rows, for a routing at random
+  const double gate_up = (Hp + TILE / 2 - 1) / (TILE / 2), down = (H + TILE - 1) / TILE;  // strips
+  const double items = active * (gate_up + down), blocks = active * (gate_up * blocks_of(H) + down * blocks_of(Hp));
+  return items < 4.8 * sm_count() || blocks < 64. * sm_count() ? ROWS : 16;
 }
 template <int G, bool GATE_UP>
 int launch_ffn_n(const void* x, const void* q0, const void* q1, const Args& p, cudaStream_t s) {
-  switch (tile_rows(p.R, p.E)) {
+  switch (p.tile) {
     case ROWS: return launch_rows<G, GATE_UP>(x, q0, q1, p, s);
     case 16: return launch_ffn<16, G, GATE_UP>(x, q0, q1, p, s);
     case 32: return launch_ffn<32, G, GATE_UP>(x, q0, q1, p, s);
@@ -1291,15 +1292,17 @@ int launch_w4_unpack(const void* q, const void* scale, int E, int rows, int cols
                            : w4::unpack<float>(q, scale, E, rows, cols, axis, group, w, s);
 }
 
-size_t expert_ffn_w4_ws_bytes(int rows, int H, int E) {
-  return w4::tile_rows(rows, E) >= 16 ? (size_t)rows * H * sizeof(bf16) : 0;
+size_t expert_ffn_w4_ws_bytes(int rows, int H, int E, int Hp) {
+  return w4::tile_rows(rows, E, H, Hp) >= 16 ? (size_t)rows * H * sizeof(bf16) : 0;
 }
 
 int launch_expert_ffn_w4(const void* x, const int32_t* src_tok, int T, const int32_t* cu, int rows, const void* q_gate,
                          const void* s_gate, const void* q_up, const void* s_up, const void* q_down, const void* s_down,
                          int E, int H, int Hp, int group, void* act, void* h, void* ws, cudaStream_t s) {
   if (rows == 0) return MOE_OK;
-  if (src_tok && w4::tile_rows(rows, E) >= 16) {
+  w4::Args a;
+  a.tile = w4::tile_rows(rows, E, H, Hp);
+  if (src_tok && a.tile >= 16) {
     w4::w4_gather_kernel<<<rows, 256, 0, s>>>(static_cast<const uint4*>(x), src_tok, T, H / 8, static_cast<uint4*>(ws),
                                               device_error_word());
     const int st = launch_status();
@@ -1307,7 +1310,6 @@ int launch_expert_ffn_w4(const void* x, const int32_t* src_tok, int T, const int
     x = ws;
     src_tok = nullptr;
   }
-  w4::Args a;
   a.src_tok = src_tok, a.x_rows = src_tok ? T : rows;
   a.cu = cu, a.E = E, a.R = rows, a.in = H, a.out = Hp, a.group = group;
   a.err = device_error_word(), a.wait_limit = tc::g_wait_limit;

@@ -88,7 +88,7 @@ size_t moe_workspace_bytes(int op, int T, int H, int E, int K, int Hp) {
     case MOE_OP_COMBINE_NORM_BWD: return H > 0 ? combine_norm_bwd_ws_bytes(T, H) : 0;
     case MOE_OP_EXPERT_FFN_W4: {
       const long long rows = (long long)T * K;
-      return H > 0 && E > 0 && Hp > 0 && rows <= 0x7fffffffll ? expert_ffn_w4_ws_bytes((int)rows, H, E) : 0;
+      return H > 0 && E > 0 && Hp > 0 && rows <= 0x7fffffffll ? expert_ffn_w4_ws_bytes((int)rows, H, E, Hp) : 0;
     }
     case MOE_OP_ORTHOGONALIZE:
     case MOE_OP_MUON_STEP: return H > 0 && E > 0 && Hp > 0 ? orthogonalize_ws_bytes(E, H, Hp) : 0;
@@ -302,7 +302,7 @@ int moe_expert_ffn_w4(const void* x, const int32_t* src_tok, int T, const int32_
     return MOE_ERR_MISALIGNED;
   if (dtype != MOE_BF16 || H % 8 != 0 || Hp % 8 != 0 || E > 1024 || H > (1 << 20) || Hp > (1 << 20))
     return MOE_ERR_UNSUPPORTED;
-  const size_t need = src_tok ? expert_ffn_w4_ws_bytes(rows, H, E) : 0;
+  const size_t need = src_tok ? expert_ffn_w4_ws_bytes(rows, H, E, Hp) : 0;
   if (rows > 0 && need > 0 && (!ws || ws_bytes < need)) return MOE_ERR_WORKSPACE;
   return launch_expert_ffn_w4(x, src_tok, T, cu_seqlens, rows, q_gate, s_gate, q_up, s_up, q_down, s_down, E, H, Hp,
                               group, act, h, ws, as_stream(stream));

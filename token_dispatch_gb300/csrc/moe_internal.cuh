@@ -170,7 +170,7 @@ int launch_w4_pack(const void* w, int E, int rows, int cols, int axis, int group
                    cudaStream_t s);
 int launch_w4_unpack(const void* q, const void* scale, int E, int rows, int cols, int axis, int group, int dtype,
                      void* w, cudaStream_t s);
-size_t expert_ffn_w4_ws_bytes(int rows, int H, int E);  // with src_tok alone
+size_t expert_ffn_w4_ws_bytes(int rows, int H, int E, int Hp);  // with src_tok alone
 int launch_expert_ffn_w4(const void* x, const int32_t* src_tok, int T, const int32_t* cu, int rows, const void* q_gate,
                          const void* s_gate, const void* q_up, const void* s_up, const void* q_down, const void* s_down,
                          int E, int H, int Hp, int group, void* act, void* h, void* ws, cudaStream_t s);
