@@ -37,24 +37,32 @@ __device__ __forceinline__ int shift_of(int i) { return 4 * (i >> 1) + 16 * (i &
 // fall below the least number the division itself is made.  Adding 1.5 * 2^23 + 8 rounds to an integer and leaves
 // code + 8 in the low bits.  (With a division, a rounding and a conversion for each value their pipes took three
 // times as long as the memory: 248 us for 64 x 2048 x 1408 bf16, axis 1.)
+//
+// Each sum's bits are 0x4b400000 + code + 8; shifted to their places they add up to the word and a constant.
 __device__ __forceinline__ unsigned word_of_codes(const float (&v)[8], float s) {
   if (isnan(s)) return 0x88888888u;
   unsigned x = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) x -= 0x4b400000u << shift_of(k);
   if (s < 1e-28f) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x |= (__float_as_uint(v[k] / s + 12582920.f) & 15u) << shift_of(k);
+    for (int k = 0; k < 8; ++k) x += __float_as_uint(v[k] / s + 12582920.f) << shift_of(k);
     return x;
   }
   const float y = 1.f / s;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const float q = v[k] * y;
-    x |= (__float_as_uint(fmaf(fmaf(-q, s, v[k]), y, q) + 12582920.f) & 15u) << shift_of(k);
+    x += __float_as_uint(fmaf(fmaf(-q, s, v[k]), y, q) + 12582920.f) * (1u << shift_of(k));
   }
   return x;
 }
 // magnitudes as integers: they order as the numbers do, with infinity and NaN above
 __device__ __forceinline__ unsigned max_abs(unsigned a, float v) { return max(a, __float_as_uint(v) & 0x7fffffffu); }
+
+// Measured, 64 x 2048 x 1408, group 32 (pack, unpack): bf16 axis 0 131 and 94 us (3.6 and 5.0 TB/s), axis 1 148 and 109;
+// fp32 axis 0 182 and 142 (4.6 and 5.9), axis 1 146 and 176.  Of bf16 the pipes of fp32 and integers bound the
+// packing, five and three operations a weight.
 
 // w [E, out, in]: a thread takes the 8 inputs of a word, the G / 8 lanes of a group share its largest; a CTA takes
 // COL_WORDS neighbours of all words.
@@ -137,12 +145,12 @@ __global__ void __launch_bounds__(ROW_NT) w4_pack_rows_kernel(const T* __restric
 #pragma unroll
     for (int k = 0; k < 32; ++k)
       raw[k] = o < out && k0 + k < in ? __ldg(reinterpret_cast<const unsigned*>(src + (long long)k * out)) : 0u;
+    {
+      unsigned a = 0;  // of bf16: the two columns' magnitudes as integers, side by side
 #pragma unroll
-    for (int c = 0; c < V; ++c) {
-      unsigned a = 0;
+      for (int k = 0; k < 32; ++k) a = V == 2 ? __vmaxu2(a, raw[k] & 0x7fff7fffu) : max(a, raw[k] & 0x7fffffffu);
 #pragma unroll
-      for (int k = 0; k < 32; ++k) a = max_abs(a, of4<T>(raw[k], c));
-      top[run][tx * V + c] = a;
+      for (int c = 0; c < V; ++c) top[run][tx * V + c] = V == 1 ? a : c ? a & 0xffff0000u : a << 16;
     }
     __syncthreads();  // and the words of the block before have been written
 #pragma unroll
@@ -174,6 +182,32 @@ __global__ void __launch_bounds__(ROW_NT) w4_pack_rows_kernel(const T* __restric
   }
 }
 
+__device__ __forceinline__ unsigned bits_of(__nv_bfloat162 v) { return *reinterpret_cast<unsigned*>(&v); }
+__device__ __forceinline__ __nv_bfloat162 pair_from(unsigned v) { return *reinterpret_cast<__nv_bfloat162*>(&v); }
+__device__ __forceinline__ __nv_bfloat162 times(__nv_bfloat162 v, float by) { return __hmul2(v, __float2bfloat162_rn(by)); }
+
+// Weights as bf16 numbers, two neighbours at a time.  The least bf16 numbers, subnormal ones and the first normal ones,
+// are the multiples k 2^-133 for k < 256, with k as their bits.  So a word masked to a pair of codes is a pair of numbers
+// already, of code 2^-133 or (4 bits up) code 2^-129, and  fma(code 2^-133, 2^133 s, -8 s)  is the weight q s, rounded
+// once (not at all where s has 5 significant bits).  2^133 s is finite for |s| < 2^-5; for other scales 128 + code is
+// made, 136 subtracted and the rest multiplied, with the same result in more operations.
+struct Scaled {
+  __nv_bfloat162 s, s133, s129, minus8;
+  __device__ __forceinline__ explicit Scaled(__nv_bfloat162 scale)
+      : s(scale), s133(times(times(scale, 0x1p100f), 0x1p33f)), s129(times(s133, 0x1p-4f)), minus8(times(scale, -8.f)) {}
+};
+__device__ __forceinline__ bool is_small(__nv_bfloat162 s) { return __hblt2(__habs2(s), __float2bfloat162_rn(0x1p-5f)); }
+// pair t of a word; SMALL: is_small(s.s)
+template <bool SMALL>
+__device__ __forceinline__ unsigned weights_of(unsigned word, int t, const Scaled& s) {
+  if (SMALL) {
+    const unsigned x = (t < 2 ? word : word >> 8) & (t & 1 ? 0x00f000f0u : 0x000f000fu);
+    return bits_of(__hfma2(pair_from(x), t & 1 ? s.s129 : s.s133, s.minus8));
+  }
+  const unsigned x = ((word >> (4 * t)) & 0x000f000fu) | 0x43004300u;
+  return bits_of(__hmul2(__hsub2(pair_from(x), __float2bfloat162_rn(136.f)), s.s));
+}
+
 // code + 8 under the exponent of 2^23 is the number 2^23 + code + 8
 __device__ __forceinline__ float value_of(unsigned word, int i, float s) {
   return (__uint_as_float(((word >> shift_of(i)) & 15u) | 0x4b000000u) - 8388616.f) * s;
@@ -201,6 +235,18 @@ w4_unpack_cols_kernel(const unsigned* __restrict__ q, const bf16* __restrict__ s
   for (int i = 0; i < COL_ITEMS; ++i) {
     const int c = at[i].word * 8;
     if (at[i].row >= rows || c >= in) continue;
+    if (sizeof(T) == 2) {
+      const Scaled sc(__nv_bfloat162(s[i], s[i]));
+      uint4 o;
+      if (is_small(sc.s))
+        o = make_uint4(weights_of<true>(x[i], 0, sc), weights_of<true>(x[i], 1, sc), weights_of<true>(x[i], 2, sc),
+                       weights_of<true>(x[i], 3, sc));
+      else
+        o = make_uint4(weights_of<false>(x[i], 0, sc), weights_of<false>(x[i], 1, sc), weights_of<false>(x[i], 2, sc),
+                       weights_of<false>(x[i], 3, sc));
+      *reinterpret_cast<uint4*>(w + at[i].row * in + c) = o;
+      continue;
+    }
     float v[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = value_of(x[i], k, to_f32(s[i]));
@@ -235,22 +281,32 @@ w4_unpack_rows_kernel(const unsigned* __restrict__ q, const bf16* __restrict__ s
     __syncthreads();
     if (o >= out) continue;
     unsigned mine[V][4];
-    float sv[V];
+    bf16 sv[V];
 #pragma unroll
     for (int c = 0; c < V; ++c) {
 #pragma unroll
       for (int v = 0; v < 4; ++v) mine[c][v] = words[tx * V + c][v * 4 + run];
-      sv[c] = to_f32(scales[tx * V + c][bb * sc + run * 32 / G]);
+      sv[c] = scales[tx * V + c][bb * sc + run * 32 / G];
     }
     T* dst = w + ((long long)e * in + k0) * out + o;
+    if (V == 2) {  // two neighbours of either column, then of either row (the number of rows is even)
+      const Scaled s0(__nv_bfloat162(sv[0], sv[0])), s1(__nv_bfloat162(sv[V - 1], sv[V - 1]));
+      auto put = [&](auto weights) {
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
-      if (k0 + k >= in) break;
-      if (V == 2) {
-        *reinterpret_cast<__nv_bfloat162*>(dst + (long long)k * out) = __floats2bfloat162_rn(
-            value_of(mine[0][k / 8], k % 8, sv[0]), value_of(mine[V - 1][k / 8], k % 8, sv[V - 1]));
-      } else {
-        dst[(long long)k * out] = from_f32<T>(value_of(mine[0][k / 8], k % 8, sv[0]));
+        for (int k = 0; k < 32; k += 2) {
+          if (k0 + k >= in) break;
+          const unsigned a = weights(mine[0][k / 8], k % 8 / 2, s0), b = weights(mine[V - 1][k / 8], k % 8 / 2, s1);
+          *reinterpret_cast<unsigned*>(dst + (long long)k * out) = __byte_perm(a, b, 0x5410);
+          *reinterpret_cast<unsigned*>(dst + (long long)(k + 1) * out) = __byte_perm(a, b, 0x7632);
+        }
+      };
+      if (is_small(s0.s) && is_small(s1.s)) put([](unsigned x, int t, const Scaled& s) { return weights_of<true>(x, t, s); });
+      else put([](unsigned x, int t, const Scaled& s) { return weights_of<false>(x, t, s); });
+    } else {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        if (k0 + k >= in) break;
+        dst[(long long)k * out] = from_f32<T>(value_of(mine[0][k / 8], k % 8, to_f32(sv[0])));
       }
     }
   }
@@ -686,11 +742,7 @@ int launch_rows(const void* x, const void* q0, const void* q1, Args p, cudaStrea
 // through shared memory.  (With the bf16 weights there too, 16 KB written and read for every 4 KB of codes,
 // shared memory would bound the kernel at half the memory's rate.)
 //
-// The least bf16 numbers, subnormal ones and the first normal ones, are the multiples k 2^-133 for k < 256, with k as
-// their bits.  So a word masked to a pair of codes is a pair of numbers already, of code 2^-133 or (4 bits up)
-// code 2^-129, and  fma(code 2^-133, 2^133 s, -8 s)  is the weight q s, rounded once (not at all where s has 5
-// significant bits).  That is 9 operations for 8 weights, 5 of them on the integer pipe.  2^133 s is finite for |s| < 2^-5;
-// a warp that meets other scales makes 128 + code, subtracts 136 and multiplies, with the same result in 15 operations.
+// The conversion (weights_of) is 9 operations for 8 weights, 5 of them on the integer pipe.
 //
 // Roles of a CTA, one to an SM: warp 0 loads codes (TMA), warp 1 issues the MMAs, warps 2 to 5 are the
 // epilogue, then SETS x 8 warps convert (a set takes every SETS-th pair of blocks, four warps a block), and the last
@@ -725,30 +777,15 @@ struct Cfg {
   static_assert(A_BASE + 2 * PAIRS * A_COLS <= 512, "tensor memory");
 };
 
-__device__ __forceinline__ unsigned bits_of(__nv_bfloat162 v) { return *reinterpret_cast<unsigned*>(&v); }
-__device__ __forceinline__ __nv_bfloat162 pair_from(unsigned v) { return *reinterpret_cast<__nv_bfloat162*>(&v); }
-__device__ __forceinline__ __nv_bfloat162 times(__nv_bfloat162 v, float by) { return __hmul2(v, __float2bfloat162_rn(by)); }
 // The 16 words of run j's weights, of which the codes are w[v]'s component j and the scale is one of `scales`.
-// SMALL: |s| < 2^-5.
 template <bool SMALL>
 __device__ __forceinline__ void convert_run(const uint4 (&w)[4], int j, unsigned scales, unsigned (&r)[16]) {
-  const __nv_bfloat162 s = pair_from(__byte_perm(scales, scales, j & 1 ? 0x3232 : 0x1010));
-  const __nv_bfloat162 s133 = times(times(s, 0x1p100f), 0x1p33f), s129 = times(s133, 0x1p-4f), minus8 = times(s, -8.f);
+  const Scaled s(pair_from(__byte_perm(scales, scales, j & 1 ? 0x3232 : 0x1010)));
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
     const unsigned word = j == 0 ? w[v].x : j == 1 ? w[v].y : j == 2 ? w[v].z : w[v].w;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      unsigned x;
-      if (SMALL) {
-        x = (t < 2 ? word : word >> 8) & (t & 1 ? 0x00f000f0u : 0x000f000fu);
-        x = bits_of(__hfma2(pair_from(x), t & 1 ? s129 : s133, minus8));
-      } else {
-        x = ((word >> (4 * t)) & 0x000f000fu) | 0x43004300u;
-        x = bits_of(__hmul2(__hsub2(pair_from(x), __float2bfloat162_rn(136.f)), s));
-      }
-      r[v * 4 + t] = x;
-    }
+    for (int t = 0; t < 4; ++t) r[v * 4 + t] = weights_of<SMALL>(word, t, s);
   }
 }
 // 32 lanes x 16 columns of tensor memory
@@ -1056,9 +1093,7 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
       tc_fence_after();
       if (real) {
         const uint2 now = spread_scales<G>(raw);
-        const __nv_bfloat162 border = __float2bfloat162_rn(0x1p-5f);
-        const bool small = __hblt2(__habs2(pair_from(now.x)), border) && __hblt2(__habs2(pair_from(now.y)), border);
-        const bool all_small = __all_sync(0xffffffffu, small);
+        const bool all_small = __all_sync(0xffffffffu, is_small(pair_from(now.x)) && is_small(pair_from(now.y)));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           unsigned r[16];
