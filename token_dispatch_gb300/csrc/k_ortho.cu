@@ -126,7 +126,7 @@ __device__ __forceinline__ Tile tile_of(int t, const Params& p, int per, uint32_
 // lanes to a piece; a lane's own row comes and goes through 2 KB of shared memory, where the four 16-byte
 // parts of a row are exchanged by the row's bits 1 and 2 (no bank conflicts).  (With a row to a lane in global
 // memory too, each access touched 32 lines, and the L1's tag stage took as long as the products: POLY at
-// 64 x 1408 x 1408 210 us.)
+// 64 x 1408 x 1408 210 us, so 140.)
 struct Piece {
   uint4 v[4];
 };
@@ -255,8 +255,10 @@ __device__ __forceinline__ void put_tile(const Result& r, const Place& p, const 
 }
 
 // The products on pairs of SMs: 256 x 256 tiles by the two-CTA MMA, TMA operands in a ring of
-// six stages, two accumulators in tensor memory so that the epilogue of a tile runs under the
-// next one's products.  Barriers as in the expert products' pair kernel: `full` the leader's
+// five or six stages, two accumulators in tensor memory so that the epilogue of a tile runs under the
+// next one's products.  Measured, 64 x 2048 x 1408 (m padded to 1536 by the tiles): GRAM 187 us, POLY 140, APPLY 325, the
+// tensor pipe 76, 63 and 88% busy; FINAL, whose epilogue reads and writes the weights, 440 with bf16 ones; the
+// whole momentum step 4.5 ms, of which its passes over gradient and momentum take 0.64 (at a copy's rate).  Barriers as in the expert products' pair kernel: `full` the leader's
 // (both CTAs' bytes), `empty` and `accf` each CTA's own, `acce` the leader's.  All waits are bounded.
 template <int MODE, int KIND = ORTHO>
 __global__ void __launch_bounds__(THREADS, 1) __cluster_dims__(2, 1, 1)
@@ -771,7 +773,7 @@ __global__ void __launch_bounds__(LOAD_NT) ns_load_kernel(const Source s, int M,
 // ------------------------------------------------------- small matrices ---
 // m <= 128 and n <= 512: a CTA takes a matrix from U to the result, X and D (then P) in shared memory and the sums in
 // tensor memory.  A step is a few thousand cycles of products and epilogues one after the other, where the chain of
-// kernels above costs three launches (8 x 128 x 256: 128 us in 18 launches).  X lies as 64-column blocks of 128 rows of 128
+// kernels above costs three launches (8 x 128 x 256: 124 us in 18 launches, 39 here).  X lies as 64-column blocks of 128 rows of 128
 // bytes, 16-byte parts exchanged by the row's low bits: the tensor core reads such a block along its rows (GRAM) and
 // down its columns (APPLY).
 constexpr int SM_ROWS = 128, SM_COLS = 512;

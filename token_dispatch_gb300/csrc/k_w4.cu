@@ -642,7 +642,8 @@ w4_rows_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ 
       block(0);
       if (2 * pair + 1 < blocks) block(1);
       ++done;
-      __syncwarp();  // the slot has been read
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the slot has been read
+      __syncwarp();
       shift_scales();
       issue(ok);
     }
@@ -1087,6 +1088,8 @@ w4_ffn_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ C
 #pragma unroll
         for (int v = 0; v < 4; ++v)
           w[v] = *reinterpret_cast<const uint4*>(from + 2 * SETS * second * CODE_BYTES + ((v ^ (row >> 1 & 3)) << 4));
+      // the codes have been read, not just asked for, before a TMA may write their place again
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(codee(s));
       if (!__all_sync(0xffffffffu, wait_bounded(done(set), (round & 1) ^ 1, &abort_flag, p))) break;
