@@ -501,7 +501,11 @@ w4_rows_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ 
   uint8_t* ring = smem + warp * STAGES * STAGE_BYTES;
   float* red = reinterpret_cast<float*>(smem + NT_WARPS * STAGES * STAGE_BYTES);
 
-  if (threadIdx.x == 0) abort_flag = 0;
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    tc::prefetch_tmap(&tm0);
+    tc::prefetch_tmap(&tm1);
+  }
   if (lane == 0) {
     for (int s = 0; s < STAGES; ++s) tc::mbar_init(tc::smem_u32(&bars[warp][s]), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
