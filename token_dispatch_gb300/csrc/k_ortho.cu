@@ -81,6 +81,7 @@ struct Params {
   Result r;
   unsigned* err;
   unsigned long long wait_limit;
+  int halves = 0;          // 1: tiles of 128 columns (256 otherwise)
   int splits = 1;          // PART: parts of K
   float4* part = nullptr;  // their sums, [part][tile][256 / 128 rows][64 quads of columns][128 rows]
 };
@@ -105,7 +106,9 @@ __device__ __forceinline__ Tile tile_of(int t, const Params& p, int per, uint32_
   }
   w.index = t;
   w.e = t / per;
-  const int r = t - w.e * per;
+  int r = t - w.e * per;
+  const int half = r & p.halves;
+  r >>= p.halves;
   if (MODE == GRAM || MODE == POLY || MODE == PART) {  // column blocks from the left, i <= j in each
     int j = (int)((sqrtf(8.f * r + 1.f) - 1.f) * 0.5f);
     while (j * (j + 1) / 2 > r) --j;
@@ -118,7 +121,7 @@ __device__ __forceinline__ Tile tile_of(int t, const Params& p, int per, uint32_
     w.j = r / mt;
   }
   w.row0 = w.i * 2 * BM + (int)rank * BM;
-  w.n0 = w.j * BN;
+  w.n0 = w.j * BN + half * (BN / 2);
   return w;
 }
 
@@ -278,7 +281,7 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
   const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
-  const int per = tiles_per_matrix<MODE>(p.m, p.n);
+  const int per = tiles_per_matrix<MODE>(p.m, p.n) << p.halves;
   const int total = p.E * per * (MODE == PART ? p.splits : 1);
   const int K = FIRST ? p.n : p.m;
   const int cols = SYM ? p.m : p.n;
@@ -286,8 +289,8 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   // the blocks of K that a tile sums over
   auto k_begin = [&](const Tile& w) { return MODE == PART ? (int)((long long)kbs * w.split / p.splits) : 0; };
   auto k_end = [&](const Tile& w) { return MODE == PART ? (int)((long long)kbs * (w.split + 1) / p.splits) : kbs; };
-  // a tile with no more than 128 columns takes MMAs of half the width (and no use of half of its second operand)
-  auto narrow = [&](const Tile& w) { return cols - w.n0 <= BN / 2; };
+  // a tile with no more than 128 columns takes MMAs of half the width, and half of the second operand
+  auto narrow = [&](const Tile& w) { return p.halves || cols - w.n0 <= BN / 2; };
   // Whether a block of the first operand (rows of tile row i) or of the second is read as it lies in the transposed
   // place, [64 of K][rows] in two boxes of 64 rows: D and P below the diagonal, and X as APPLY's second operand.
   auto a_turned = [&](int i, int kb) { return !FIRST && kb / 4 < i; };
@@ -337,7 +340,8 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     const uint32_t full0 = cluster_addr(full_bar(0), 0);  // the leader's, 8 bytes apart
     for (int t = pair; ok && t < total; t += n_pairs) {
       const Tile w = tile_of<MODE>(t, p, per, rank);
-      const int b0 = w.n0 + (int)rank * (narrow(w) ? BN / 4 : BN / 2);
+      const bool half = narrow(w);
+      const int b0 = w.n0 + (int)rank * (half ? BN / 4 : BN / 2);
       for (int kb = k_begin(w); kb < k_end(w); ++kb) {
         ok = __all_sync(0xffffffffu, wait_bounded(empty_bar(stage), phase ^ 1u, &abort_flag, p));
         if (!ok) break;
@@ -345,7 +349,7 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         const uint32_t fb = full0 + 8 * stage;
         const bool at = a_turned(w.i, kb), bt = b_turned(w.j, kb);
         if (elect_one()) {
-          if (leader) mbar_expect_tx(full_bar(stage), 2 * STAGE_BYTES);
+          if (leader) mbar_expect_tx(full_bar(stage), half ? 2 * (STAGE_BYTES - OPERAND_BYTES / 2) : 2 * STAGE_BYTES);
           // the maps of the turned boxes: of D (POLY), of P and of X (APPLY: P's is tmA2)
           if (at) {
 #pragma unroll
@@ -357,7 +361,9 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           if (bt) {
 #pragma unroll
             for (int c = 0; c < 2; ++c)
-              tma_load_3d_pair(b_dst + c * (64 * BK * 2), &tmT, fb, b0 + c * 64, kb * BK, w.e);
+              if (c == 0 || !half) tma_load_3d_pair(b_dst + c * (64 * BK * 2), &tmT, fb, b0 + c * 64, kb * BK, w.e);
+          } else if (half) {  // the map of 64 rows, as it lies
+            tma_load_3d_pair(b_dst, &tmT, fb, kb * BK, b0, w.e);
           } else {
             tma_load_3d_pair(b_dst, &tmA, fb, kb * BK, b0, w.e);
           }
@@ -432,7 +438,7 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int CHUNKS = BN / 32 / 2;  // of 32 columns, of a warp
     const int q = warp & 3;  // TMEM lane quadrant of this warp
-    const int c_begin = ((warp - 2) >> 2) * CHUNKS;
+    const int n_chunks = CHUNKS >> p.halves, c_begin = ((warp - 2) >> 2) * n_chunks;
     uint8_t* stg = stage_out + (warp - 2) * Cfg<MODE>::WARP_BYTES;
     float* diag = reinterpret_cast<float*>(stg + 2048);  // POLY
     float* wide = reinterpret_cast<float*>(stg);         // FINAL
@@ -443,7 +449,7 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       const Tile w = tile_of<MODE>(t, p, per, rank);
       const int row0 = w.row0 + q * 32, row = row0 + lane;
       const bool row_ok = row < p.m;
-      const int c_end = min(c_begin + CHUNKS, (cols - w.n0 + 31) / 32);
+      const int c_end = min(c_begin + n_chunks, (cols - w.n0 + 31) / 32);
       // What the epilogue reads is asked for before the sums are waited for.
       const long long ldi = MODE == POLY ? p.lda : p.ldx;
       const __half* in = p.in + (long long)w.e * p.m * ldi;
@@ -1098,13 +1104,18 @@ int launch_next(void (*k)(P...), dim3 grid, int threads, size_t smem, cudaStream
 }
 
 template <int MODE, int KIND = ORTHO>
-int launch_gemm(const CUtensorMap& a, const CUtensorMap& t, const CUtensorMap& a2, const Params& p, cudaStream_t s) {
+int launch_gemm(const CUtensorMap& a, const CUtensorMap& t, const CUtensorMap& a2, Params p, cudaStream_t s) {
   auto k = ns_gemm_kernel<MODE, KIND>;
   constexpr size_t smem = Cfg<MODE>::SMEM;
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
     return MOE_ERR_CUDA;
-  const long long tiles = (long long)p.E * tiles_per_matrix<MODE>(p.m, p.n) * (MODE == PART ? p.splits : 1);
+  const long long whole = (long long)p.E * tiles_per_matrix<MODE>(p.m, p.n);
   long long pairs = sm_count() / 2;
+  // Tiles of half the columns where each still finds a pair of its own.  Five steps, in us, with whole tiles and so:
+  // 1 x 777 x 1001 178 and 139, 4 x 768 x 768 171 and 138, 1 x 512 x 512 143 and 114; with halves of up to as many
+  // whole tiles as pairs 2 x 2048 x 1408 288 against 260, 3 x 1001 x 777 166 against 162.
+  p.halves = MODE != PART && 2 * whole <= pairs;
+  const long long tiles = (whole << p.halves) * (MODE == PART ? p.splits : 1);
   if (tiles < pairs) pairs = tiles;
   return launch_next(k, dim3((unsigned)(2 * pairs)), THREADS, smem, s, a, t, a2, p);
 }
