@@ -84,6 +84,22 @@ def test_matches_oracle(shape, dtype):
     assert torch.equal(out, run(x, dtype))
 
 
+@pytest.mark.parametrize("shape", [(1, 100, 700), (1, 1, 600), (20, 129, 530), (40, 130, 257), (70, 257, 130), (1, 900, 384)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_few_and_many_tiles(shape):
+    """Matrices past what one CTA takes: few tiles, which are halved (a second half may be empty), more that are
+    whole, and the last with its sums split."""
+    u = synth.store(matrices(np.random.default_rng(sum(shape)), *shape) * 1e-3, "f32")
+    x = u.host.to(DEV)
+    out = run(x, "f32")
+    assert torch.equal(out, run(x, "f32"))
+    assert L.moe_last_device_error() == L.MOE_OK
+    got = to64(out)
+    for e in range(shape[0]):
+        exact, off = bound(u.ref[e])
+        assert np.linalg.norm(got[e] - exact) <= off + 2.0 ** -8 * np.linalg.norm(exact), e
+
+
 @pytest.mark.parametrize("steps,coef", [(1, COEF), (2, (1.5, -0.5, 0.0)), (12, (1.875, -1.25, 0.375))])
 def test_other_coefficients_and_steps(steps, coef):
     u = matrices(np.random.default_rng(5), 2, 96, 160)
@@ -131,7 +147,7 @@ def muon(w, g, m, dtype, beta=0.95, nesterov=True, lr=0.02, decay=0.1, scale=1.5
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("nesterov", [False, True])
-@pytest.mark.parametrize("shape", [(3, 64, 40), (2, 100, 257), (1, 301, 77), (2, 5, 3)],
+@pytest.mark.parametrize("shape", [(3, 64, 40), (2, 100, 257), (1, 301, 77), (2, 5, 3), (1, 300, 520), (30, 642, 130)],
                          ids=lambda s: "x".join(map(str, s)))
 def test_muon_step_matches_oracle(shape, nesterov, dtype):
     rng = np.random.default_rng(sum(shape) + nesterov)
