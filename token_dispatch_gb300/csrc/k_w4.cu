@@ -7,8 +7,8 @@
 // bf16.  Codes lie in blocks of 128 inputs, 16 words of 8 codes (the last block is padded with
 // zeros).  Word 4 j + w of a block (inputs 32 j + 8 w ..) is stored at w * 4 + j, and code i of a word in bits
 // 4 (i / 2) + 16 (i % 2): a lane of a warp-level MMA then reads 16 neighbouring bytes that hold its
-// inputs of four steps of 32, and every pair of neighbours comes out of a word by a shift and
-// a mask as two bf16 numbers 128 + (q + 8).
+// inputs of four steps of 32, and every pair of neighbours comes out of a word by a shift and a mask, each in a half
+// of its own.
 #include <math.h>
 
 #include "tc_ptx.cuh"
@@ -414,10 +414,11 @@ struct ItemSearch {
 
 // ------------------------------------------------------ products of few rows ---
 // Weights are the MMA's A operand (16 outputs x 16 inputs), up to 8 routed rows its B operand, so a
-// weight is read and turned into bf16 once for the tile's rows.  A pair of codes comes out of its word as
-// w' = 128 + (q + 8) by a shift and a lop3 (bf16 holds whole numbers up to 256);
-// sum q x = sum w' x - 136 sum x,  and the last term, by an MMA whose A is -136 throughout and that the others add to,
-// saves the subtraction of each weight.  The group's scale is applied to its fp32 sums.
+// weight is read and turned into bf16 once for the tile's rows.  A pair of codes comes out of its word by a mask and
+// an fma as two numbers q 2^-10: exact, so a code of 0 leaves no trace of its entry, and small enough that no
+// sum over a group of 128 leaves fp32's range while its result is inside.  (As numbers 128 + (q + 8), with 136 sum x
+// taken off by another MMA, an infinite x was NaN in every output, and an entry of 2^20 left errors of some 2^20 2^-16
+// scales everywhere.)  The group's scale is applied to its fp32 sums, 2^10 to the whole ones.
 //
 // An item is a strip of outputs (16 of gate and the same of up, or 32 of down) for one tile of rows.  WK
 // warps share its inputs, each every WK-th pair of blocks; their sums meet in shared memory in a
@@ -426,9 +427,9 @@ struct ItemSearch {
 // pieces of 8 rows took the L1's tag stage, and too few of them were under way.)
 // The rows x are read through L1, where the strips of an expert find them again.
 //
-// Measured, with the second product: one row to 8 of 384 experts of 7168 x 2048, groups of 128, 56 us (3.2 TB/s of
-// codes and scales).  The integer pipe (55%) and the warp-level MMAs (33%) take turns in too few warps to hide
-// each other; two or four tiles of rows a weight, more warps with fewer registers (spills) and asking L2 for the
+// Measured, with the second product: one row to 8 of 384 experts of 7168 x 2048, groups of 128, 50 us (3.6 TB/s of
+// codes and scales; 56 with the offset taken off by MMAs).  Conversion and warp-level MMAs take turns in too few warps to
+// hide each other; two or four tiles of rows a weight, more warps with fewer registers (spills) and asking L2 for the
 // weights ahead brought nothing.
 //
 // A stage holds 32 rows of 128 bytes, swizzled: 16-byte piece c of row r lies at c ^ (r & 7).  Lane
@@ -448,11 +449,12 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], const unsigned (&a)[4], 
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
-// codes of a word's pair t as bf16 numbers 128 + (q + 8)
+// codes of a word's pair t as bf16 numbers q 2^-10; masked they are the numbers code 2^-133 or code 2^-129 (see Scaled)
+constexpr float UNIT = 1024.f;
 __device__ __forceinline__ unsigned pair_of(unsigned word, int t) {
-  unsigned v;  // (word >> 4 t) & 0x000f000f | 0x43004300
-  asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(v) : "r"(word >> (4 * t)), "r"(0x43004300u));
-  return v;
+  const unsigned x = (t < 2 ? word : word >> 8) & (t & 1 ? 0x00f000f0u : 0x000f000fu);
+  // times 2^119 or 2^123, minus 2^-7
+  return bits_of(__hfma2(pair_from(x), pair_from(t & 1 ? 0x7b007b00u : 0x7d007d00u), pair_from(0xbc00bc00u)));
 }
 __device__ __forceinline__ unsigned word_of(const uint4& v, int j) {
   return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
@@ -619,14 +621,6 @@ w4_rows_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ 
 #pragma unroll
         for (int k = 0; k < SC; ++k) {
           float c[2][4] = {};
-          const unsigned minus136[4] = {0xc308c308u, 0xc308c308u, 0xc308c308u, 0xc308c308u};
-#pragma unroll
-          for (int j = k * RUNS; j < (k + 1) * RUNS; ++j) {
-            mma_bf16(c[0], minus136, xv[half][j].x, xv[half][j].y, c[0]);
-            mma_bf16(c[0], minus136, xv[half][j].z, xv[half][j].w, c[0]);
-          }
-#pragma unroll
-          for (int m = 0; m < 4; ++m) c[1][m] = c[0][m];
 #pragma unroll
           for (int j = k * RUNS; j < (k + 1) * RUNS; ++j)
 #pragma unroll
@@ -667,6 +661,7 @@ w4_rows_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ 
       for (int k = 0; k < wk; ++k)
 #pragma unroll
         for (int t = 0; t < 2; ++t) v[t] += strip[k * SUMS + (t * 4 + m) * 32];
+      v[0] *= UNIT, v[1] *= UNIT;
       const int r = 2 * tg + (m & 1), n = it.n0 + prow + 8 * (m >> 1);
       if (r >= it.rows) continue;
       bf16* dst = p.y + (long long)(it.r0 + r) * p.out;
