@@ -1,0 +1,24 @@
+"""Rules of the kernels' sources that no run can check: the cases that they are for must not come up on a GPU.  CPU only."""
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "token_dispatch_gb300", "csrc")
+
+
+def source(name):
+    """A source without its comments, on one line."""
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"\s+", " ", re.sub(r"//[^\n]*", "", f.read()))
+
+
+@pytest.mark.parametrize("name", ["k_ortho.cu", "k_w4.cu"])
+def test_warps_agree_on_the_end_of_a_wait_for_sums(name):
+    """A bounded wait that gives up may end differently in the lanes of a warp.  What follows a wait for sums in tensor
+    memory (tcgen05.ld, __syncwarp) is for the whole warp: it asks all lanes before it goes on or leaves."""
+    text = source(name)
+    waits = [m.start() for m in re.finditer(r"wait_(?:bounded|lazily)\((?:accf|dw_bar)", text)]
+    assert waits
+    for at in waits:
+        assert text[:at].endswith("__all_sync(0xffffffffu, "), text[at - 60:at + 60]

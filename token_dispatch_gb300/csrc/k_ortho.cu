@@ -479,7 +479,8 @@ ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       };
       Old<KIND> old[2];
       if (MODE == FINAL && c_begin < c_end) old[0].load(p.r, place(c_begin), lane);
-      if (!wait_bounded(accf_bar(acc), ((uint32_t)i >> 1) & 1u, &abort_flag, p)) break;
+      // all lanes or none: what follows is for the whole warp
+      if (!__all_sync(0xffffffffu, wait_bounded(accf_bar(acc), ((uint32_t)i >> 1) & 1u, &abort_flag, p))) break;
       tc_fence_after();
       const uint32_t tbase = tmem_base + acc * BN + ((uint32_t)(q * 32) << 16);
 #pragma unroll
