@@ -13,7 +13,7 @@ def source(name):
         return re.sub(r"\s+", " ", re.sub(r"//[^\n]*", "", f.read()))
 
 
-@pytest.mark.parametrize("name", ["k_ortho.cu", "k_w4.cu"])
+@pytest.mark.parametrize("name", ["k_ortho.cu", "k_w4.cu", "k_gemm_tc.cu"])
 def test_warps_agree_on_the_end_of_a_wait_for_sums(name):
     """A bounded wait that gives up may end differently in the lanes of a warp.  What follows a wait for sums in tensor
     memory (tcgen05.ld, __syncwarp) is for the whole warp: it asks all lanes before it goes on or leaves."""

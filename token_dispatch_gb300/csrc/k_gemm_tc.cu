@@ -45,7 +45,8 @@
 // Every mbarrier wait is bounded: past the limit the kernel records
 // MOE_ERR_TIMEOUT in the device error word, raises an abort flag that the other
 // roles poll, waits (bounded) for its own copies and MMAs in flight, frees TMEM
-// and returns.
+// and returns.  The lanes of an epilogue warp agree on a wait's end, as what follows it
+// (tcgen05.ld, __syncwarp) is for the whole warp.
 #include "tc_ptx.cuh"
 
 namespace moe {
@@ -752,7 +753,7 @@ tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     int i = 0;
     for (int t = blockIdx.x; t < total_tiles; t += gridDim.x, ++i) {
       const int acc = i & 1;
-      if (!wait_bounded(accf_bar(acc), ((uint32_t)i >> 1) & 1u, &abort_flag, p)) break;
+      if (!__all_sync(0xffffffffu, wait_bounded(accf_bar(acc), ((uint32_t)i >> 1) & 1u, &abort_flag, p))) break;
       tc_fence_after();
       const Work wk = work(t);
       const TileInfo& ti = wk.ti;
@@ -1401,7 +1402,7 @@ tc_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
     int out_chunk = 0;  // grouped K: this warp's output chunks so far (staging tile rotation)
     for (int t = pair; t < total_tiles; t += n_pairs, ++i) {
       const int acc = i & 1;
-      if (!wait_bounded(accf_bar(acc), ((uint32_t)i >> 1) & 1u, &abort_flag, p)) break;
+      if (!__all_sync(0xffffffffu, wait_bounded(accf_bar(acc), ((uint32_t)i >> 1) & 1u, &abort_flag, p))) break;
       tc_fence_after();
       const PairWork wk = pair_work(t);
       const TileInfo& ti = wk.ti;
@@ -1728,7 +1729,7 @@ router_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
     if (do_dx) {
       for (int b = b_lo + eg, i = eg; b < b_hi; b += 2, i += 2) {
         const int acc = eg;
-        if (!wait_bounded(accf_bar(acc), ((uint32_t)i >> 1) & 1u, &abort_flag, p)) break;
+        if (!__all_sync(0xffffffffu, wait_bounded(accf_bar(acc), ((uint32_t)i >> 1) & 1u, &abort_flag, p))) break;
         tc_fence_after();
         TileInfo ti;
         ti.g = 0;
@@ -1741,7 +1742,7 @@ router_bwd_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_const
         mbar_arrive(acce_bar(acc));
       }
     }
-    if (do_dw && wait_bounded(dw_bar, 0, &abort_flag, p)) {
+    if (do_dw && __all_sync(0xffffffffu, wait_bounded(dw_bar, 0, &abort_flag, p))) {
       // TMEM lane = column h of W_r; dW[h, e] = hi + mid + lo (fixed order);
       // group eg writes experts 32 eg .. 32 eg + 31; a CTA without tokens
       // writes zeros
