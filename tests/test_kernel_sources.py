@@ -22,3 +22,14 @@ def test_warps_agree_on_the_end_of_a_wait_for_sums(name):
     assert waits
     for at in waits:
         assert text[:at].endswith("__all_sync(0xffffffffu, "), text[at - 60:at + 60]
+
+
+@pytest.mark.parametrize("name", ["k_ortho.cu", "k_w4.cu", "k_gemm_tc.cu"])
+def test_products_under_way_are_waited_for_before_tensor_memory_is_given_back(name):
+    """A kernel that gave up on a wait may still have products under way: it waits for them, with a limit of its own,
+    before it frees the tensor memory that they write."""
+    text = source(name)
+    spans = re.findall(r"tcgen05\.alloc.*?tcgen05\.dealloc", text)
+    assert spans and len(spans) == text.count("tcgen05.alloc")
+    for span in spans:
+        assert "DRAIN_LIMIT" in span, span[:80]

@@ -1030,6 +1030,12 @@ __global__ void __launch_bounds__(SM_NT, 1) ns_small_kernel(const SmallParams p)
       put_tile<KIND>(p.r, place, old, wide, lane);
     }
   }
+  if (!ok && warp == 0) {  // after a wait that gave up: nothing may still write the tensor memory that is freed
+    const long long t0 = clock64();
+    while (!mbar_try_wait(smem_u32(&bar), phase ^ 1u)) {
+      if ((unsigned long long)(clock64() - t0) > DRAIN_LIMIT) { set_error(p.err, DEV_TIMEOUT); break; }
+    }
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
