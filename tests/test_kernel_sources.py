@@ -33,3 +33,33 @@ def test_products_under_way_are_waited_for_before_tensor_memory_is_given_back(na
     assert spans and len(spans) == text.count("tcgen05.alloc")
     for span in spans:
         assert "DRAIN_LIMIT" in span, span[:80]
+
+
+def kernels(text):
+    """(signature, body) of every __global__ function of a source."""
+    for m in re.finditer(r"__global__", text):
+        head = text.index("{", m.start())
+        depth, at = 1, head + 1
+        while depth:
+            depth += {"{": 1, "}": -1}.get(text[at], 0)
+            at += 1
+        yield text[m.start():head], text[head:at]
+
+
+@pytest.mark.parametrize("name", ["k_ortho.cu", "k_combine_norm.cu"])
+def test_what_the_kernel_before_writes_is_not_read_as_constant(name):
+    """A kernel that begins while the one before it still writes waits for that one's end (griddepcontrol.wait) and then
+    reads what it left.  The read-only path (__ldg, or const __restrict__, which the compiler may read by it) is
+    defined for data that nobody writes during the kernel."""
+    constant = {"column_sums_kernel": {"w_post", "res_scale"}}  # what the caller gave
+    seen = 0
+    for head, body in kernels(source(name)):
+        if "griddepcontrol.wait" not in body:
+            continue
+        seen += 1
+        kernel = re.search(r"(\w+)\s*\($", head[:head.rindex("(") + 1]) or re.search(r"(\w+_kernel)", head)
+        allowed = constant.get(kernel.group(1), set())
+        read_only = set(re.findall(r"const \w+\s*\*\s*__restrict__ (\w+)", head)) - allowed
+        assert not read_only, (kernel.group(1), read_only)
+        assert "__ldg(" not in body, kernel.group(1)
+    assert seen

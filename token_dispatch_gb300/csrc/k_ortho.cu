@@ -705,9 +705,9 @@ __device__ __forceinline__ float2 factor_of(const double (&v)[3], double eps) {
   return make_float2(ldexpf(1.f, -(e / 2)), (float)ldexp(1024.0 / x, -(e - e / 2)));
 }
 
-// The factor of each matrix, a warp a matrix.
-__global__ void __launch_bounds__(32) ns_factor_kernel(const double* __restrict__ part, int parts, double eps,
-                                                       float2* __restrict__ factor) {
+// The factor of each matrix, a warp a matrix.  (Here and in what follows, what the kernel before wrote is read by plain
+// loads: it may still have been writing when this one began.)
+__global__ void __launch_bounds__(32) ns_factor_kernel(const double* part, int parts, double eps, float2* factor) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x;
@@ -729,14 +729,14 @@ constexpr int LT = 64;
 constexpr int LOAD_NT = 256;
 template <int FROM, bool VEC>
 __global__ void __launch_bounds__(LOAD_NT) ns_load_kernel(const Source s, int M, int N, bool tall, long long ldx,
-                                                          const float2* __restrict__ factor, __half* __restrict__ x) {
+                                                          const float2* factor, __half* x) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ __align__(16) __half tile[LT][LT + 4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.z;
   const int r0 = blockIdx.y * LT, c0 = blockIdx.x * LT;
   const long long base = (long long)e * M * N;
-  const float2 f = __ldg(factor + e);
+  const float2 f = factor[e];
   if (VEC) {
     const int rr = threadIdx.x >> 4, cc = (threadIdx.x & 15) * 4;
     float4 u[LT / 16];
