@@ -298,6 +298,7 @@ class MoDBuffers:
 def mod_forward(m: MoDBuffers, x, w_mod, w_router, w_gate, w_up, w_down, stream=None):
     """MoD + MoE forward: y = x + s * MoE(x) on the selected tokens, y = x elsewhere."""
     b = m.moe
+    _check_w4(b, w_gate, w_up, w_down)
     L.mod_select(x, w_mod, m.B, m.L, m.H, m.C, m.cdt, m.score, m.sel, m.sel_score, m.mask, m.x_sel,
                  m.y, stream=stream)
     moe_forward(b, m.x_sel, w_router, None, w_gate, w_up, w_down, stream=stream,
