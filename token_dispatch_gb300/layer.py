@@ -116,6 +116,21 @@ def _dtype_of(w):
     return L.MOE_F32 if w.dtype == torch.float32 else L.MOE_BF16
 
 
+def _check_three(what, tensors, n, device, types=(torch.float32, torch.bfloat16), optional=False):
+    """Three expert tensors (optional: or None, or raw addresses) that three calls, one after the other, are to take: what the
+    third one would refuse is refused before the first is made."""
+    if len(tensors) != 3:
+        raise ValueError(f"{what}: one for each of the three expert tensors")
+    for t in tensors:
+        if optional and (t is None or type(t) is int):
+            continue
+        if not torch.is_tensor(t):
+            raise ValueError(f"{what}: tensors, not {type(t).__name__}")
+        if t.dtype not in types or t.numel() < n or not t.is_contiguous() or t.device != device or t.data_ptr() % 16:
+            raise ValueError(f"{what}: contiguous 16-byte aligned tensors of {' or '.join(map(str, types))} and {n} "
+                             f"elements on {device}, not {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+
+
 class ExpertsW4:
     """The experts' three tensors [E, H, Hp] in 4 bits (moe_w4_pack), in the place of w_gate, w_up and
     w_down of moe_forward, mod_forward and moe_block_forward (as w_gate; w_up and w_down are then None).
@@ -135,6 +150,7 @@ class ExpertsW4:
         self.q_down, self.s_down = packed(H, Hp)
 
     def _each(self, w_gate, w_up, w_down):
+        _check_three("ExpertsW4", (w_gate, w_up, w_down), self.E * self.H * self.Hp, self.q_gate.device)
         return ((w_gate, 0, self.q_gate, self.s_gate), (w_up, 0, self.q_up, self.s_up),
                 (w_down, 1, self.q_down, self.s_down))
 
@@ -170,6 +186,9 @@ class ExpertMuon:
         tensors that the forward reads, written too."""
         if (b.E, b.H, b.Hp) != (self.E, self.H, self.Hp):
             raise ValueError("ExpertMuon: the buffers are of another layer's sizes")
+        n, dev = self.E * self.H * self.Hp, self.m_gate.device
+        _check_three("ExpertMuon", (w_gate, w_up, w_down), n, dev)
+        _check_three("ExpertMuon, low", low, n, dev, (torch.bfloat16,), optional=True)
         if scale is None:
             scale = 0.2 * math.sqrt(max(self.H, self.Hp))
         for w, dw, m, lo in ((w_gate, b.dw_gate, self.m_gate, low[0]), (w_up, b.dw_up, self.m_up, low[1]),
