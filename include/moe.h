@@ -563,8 +563,11 @@ MOE_API int moe_expert_ffn_w4(const void* x, const int32_t* src_tok, int T, cons
  *   The norm neither over- nor underflows.  A matrix of zeros gives zeros; one that holds a NaN or
  *   an infinity gives NaN; the others of the batch are not touched by it.
  *   1 <= steps <= 64; a, b, c finite; eps >= 0, finite; 1 <= M, N <= 65536; E <= 65535.  Any M and N.
- *   Workspace: moe_workspace_bytes(MOE_OP_ORTHOGONALIZE, 0, M, E, 0, N) bytes, about 4 to 8 bytes
- *   for each element of x.  Calls that may run at the same time need distinct workspaces.
+ *   Workspace: moe_workspace_bytes(MOE_OP_ORTHOGONALIZE, 0, M, E, 0, N) bytes.  With m = min(M, N) and n = max(M, N),
+ *   both rounded up to 64 where they count columns: 4 m (n + m) + 8 m + 6152 bytes a matrix (4 to 8 for each element of large
+ *   ones), and where up to 25 tiles of 256 x 256 of X X^T are too few for the GPU and n is long, one fp32 tile for
+ *   each of up to 76 parts (20 MB).  It is asked for at every size.  Calls that may run at the same time need distinct
+ *   workspaces.
  */
 MOE_API int moe_orthogonalize(const void* x, int E, int M, int N, int dtype, int steps, float a, float b, float c,
               float eps, void* out, void* ws, size_t ws_bytes, void* stream);
