@@ -558,8 +558,12 @@ MOE_API int moe_expert_ffn_w4(const void* x, const int32_t* src_tok, int T, cons
  *   with fp32 sums, the diagonals of X X^T and of the polynomial fp32: for matrices of noise with
  *   some directions that stand out the result is within about 2e-3 of exact arithmetic (2-norm, relative).
  *   What is far below x's root mean square singular value (some 2^-11 of it) is not resolved: such
- *   directions come out small, not as in exact arithmetic.  With coefficients that let an element of X
- *   pass 63 on the way that element is infinite.
+ *   directions come out small, not as in exact arithmetic.  Where they are most of them, that is the larger error: the
+ *   rounding of X puts noise into the empty directions of a matrix of low rank r (the gradient of an expert that had r
+ *   rows), and five steps with these coefficients make it up to 3.4445^5 = 485 times larger: 0.1 to 0.15 in the Frobenius
+ *   norm at any size, where the result has about sqrt(r).  Relative to it 0.15 for r = 1, 0.04 for 8, 0.02 for 64.
+ *   With coefficients that let an element of X, of X X^T off its diagonal or of the polynomial off its own pass 63 on the way,
+ *   that element is infinite.
  *   The norm neither over- nor underflows.  A matrix of zeros gives zeros; one that holds a NaN or
  *   an infinity gives NaN; the others of the batch are not touched by it.
  *   1 <= steps <= 64; a, b, c finite; eps >= 0, finite; 1 <= M, N <= 65536; E <= 65535.  Any M and N.

@@ -1,5 +1,5 @@
 """Matrices past what one CTA takes, through the whole chain of kernels: coefficients and step counts, sizes of numbers,
-zeros, NaN and infinities; each against float64."""
+zeros, NaN and infinities, and matrices of low rank; each against float64."""
 import numpy as np
 import pytest
 import torch
@@ -8,7 +8,7 @@ import oracle as O
 from token_dispatch_gb300 import _lib as L
 from token_dispatch_gb300 import synth
 from tests.gpu_util import DEV, to64
-from tests.test_gpu_ortho import COEF, EPS, held, matrices, muon, run
+from tests.test_gpu_ortho import COEF, EPS, bound, held, matrices, muon, run
 
 pytestmark = pytest.mark.gpu
 
@@ -110,3 +110,20 @@ def test_momentum_step_with_zeros_nan_and_infinities(M, N):
     assert (m_out[0] == 0).all() and got[1].isnan().all() and got[2].isnan().all()
     keep = np.float32(1 - float(np.float32(0.02)) * float(np.float32(0.1)))
     assert torch.equal(got[0], w[0] * float(keep))
+
+
+@pytest.mark.parametrize("rank", [1, 8, 64])
+@pytest.mark.parametrize("shape", [(2, 96, 160), (2, 200, 300), (1, 333, 257), (1, 384, 900), (1, 512, 768)],
+                         ids=lambda s: "x".join(map(str, s)) if isinstance(s, tuple) else str(s))
+def test_matrices_of_low_rank(shape, rank):
+    """What an expert's gradient is after a step in which it had few rows.  The roundings of X put noise into the
+    directions that should stay empty, and the steps make it larger: the bound is the model's of those roundings."""
+    rng = np.random.default_rng(rank)
+    u = np.float32(rng.standard_normal(shape[:2] + (rank,)) @ rng.standard_normal((shape[0], rank, shape[2])))
+    out = run(torch.from_numpy(u).to(DEV), "f32")
+    assert L.moe_last_device_error() == L.MOE_OK
+    got = to64(out)
+    for e in range(shape[0]):
+        exact, off = bound(np.float64(u[e]))
+        assert np.linalg.norm(got[e] - exact) <= off + 2.0 ** -8 * np.linalg.norm(exact), e
+    assert torch.equal(out, run(torch.from_numpy(u).to(DEV), "f32"))
