@@ -23,6 +23,11 @@ def w4_pack(w, axis, group):
         bad = ~(a < 2.0 ** 127)
         m, e = np.frexp((np.where(bad, 0, a) * (np.float32(1) / np.float32(7))).astype(np.float32).astype(np.float64))
         s = np.maximum(np.ldexp(np.ceil(m * 32), e - 5), 2.0 ** -126)
+        m, e = np.frexp(s)  # the number of 5 significant bits below s, where the group fits it without error
+        lo = s - np.ldexp(1.0, e - np.where(m > 0.5, 5, 6))
+        step = lo[..., None]
+        low = (lo >= 2.0 ** -126) & (7 * lo == a) & (np.rint(x / step) * step == x).all(axis=3)
+        s = np.where(low, lo, s)
         q = np.rint(np.where(bad[..., None], 0, x) / s[..., None].astype(np.float32))
     s[bad] = np.nan
     code = (q.astype(np.int64) + 8).reshape(E, out, B, 4, 4, 8)  # block, run of 32, word, input

@@ -30,6 +30,19 @@ __device__ __forceinline__ float scale_of(float amax) {
   const float s = __uint_as_float((__float_as_uint(amax * (1.f / 7.f)) + 0x7ffffu) & ~0x7ffffu);
   return fmaxf(s, 1.1754943508222875e-38f);
 }
+// That product lies above the 7th part where amax is 7 times a number of 5 bits with a significand of 1.375 or more:
+// the scale is then a step too large, and weights that were restored from codes would come out as others.  So a group
+// that fits the number below its scale without error takes that: the number, or 0 where there is none to be tried
+// (7% of the groups of 32 bf16 weights have one to be tried; 64 x 2048 x 1408 bf16, axis 1: 148 us without, 158 so).
+__device__ __forceinline__ float below(float s, float amax) {
+  const float lo = __uint_as_float(__float_as_uint(s) - 0x80000u);
+  return lo >= 1.1754943508222875e-38f && 7.f * lo == amax ? lo : 0.f;
+}
+// whether v is k lo with a whole k, |v| <= 7 lo
+__device__ __forceinline__ bool fits(float v, float lo) {
+  const float k = v * __fdividef(1.f, lo) + 12582912.f - 12582912.f;
+  return k * lo == v;
+}
 __device__ __forceinline__ int shift_of(int i) { return 4 * (i >> 1) + 16 * (i & 1); }
 // A word of 8 codes.  w / s is the quotient rounded to fp32, and then to the nearest integer, halves to even.  It is
 // formed by Markstein's theorem (IBM J. Res. Dev. 34, 1990): with y = 1 / s rounded, q = w y and r = w - q s exact,
@@ -60,9 +73,9 @@ __device__ __forceinline__ unsigned word_of_codes(const float (&v)[8], float s) 
 // magnitudes as integers: they order as the numbers do, with infinity and NaN above
 __device__ __forceinline__ unsigned max_abs(unsigned a, float v) { return max(a, __float_as_uint(v) & 0x7fffffffu); }
 
-// Measured, 64 x 2048 x 1408, group 32 (pack, unpack): bf16 axis 0 131 and 94 us (3.6 and 5.0 TB/s), axis 1 148 and 109;
-// fp32 axis 0 182 and 142 (4.6 and 5.9), axis 1 146 and 176.  Of bf16 the pipes of fp32 and integers bound the
-// packing, five and three operations a weight.
+// Measured, 64 x 2048 x 1408, group 32 (pack, unpack): bf16 axis 0 126 and 93 us (3.8 and 5.1 TB/s), axis 1 158 and 108;
+// fp32 axis 0 152 and 141 (5.5 and 5.9), axis 1 152 and 176.  What bounds packing is that a warp's loads, conversion and
+// stores take turns: 48 registers for 59, so more warps, took axis 1 of bf16 from 164 to 158 us.
 
 // w [E, out, in]: a thread takes the 8 inputs of a word, the G / 8 lanes of a group share its largest; a CTA takes
 // COL_WORDS neighbours of all words.
@@ -84,34 +97,42 @@ __global__ void __launch_bounds__(COL_NT) w4_pack_cols_kernel(const T* __restric
   const int words = blocks * WORDS;
   const long long begin = (long long)blockIdx.x * COL_WORDS, first_row = begin / words;
   const int first_word = (int)(begin - first_row * words);
-  float v[COL_ITEMS][8];
-  Spot at[COL_ITEMS];
+  constexpr int N = Vec16<T>::N;
+  uint4 raw[COL_ITEMS][8 / N];  // unpacked one word at a time: more warps to an SM
 #pragma unroll
   for (int i = 0; i < COL_ITEMS; ++i) {
-    at[i] = spot_of(first_row, first_word, i * COL_NT + threadIdx.x, words);
-    const int c = at[i].word * 8;
+    const Spot at = spot_of(first_row, first_word, i * COL_NT + threadIdx.x, words);
+    const int c = at.word * 8;
 #pragma unroll
-    for (int k = 0; k < 8; k += Vec16<T>::N) {
-      if (at[i].row < rows && c + k < in) {
-        Vec16<T>::load(w + at[i].row * in + c + k, v[i] + k);
-      } else {
-#pragma unroll
-        for (int u = 0; u < Vec16<T>::N; ++u) v[i][k + u] = 0.f;
-      }
-    }
+    for (int k = 0; k < 8; k += N)
+      raw[i][k / N] = at.row < rows && c + k < in ? __ldg(reinterpret_cast<const uint4*>(w + at.row * in + c + k))
+                                                  : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
   for (int i = 0; i < COL_ITEMS; ++i) {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; k += N) Vec16<T>::load_raw_unpack(raw[i][k / N], v + k);
     unsigned top = 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) top = max_abs(top, v[i][k]);
+    for (int k = 0; k < 8; ++k) top = max_abs(top, v[k]);
 #pragma unroll
     for (int o = 1; o < G / 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (at[i].row >= rows) continue;
-    const float s = scale_of(__uint_as_float(top));
-    const int word = at[i].word, place = word % WORDS;
-    q[(at[i].row * blocks + word / WORDS) * WORDS + place % 4 * 4 + place / 4] = word_of_codes(v[i], s);
-    if (word % (G / 8) == 0) scale[at[i].row * (blocks * BLOCK / G) + word / (G / 8)] = __float2bfloat16_rn(s);
+    float s = scale_of(__uint_as_float(top));
+    const float lo = below(s, __uint_as_float(top));
+    bool all = lo > 0.f && fits(v[0], lo);
+    if (__any_sync(0xffffffffu, all)) {  // of other weights the first tells it nearly always
+#pragma unroll
+      for (int k = 1; k < 8; ++k) all = all && fits(v[k], lo);
+      // the lanes of this one's group
+      const unsigned group = ((1u << (G / 8)) - 1) << (threadIdx.x & 31 & ~(G / 8 - 1));
+      if ((__ballot_sync(0xffffffffu, all) & group) == group) s = lo;
+    }
+    const Spot at = spot_of(first_row, first_word, i * COL_NT + threadIdx.x, words);
+    if (at.row >= rows) continue;
+    const int word = at.word, place = word % WORDS;
+    q[(at.row * blocks + word / WORDS) * WORDS + place % 4 * 4 + place / 4] = word_of_codes(v, s);
+    if (word % (G / 8) == 0) scale[at.row * (blocks * BLOCK / G) + word / (G / 8)] = __float2bfloat16_rn(s);
   }
 }
 
@@ -134,6 +155,7 @@ __global__ void __launch_bounds__(ROW_NT) w4_pack_rows_kernel(const T* __restric
   constexpr int V = PER4<T>, COLS = 64 * V, SC = BLOCK / G;
   __shared__ unsigned words[COLS][WORDS + 1];
   __shared__ unsigned top[4][COLS];
+  __shared__ bool fit[4][COLS];
   __shared__ bf16 scales[COLS][ROW_BLOCKS * SC];
   const int tx = threadIdx.x & 63, run = threadIdx.x >> 6, e = blockIdx.z;
   const int o0 = blockIdx.x * COLS, o = o0 + tx * V, b0 = blockIdx.y * ROW_BLOCKS;
@@ -153,14 +175,43 @@ __global__ void __launch_bounds__(ROW_NT) w4_pack_rows_kernel(const T* __restric
       for (int c = 0; c < V; ++c) top[run][tx * V + c] = V == 1 ? a : c ? a & 0xffff0000u : a << 16;
     }
     __syncthreads();  // and the words of the block before have been written
+    constexpr int RUNS = G / 32;
+    const int r0 = run / RUNS * RUNS;
+    float scale_c[V], lower[V];
+    bool all[V], any = false;  // whether this thread's part of the column's group fits the lower scale
 #pragma unroll
     for (int c = 0; c < V; ++c) {
-      constexpr int RUNS = G / 32;
-      const int r0 = run / RUNS * RUNS;
       unsigned a = top[r0][tx * V + c];
 #pragma unroll
       for (int r = 1; r < RUNS; ++r) a = max(a, top[r0 + r][tx * V + c]);
-      const float s = scale_of(__uint_as_float(a));
+      scale_c[c] = scale_of(__uint_as_float(a));
+      lower[c] = below(scale_c[c], __uint_as_float(a));
+      all[c] = lower[c] > 0.f && fits(of4<T>(raw[0], c), lower[c]);
+      any |= all[c];
+    }
+    // Of other weights the first few tell it; a loop that reads them again keeps the registers and the code small.
+#pragma unroll 1
+    for (int k = 1; k < 32 && __any_sync(0xffffffffu, any); ++k) {
+      const unsigned x = o < out && k0 + k < in ? __ldg(reinterpret_cast<const unsigned*>(src + (long long)k * out)) : 0u;
+      any = false;
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        all[c] = all[c] && fits(of4<T>(x, c), lower[c]);
+        any |= all[c];
+      }
+    }
+    if (RUNS > 1) {
+#pragma unroll
+      for (int c = 0; c < V; ++c) fit[run][tx * V + c] = all[c];
+      __syncthreads();
+#pragma unroll
+      for (int c = 0; c < V; ++c)
+#pragma unroll
+        for (int r = 0; r < RUNS; ++r) all[c] = all[c] && fit[r0 + r][tx * V + c];
+    }
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      const float s = all[c] ? lower[c] : scale_c[c];
       if (run == r0) scales[tx * V + c][bb * SC + run / RUNS] = __float2bfloat16_rn(s);
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
