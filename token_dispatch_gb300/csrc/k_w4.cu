@@ -74,8 +74,9 @@ __device__ __forceinline__ unsigned word_of_codes(const float (&v)[8], float s) 
 __device__ __forceinline__ unsigned max_abs(unsigned a, float v) { return max(a, __float_as_uint(v) & 0x7fffffffu); }
 
 // Measured, 64 x 2048 x 1408, group 32 (pack, unpack): bf16 axis 0 126 and 93 us (3.8 and 5.1 TB/s), axis 1 158 and 108;
-// fp32 axis 0 152 and 141 (5.5 and 5.9), axis 1 152 and 176.  What bounds packing is that a warp's loads, conversion and
-// stores take turns: 48 registers for 59, so more warps, took axis 1 of bf16 from 164 to 158 us.
+// fp32 axis 0 152 and 141 (5.5 and 5.9), axis 1 152 and 176.  Of bf16 along axis 1 issue slots (78%) and the integer pipe
+// (75%) bound the packing, along axis 0 that a warp's loads, conversion and barriers take turns (68% and 63%, 24 warps an
+// SM).  Two words a lane unpacked at a time instead of four: 59 -> 48 registers, axis 1 of bf16 164 -> 158 us.
 
 // w [E, out, in]: a thread takes the 8 inputs of a word, the G / 8 lanes of a group share its largest; a CTA takes
 // COL_WORDS neighbours of all words.
@@ -479,8 +480,8 @@ struct ItemSearch {
 // The rows x are read through L1, where the strips of an expert find them again.
 //
 // Measured, with the second product: one row to 8 of 384 experts of 7168 x 2048, groups of 128, 50 us (3.6 TB/s of
-// codes and scales; 56 with the offset taken off by MMAs).  Conversion and warp-level MMAs take turns in too few warps to
-// hide each other; two or four tiles of rows a weight, more warps with fewer registers (spills) and asking L2 for the
+// codes and scales; 56 with the offset taken off by MMAs).  Loads under way, the integer pipe (44%, 34% in the second product)
+// and the warp-level MMAs (22%, 17%) take turns in 16 warps an SM, too few to hide each other; two or four tiles of rows a weight, more warps with fewer registers (spills) and asking L2 for the
 // weights ahead brought nothing.
 //
 // A stage holds 32 rows of 128 bytes, swizzled: 16-byte piece c of row r lies at c ^ (r & 7).  Lane
@@ -800,10 +801,10 @@ int launch_rows(const void* x, const void* q0, const void* q1, Args p, cudaStrea
 // warp loads the rows x.  All loops run over the same sequence of tiles and blocks, so loads and
 // conversion do not stop between tiles.  Every wait is bounded.
 //
-// Measured, with the second product: 4 rows to each of 8 experts of 4096 x 14336, groups of 64, 163 us (4.6 TB/s of codes
-// and scales); 6 to each of 64 experts of 2048 x 1408, groups of 32, 80 us (3.9); 384 to each, groups of 128, 406 us
-// (1.05 PFLOP/s).  What bounds it for few rows are issue slots: 72% of all and 83% of the scheduler's that also has the
-// MMA warp, start and end of the launches included.  (6 rows: with 16 + code and fma(., s, -24 s), three more shifts
+// Measured, with the second product: 4 rows to each of 8 experts of 4096 x 14336, groups of 64, 166 us (4.5 TB/s of codes
+// and scales); 6 to each of 64 experts of 2048 x 1408, groups of 32, 80 us (3.9); 384 to each, groups of 128, 404-420 us
+// (1.03 PFLOP/s).  What bounds it for few rows are issue slots: 65 to 75% of all and 72 to 93% of the scheduler's that also
+// has the MMA warp, start and end of the launches included.  (6 rows: with 16 + code and fma(., s, -24 s), three more shifts
 // a word, 90 us; with a subtraction and a product 92; a set of four warps for a whole pair 82 us for 54% of the
 // slots, as fewer warps wait longer.)  For 128 rows MMAs and conversion take turns: tensor memory has no room for a
 // third pair of blocks.  Shifts as products on the other pipe, the scales asked for earlier or through L2,
@@ -1274,18 +1275,26 @@ int launch_ffn(const void* x, const void* q0, const void* q1, const Args& p, cud
 // Up to 4 rows the warp-level form (ROWS) finishes sooner what is small, as its items are finer and its start is
 // shorter; the other one does more in the same time.  Measured (ROWS, the other one):
 //   experts, T, K               items an SM  blocks an SM
-//   8 of 2048 x 5632, 8, 2              4.7            96     44   46
-//   12, 2                               5.2           106     59   53
-//   8 of 4096 x 14336, 1, 2             3.0           125     60   73
-//   2, 2                                5.3           223     94   88
-//   8, 2                               11.6           488    134  140
-//   16, 2                              13.2           556    212  173
-//   64 of 2048 x 1408, 2, 6             2.7            38     32   33
-//   4, 6                                5.0            69     50   44
-//   16, 6                              12.4           173     91   74
-//   384 of 7168 x 2048, 1, 8            4.6           140     61   64
-//   2, 8                                9.0           277    110  103
-//   48 of 1000 x 712, 64, 3             6.2            45     32   36
+//   8 of 2048 x 5632, 8, 2              4.7            96     41   46
+//   12, 2                               5.2           106     57   52
+//   8 of 4096 x 14336, 1, 2             3.0           125     58   73
+//   2, 2                                5.3           223     87   87
+//   8, 2                               11.6           488    126  138
+//   16, 2                              13.2           556    195  173
+//   64 of 2048 x 1408, 2, 6             2.7            38     30   34
+//   4, 6                                5.0            69     46   44
+//   16, 6                              12.4           173     83   74
+//   384 of 7168 x 2048, 1, 8            4.6           140     56   63
+//   2, 8                                9.0           277     99  104
+//   4, 8                               17.9           552    170  168
+//   48 of 1000 x 712, 64, 3             6.2            45     30   37
+// (the rule costs up to 9% where it takes the slower one: 8 of 4096 x 14336 at 8 tokens).
+// Routings are at random there; a crowded expert takes several tiles, each of which converts its weights again, but few
+// experts do.  With one expert that has a third of all rows (rows of a tile 16, 32, 64, 128; the chosen one in brackets):
+//   64 of 2048 x 1408, T 64, K 6    [93]   92  102  117   (at random [88]  90  101  118)
+//   256, 6                          132   104 [110] 127   (149  94 [104] 125)
+//   512, 6                          236   151 [116] 138   (233 151 [105] 129)
+//   8 of 2048 x 5632, 64, 2          69  [60]  61   71   (70 [56]  60  70)
 inline int tile_rows(int R, int E, int H, int Hp) {
   const int mean = R / E;
   if (mean > 4) return mean <= 8 ? 16 : mean <= 20 ? 32 : mean <= 48 ? 64 : 128;
