@@ -500,8 +500,8 @@ MOE_API int moe_ckpt_swiglu(const int8_t* q, const uint8_t* scale, int rows, int
  *     every `group` (32, 64 or 128) neighbours along `axis` of one output share a scale;
  *     with a = max |w| of the group, s = the least number of 5 significant bits >= a * (1 / 7) (both
  *     rounded to fp32), at least 2^-126.  Where a is 7 times a lower such number, as 1 / 7 in fp32 is above 1/7, and
- *     every weight of the group is a whole multiple of it, s is that number: what moe_w4_unpack restored of a packed tensor
- *     packs to the same codes and scales.  code = w / s (in fp32) rounded to the nearest
+ *     every weight of the group is a whole multiple of it, s is that number: what moe_w4_unpack restored of a tensor
+ *     packed here (of magnitudes below 2^126) packs to the same codes and scales.  code = w / s (in fp32) rounded to the nearest
  *     integer, halves to even: -7..7.  code * s has at most 8 significant bits and is exact in
  *     bf16.  A value is off by at most s / 2 (1 + 2^-20), and s <= 17/16 * a / 7 * (1 + 2^-20) where that
  *     is above 2^-126.

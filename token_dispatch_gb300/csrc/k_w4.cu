@@ -470,7 +470,7 @@ struct ItemSearch {
 // an fma as two numbers q 2^-10: exact, so a code of 0 leaves no trace of its entry, and small enough that no
 // sum over a group of 128 leaves fp32's range while its result is inside.  (As numbers 128 + (q + 8), with 136 sum x
 // taken off by another MMA, an infinite x was NaN in every output, and an entry of 2^20 left errors of some 2^20 2^-16
-// scales everywhere.)  The group's scale is applied to its fp32 sums, 2^10 to the whole ones.
+// scales everywhere.  Sums below 2^-116 lose bits so, to 2^-140 or thereabouts; bf16 ends at 2^-133.)  The group's scale is applied to its fp32 sums, 2^10 to the whole ones.
 //
 // An item is a strip of outputs (16 of gate and the same of up, or 32 of down) for one tile of rows.  WK
 // warps share its inputs, each every WK-th pair of blocks; their sums meet in shared memory in a
